@@ -53,6 +53,18 @@ moe_status check_desc(const moe_layer_desc* D) {
   return MOE_OK;
 }
 
+moe_status check_norm(const moe_norm_desc* D) {
+  if (!D) return MOE_ERR_INVALID_ARG;
+  if (D->T < 0 || D->d <= 0) return MOE_ERR_INVALID_ARG;
+  if (D->kind != MOE_NORM_LAYER && D->kind != MOE_NORM_RMS) return MOE_ERR_INVALID_ARG;
+  if ((D->dtype != MOE_F32 && D->dtype != MOE_BF16) ||
+      (D->wdtype != MOE_F32 && D->wdtype != MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (!(D->eps >= 0.f) || !isfinite(D->eps)) return MOE_ERR_INVALID_ARG;
+  if (D->d > kNormMaxD || D->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 struct Ws {
   int* flags;
   float* logits;
@@ -587,6 +599,106 @@ moe_status moe_combine(const moe_layer_desc* desc, const void* y_perm, const int
   return cuda_status(launch_combine(desc->dtype, y_perm, slot_row, topk_w, residual, desc->T,
                                     desc->d, desc->k, desc->S, y,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dispatch_rows(const moe_layer_desc* desc, const void* x,
+                             const int32_t* expert_offsets, const int32_t* slot_row,
+                             void* x_perm, void* stream) {
+  const NvtxRange nvtx("moe_dispatch_rows");
+  const moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (desc->T == 0) return MOE_OK;
+  if (!x || !expert_offsets || !slot_row || !x_perm) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(expert_offsets) || !aligned16(slot_row) || !aligned16(x_perm))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_dispatch_rows(desc->dtype, x, slot_row,
+                                          expert_offsets + desc->E + desc->S, desc->T,
+                                          desc->k + desc->S, desc->d, x_perm,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dispatch_rows_backward(const moe_layer_desc* desc, const void* dx_perm,
+                                      const int32_t* slot_row, void* dx, void* stream) {
+  const NvtxRange nvtx("moe_dispatch_rows_backward");
+  const moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (desc->T == 0) return MOE_OK;
+  if (!dx_perm || !slot_row || !dx) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dx_perm) || !aligned16(slot_row) || !aligned16(dx)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_dispatch_rows_backward(desc->dtype, dx_perm, slot_row, desc->T,
+                                                   desc->d, desc->k + desc->S, dx,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_combine_backward(const moe_layer_desc* desc, const float* dy, const void* y_perm,
+                                const int32_t* expert_offsets, const int32_t* slot_row,
+                                const float* topk_w, void* dy_perm, float* dtopk_w,
+                                void* stream) {
+  const NvtxRange nvtx("moe_combine_backward");
+  const moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (desc->T == 0) return MOE_OK;
+  if (!dy || !expert_offsets || !slot_row || !dy_perm) return MOE_ERR_INVALID_ARG;
+  if (dtopk_w && (!topk_w || !y_perm)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(y_perm) || !aligned16(expert_offsets) ||
+      !aligned16(slot_row) || !aligned16(topk_w) || !aligned16(dy_perm) || !aligned16(dtopk_w))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_combine_backward(
+      desc->dtype, dy, y_perm, expert_offsets + desc->E + desc->S, slot_row, topk_w, desc->T,
+      desc->d, desc->k, desc->S, dy_perm, dtopk_w, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_norm_forward(const moe_norm_desc* desc, const void* x, const void* gamma,
+                            const void* beta, void* y, float* mean, float* rstd, void* stream) {
+  const NvtxRange nvtx("moe_norm_forward");
+  const moe_status st = check_norm(desc);
+  if (st != MOE_OK) return st;
+  if (desc->kind == MOE_NORM_RMS && (beta || mean)) return MOE_ERR_INVALID_ARG;
+  if (desc->T == 0) return MOE_OK;
+  if (!x || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) ||
+      !aligned16(mean) || !aligned16(rstd))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_norm_forward(*desc, x, gamma, beta, y, mean, rstd,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_norm_workspace_size(const moe_norm_desc* desc, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_norm(desc);
+  if (st != MOE_OK) return st;
+  *bytes = align256((size_t)norm_backward_blocks(*desc) * desc->d * 2 * sizeof(float));
+  return MOE_OK;
+}
+
+moe_status moe_norm_backward(const moe_norm_desc* desc, const void* dy, const void* x,
+                             const void* gamma, const float* mean, const float* rstd, void* dx,
+                             float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  const NvtxRange nvtx("moe_norm_backward");
+  const moe_status st = check_norm(desc);
+  if (st != MOE_OK) return st;
+  const bool rms = desc->kind == MOE_NORM_RMS;
+  if (rms && (dbeta || mean)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dgamma) || !aligned16(dbeta)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (desc->T == 0) {  // sums over no rows
+    for (float* sum : {dgamma, dbeta})
+      if (sum && cudaMemsetAsync(sum, 0, (size_t)desc->d * sizeof(float), s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!dy || !x || !rstd || !dx || (!rms && !mean)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(gamma) || !aligned16(mean) ||
+      !aligned16(rstd) || !aligned16(dx))
+    return MOE_ERR_INVALID_ARG;
+  if (dgamma || dbeta) {
+    size_t need = 0;
+    (void)moe_norm_workspace_size(desc, &need);
+    if (!workspace || !aligned16(workspace) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  }
+  return cuda_status(launch_norm_backward(*desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta,
+                                          static_cast<float*>(workspace), s));
 }
 
 moe_status moe_quantize_q8_0(int n_mats, int rows, int K, int src_dtype, const void* w, void* q,

@@ -128,6 +128,12 @@ struct ExpertLoadJobs {
 cudaError_t launch_load_experts(const ExpertLoadJobs& jobs, int n, const void* const host[3],
                                 void* const pool[3], size_t mat_bytes, cudaStream_t s);
 
+// The public dispatch: the same without flags; the rows from *total_rows to
+// T * ks are set to zero.
+cudaError_t launch_dispatch_rows(int dtype, const void* x, const int32_t* slot_row,
+                                 const int32_t* total_rows, int T, int ks, int d, void* x_perm,
+                                 cudaStream_t s);
+
 cudaError_t launch_gather_rows(int dtype, const void* x, const int32_t* tok_idx,
                                const int32_t* total_rows, int P, int T, int d, void* x_perm,
                                int* flags, cudaStream_t s);
@@ -170,6 +176,28 @@ cudaError_t launch_combine_partial(int dtype, const void* y_perm, const int32_t*
 // (expert, token) of every slot flagged in missing [T, k+S], token-major
 cudaError_t launch_missing_pairs(const int32_t* ids, const int32_t* missing, int T, int k,
                                  int S, int E, int32_t* pairs, int32_t* n_pairs,
+                                 cudaStream_t s);
+
+// Gradients of the dispatch and of the combine (row_grads.cu).
+cudaError_t launch_dispatch_rows_backward(int dtype, const void* dx_perm,
+                                          const int32_t* slot_row, int T, int d, int ks,
+                                          void* dx, cudaStream_t s);
+cudaError_t launch_combine_backward(int dtype, const float* dy, const void* y_perm,
+                                    const int32_t* total_rows, const int32_t* slot_row,
+                                    const float* topk_w, int T, int d, int k, int S,
+                                    void* dy_perm, float* dtopk_w, cudaStream_t s);
+
+// Layer norm / RMS norm of rows (norm.cu).  The backward pass writes the
+// blocks' partial sums of dgamma and dbeta, [2][norm_backward_blocks][d] fp32,
+// and adds them up in a second launch.
+constexpr int kNormMaxD = 16384;  // 1024 threads of 16 columns
+int norm_backward_blocks(const moe_norm_desc& D);
+cudaError_t launch_norm_forward(const moe_norm_desc& D, const void* x, const void* gamma,
+                                const void* beta, void* y, float* mean, float* rstd,
+                                cudaStream_t s);
+cudaError_t launch_norm_backward(const moe_norm_desc& D, const void* dy, const void* x,
+                                 const void* gamma, const float* mean, const float* rstd,
+                                 void* dx, float* dgamma, float* dbeta, float* partial,
                                  cudaStream_t s);
 
 int num_sms();

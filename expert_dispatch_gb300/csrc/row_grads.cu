@@ -1,0 +1,178 @@
+// row_grads.cu -- gradients of the row movement around the expert FFN.
+//
+// The dispatch copies each token's row to its slots, x_perm[slot_row[t, j]] =
+// x[t], so its gradient adds the slots' rows up again; the combine is
+//   y[t] = sum_{j<k} w[t, j] y_perm[slot_row[t, j]] + sum_s y_perm[slot_row[t, k+s]],
+// so its gradients are
+//   dy_perm[slot_row[t, j]] = w[t, j] dy[t]   (w = 1 for a shared slot),
+//   dw[t, j]                = <dy[t], y_perm[slot_row[t, j]]>.
+// Sums and products are fp32 in slot order; rows are rounded to the layer's
+// dtype once, when they are written.  Every output row has one writer, so
+// there are no atomics and the results do not depend on any order of blocks.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxSlots = 36;  // k <= 32, S <= 4
+
+// 8 consecutive elements.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, size_t at, float (&v)[8]) {
+  if (BF16) {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, size_t at, const float (&v)[8]) {
+  if (BF16) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) =
+        make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Block (token t, 1024-column slice); each thread owns 8 consecutive columns.
+template <bool BF16>
+__global__ void __launch_bounds__(128)
+    dispatch_rows_backward_kernel(const void* __restrict__ dx_perm,
+                                  const int32_t* __restrict__ slot_row, int d, int ks, int P,
+                                  void* __restrict__ dx) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int rows_s[kMaxSlots];
+  const int t = blockIdx.x;
+  if (threadIdx.x < ks) {
+    const int r = slot_row[(size_t)t * ks + threadIdx.x];
+    rows_s[threadIdx.x] = (r < 0 || r >= P) ? -1 : r;
+  }
+  __syncthreads();
+  const int c = blockIdx.y * 1024 + threadIdx.x * 8;
+  if (c >= d) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < ks; ++j) {
+    const int r = rows_s[j];
+    if (r < 0) continue;
+    float v[8];
+    load8<BF16>(dx_perm, (size_t)r * d + c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+  }
+  store8<BF16>(dx, (size_t)t * d + c, acc);
+}
+
+// Block per token: for each slot, the row's gradient is written and the dot
+// product with dy[t] summed over the block.  The rows from *total_rows to P
+// that dropped slots leave over are set to zero, each block taking every
+// gridDim.x-th of them.
+constexpr int kCombineBwdThreads = 256;
+
+template <bool BF16>
+__global__ void __launch_bounds__(kCombineBwdThreads)
+    combine_backward_kernel(const float* __restrict__ dy, const void* __restrict__ y_perm,
+                            const int32_t* __restrict__ total_rows,
+                            const int32_t* __restrict__ slot_row,
+                            const float* __restrict__ topk_w, int d, int k, int ks, int P,
+                            void* __restrict__ dy_perm, float* __restrict__ dtopk_w) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int rows_s[kMaxSlots];
+  __shared__ float w_s[kMaxSlots];
+  __shared__ float red[2][kCombineBwdThreads / 32];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int total = min(max(*total_rows, 0), P);
+  if (tid < ks) {
+    const int r = slot_row[(size_t)t * ks + tid];
+    rows_s[tid] = (r < 0 || r >= total) ? -1 : r;
+    w_s[tid] = (tid < k && topk_w) ? topk_w[(size_t)t * k + tid] : 1.f;
+  }
+  __syncthreads();
+  for (int j = 0; j < ks; ++j) {
+    const int r = rows_s[j];
+    float dot = 0.f;
+    if (r >= 0) {
+      const float w = w_s[j];
+      for (int c = tid * 8; c < d; c += kCombineBwdThreads * 8) {
+        float g[8], o[8];
+        load8<false>(dy, (size_t)t * d + c, g);
+        if (dtopk_w && j < k) {
+          float v[8];
+          load8<BF16>(y_perm, (size_t)r * d + c, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = w * g[i];
+        store8<BF16>(dy_perm, (size_t)r * d + c, o);
+      }
+    }
+    if (dtopk_w && j < k) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if ((tid & 31) == 0) red[j & 1][tid >> 5] = dot;
+      __syncthreads();
+      if (tid == 0) {
+        float s = 0.f;
+        for (int i = 0; i < kCombineBwdThreads / 32; ++i) s += red[j & 1][i];
+        dtopk_w[(size_t)t * k + j] = s;
+      }
+    }
+  }
+  const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (long long r = (long long)total + t; r < P; r += gridDim.x)
+    for (int c = tid * 8; c < d; c += kCombineBwdThreads * 8)
+      store8<BF16>(dy_perm, (size_t)r * d + c, zero);
+}
+
+}  // namespace
+
+cudaError_t launch_dispatch_rows_backward(int dtype, const void* dx_perm,
+                                          const int32_t* slot_row, int T, int d, int ks,
+                                          void* dx, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  ProfScope pr("dispatch_rows_backward", s);
+  const dim3 grid(T, (d + 1023) / 1024);
+  (void)launch_kernel(dtype == MOE_BF16 ? dispatch_rows_backward_kernel<true>
+                                        : dispatch_rows_backward_kernel<false>,
+                      grid, 128, 0, s, dx_perm, slot_row, d, ks, T * ks, dx);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_backward(int dtype, const float* dy, const void* y_perm,
+                                    const int32_t* total_rows, const int32_t* slot_row,
+                                    const float* topk_w, int T, int d, int k, int S,
+                                    void* dy_perm, float* dtopk_w, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  ProfScope pr("combine_backward", s);
+  (void)launch_kernel(dtype == MOE_BF16 ? combine_backward_kernel<true>
+                                        : combine_backward_kernel<false>,
+                      T, kCombineBwdThreads, 0, s, dy, y_perm, total_rows, slot_row, topk_w, d, k,
+                      k + S, T * (k + S), dy_perm, dtopk_w);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

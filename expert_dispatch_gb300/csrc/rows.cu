@@ -114,8 +114,10 @@ constexpr int kScatterMaxSlots = 36;  // k <= 32, S <= 4
 // memory (a dropped slot, -1, is skipped; a row outside the batch rows or
 // beyond the T * ks rows of x_perm is flagged and skipped), then each thread
 // loads up to kScatterBatch 16-byte vectors of x[t] and stores them to every
-// slot row.  TO_F16: bf16 in, fp16 out.
-template <bool TO_F16>
+// slot row.  TO_F16: bf16 in, fp16 out.  ZERO_TAIL: the rows from *total_rows
+// to T * ks that dropped slots leave over are set to zero, each block taking
+// every gridDim.x-th of them.
+template <bool TO_F16, bool ZERO_TAIL>
 __global__ void __launch_bounds__(kScatterThreads)
     scatter_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ slot_row,
                         const int32_t* __restrict__ total_rows, int ks, int vec_per_row,
@@ -154,6 +156,12 @@ __global__ void __launch_bounds__(kScatterThreads)
         if (v < vec_per_row) dst[v] = buf[i];
       }
     }
+  }
+  if (ZERO_TAIL) {
+    const long long cap = (long long)gridDim.x * ks;
+    for (long long r = (long long)max(*total_rows, 0) + t; r < cap; r += gridDim.x)
+      for (int v = threadIdx.x; v < vec_per_row; v += kScatterThreads)
+        x_perm[(size_t)r * vec_per_row + v] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (TO_F16 && __syncthreads_or(overflow) && threadIdx.x == 0) flag_error(flags, kErrDeviceInput);
 }
@@ -444,9 +452,22 @@ cudaError_t launch_scatter_rows(int dtype, bool to_f16, const void* x, const int
   if (ks > kScatterMaxSlots) return cudaErrorInvalidValue;
   const int vec = (int)(d * dtype_size(dtype) / 16);
   ProfScope pr("scatter_rows", s);
-  auto kern = to_f16 ? scatter_rows_kernel<true> : scatter_rows_kernel<false>;
+  auto kern = to_f16 ? scatter_rows_kernel<true, false> : scatter_rows_kernel<false, false>;
   (void)launch_kernel(kern, T, kScatterThreads, 0, s, static_cast<const uint4*>(x), slot_row,
                       total_rows, ks, vec, static_cast<uint4*>(x_perm), flags);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dispatch_rows(int dtype, const void* x, const int32_t* slot_row,
+                                 const int32_t* total_rows, int T, int ks, int d, void* x_perm,
+                                 cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  if (ks > kScatterMaxSlots) return cudaErrorInvalidValue;
+  const int vec = (int)(d * dtype_size(dtype) / 16);
+  ProfScope pr("dispatch_rows", s);
+  (void)launch_kernel(scatter_rows_kernel<false, true>, T, kScatterThreads, 0, s,
+                      static_cast<const uint4*>(x), slot_row, total_rows, ks, vec,
+                      static_cast<uint4*>(x_perm), nullptr);
   return cudaGetLastError();
 }
 

@@ -10,7 +10,8 @@ Entry points carry the C names: moe_workspace_size, moe_workspace_init,
 moe_route, moe_plan_dispatch, moe_expert_ffn, moe_combine, moe_layer_forward,
 moe_get_device_status, moe_status_string, moe_launch_count,
 moe_profile_enable, moe_profile_query, moe_profile_list, the Q8_0 and no-alloc variants, the
-slot cache (moe_slot_cache_*) and the expert tier (moe_tier_*).
+slot cache (moe_slot_cache_*), the expert tier (moe_tier_*) and the training operators
+(moe_dispatch_rows, moe_norm_* and the gradients moe_*_backward).
 """
 from __future__ import annotations
 
@@ -34,6 +35,8 @@ MOE_GATE_SOFTMAX_TOPK = 0
 MOE_GATE_SIGMOID_BIAS = 1
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_NORM_LAYER = 0
+MOE_NORM_RMS = 1
 
 EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_plan_dispatch",
             "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_get_device_status",
@@ -47,7 +50,9 @@ EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_plan_d
             "moe_tier_prefetch", "moe_tier_forward", "moe_tier_get_stats", "moe_host_alloc",
             "moe_host_free", "moe_check_bounded_wait", "moe_layer_forward_host",
             "moe_layer_forward_q8_host", "moe_layer_forward_host_pipelined",
-            "moe_layer_forward_q8_host_pipelined")
+            "moe_layer_forward_q8_host_pipelined", "moe_dispatch_rows",
+            "moe_dispatch_rows_backward", "moe_combine_backward", "moe_norm_forward",
+            "moe_norm_workspace_size", "moe_norm_backward")
 
 
 class MoeError(RuntimeError):
@@ -67,6 +72,12 @@ class LayerDesc(ctypes.Structure):
 class Q8WeightStruct(ctypes.Structure):
     """moe_q8_weight"""
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    """moe_norm_desc"""
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class TierStats(ctypes.Structure):
@@ -133,6 +144,13 @@ def lib():
                                                    vp]
     L.moe_layer_forward_q8_host_pipelined.argtypes = [D, i32, vp, vp, vp, vp, Q, Q, Q, vp, vp, sz,
                                                       vp]
+    N = ctypes.POINTER(NormDesc)
+    L.moe_dispatch_rows.argtypes = [D, vp, vp, vp, vp, vp]
+    L.moe_dispatch_rows_backward.argtypes = [D, vp, vp, vp, vp]
+    L.moe_combine_backward.argtypes = [D, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_norm_forward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_norm_workspace_size.argtypes = [N, ctypes.POINTER(sz)]
+    L.moe_norm_backward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     vpp = ctypes.POINTER(ctypes.c_void_p)
     ip = ctypes.POINTER(ctypes.c_int32)
     TS = ctypes.POINTER(TierStats)
@@ -442,6 +460,142 @@ def moe_layer_forward_q8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, residual
         _p(topk_ids_out, torch.int32, "topk_ids_out"), _p(topk_w_out, torch.float32, "topk_w_out"),
         _p(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream))
     _check(st, "moe_layer_forward_q8")
+
+
+# ---------------------------------------------------------------- training
+def moe_dispatch_rows(desc, x, expert_offsets, slot_row, x_perm, stream=None):
+    """x_perm[slot_row[t, j]] = x[t]; rows left over by dropped pairs are zero."""
+    dt = _act_dtype(desc)
+    ks = desc.k + desc.S
+    _need(x, (desc.T, desc.d), "x")
+    _need(expert_offsets, (desc.E + desc.S + 1,), "expert_offsets")
+    _need(slot_row, (desc.T, ks), "slot_row")
+    _need(x_perm, (desc.T * ks, desc.d), "x_perm")
+    st = lib().moe_dispatch_rows(
+        ctypes.byref(desc), _p(x, dt, "x"), _p(expert_offsets, torch.int32, "expert_offsets"),
+        _p(slot_row, torch.int32, "slot_row"), _p(x_perm, dt, "x_perm"), _stream(stream))
+    _check(st, "moe_dispatch_rows")
+
+
+def moe_dispatch_rows_backward(desc, dx_perm, slot_row, dx, stream=None):
+    """dx[t] = sum_j dx_perm[slot_row[t, j]]."""
+    dt = _act_dtype(desc)
+    ks = desc.k + desc.S
+    _need(dx_perm, (desc.T * ks, desc.d), "dx_perm")
+    _need(slot_row, (desc.T, ks), "slot_row")
+    _need(dx, (desc.T, desc.d), "dx")
+    st = lib().moe_dispatch_rows_backward(
+        ctypes.byref(desc), _p(dx_perm, dt, "dx_perm"), _p(slot_row, torch.int32, "slot_row"),
+        _p(dx, dt, "dx"), _stream(stream))
+    _check(st, "moe_dispatch_rows_backward")
+
+
+def moe_combine_backward(desc, dy, y_perm, expert_offsets, slot_row, topk_w, dy_perm, dtopk_w,
+                         stream=None):
+    """Gradients of moe_combine: dy_perm (rows) and, unless None, dtopk_w (gate weights)."""
+    dt = _act_dtype(desc)
+    ks = desc.k + desc.S
+    _need(dy, (desc.T, desc.d), "dy")
+    _need(expert_offsets, (desc.E + desc.S + 1,), "expert_offsets")
+    _need(slot_row, (desc.T, ks), "slot_row")
+    _need(dy_perm, (desc.T * ks, desc.d), "dy_perm")
+    if y_perm is not None:
+        _need(y_perm, (desc.T * ks, desc.d), "y_perm")
+    for t, what in ((topk_w, "topk_w"), (dtopk_w, "dtopk_w")):
+        if t is not None:
+            _need(t, (desc.T, desc.k), what)
+    st = lib().moe_combine_backward(
+        ctypes.byref(desc), _p(dy, torch.float32, "dy"), _p(y_perm, dt, "y_perm"),
+        _p(expert_offsets, torch.int32, "expert_offsets"), _p(slot_row, torch.int32, "slot_row"),
+        _p(topk_w, torch.float32, "topk_w"), _p(dy_perm, dt, "dy_perm"),
+        _p(dtopk_w, torch.float32, "dtopk_w"), _stream(stream))
+    _check(st, "moe_combine_backward")
+
+
+_MOE_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def make_norm_desc(x, gamma=None, kind=MOE_NORM_LAYER, eps=1e-6) -> NormDesc:
+    """The record of a norm over the rows of x [T, d] with gamma's dtype."""
+    if x.dim() != 2:
+        raise ValueError("x has shape %s, expected [T, d]" % (tuple(x.shape),))
+    w = torch.float32 if gamma is None else gamma.dtype
+    if x.dtype not in _MOE_DTYPE or w not in _MOE_DTYPE:
+        raise TypeError("x and gamma must be fp32 or bf16")
+    return NormDesc(x.shape[0], x.shape[1], kind, _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
+
+
+def _norm_param(desc, t, what):
+    if t is None:
+        return None
+    _need(t, (desc.d,), what)
+    return _p(t, torch.float32 if desc.wdtype == MOE_F32 else torch.bfloat16, what)
+
+
+def _norm_stat(desc, t, what):
+    if t is not None:
+        _need(t, (desc.T,), what)
+    return _p(t, torch.float32, what)
+
+
+def moe_norm_forward(desc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
+    dt = _act_dtype(desc)
+    _need(x, (desc.T, desc.d), "x")
+    _need(y, (desc.T, desc.d), "y")
+    st = lib().moe_norm_forward(
+        ctypes.byref(desc), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
+        _norm_param(desc, beta, "beta"), _p(y, dt, "y"), _norm_stat(desc, mean, "mean"),
+        _norm_stat(desc, rstd, "rstd"), _stream(stream))
+    _check(st, "moe_norm_forward")
+
+
+def moe_norm_workspace_size(desc: NormDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_norm_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "moe_norm_workspace_size")
+    return n.value
+
+
+def moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
+    """dx, and dgamma / dbeta [d] fp32 unless None (both None: ws may be None)."""
+    dt = _act_dtype(desc)
+    for t, what in ((dy, "dy"), (x, "x"), (dx, "dx")):
+        _need(t, (desc.T, desc.d), what)
+    for t, what in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+        if t is not None:
+            _need(t, (desc.d,), what)
+    st = lib().moe_norm_backward(
+        ctypes.byref(desc), _p(dy, dt, "dy"), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
+        _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), _p(dx, dt, "dx"),
+        _p(dgamma, torch.float32, "dgamma"), _p(dbeta, torch.float32, "dbeta"),
+        _p(ws, torch.uint8, "workspace"), 0 if ws is None else ws.numel(), _stream(stream))
+    _check(st, "moe_norm_backward")
+
+
+def norm(x, gamma=None, beta=None, kind=MOE_NORM_LAYER, eps=1e-6, stats=False):
+    """(y, mean, rstd) of moe_norm_forward in fresh tensors, on the current stream;
+    mean and rstd are None without stats (mean always for MOE_NORM_RMS)."""
+    desc = make_norm_desc(x, gamma if gamma is not None else beta, kind, eps)
+    y = torch.empty_like(x)
+    mean = rstd = None
+    if stats:
+        rstd = torch.empty(desc.T, dtype=torch.float32, device=x.device)
+        if kind != MOE_NORM_RMS:
+            mean = torch.empty_like(rstd)
+    moe_norm_forward(desc, x, gamma, beta, y, mean, rstd)
+    return y, mean, rstd
+
+
+def norm_backward(dy, x, gamma, mean, rstd, kind=MOE_NORM_LAYER):
+    """(dx, dgamma, dbeta) of moe_norm_backward in fresh tensors, on the current
+    stream; dbeta is None for MOE_NORM_RMS."""
+    desc = make_norm_desc(x, gamma, kind)
+    dx = torch.empty_like(x)
+    dgamma = torch.empty(desc.d, dtype=torch.float32, device=x.device)
+    dbeta = None if kind == MOE_NORM_RMS else torch.empty_like(dgamma)
+    ws = torch.empty(moe_norm_workspace_size(desc), dtype=torch.uint8, device=x.device)
+    moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws)
+    return dx, dgamma, dbeta
 
 
 def moe_get_device_status(ws, clear=False, stream=None) -> int:

@@ -415,6 +415,82 @@ moe_status moe_layer_forward_q8_host_pipelined(const moe_layer_desc* desc, int n
                                                const moe_q8_weight* Wd, float* const* y_host,
                                                void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- training
+   What a training step needs around the expert FFN: the norm in front of the
+   router, the row movement as calls of its own, and their gradients.  The
+   pages describe the forward only; these are the derivatives of its formulas. */
+
+/* moe_dispatch_rows -- the rows of every batch, from the plan:
+     x_perm[slot_row[t, j]] = x[t]   for every pair (t, j), j < k + S.
+     expert_offsets [E+S+1], slot_row [T, k+S]: from moe_plan_dispatch.
+     x_perm [T*(k+S), d] out, the layer's dtype.  The rows from
+                    expert_offsets[E+S] on (left over by dropped pairs, whose
+                    slot_row is -1) are set to zero.
+   A slot_row outside [0, expert_offsets[E+S]) is skipped. */
+moe_status moe_dispatch_rows(const moe_layer_desc* desc, const void* x,
+                             const int32_t* expert_offsets, const int32_t* slot_row,
+                             void* x_perm, void* stream);
+
+/* moe_dispatch_rows_backward -- its gradient with respect to x:
+     dx[t] = sum_j dx_perm[slot_row[t, j]], added in fp32 in slot order and
+   rounded once to the layer's dtype; a token without any row gets zeros.
+     dx_perm [T*(k+S), d], dx [T, d] out: the layer's dtype. */
+moe_status moe_dispatch_rows_backward(const moe_layer_desc* desc, const void* dx_perm,
+                                      const int32_t* slot_row, void* dx, void* stream);
+
+/* moe_combine_backward -- the gradients of moe_combine with respect to its rows
+   and gate weights (that of the residual is dy itself):
+     dy_perm[slot_row[t, j]] = topk_w[t, j] * dy[t]   (factor 1 for shared slots)
+     dtopk_w[t, j]           = <dy[t], y_perm[slot_row[t, j]]>,  j < k
+   with fp32 products and sums; dy_perm is rounded once.
+     dy      [T, d] fp32.
+     y_perm  [T*(k+S), d] the layer's dtype: the rows moe_combine read; read
+             only for dtopk_w (may be NULL without it).
+     topk_w  [T, k] fp32, or NULL when moe_combine was called without weights
+             (the factor is 1, and dtopk_w must be NULL).
+     dy_perm [T*(k+S), d] out, the layer's dtype; rows from
+             expert_offsets[E+S] on are set to zero.
+     dtopk_w [T, k] fp32 out, or NULL.  A dropped pair's entry is 0. */
+moe_status moe_combine_backward(const moe_layer_desc* desc, const float* dy, const void* y_perm,
+                                const int32_t* expert_offsets, const int32_t* slot_row,
+                                const float* topk_w, void* dy_perm, float* dtopk_w,
+                                void* stream);
+
+/* Row norms.  Any d from 1 to 16384 (beyond: MOE_ERR_UNSUPPORTED) and any
+   T up to 2^30. */
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+typedef struct {
+  int32_t T;       /* rows */
+  int32_t d;       /* row length */
+  int32_t kind;    /* moe_norm_kind */
+  int32_t dtype;   /* moe_dtype of x, y, dy and dx */
+  int32_t wdtype;  /* moe_dtype of gamma and beta */
+  float eps;       /* >= 0, added to the variance (forward) */
+} moe_norm_desc;
+
+/* moe_norm_forward -- y = (x - mean) * rstd * gamma + beta per row, with
+   rstd = 1 / sqrt(var + eps) and var = mean((x - mean)^2); MOE_NORM_RMS takes
+   mean as 0 and has no beta (MOE_ERR_INVALID_ARG).  All in fp32, y rounded
+   once.  gamma [d], beta [d]: NULL stands for ones, zeros.  mean [T], rstd [T]
+   fp32 out, or NULL.  y may be x. */
+moe_status moe_norm_forward(const moe_norm_desc* desc, const void* x, const void* gamma,
+                            const void* beta, void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace moe_norm_backward needs for dgamma and dbeta. */
+moe_status moe_norm_workspace_size(const moe_norm_desc* desc, size_t* bytes);
+
+/* moe_norm_backward -- with h = (x - mean) * rstd and w = dy * gamma:
+     dx     = rstd * (w - mean(w) - h * mean(w * h))   (MOE_NORM_RMS: without mean(w))
+     dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy
+     x, mean (NULL for MOE_NORM_RMS), rstd: as moe_norm_forward read and wrote.
+     dgamma, dbeta [d] fp32 out, each or NULL (dbeta NULL for MOE_NORM_RMS);
+     summed in a fixed order.  Without both no workspace is needed.
+   dx may be dy.  T == 0 sets dgamma and dbeta to zero. */
+moe_status moe_norm_backward(const moe_norm_desc* desc, const void* dy, const void* x,
+                             const void* gamma, const float* mean, const float* rstd, void* dx,
+                             float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                             void* stream);
+
 /* Synchronizes `stream`, then reports the sticky device flag held in the
    workspace: MOE_OK, MOE_ERR_DEVICE_INPUT or MOE_ERR_TIMEOUT (MOE_ERR_CUDA if
    the copy itself fails).  clear != 0 resets the flag afterwards.          */
@@ -450,7 +526,8 @@ int64_t moe_launch_count(void);
    plan_small, plan_mark, plan_scan, plan_place, gather_rows, scatter_rows,
    ffn_gateup_simt, ffn_down_simt, ffn_gateup_tc, ffn_down_tc,
    ffn_gateup_tc_q8, ffn_down_tc_q8, quantize_q8_0, combine, combine_partial,
-   missing_pairs, load_experts (the expert tier's loads of host-resident
+   missing_pairs, dispatch_rows, dispatch_rows_backward, combine_backward,
+   norm_forward, norm_backward, norm_reduce, load_experts (the expert tier's loads of host-resident
    experts into HBM slots).
    moe_profile_list() gives the named kernel's recorded launches one by one,
    in launch order: the first max_n durations (ms) and the bytes each launch

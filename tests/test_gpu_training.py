@@ -1,0 +1,389 @@
+"""The training operators on the GPU against their formulas in 64 bits.
+
+Tolerances.  A result rounded to type t is off by at most half a step,
+H = finfo(t).eps / 2 relative to it (0 is added for fp32, whose own rounding is
+among the fp32 operations).  Before that everything is fp32: with u = 2^-24, a
+sum of n terms added in chains and trees of at most m additions is off by at
+most m u times the sum of the terms' sizes, and every product, difference or
+quotient by u of its result.  The bounds below add these up, element by element;
+m is what the kernels' split allows at most (a thread adds at most 64 terms of a
+row, then two 5-step trees, so 80; the factors that follow it count the handful
+of operations around each sum).
+"""
+import numpy as np
+import pytest
+import torch
+
+from expert_dispatch_gb300 import moe
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def H(t):
+    return 0.0 if t == torch.float32 else torch.finfo(t).eps / 2
+
+
+def rnd(shape, seed, dtype=torch.float32, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def close(got, want, tol):
+    err = (got.double() - want).abs()
+    bad = err > tol
+    assert not bool(bad.any()), (float(err.max()), float((err / tol.clamp(min=1e-300)).max()),
+                                 torch.nonzero(bad)[:4].tolist())
+
+
+# ---------------------------------------------------------------- norm
+def ref_norm(x, g, b, rms, eps):
+    x = x.double()
+    mu = torch.zeros_like(x[:, 0]) if rms else x.mean(1)
+    var = (x - mu[:, None]).square().mean(1)
+    r = 1 / torch.sqrt(var + eps)
+    h = (x - mu[:, None]) * r[:, None]
+    y = h * (1 if g is None else g.double()) + (0 if b is None else b.double())
+    return y, mu, r, h
+
+
+def check_forward(x, g, b, rms, eps=1e-6):
+    kind = moe.MOE_NORM_RMS if rms else moe.MOE_NORM_LAYER
+    y, mean, rstd = moe.norm(x, g, b, kind=kind, eps=eps, stats=True)
+    want, mu, r, h = ref_norm(x, g, b, rms, eps)
+    size = x.double().abs().mean(1)  # the size of the mean's terms
+    d_mu = 80 * U * size
+    # a relative error of var: 90 u of its own sum, and the mean's error enters squared
+    d_r = r * (50 * U + (d_mu * r).square())
+    if rms:
+        assert mean is None
+    else:
+        close(mean, mu, d_mu)
+    close(rstd, r, d_r)
+    ga = torch.ones_like(want) if g is None else g.double().abs().expand_as(want)
+    d_h = (d_mu * r)[:, None] + h.abs() * (d_r / r + 4 * U)[:, None]
+    close(y, want, H(x.dtype) * want.abs() + ga * d_h * (1 + H(x.dtype)) +
+          4 * U * (ga * h.abs() + want.abs()))
+
+
+SIZES = [(1, 1), (1, 7168), (3, 2), (5, 8), (7, 31), (2, 64), (33, 72), (4, 264), (3, 257),
+         (19, 1000), (9, 1111), (6, 2048), (5, 4100), (2, 4096), (3, 8191), (2, 8192), (2, 16383),
+         (2, 16384)]
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", SIZES)
+def test_norm_forward(T, d, dtype, rms):
+    x = rnd((T, d), 1, scale=3.0) + 5.0  # a mean larger than the spread
+    x = x.to(DT[dtype])
+    for wdt in (torch.float32, torch.bfloat16):
+        check_forward(x, rnd((d,), 2, wdt), None if rms else rnd((d,), 3, wdt), rms)
+    check_forward(x, None, None, rms)
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", SIZES + [(700, 520), (1300, 33), (613, 7168), (5000, 64)])
+def test_norm_backward(T, d, dtype, rms):
+    dt = DT[dtype]
+    x = (rnd((T, d), 1, scale=2.0) + 1.5).to(dt)
+    dy = rnd((T, d), 2, dt)
+    g = rnd((d,), 3, torch.bfloat16 if T % 2 else torch.float32)
+    kind = moe.MOE_NORM_RMS if rms else moe.MOE_NORM_LAYER
+    _, mean, rstd = moe.norm(x, g, None, kind=kind, stats=True)
+    dx, dg, db = moe.norm_backward(dy, x, g, mean, rstd, kind=kind)
+    # the formula, on the statistics the kernel was given
+    X, D, G, r = x.double(), dy.double(), g.double(), rstd.double()[:, None]
+    h = (X if rms else X - mean.double()[:, None]) * r
+    w = D * G
+    c1 = (w * h).mean(1, keepdim=True)
+    c2 = torch.zeros_like(c1) if rms else w.mean(1, keepdim=True)
+    want = r * (w - c2 - h * c1)
+    a1, a2 = (w * h).abs().mean(1, keepdim=True), w.abs().mean(1, keepdim=True)
+    tol = r * U * (8 * w.abs() + 100 * a2 * (not rms) + h.abs() * 110 * a1)
+    close(dx, want, H(dt) * want.abs() + tol * (1 + H(dt)))
+    # rows: a thread's chain of T / 304 rows, 8 groups, 304 / 32 blocks and a 5-step tree
+    chain = (T / 304 + 40) * U
+    close(dg, (D * h).sum(0), chain * (D * h).abs().sum(0))
+    if rms:
+        assert db is None
+    else:
+        close(db, D.sum(0), chain * D.abs().sum(0))
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+def test_norm_backward_against_differences(rms):
+    """Central differences of the forward formula in 64 bits: truncation is of the order
+    of the step squared, 1e-10 here, and the noise 1e-16 / 1e-5; fp32 decides."""
+    T, d = 3, 21
+    x, dy, g = rnd((T, d), 4), rnd((T, d), 5), rnd((d,), 6)
+    kind = moe.MOE_NORM_RMS if rms else moe.MOE_NORM_LAYER
+    _, mean, rstd = moe.norm(x, g, None, kind=kind, stats=True)
+    dx, dg, db = moe.norm_backward(dy, x, g, mean, rstd, kind=kind)
+    b = torch.zeros(d, dtype=torch.float64, device="cuda")
+    args = [x.double(), g.double(), b]
+
+    def loss(a):
+        return float((ref_norm(a[0], a[1], None if rms else a[2], rms, 1e-6)[0] * dy.double()).sum())
+
+    for got, which in ((dx, 0), (dg, 1), (db, 2)):
+        if got is None:
+            continue
+        num = torch.zeros_like(args[which])
+        for i in range(num.numel()):
+            ends = []
+            for s in (1e-5, -1e-5):
+                a = [t.clone() for t in args]
+                a[which].view(-1)[i] += s
+                ends.append(loss(a))
+            num.view(-1)[i] = (ends[0] - ends[1]) / 2e-5
+        assert float((got.double() - num).abs().max()) < 1e-5 * max(1.0, float(num.abs().max()))
+
+
+def test_norm_parts_can_be_left_out():
+    x, dy, g = rnd((9, 72), 1), rnd((9, 72), 2), rnd((72,), 3)
+    y, mean, rstd = moe.norm(x, g, stats=True)
+    dx, dg, db = moe.norm_backward(dy, x, g, mean, rstd)
+    y2, m2, r2 = moe.norm(x, g)
+    assert m2 is None and r2 is None and torch.equal(y, y2)
+    desc = moe.make_norm_desc(x, g)
+    ws = torch.empty(moe.moe_norm_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    for want_g, want_b in ((0, 0), (1, 0), (0, 1)):
+        a, b, c = torch.empty_like(dx), torch.empty_like(dg), torch.empty_like(db)
+        moe.moe_norm_backward(desc, dy, x, g, mean, rstd, a, b if want_g else None,
+                              c if want_b else None, ws if want_g or want_b else None)
+        assert torch.equal(a, dx)
+        assert not want_g or torch.equal(b, dg)
+        assert not want_b or torch.equal(c, db)
+    # in place: y over x, dx over dy
+    xi, di = x.clone(), dy.clone()
+    moe.moe_norm_forward(desc, xi, g, None, xi)
+    moe.moe_norm_backward(desc, di, x, g, mean, rstd, di, None, None, None)
+    assert torch.equal(xi, y) and torch.equal(di, dx)
+
+
+def test_norm_no_rows():
+    x = torch.empty((0, 40), device="cuda")
+    g = rnd((40,), 1)
+    y, mean, rstd = moe.norm(x, g, stats=True)
+    assert y.shape == (0, 40) and mean.numel() == 0
+    dx, dg, db = moe.norm_backward(x, x, g, mean, rstd)
+    assert dx.shape == (0, 40) and not dg.any() and not db.any()
+
+
+def test_norm_odd_values_stay_in_their_row():
+    x = rnd((6, 200), 1)
+    x[1] = 0.0           # no spread: rstd = 1 / sqrt(eps)
+    x[2] = 7.0
+    x[3, 5] = float("nan")
+    x[4, 9] = float("inf")
+    y, mean, rstd = moe.norm(x, stats=True, eps=1e-4)
+    assert not y[1].any() and not y[2].any()
+    assert torch.allclose(rstd[1:3], torch.full((2,), 100.0, device="cuda"), rtol=1e-6)
+    assert y[3].isnan().all() and y[4].isnan().all()
+    keep = [0, 5]
+    want, mu, r, _ = ref_norm(x[keep], None, None, False, 1e-4)
+    assert torch.allclose(y[keep].double(), want, atol=1e-5)
+    # rows of a large common offset keep the digits their spread has
+    big = rnd((4, 512), 2) + 3000.0
+    check_forward(big, None, None, False)
+
+
+# ---------------------------------------------------------------- rows
+def plan(T, E, k, S, seed, drop=0.0, all_dropped=()):
+    """slot_row, expert_offsets and weights of a random routing, planned on the CPU."""
+    rs = np.random.RandomState(seed)
+    ids = np.stack([rs.permutation(E)[:k] for _ in range(T)]) if T else np.zeros((0, k), int)
+    gone = rs.rand(T, k) < drop
+    for t in all_dropped:
+        gone[t] = True
+    lists = [[] for _ in range(E + S)]
+    for t in range(T):
+        for j in range(k):
+            if not gone[t, j]:
+                lists[ids[t, j]].append((t, j))
+        for s in range(S):
+            lists[E + s].append((t, k + s))
+    slot = np.full((T, k + S), -1, np.int32)
+    off, r = [0], 0
+    for lst in lists:
+        for t, j in lst:
+            slot[t, j] = r
+            r += 1
+        off.append(r)
+    w = rs.rand(T, k).astype(np.float32)
+    cu = lambda a: torch.from_numpy(np.asarray(a)).cuda()  # noqa: E731
+    return cu(slot), cu(np.asarray(off, np.int32)), cu(w)
+
+
+CASES = [dict(T=1, d=64, E=4, k=1, S=0), dict(T=1, d=7168, E=8, k=8, S=1),
+         dict(T=37, d=128, E=16, k=2, S=0), dict(T=5, d=192, E=3, k=3, S=4, drop=0.4),
+         dict(T=200, d=1088, E=60, k=6, S=2, drop=0.2), dict(T=64, d=4096, E=32, k=8, S=0),
+         dict(T=9, d=2048, E=40, k=32, S=4), dict(T=300, d=64, E=384, k=8, S=1, drop=0.9)]
+
+
+def rows_case(c, dtype, seed=0):
+    T, d, E, k, S = (c[n] for n in "TdEkS")
+    desc = moe.make_desc(T, d, E, k, 128, S, dtype=moe.MOE_BF16 if dtype == "bf16" else moe.MOE_F32)
+    slot, off, w = plan(T, E, k, S, seed, c.get("drop", 0.0), c.get("all_dropped", ()))
+    return desc, slot, off, w
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", CASES + [dict(T=6, d=8 * 9, E=4, k=2, S=0, f32=True)])
+def test_dispatch_and_back(c, dtype):
+    if c.get("f32") and dtype == "bf16":
+        pytest.skip("bf16 layers have d % 64 == 0")
+    desc, slot, off, w = rows_case(c, dtype)
+    dt, ks, P = DT[dtype], desc.k + desc.S, desc.T * (desc.k + desc.S)
+    x = rnd((desc.T, desc.d), 1, dt)
+    xp = torch.full((P, desc.d), float("nan"), dtype=dt, device="cuda")
+    moe.moe_dispatch_rows(desc, x, off, slot, xp)
+    want = torch.zeros_like(xp)
+    at = slot.view(-1).long()
+    tok = torch.arange(desc.T, device="cuda").repeat_interleave(ks)
+    want[at[at >= 0]] = x[tok[at >= 0]]
+    assert torch.equal(xp, want)
+    # back: the slots' gradients summed per token
+    g = rnd((P, desc.d), 2, dt)
+    dx = torch.empty_like(x)
+    moe.moe_dispatch_rows_backward(desc, g, slot, dx)
+    G = torch.where((at >= 0)[:, None], g.double()[at.clamp(min=0)], 0.0).view(desc.T, ks, -1)
+    close(dx, G.sum(1), H(dt) * G.sum(1).abs() + ks * U * 1.01 * G.abs().sum(1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", CASES)
+def test_combine_backward(c, dtype):
+    desc, slot, off, w = rows_case(c, dtype, seed=3)
+    dt, k, ks, P = DT[dtype], desc.k, desc.k + desc.S, desc.T * (desc.k + desc.S)
+    dy = rnd((desc.T, desc.d), 1)
+    yp = rnd((P, desc.d), 2, dt)
+    yp[int(off[-1]):] = float("nan")  # rows that no pair has are not read
+    dyp = torch.full_like(yp, float("nan"))
+    dw = torch.full((desc.T, k), float("nan"), device="cuda")
+    moe.moe_combine_backward(desc, dy, yp, off, slot, w, dyp, dw)
+    at = slot.view(-1).long()
+    there = at >= 0
+    tok = torch.arange(desc.T, device="cuda").repeat_interleave(ks)
+    W = torch.cat([w.double(), torch.ones((desc.T, desc.S), device="cuda").double()], 1).view(-1)
+    D = dy.double()[tok]
+    want = torch.zeros((P, desc.d), dtype=torch.float64, device="cuda")
+    want[at[there]] = (W[:, None] * D)[there]
+    close(dyp, want, (H(dt) + U * 1.01) * want.abs())
+    prod = torch.where(there[:, None], D * yp.double()[at.clamp(min=0)], 0.0)
+    dot, size = prod.sum(1).view(-1, ks)[:, :k], prod.abs().sum(1).view(-1, ks)[:, :k]
+    # chain: at most d / 256 products and sums a thread (8 at least), then trees of 8 steps
+    close(dw, dot, (desc.d / 128 + 32) * U * size)
+    # without the weights' gradient the rows' is the same; without weights the factor is 1
+    a, b = torch.empty_like(dyp), torch.empty_like(dyp)
+    moe.moe_combine_backward(desc, dy, None, off, slot, w, a, None)
+    assert torch.equal(a, dyp)
+    moe.moe_combine_backward(desc, dy, None, off, slot, None, b, None)
+    want[at[there]] = D[there]
+    close(b, want, H(dt) * want.abs())
+
+
+def test_combine_backward_is_the_derivative_of_moe_combine():
+    """y is linear in the rows and in the weights, so a difference of moe_combine's own
+    results is exact up to fp32: <dy, combine(rows + e) - combine(rows)> = <dy_perm, e>."""
+    desc, slot, off, w = rows_case(dict(T=21, d=128, E=8, k=3, S=1, drop=0.2), "f32", 5)
+    P = desc.T * 4
+    dy, yp, e, we = rnd((21, 128), 1), rnd((P, 128), 2), rnd((P, 128), 3), rnd((21, 3), 4)
+    dyp, dw = torch.empty_like(yp), torch.empty_like(w)
+    moe.moe_combine_backward(desc, dy, yp, off, slot, w, dyp, dw)
+    y0, y1, y2 = (torch.empty((21, 128), device="cuda") for _ in range(3))
+    moe.moe_combine(desc, yp, slot, w, None, y0)
+    moe.moe_combine(desc, yp + e, slot, w, None, y1)
+    moe.moe_combine(desc, yp, slot, w + we, None, y2)
+    n = int(off[-1])
+    size = float(dy.abs().double().sum())  # sums of about 128 * 21 products of order 1
+    d1 = float((dy.double() * (y1.double() - y0.double())).sum())
+    assert abs(d1 - float((dyp[:n].double() * e[:n].double()).sum())) < 64 * U * size
+    d2 = float((dy.double() * (y2.double() - y0.double())).sum())
+    assert abs(d2 - float((dw.double() * we.double()).sum())) < 64 * U * size * 8
+
+
+def test_rows_all_dropped_and_none():
+    c = dict(T=7, d=64, E=4, k=2, S=0, all_dropped=range(7))
+    desc, slot, off, w = rows_case(c, "bf16")
+    x = rnd((7, 64), 1, torch.bfloat16)
+    xp = torch.full((14, 64), float("nan"), dtype=x.dtype, device="cuda")
+    moe.moe_dispatch_rows(desc, x, off, slot, xp)
+    assert not xp.any()
+    dx = torch.full_like(x, float("nan"))
+    moe.moe_dispatch_rows_backward(desc, torch.full_like(xp, float("nan")), slot, dx)
+    assert not dx.any()
+    dyp, dw = torch.full_like(xp, float("nan")), torch.full((7, 2), float("nan"), device="cuda")
+    moe.moe_combine_backward(desc, rnd((7, 64), 2), xp, off, slot, w, dyp, dw)
+    assert not dyp.any() and not dw.any()
+    empty = moe.make_desc(0, 64, 4, 2, 64)
+    z = torch.empty((0, 64), dtype=x.dtype, device="cuda")
+    i = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    moe.moe_dispatch_rows(empty, z, off, i, z)
+    moe.moe_dispatch_rows_backward(empty, z, i, z)
+
+
+def test_rows_outside_the_batches_are_skipped():
+    """Entries that name no batch row are treated as dropped, whatever they hold."""
+    desc, slot, off, w = rows_case(dict(T=12, d=64, E=4, k=2, S=1), "bf16", 7)
+    bad = slot.clone()
+    for i, v in enumerate((-7, 36, 1 << 30, -(1 << 31), (1 << 31) - 1)):
+        bad[2 * i, i % 3] = v
+    clean = torch.where((bad < 0) | (bad >= 36), torch.full_like(bad, -1), bad)
+    x, dy = rnd((12, 64), 1, torch.bfloat16), rnd((12, 64), 2)
+    g = rnd((36, 64), 3, torch.bfloat16)
+    out = []
+    for s in (bad, clean):
+        xp, dyp = (torch.full((36, 64), 9.0, dtype=x.dtype, device="cuda") for _ in range(2))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        moe.moe_dispatch_rows(desc, x, off, s, xp)
+        moe.moe_dispatch_rows_backward(desc, g, s, dx)
+        moe.moe_combine_backward(desc, dy, g, off, s, w, dyp, dw)
+        out.append((xp, dx, dyp, dw))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- streams and graphs
+def test_on_another_stream_and_in_a_graph():
+    desc, slot, off, w = rows_case(dict(T=50, d=256, E=8, k=2, S=1), "bf16", 9)
+    P = 150
+    x, dy = rnd((50, 256), 1, torch.bfloat16), rnd((50, 256), 2)
+    g = rnd((256,), 3)
+    nd = moe.make_norm_desc(x, g)
+    ws = torch.empty(moe.moe_norm_workspace_size(nd), dtype=torch.uint8, device="cuda")
+
+    def buffers():
+        e = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+        f = torch.float32
+        return dict(y=e(50, 256), mean=e(50, t=f), rstd=e(50, t=f), xp=e(P, 256), dyp=e(P, 256),
+                    dw=e(50, 2, t=f), dh=e(50, 256), dx=e(50, 256), dg=e(256, t=f), db=e(256, t=f))
+
+    def step(b, stream=None):
+        moe.moe_norm_forward(nd, x, g, None, b["y"], b["mean"], b["rstd"], stream)
+        moe.moe_dispatch_rows(desc, b["y"], off, slot, b["xp"], stream)
+        moe.moe_combine_backward(desc, dy, b["xp"], off, slot, w, b["dyp"], b["dw"], stream)
+        moe.moe_dispatch_rows_backward(desc, b["dyp"], slot, b["dh"], stream)
+        moe.moe_norm_backward(nd, b["dh"], x, g, b["mean"], b["rstd"], b["dx"], b["dg"], b["db"],
+                              ws, stream)
+
+    want, other, graphed = buffers(), buffers(), buffers()
+    step(want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    step(other, s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(graphed)
+    for t in graphed.values():
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in want:
+        assert torch.equal(want[n], other[n]), n
+        assert torch.equal(want[n], graphed[n]), n

@@ -1,0 +1,152 @@
+"""Argument checks of the training operators that need no GPU: every refusal comes
+back before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+from expert_dispatch_gb300 import build as moe_build
+from expert_dispatch_gb300 import moe
+
+FAKE = ctypes.c_void_p(0x10000)  # never dereferenced: validation fails first
+ODD = ctypes.c_void_p(0x10004)
+
+
+@pytest.fixture(scope="module")
+def L():
+    moe_build.build()
+    return moe.lib()
+
+
+def _layer(**kw):
+    base = dict(T=8, d=64, E=4, k=2, I=64, S=1, dtype=moe.MOE_BF16)
+    base.update(kw)
+    return ctypes.byref(moe.make_desc(**base))
+
+
+def _norm(**kw):
+    base = dict(T=8, d=96, kind=moe.MOE_NORM_LAYER, dtype=moe.MOE_BF16, wdtype=moe.MOE_F32,
+                eps=1e-6)
+    base.update(kw)
+    return ctypes.byref(moe.NormDesc(*base.values()))
+
+
+@pytest.mark.parametrize("call,n_ptr", [("moe_dispatch_rows", 4), ("moe_dispatch_rows_backward", 3)])
+def test_row_calls_refuse(L, call, n_ptr):
+    fn = getattr(L, call)
+    ok = [FAKE] * n_ptr
+    for i in range(n_ptr):
+        for bad in (None, ODD):
+            args = list(ok)
+            args[i] = bad
+            assert fn(_layer(), *args, None) == moe.MOE_ERR_INVALID_ARG, (i, bad)
+    assert fn(None, *ok, None) == moe.MOE_ERR_INVALID_ARG
+    assert fn(_layer(k=0), *ok, None) == moe.MOE_ERR_INVALID_ARG
+    assert fn(_layer(d=72), *ok, None) == moe.MOE_ERR_UNSUPPORTED
+    assert fn(_layer(T=0), *[None] * n_ptr, None) == moe.MOE_OK
+
+
+def test_combine_backward_refuses(L):
+    fn = L.moe_combine_backward
+    # dy, y_perm, expert_offsets, slot_row, topk_w, dy_perm, dtopk_w
+    ok = [FAKE] * 7
+    for i in range(7):
+        args = list(ok)
+        args[i] = ODD
+        assert fn(_layer(), *args, None) == moe.MOE_ERR_INVALID_ARG, i
+    for i in (0, 1, 2, 3, 4, 5):  # with dtopk_w, y_perm and topk_w are needed too
+        args = list(ok)
+        args[i] = None
+        assert fn(_layer(), *args, None) == moe.MOE_ERR_INVALID_ARG, i
+    assert fn(_layer(E=0), *ok, None) == moe.MOE_ERR_INVALID_ARG
+    assert fn(_layer(T=0), *[None] * 7, None) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(T=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(d=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(kind=2), moe.MOE_ERR_INVALID_ARG),
+    (dict(dtype=5), moe.MOE_ERR_INVALID_ARG),
+    (dict(wdtype=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=-1e-6), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=float("nan")), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=float("inf")), moe.MOE_ERR_INVALID_ARG),
+    (dict(d=16385), moe.MOE_ERR_UNSUPPORTED),
+    (dict(T=(1 << 30) + 1), moe.MOE_ERR_UNSUPPORTED),
+])
+def test_norm_descriptors_refused(L, bad, status):
+    n = ctypes.c_size_t(0)
+    assert L.moe_norm_workspace_size(_norm(**bad), ctypes.byref(n)) == status
+    assert L.moe_norm_forward(_norm(**bad), *[FAKE] * 6, None) == status
+    assert L.moe_norm_backward(_norm(**bad), *[FAKE] * 9, 1 << 30, None) == status
+
+
+def test_norm_workspace(L):
+    n = ctypes.c_size_t(0)
+    assert L.moe_norm_workspace_size(_norm(), None) == moe.MOE_ERR_INVALID_ARG
+    assert L.moe_norm_workspace_size(_norm(T=0), ctypes.byref(n)) == moe.MOE_OK and n.value == 0
+    sizes = []
+    for T in (1, 100, 10 ** 6, 1 << 30):
+        assert L.moe_norm_workspace_size(_norm(T=T), ctypes.byref(n)) == moe.MOE_OK
+        assert n.value >= 2 * 96 * 4 and n.value % 256 == 0
+        sizes.append(n.value)
+    assert sizes == sorted(sizes) and sizes[2] == sizes[3]  # bounded however many rows
+
+
+def test_norm_forward_refuses(L):
+    fn = L.moe_norm_forward
+    ok = [FAKE] * 6  # x, gamma, beta, y, mean, rstd
+    for i in range(6):
+        args = list(ok)
+        args[i] = ODD
+        assert fn(_norm(), *args, None) == moe.MOE_ERR_INVALID_ARG, i
+    for i in (0, 3):
+        args = list(ok)
+        args[i] = None
+        assert fn(_norm(), *args, None) == moe.MOE_ERR_INVALID_ARG, i
+    rms = dict(kind=moe.MOE_NORM_RMS)
+    assert fn(_norm(**rms), FAKE, FAKE, FAKE, FAKE, None, FAKE, None) == moe.MOE_ERR_INVALID_ARG
+    assert fn(_norm(**rms), FAKE, FAKE, None, FAKE, FAKE, FAKE, None) == moe.MOE_ERR_INVALID_ARG
+    assert fn(_norm(T=0), *[None] * 6, None) == moe.MOE_OK
+
+
+def test_norm_backward_refuses(L):
+    fn = L.moe_norm_backward
+    big = 1 << 30
+    ok = [FAKE] * 9  # dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace
+    for i in range(8):
+        args = list(ok)
+        args[i] = ODD
+        assert fn(_norm(), *args, big, None) == moe.MOE_ERR_INVALID_ARG, i
+    for i in (0, 1, 3, 4, 5):
+        args = list(ok)
+        args[i] = None
+        assert fn(_norm(), *args, big, None) == moe.MOE_ERR_INVALID_ARG, i
+    n = ctypes.c_size_t(0)
+    assert L.moe_norm_workspace_size(_norm(), ctypes.byref(n)) == moe.MOE_OK
+    assert fn(_norm(), *ok, n.value - 1, None) == moe.MOE_ERR_WORKSPACE
+    assert fn(_norm(), *ok[:8], None, n.value, None) == moe.MOE_ERR_WORKSPACE
+    assert fn(_norm(), *ok[:8], ODD, n.value, None) == moe.MOE_ERR_WORKSPACE
+    rms = dict(kind=moe.MOE_NORM_RMS)
+    assert fn(_norm(**rms), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, big,
+              None) == moe.MOE_ERR_INVALID_ARG  # mean
+    assert fn(_norm(**rms), FAKE, FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, FAKE, big,
+              None) == moe.MOE_ERR_INVALID_ARG  # dbeta
+    # no rows and nothing to sum: nothing is launched
+    assert fn(_norm(T=0), *[None] * 9, 0, None) == moe.MOE_OK
+
+
+def test_binding_checks_tensors():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.norm(x)
+    with pytest.raises(ValueError, match="shape"):
+        moe.norm(torch.zeros(4, 2, 64))
+    with pytest.raises(TypeError):
+        moe.norm(torch.zeros(4, 64, dtype=torch.float64))
+    d = moe.make_desc(4, 64, 4, 2, 64)
+    with pytest.raises(ValueError, match="slot_row"):
+        moe.moe_dispatch_rows_backward(d, torch.zeros(8, 64), torch.zeros(4, 3), x)
+    with pytest.raises(ValueError, match="topk_w"):
+        moe.moe_combine_backward(d, torch.zeros(4, 64), None, torch.zeros(5), torch.zeros(4, 2),
+                                 torch.zeros(4, 3), torch.zeros(8, 64), None)
