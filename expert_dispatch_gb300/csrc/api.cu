@@ -65,6 +65,23 @@ moe_status check_norm(const moe_norm_desc* D) {
   return MOE_OK;
 }
 
+moe_status check_ortho(const moe_ortho_desc* D) {
+  if (!D) return MOE_ERR_INVALID_ARG;
+  if (D->n_mats < 0 || D->rows <= 0 || D->cols <= 0) return MOE_ERR_INVALID_ARG;
+  if (D->dtype != MOE_F32 && D->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (D->steps < 1 || D->steps > 32) return MOE_ERR_INVALID_ARG;
+  if (!(D->eps >= 0.f) || !isfinite(D->eps)) return MOE_ERR_INVALID_ARG;
+  if (D->rows > 65536 || D->cols > 65536) return MOE_ERR_UNSUPPORTED;
+  // row coordinates and tile counts of the stack stay well within 31 bits, the
+  // matrices within a grid's z dimension
+  const long long mp = (((D->rows < D->cols ? D->rows : D->cols) + 63) / 64) * 64;
+  const long long np = (((D->rows < D->cols ? D->cols : D->rows) + 63) / 64) * 64;
+  const long long tiles = ((mp + 255) / 256) * ((np + 63) / 64);
+  if (D->n_mats > 65535 || D->n_mats * np > (1ll << 30) || D->n_mats * tiles > (1ll << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 struct Ws {
   int* flags;
   float* logits;
@@ -699,6 +716,27 @@ moe_status moe_norm_backward(const moe_norm_desc* desc, const void* dy, const vo
   }
   return cuda_status(launch_norm_backward(*desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta,
                                           static_cast<float*>(workspace), s));
+}
+
+moe_status moe_ortho_workspace_size(const moe_ortho_desc* desc, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_ortho(desc);
+  if (st != MOE_OK) return st;
+  *bytes = desc->n_mats == 0 ? 0 : ortho_layout(*desc).total;
+  return MOE_OK;
+}
+
+moe_status moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* out,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  const NvtxRange nvtx("moe_orthogonalize");
+  const moe_status st = check_ortho(desc);
+  if (st != MOE_OK) return st;
+  if (desc->n_mats == 0) return MOE_OK;
+  if (!g || !out || g == out || !aligned16(g) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || ws_bytes < ortho_layout(*desc).total)
+    return MOE_ERR_WORKSPACE;
+  return cuda_status(
+      launch_orthogonalize(*desc, g, out, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_quantize_q8_0(int n_mats, int rows, int K, int src_dtype, const void* w, void* q,

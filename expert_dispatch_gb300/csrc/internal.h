@@ -200,6 +200,24 @@ cudaError_t launch_norm_backward(const moe_norm_desc& D, const void* dy, const v
                                  void* dx, float* dgamma, float* dbeta, float* partial,
                                  cudaStream_t s);
 
+// Newton-Schulz orthogonalisation (ortho.cu): workspace regions for matrices
+// padded to mp x np (m = min(rows, cols) and n = max, rounded up to 64).  The
+// workspace begins with int32[4] flags ([0] error bits); the offsets count
+// from the next multiple of 256 behind them.
+struct OrthoLayout {
+  size_t partial;  // partial sums of squares
+  size_t scales;
+  size_t x;        // fp16 [n_mats, mp, np]
+  size_t xt[2];    // fp16 [n_mats, np, mp]
+  size_t gram;     // fp16 [n_mats, mp, mp]
+  size_t poly;     // fp16 [n_mats, mp, mp]
+  size_t total;
+  int mp, np;
+};
+OrthoLayout ortho_layout(const moe_ortho_desc& D);
+cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* out, void* ws,
+                                 cudaStream_t s);
+
 int num_sms();
 
 // Expert residency in a bounded set of device slots (slot_cache.cu).

@@ -52,7 +52,8 @@ EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_plan_d
             "moe_layer_forward_q8_host", "moe_layer_forward_host_pipelined",
             "moe_layer_forward_q8_host_pipelined", "moe_dispatch_rows",
             "moe_dispatch_rows_backward", "moe_combine_backward", "moe_norm_forward",
-            "moe_norm_workspace_size", "moe_norm_backward")
+            "moe_norm_workspace_size", "moe_norm_backward", "moe_ortho_workspace_size",
+            "moe_orthogonalize")
 
 
 class MoeError(RuntimeError):
@@ -78,6 +79,12 @@ class NormDesc(ctypes.Structure):
     """moe_norm_desc"""
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class OrthoDesc(ctypes.Structure):
+    """moe_ortho_desc"""
+    _fields_ = [("n_mats", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class TierStats(ctypes.Structure):
@@ -151,6 +158,9 @@ def lib():
     L.moe_norm_forward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp]
     L.moe_norm_workspace_size.argtypes = [N, ctypes.POINTER(sz)]
     L.moe_norm_backward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    O = ctypes.POINTER(OrthoDesc)
+    L.moe_ortho_workspace_size.argtypes = [O, ctypes.POINTER(sz)]
+    L.moe_orthogonalize.argtypes = [O, vp, vp, vp, sz, vp]
     vpp = ctypes.POINTER(ctypes.c_void_p)
     ip = ctypes.POINTER(ctypes.c_int32)
     TS = ctypes.POINTER(TierStats)
@@ -596,6 +606,44 @@ def norm_backward(dy, x, gamma, mean, rstd, kind=MOE_NORM_LAYER):
     ws = torch.empty(moe_norm_workspace_size(desc), dtype=torch.uint8, device=x.device)
     moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws)
     return dx, dgamma, dbeta
+
+
+def make_ortho_desc(g, steps=5, eps=1e-7) -> OrthoDesc:
+    """The record of orthogonalising the stack g [n_mats, rows, cols]."""
+    if g.dim() != 3:
+        raise ValueError("g has shape %s, expected [n_mats, rows, cols]" % (tuple(g.shape),))
+    if g.dtype not in _MOE_DTYPE:
+        raise TypeError("g must be fp32 or bf16")
+    return OrthoDesc(*g.shape, _MOE_DTYPE[g.dtype], steps, eps)
+
+
+def moe_ortho_workspace_size(desc: OrthoDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_ortho_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "moe_ortho_workspace_size")
+    return n.value
+
+
+def moe_orthogonalize(desc, g, out, ws, stream=None):
+    """out (bf16) from g: every matrix orthogonalised; ws of moe_ortho_workspace_size bytes."""
+    shape = (desc.n_mats, desc.rows, desc.cols)
+    _need(g, shape, "g")
+    _need(out, shape, "out")
+    st = lib().moe_orthogonalize(
+        ctypes.byref(desc), _p(g, _act_dtype(desc), "g"), _p(out, torch.bfloat16, "out"),
+        _p(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream))
+    _check(st, "moe_orthogonalize")
+
+
+def orthogonalize(g, steps=5, eps=1e-7):
+    """moe_orthogonalize of g [n_mats, rows, cols] or [rows, cols] (fp32 or bf16) into a
+    fresh bf16 tensor, on the current stream."""
+    stack = g if g.dim() == 3 else g.unsqueeze(0)
+    desc = make_ortho_desc(stack, steps, eps)
+    out = torch.empty(stack.shape, dtype=torch.bfloat16, device=g.device)
+    ws = torch.empty(max(moe_ortho_workspace_size(desc), 16), dtype=torch.uint8, device=g.device)
+    moe_orthogonalize(desc, stack, out, ws)
+    return out.view(g.shape)
 
 
 def moe_get_device_status(ws, clear=False, stream=None) -> int:

@@ -491,6 +491,40 @@ moe_status moe_norm_backward(const moe_norm_desc* desc, const void* dy, const vo
                              float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
                              void* stream);
 
+/* Orthogonalised updates for a stack of weight matrices (the Muon optimiser's
+   treatment of a matrix's averaged gradient), G [n_mats, rows, cols]: every
+   matrix becomes, after a few Newton-Schulz products, close to the U V^T of
+   its own singular value decomposition.
+     X = G / (|G|_F + eps);  steps times:  A = X X^T,
+     X = (a I + b A + c A A) X,  (a, b, c) = (3.4445, -4.7750, 2.0315)
+   (on the transpose where rows > cols).  Five steps bring singular values
+   from 1e-2 |G|_F up to between about 0.7 and 1.2. */
+typedef struct {
+  int32_t n_mats;  /* matrices, each its own problem */
+  int32_t rows;
+  int32_t cols;
+  int32_t dtype;   /* moe_dtype of G */
+  int32_t steps;   /* 1 .. 32 */
+  float eps;       /* >= 0 */
+} moe_ortho_desc;
+
+/* Bytes of workspace moe_orthogonalize needs (0 when n_mats == 0). */
+moe_status moe_ortho_workspace_size(const moe_ortho_desc* desc, size_t* bytes);
+
+/* moe_orthogonalize -- out [n_mats, rows, cols] bf16 from g [n_mats, rows, cols].
+   The products have fp16 operands (scaled by powers of two) and fp32
+   accumulators; for well-conditioned matrices the result is off by about 1e-3
+   of its norm before its rounding to bf16, more where a few directions hold
+   almost all of the norm (2e-2 where the others have 1 % of it).
+   A zero matrix gives zeros; one that holds a NaN or an infinity gives NaNs,
+   the others of the stack are not touched by it.
+   rows and cols from 1 to 65536, n_mats up to 65535 and n_mats * max(rows, cols)
+   (rounded up to 64) up to 2^30 (beyond: MOE_ERR_UNSUPPORTED).  out may not
+   be g.  moe_get_device_status(workspace, ...) reports a bounded wait that
+   expired. */
+moe_status moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* out,
+                             void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reports the sticky device flag held in the
    workspace: MOE_OK, MOE_ERR_DEVICE_INPUT or MOE_ERR_TIMEOUT (MOE_ERR_CUDA if
    the copy itself fails).  clear != 0 resets the flag afterwards.          */
@@ -527,7 +561,8 @@ int64_t moe_launch_count(void);
    ffn_gateup_simt, ffn_down_simt, ffn_gateup_tc, ffn_down_tc,
    ffn_gateup_tc_q8, ffn_down_tc_q8, quantize_q8_0, combine, combine_partial,
    missing_pairs, dispatch_rows, dispatch_rows_backward, combine_backward,
-   norm_forward, norm_backward, norm_reduce, load_experts (the expert tier's loads of host-resident
+   norm_forward, norm_backward, norm_reduce, ortho_sumsq, ortho_start,
+   ortho_gram, ortho_poly, ortho_apply, load_experts (the expert tier's loads of host-resident
    experts into HBM slots).
    moe_profile_list() gives the named kernel's recorded launches one by one,
    in launch order: the first max_n durations (ms) and the bytes each launch

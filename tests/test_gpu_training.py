@@ -348,6 +348,121 @@ def test_rows_outside_the_batches_are_skipped():
         assert torch.equal(a, b)
 
 
+# ---------------------------------------------------------------- orthogonalisation
+# Tolerance: the output's rounding to bf16, 2^-8 of each value, and the products'
+# operands: a step rounds X, A and B to fp16, 2^-11 of each value at most and about a
+# third of that on average; a step's polynomial passes an error on amplified by its
+# slope, 3.4 where a singular value is still small (which grows by the same factor) and
+# at most 3.9 near 1.2.  For matrices whose singular values grow together the errors of
+# the five steps do not outgrow the result: 8 * 2^-11 of its norm is allowed, and six
+# times that, of the root mean square, for the worst single value.
+NS_TOL = 8 * 2.0 ** -11
+
+
+def ref_ortho(g, steps, eps):
+    a, b, c = 3.4445, -4.7750, 2.0315
+    x = g.double()
+    tall = x.shape[1] > x.shape[2]
+    x = x.transpose(1, 2) if tall else x
+    x = x / (x.square().sum((1, 2), keepdim=True).sqrt() + eps)
+    for _ in range(steps):
+        gram = x @ x.transpose(1, 2)
+        x = a * x + (b * gram + c * gram @ gram) @ x
+    return x.transpose(1, 2) if tall else x
+
+
+def check_ortho(got, want):
+    assert got.dtype == torch.bfloat16 and got.shape == want.shape
+    err = (got.double() - want)
+    norm = want.square().sum((1, 2)).sqrt()
+    rms = want.square().mean((1, 2)).sqrt()
+    rel = err.square().sum((1, 2)).sqrt() / norm
+    assert bool((rel <= 2.0 ** -8 + NS_TOL).all()), rel
+    close(got, want, 2.0 ** -8 * want.abs() + 6 * NS_TOL * rms[:, None, None])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,cols", [
+    (1, 1, 1), (2, 3, 5), (2, 1, 300), (1, 300, 1), (1, 64, 64), (3, 65, 130), (2, 130, 65),
+    (1, 257, 1001), (2, 300, 260), (1, 512, 512), (1, 1000, 64), (5, 128, 512), (1, 256, 4096),
+    (40, 100, 90), (1, 520, 776), (2, 1032, 600)])
+def test_ortho(n, rows, cols, dtype):
+    g = rnd((n, rows, cols), rows + cols, DT[dtype], 0.02)
+    check_ortho(moe.orthogonalize(g), ref_ortho(g, 5, 1e-7))
+
+
+@pytest.mark.parametrize("steps", [1, 2, 8])
+def test_ortho_steps(steps):
+    g = rnd((2, 200, 330), steps)
+    check_ortho(moe.orthogonalize(g, steps=steps), ref_ortho(g, steps, 1e-7))
+
+
+def test_ortho_singular_values_meet_one():
+    """Singular values from 1 down to 0.05 of the largest end between 0.6 and 1.3."""
+    q1, q2 = (torch.linalg.qr(rnd((160, 160), s).double())[0] for s in (1, 2))
+    sv = torch.logspace(0, -1.3, 160, device="cuda").double()
+    g = (q1 * sv) @ q2
+    out = moe.orthogonalize(g.float())
+    check_ortho(out[None], ref_ortho(g.float()[None], 5, 1e-7))
+    s = torch.linalg.svdvals(out.double())
+    assert 0.6 < float(s.min()) and float(s.max()) < 1.3
+
+
+def test_ortho_scales_by_powers_of_two_change_nothing():
+    g = rnd((3, 90, 140), 1)
+    want = moe.orthogonalize(g, eps=0.0)
+    for e in (-100, -70, 40, 100, 120):
+        assert torch.equal(moe.orthogonalize(g * 2.0 ** e, eps=0.0), want), e
+    for e in (-40, 46):  # the norm's sum is split between ranges here: rounded otherwise
+        check_ortho(moe.orthogonalize(g * 2.0 ** e, eps=0.0), ref_ortho(g, 5, 0.0))
+    # a stack of very different sizes: each matrix has its own scale
+    mixed = g * torch.tensor([2.0 ** -90, 1.0, 2.0 ** 90], device="cuda")[:, None, None]
+    assert torch.equal(moe.orthogonalize(mixed, eps=0.0), want)
+    # eps counts where the norm is of its size
+    small = g * 1e-9
+    check_ortho(moe.orthogonalize(small, eps=1e-7), ref_ortho(small, 5, 1e-7))
+
+
+def test_ortho_zero_and_nan_matrices():
+    g = rnd((5, 70, 200), 2)
+    want = moe.orthogonalize(g)
+    for eps in (1e-7, 0.0):
+        bad = g.clone()
+        bad[1] = 0
+        bad[2, 3, 4] = float("nan")
+        bad[3, 69, 199] = float("inf")
+        out = moe.orthogonalize(bad, eps=eps)
+        assert not out[1].any() and out[2].isnan().all() and out[3].isnan().all()
+        if eps:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[4], want[4])
+
+
+def test_ortho_workspace_stream_and_graph():
+    g = rnd((2, 100, 260), 3, torch.bfloat16)
+    want = moe.orthogonalize(g)
+    desc = moe.make_ortho_desc(g)
+    size = moe.moe_ortho_workspace_size(desc)
+    room = torch.full((size + 64,), 255, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for off in (0, 16, 48):  # any 16-byte address
+        out = torch.empty_like(want)
+        moe.moe_orthogonalize(desc, g, out, room[off:off + size], s)
+        assert moe.moe_get_device_status(room[off:off + size], stream=s) == moe.MOE_OK
+        assert torch.equal(out, want) and bool((room[off + size:] == 255).all())
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_orthogonalize(desc, g, out, room[:size])
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    none = torch.empty((0, 8, 8), device="cuda")
+    assert moe.orthogonalize(none).shape == (0, 8, 8)
+    assert torch.equal(moe.orthogonalize(g[1]), want[1])
+
+
 # ---------------------------------------------------------------- streams and graphs
 def test_on_another_stream_and_in_a_graph():
     desc, slot, off, w = rows_case(dict(T=50, d=256, E=8, k=2, S=1), "bf16", 9)

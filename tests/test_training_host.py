@@ -136,6 +136,48 @@ def test_norm_backward_refuses(L):
     assert fn(_norm(T=0), *[None] * 9, 0, None) == moe.MOE_OK
 
 
+def _ortho(**kw):
+    base = dict(n_mats=2, rows=96, cols=40, dtype=moe.MOE_BF16, steps=5, eps=1e-7)
+    base.update(kw)
+    return ctypes.byref(moe.OrthoDesc(*base.values()))
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n_mats=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(rows=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(cols=-4), moe.MOE_ERR_INVALID_ARG),
+    (dict(dtype=2), moe.MOE_ERR_INVALID_ARG),
+    (dict(steps=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(steps=33), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=-1.0), moe.MOE_ERR_INVALID_ARG),
+    (dict(eps=float("nan")), moe.MOE_ERR_INVALID_ARG),
+    (dict(rows=65537), moe.MOE_ERR_UNSUPPORTED),
+    (dict(cols=65537), moe.MOE_ERR_UNSUPPORTED),
+    (dict(n_mats=65536), moe.MOE_ERR_UNSUPPORTED),
+    (dict(n_mats=20000, cols=65536), moe.MOE_ERR_UNSUPPORTED),
+])
+def test_ortho_descriptors_refused(L, bad, status):
+    n = ctypes.c_size_t(0)
+    assert L.moe_ortho_workspace_size(_ortho(**bad), ctypes.byref(n)) == status
+    assert L.moe_orthogonalize(_ortho(**bad), FAKE, ctypes.c_void_p(0x20000), FAKE, 1 << 40,
+                               None) == status
+
+
+def test_ortho_refuses(L):
+    n = ctypes.c_size_t(0)
+    assert L.moe_ortho_workspace_size(_ortho(), None) == moe.MOE_ERR_INVALID_ARG
+    assert L.moe_ortho_workspace_size(_ortho(n_mats=0), ctypes.byref(n)) == moe.MOE_OK
+    assert n.value == 0
+    assert L.moe_ortho_workspace_size(_ortho(), ctypes.byref(n)) == moe.MOE_OK and n.value > 0
+    out, fn = ctypes.c_void_p(0x20000), L.moe_orthogonalize
+    for g, o in ((None, out), (FAKE, None), (ODD, out), (FAKE, ODD), (FAKE, FAKE)):
+        assert fn(_ortho(), g, o, FAKE, n.value, None) == moe.MOE_ERR_INVALID_ARG
+    assert fn(_ortho(), FAKE, out, FAKE, n.value - 1, None) == moe.MOE_ERR_WORKSPACE
+    assert fn(_ortho(), FAKE, out, None, n.value, None) == moe.MOE_ERR_WORKSPACE
+    assert fn(_ortho(), FAKE, out, ODD, n.value, None) == moe.MOE_ERR_WORKSPACE
+    assert fn(_ortho(n_mats=0), None, None, None, 0, None) == moe.MOE_OK
+
+
 def test_binding_checks_tensors():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
@@ -144,6 +186,12 @@ def test_binding_checks_tensors():
         moe.norm(torch.zeros(4, 2, 64))
     with pytest.raises(TypeError):
         moe.norm(torch.zeros(4, 64, dtype=torch.float64))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.orthogonalize(x)
+    with pytest.raises(TypeError):
+        moe.orthogonalize(x.half())
+    with pytest.raises(ValueError, match="shape"):
+        moe.make_ortho_desc(x)
     d = moe.make_desc(4, 64, 4, 2, 64)
     with pytest.raises(ValueError, match="slot_row"):
         moe.moe_dispatch_rows_backward(d, torch.zeros(8, 64), torch.zeros(4, 3), x)
