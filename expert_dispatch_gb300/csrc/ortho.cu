@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -36,7 +37,8 @@ namespace {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 1024.f, kScaleA = 16384.f, kScaleB = 4096.f;
-constexpr int kSumBlocks = 64;  // most blocks of the norm's sum, per matrix
+constexpr int kPairUnits = 48;   // least 256 x 256 tiles for the SM pairs
+constexpr int kSumBlocks = 128;  // most blocks of the norm's sum, per matrix
 
 struct Scale {
   float f1, f2;  // X = g * f1 * f2, powers of two (one factor could leave fp32's range)
@@ -45,23 +47,40 @@ struct Scale {
 };
 
 // ---------------------------------------------------------------- norm and first X
-__device__ __forceinline__ float load_elem(const void* g, int bf16, size_t i) {
-  return bf16 ? load_as_f32(static_cast<const __nv_bfloat16*>(g), i)
-              : static_cast<const float*>(g)[i];
+// V consecutive elements as fp32: 16 aligned bytes, or one element.
+template <typename T, int V>
+__device__ __forceinline__ void load_elems(const T* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = load_as_f32(p, 0);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
 }
 
 constexpr float kBig = 0x1p45f, kSmall = 0x1p-45f, kUp = 0x1p84f, kDown = 0x1p-84f;
 
 // Sums of squares of one matrix, block blockIdx.x of gridDim.x; three sums so
 // that no square over- or underflows: of values above 2^45 times 2^-84, of
-// values below 2^-45 times 2^84, and of the rest.
+// values below 2^-45 times 2^84, and of the rest.  A matrix that starts off a
+// 16-byte boundary is read in vectors from the next one on.
+template <typename T>
 __global__ void __launch_bounds__(512)
-    ortho_sumsq_kernel(const void* g, int bf16, size_t per_mat, float* partial, int* flags) {
+    ortho_sumsq_kernel(const T* g, size_t per_mat, float* partial, int* flags) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[3][16];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flags[0] = 0;
-  const size_t base = (size_t)blockIdx.y * per_mat;
+  constexpr int V = 16 / (int)sizeof(T);
+  const T* p = g + (size_t)blockIdx.y * per_mat;
   float s[3] = {0.f, 0.f, 0.f};
   auto add = [&](float x) {
     const float ax = fabsf(x);
@@ -73,9 +92,30 @@ __global__ void __launch_bounds__(512)
       s[1] = fmaf(x, x, s[1]);
     }
   };
+  const size_t tid = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
   const size_t stride = (size_t)gridDim.x * blockDim.x;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < per_mat; i += stride)
-    add(load_elem(g, bf16, base + i));
+  const size_t off = (reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T);
+  const size_t head = off ? (V - off < per_mat ? V - off : per_mat) : 0;
+  const size_t nv = (per_mat - head) / V, tail = head + nv * V;
+  if (tid < head) add(load_as_f32(p, tid));
+  if (tid < per_mat - tail) add(load_as_f32(p, tail + tid));
+  constexpr int U = 4;  // vectors in flight
+  for (size_t i = tid; i < nv; i += U * stride) {
+    float v[U][V];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (i + k * stride < nv) {
+        load_elems<T, V>(p + head + (i + k * stride) * V, v[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) add(v[k][j]);
+  }
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
 #pragma unroll
@@ -127,17 +167,49 @@ __device__ Scale matrix_scale(const float* partial, int n, float eps) {
   return r;
 }
 
-// First X [mp, np] and X^T [np, mp] in fp16, padded with zeros: a 64 x 64 tile a
-// block, through shared memory.
+// First X in fp16, padded with zeros, in the input's own layout, same
+// [rows, cols] padded to [rp, cp], and transposed, turned [cp, rp]: a 64 x 64
+// tile a block.  A thread loads and stores 8 elements of a row at a time; the
+// transposed copy goes through shared memory.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-    ortho_start_kernel(const void* g, int bf16, int rows, int cols, int m, int n, int mp, int np,
-                       float eps, const float* partial, int n_partial, Scale* scales, __half* x,
-                       __half* xt) {
+    ortho_start_kernel(const T* g, int rows, int cols, int rp, int cp, float eps,
+                       const float* partial, int n_partial, Scale* scales, __half* same,
+                       __half* turned) {
   pdl_wait();
   pdl_trigger();
   __shared__ Scale sc;
-  __shared__ __half tile[64][66];
-  const int mat = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;  // of [mp, np]
+  __shared__ uint32_t tile[64][33];  // two elements a word
+  const int mat = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  const T* src = g + (size_t)mat * rows * cols;
+  const int tc = (threadIdx.x & 7) * 8, tr = threadIdx.x >> 3;  // 8 columns of rows tr, tr + 32
+  float v[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + tr + 32 * h, c = c0 + tc;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[h][j] = 0.f;
+    if (r < rows && c < cols) {
+      const T* p = src + (size_t)r * cols + c;
+      if constexpr (VEC && sizeof(T) == 2) {  // cols % 8 == 0
+        load_elems<T, 8>(p, v[h]);
+      } else if constexpr (VEC) {  // cols % 4 == 0
+        float q[4];
+        load_elems<T, 4>(p, q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[h][j] = q[j];
+        if (c + 4 < cols) {
+          load_elems<T, 4>(p + 4, q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[h][4 + j] = q[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < cols) v[h][j] = load_as_f32(p, j);
+      }
+    }
+  }
   if (threadIdx.x < 32) {
     const Scale own = matrix_scale(partial + (size_t)mat * n_partial * 3, n_partial, eps);
     if (threadIdx.x == 0) {
@@ -147,25 +219,30 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const float f1 = sc.f1, f2 = sc.f2;
-  const bool tall = rows > cols;
-  const size_t base = (size_t)mat * rows * cols;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  // read along the input's rows; `tile` is indexed [row of X][column of X]
-  for (int i = ty; i < 64; i += 4) {
-    const int xr = tall ? r0 + tx : r0 + i, xc = tall ? c0 + i : c0 + tx;
-    float v = 0.f;
-    if (xr < m && xc < n)
-      v = load_elem(g, bf16, base + (tall ? (size_t)xc * cols + xr : (size_t)xr * cols + xc));
-    const __half h = __float2half_rn(v * f1 * f2);
-    if (tall)
-      tile[tx][i] = h;
-    else
-      tile[i][tx] = h;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 p = __floats2half2_rn(v[h][2 * j] * f1 * f2, v[h][2 * j + 1] * f1 * f2);
+      u[j] = *reinterpret_cast<const uint32_t*>(&p);
+      tile[tr + 32 * h][tc / 2 + j] = u[j];
+    }
+    *reinterpret_cast<uint4*>(same + ((size_t)mat * rp + r0 + tr + 32 * h) * cp + c0 + tc) =
+        make_uint4(u[0], u[1], u[2], u[3]);
   }
   __syncthreads();
-  for (int i = ty; i < 64; i += 4) {
-    x[((size_t)mat * mp + r0 + i) * np + c0 + tx] = tile[i][tx];
-    xt[((size_t)mat * np + c0 + i) * mp + r0 + tx] = tile[tx][i];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = tr + 32 * h;  // this thread writes rows r0 + tc .. + 7 of column c
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = tile[tc + 2 * j][c / 2], b = tile[tc + 2 * j + 1][c / 2];
+      u[j] = c & 1 ? (a >> 16) | (b & 0xffff0000u) : (a & 0xffffu) | (b << 16);
+    }
+    *reinterpret_cast<uint4*>(turned + ((size_t)mat * cp + c0 + c) * rp + r0 + tc) =
+        make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -209,15 +286,15 @@ struct Cfg {
   static_assert(SMEM_TOTAL <= 232448, "shared memory");
 };
 
-// Tiles of one matrix.  Symmetric products take the tiles that meet the lower
-// triangle: row block i spans R column tiles and has (i + 1) R of them, less
-// what the last one lacks.
-template <int BN, bool SYM>
+// Tiles of BM x BN of one matrix.  Symmetric products take the tiles that meet
+// the lower triangle: row block i spans R column tiles and has (i + 1) R of
+// them, less what the last one lacks.
+template <int BM, int BN, bool SYM>
 struct Tiles {
-  static constexpr int R = 256 / BN;
+  static constexpr int R = BM / BN;
   int mt, nt;
   __host__ __device__ Tiles(int rowsP, int rowsQ)
-      : mt((rowsP + 255) / 256), nt((rowsQ + BN - 1) / BN) {}
+      : mt((rowsP + BM - 1) / BM), nt((rowsQ + BN - 1) / BN) {}
   __host__ __device__ int count() const {
     if (!SYM) return mt * nt;
     return R * mt * (mt + 1) / 2 - (mt * R - nt);
@@ -232,34 +309,30 @@ struct Tiles {
     while (u >= (i + 1) * R) u -= ++i * R;
     j = u;
   }
+  // whether a tile has a mirror image outside the row block's own square
+  __device__ bool mirrored(int i, int j) const { return SYM && (j + 1) * BN <= i * BM; }
 };
 
-__device__ __forceinline__ void store_row16(__half* p, const float (&v)[16]) {
-  uint32_t u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
-               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-               : "memory");
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 16 values of row `row` of the last product, columns c0 .. c0 + 15.
-__device__ __forceinline__ void store_result16(const Product& p, int mat, int row, int c0,
-                                               const float (&v)[16]) {
+// W columns of row `row` of the last product, from column c0 on.
+template <int W>
+__device__ __forceinline__ void store_result(const Product& p, int mat, int row, int c0,
+                                             const float (&v)[W]) {
   __nv_bfloat16* base = p.result + (size_t)mat * p.m * p.n;
   if (p.tall) {  // [n, m]: a warp's lanes hold consecutive elements
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < W; ++j)
       if (c0 + j < p.n) base[(size_t)(c0 + j) * p.m + row] = __float2bfloat16_rn(v[j]);
     return;
   }
   __nv_bfloat16* dst = base + (size_t)row * p.n + c0;
   if (p.n % 8 == 0) {  // 16-byte aligned rows
 #pragma unroll
-    for (int j = 0; j < 16; j += 8) {
+    for (int j = 0; j < W; j += 8) {
       if (c0 + j >= p.n) break;
       uint32_t w[4];
 #pragma unroll
@@ -272,8 +345,69 @@ __device__ __forceinline__ void store_result16(const Product& p, int mat, int ro
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < W; ++j)
     if (c0 + j < p.n) dst[j] = __float2bfloat16_rn(v[j]);
+}
+
+// The factor of a product's accumulators.
+template <int OP>
+__device__ __forceinline__ float product_scale(const Product& p, int mat) {
+  const float rho = p.first ? p.scales[mat].rho : 1.f;
+  return OP == kGram    ? rho * rho * (kScaleA / (kScaleX * kScaleX))
+         : OP == kPoly  ? kC * (kScaleB / (kScaleA * kScaleA))
+         : OP == kApply ? rho / kScaleB
+                        : rho / (kScaleB * kScaleX);
+}
+
+// Accumulators of W columns (8 or 16) of row `row` from column c0 on, already
+// scaled, to the product's outputs: along the row in one 16- or 32-byte store,
+// and column by column (64 bytes a warp) for the mirrored or transposed copy.
+template <int OP, int W>
+__device__ __forceinline__ void store_product(const Product& p, int mat, int row, int c0,
+                                              bool mirror, float (&v)[W]) {
+  if (OP == kLast) {
+    if (row < p.m) store_result<W>(p, mat, row, c0, v);
+    return;
+  }
+  if (row >= p.rowsP) return;
+  const size_t at = ((size_t)mat * p.rowsP + row) * p.rowsQ + c0;
+  if (OP == kPoly) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.gram + at);
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) {
+      const uint4 g = src[i];
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&gw[j]));
+        v[8 * i + 2 * j] = fmaf(kB * (kScaleB / kScaleA), f.x, v[8 * i + 2 * j]);
+        v[8 * i + 2 * j + 1] = fmaf(kB * (kScaleB / kScaleA), f.y, v[8 * i + 2 * j + 1]);
+      }
+    }
+    if (row < p.m) {
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        if (row == c0 + j) v[j] += kA * kScaleB;
+    }
+  }
+  uint32_t u[W / 2];
+#pragma unroll
+  for (int j = 0; j < W / 2; ++j) u[j] = pack_half2(v[2 * j], v[2 * j + 1]);
+  if constexpr (W == 16) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p.out + at),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]),
+                 "r"(u[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p.out + at) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  if (mirror || OP == kApply) {
+    uint16_t* t = reinterpret_cast<uint16_t*>(OP == kApply ? p.out_t : p.out) +
+                  ((size_t)mat * p.rowsQ + c0) * p.rowsP + row;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      t[(size_t)j * p.rowsP] = (uint16_t)(j & 1 ? u[j / 2] >> 16 : u[j / 2] & 0xffffu);
+  }
 }
 
 template <int OP, int BN, int STAGES>
@@ -298,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = (int)(blockIdx.x >> 1), n_pairs = (int)(gridDim.x >> 1);
-  const Tiles<BN, SYM> tiles(p.rowsP, p.rowsQ);
+  const Tiles<256, BN, SYM> tiles(p.rowsP, p.rowsQ);
   const int per_mat = tiles.count(), total = per_mat * p.n_mats;
   const int KB = p.K / 64;
 
@@ -417,9 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9, both CTAs)
     // A warp reads its TMEM lane quarter (row = lane); the two warps of a
-    // quarter take one half of the columns each, 16 at a time: one 32-byte
-    // store along the row, and 16 stores of 64 bytes a warp for the mirrored
-    // or transposed copy.
+    // quarter take one half of the columns each, 16 at a time.
     const int q = warp & 3, half = (warp - 2) >> 2;
     int it = 0;
     for (int u = pair; u < total; u += n_pairs, ++it) {
@@ -431,13 +563,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int row = ti * 256 + (int)rank * 128 + q * 32 + lane;
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-      const float rho = p.first ? p.scales[mat].rho : 1.f;
-      const float alpha = OP == kGram    ? rho * rho * (kScaleA / (kScaleX * kScaleX))
-                          : OP == kPoly  ? kC * (kScaleB / (kScaleA * kScaleA))
-                          : OP == kApply ? rho / kScaleB
-                                         : rho / (kScaleB * kScaleX);
-      const bool mirror = SYM && (tj + 1) * BN <= ti * 256;
-      const size_t out_row = ((size_t)mat * p.rowsP + row) * p.rowsQ;
+      const float alpha = product_scale<OP>(p, mat);
+      const bool mirror = tiles.mirrored(ti, tj);
 #pragma unroll 1
       for (int cc = half * (BN / 2); cc < (half + 1) * (BN / 2); cc += 16) {
         const int c0 = tj * BN + cc;
@@ -448,29 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
-        if (OP == kLast) {
-          if (row < p.m) store_result16(p, mat, row, c0, v);
-        } else if (row < p.rowsP) {
-          if (OP == kPoly) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.gram + out_row + c0);
-            const uint4 g0 = src[0], g1 = src[1];
-            const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __half2 h = *reinterpret_cast<const __half2*>(&gw[j / 2]);
-              const float g = __half2float(j & 1 ? __high2half(h) : __low2half(h));
-              v[j] = fmaf(kB * (kScaleB / kScaleA), g, v[j]);
-              if (row == c0 + j && row < p.m) v[j] += kA * kScaleB;
-            }
-          }
-          store_row16(p.out + out_row + c0, v);
-          if (mirror || OP == kApply) {
-            __half* t = OP == kApply ? p.out_t : p.out;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              t[((size_t)mat * p.rowsQ + c0 + j) * p.rowsP + row] = __float2half_rn(v[j]);
-          }
-        }
+        store_product<OP, 16>(p, mat, row, c0, mirror, v);
         __syncwarp();  // the next tcgen05.ld is the whole warp's
       }
       tc_fence_before();
@@ -489,10 +594,195 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int OP, int BN, int STAGES>
-cudaError_t launch_product(const void* P, const void* Q, const Product& p, cudaStream_t s) {
-  using C = Cfg<BN, STAGES>;
-  auto kern = ortho_product_kernel<OP, BN, STAGES>;
+// The same products where they have few tiles: one CTA a tile of 128 x 64, or
+// a cluster of `split` CTAs that share the tile's reduction length.  There a
+// CTA leaves its partial sums in its shared memory, and after a cluster
+// barrier each adds up its share of the columns over the cluster in rank order.
+constexpr int kSmallN = 64, kSmallStages = 4, kSmallWarps = 6;  // producer, MMA, 4 epilogue
+constexpr int kSmallThreads = 32 * kSmallWarps;
+
+struct SmallCfg {
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = kSmallN * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int BAR_OFF = kSmallStages * STAGE_BYTES;
+  static constexpr int MISC_OFF = BAR_OFF + (2 * kSmallStages + 2) * 8;
+  static constexpr int SMEM_TOTAL = MISC_OFF + 16 + 1024;
+  static_assert(kSmallN * 128 * 4 <= BAR_OFF, "partial sums reuse the stages");
+};
+
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kSmallThreads)
+    ortho_small_kernel(const __grid_constant__ CUtensorMap tmP,
+                       const __grid_constant__ CUtensorMap tmQ, const Product p, int split) {
+  using C = SmallCfg;
+  constexpr bool SYM = OP == kGram || OP == kPoly;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::BAR_OFF;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kSmallStages + s); };
+  const uint32_t accf = bar0 + 8u * (2 * kSmallStages), drain_bar = accf + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = (int)blockIdx.x / split, rank = (int)blockIdx.x - unit * split;
+  const Tiles<128, kSmallN, SYM> tiles(p.rowsP, p.rowsQ);
+  const int per_mat = tiles.count(), mat = unit / per_mat;
+  int ti, tj;
+  tiles.at(unit - mat * per_mat, ti, tj);
+  const int KB = p.K / 64, kb0 = KB * rank / split, kb1 = KB * (rank + 1) / split;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSmallStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kSmallN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // the operands, A and the scales are the predecessors' outputs
+  pdl_trigger();
+
+  const int q = warp & 3;  // epilogue warps 2..5: the TMEM lane quarter
+  const int row = ti * 128 + q * 32 + lane;
+  const bool mirror = tiles.mirrored(ti, tj);
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      const int prow = mat * p.rowsP + ti * 128, qrow = mat * p.rowsQ + tj * kSmallN;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(full_bar(stage), C::STAGE_BYTES);
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        const uint32_t s = sbase + stage * C::STAGE_BYTES;
+        tma_load_2d(s, &tmP, full_bar(stage), kb * 64, prow);
+        tma_load_2d(s + C::A_BYTES, &tmQ, full_bar(stage), kb * 64, qrow);
+        if (++stage == kSmallStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      for (int s = 0; s < kSmallStages; ++s)  // every stage armed has received its copies
+        if (armed & (1u << s)) tc::mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(128, kSmallN);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(full_bar(stage), phase, abort_flag, p.err))) break;
+        tc_fence_after();
+        const uint32_t s = sbase + stage * C::STAGE_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(tmem_base, smem_desc_sw128(s + kk * 32),
+                    smem_desc_sw128(s + C::A_BYTES + kk * 32), idesc, kb != kb0 || kk ? 1u : 0u);
+        umma_commit(empty_bar(stage));
+        if (++stage == kSmallStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) umma_commit(accf);
+      umma_commit(drain_bar);  // every MMA has completed before the TMEM is freed
+      tc::mbar_wait_drain(drain_bar, 0, p.err);
+    }
+  } else if (tc::mbar_wait_warp(accf, 0, abort_flag, p.err)) {
+    tc_fence_after();
+    const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+    const float alpha = product_scale<OP>(p, mat);
+    float* part = reinterpret_cast<float*>(smem);  // [kSmallN][128]
+#pragma unroll 1
+    for (int cc = 0; cc < kSmallN; cc += 16) {
+      const int c0 = tj * kSmallN + cc;
+      if (c0 >= p.rowsQ) break;  // warp-uniform
+      uint32_t a[16];
+      tmem_ld16(tb + cc, a);
+      tmem_ld_wait();
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
+      if (split == 1) {
+        store_product<OP, 16>(p, mat, row, c0, mirror, v);
+      } else {
+        // the stages' last reader was the MMA that this warp waited for
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(cc + j) * 128 + q * 32 + lane] = v[j];
+      }
+      __syncwarp();  // the next tcgen05.ld is the whole warp's
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kSmallN);
+  }
+  if (split == 1) return;
+  cluster_sync();  // every CTA's partial sums are in place
+  if (warp >= 2) {
+    const int cols = kSmallN / split;
+    for (int cc = rank * cols; cc < (rank + 1) * cols; cc += 8) {
+      const int c0 = tj * kSmallN + cc;
+      if (c0 >= p.rowsQ) break;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < split; ++r) {
+        const uint32_t peer = mapa_shared(sbase + (uint32_t)(cc * 128 + q * 32 + lane) * 4u, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += ld_shared_cluster(peer + (uint32_t)j * 512u);
+      }
+      store_product<OP, 8>(p, mat, row, c0, mirror, v);
+    }
+  }
+  cluster_sync();  // a CTA's shared memory stays until its peers have read it
+}
+
+// ---------------------------------------------------------------- host
+// Tensor maps of one K-major operand, boxes of 64 columns.
+struct OperandMaps {
+  CUtensorMap rows128, rows64;
+};
+
+bool make_maps(OperandMaps* o, const void* base, int K, long long rows) {
+  return make_tmap_2d(&o->rows128, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K,
+                      (uint64_t)rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         make_tmap_2d(&o->rows64, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)K,
+                      (uint64_t)rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+constexpr const char* kOpName[] = {"ortho_gram", "ortho_poly", "ortho_apply", "ortho_apply"};
+
+template <int OP>
+cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, const Product& p,
+                         long long units, cudaStream_t s) {
+  using C = Cfg<256, 6>;
+  auto kern = ortho_product_kernel<OP, 256, 6>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -500,6 +790,7 @@ cudaError_t launch_product(const void* P, const void* Q, const Product& p, cudaS
   // pairs that fit on the device at once; the grid never exceeds it
   static int max_clusters[64] = {};
   static std::mutex mu;
+  int most;
   {
     std::lock_guard<std::mutex> lock(mu);
     if (max_clusters[dev] == 0) {
@@ -515,29 +806,90 @@ cudaError_t launch_product(const void* P, const void* Q, const Product& p, cudaS
       if (n <= 0) return cudaErrorInvalidConfiguration;
       max_clusters[dev] = n;
     }
+    most = max_clusters[dev];
   }
-  CUtensorMap tp, tq;
-  if (!make_tmap_2d(&tp, P, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)p.K,
-                    (uint64_t)p.n_mats * p.rowsP, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tq, Q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (uint64_t)p.K,
-                    (uint64_t)p.n_mats * p.rowsQ, 64, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  const Tiles<BN, OP == kGram || OP == kPoly> tiles(p.rowsP, p.rowsQ);
-  const long long units = (long long)tiles.count() * p.n_mats;
-  const long long pairs = units < max_clusters[dev] ? units : max_clusters[dev];
-  ProfScope pr(OP == kGram ? "ortho_gram" : OP == kPoly ? "ortho_poly" : "ortho_apply", s);
-  (void)launch_kernel(kern, (unsigned)(2 * pairs), kThreads, C::SMEM_TOTAL, s, tp, tq, p);
+  const long long pairs = units < most ? units : most;
+  ProfScope pr(kOpName[OP], s);
+  (void)launch_kernel(kern, (unsigned)(2 * pairs), kThreads, C::SMEM_TOTAL, s, P.rows128,
+                      Q.rows128, p);
   return cudaGetLastError();
 }
 
 template <int OP>
-cudaError_t product(const void* P, const void* Q, const Product& p, cudaStream_t s) {
-  return launch_product<OP, 256, 6>(P, Q, p, s);
+cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Product& p,
+                         long long units, cudaStream_t s) {
+  using C = SmallCfg;
+  auto kern = ortho_small_kernel<OP>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  static std::atomic<bool> configured[64] = {};
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  // the reduction is shared while that leaves at most two CTAs an SM and each
+  // at least four of its blocks
+  int split = 1;
+  while (split < 8 && units * split <= num_sms() && p.K / 64 / (2 * split) >= 4) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * split));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = C::SMEM_TOTAL;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  ProfScope pr(kOpName[OP], s);
+  count_launch();
+  (void)cudaLaunchKernelEx(&cfg, kern, P.rows128, Q.rows64, p, split);
+  return cudaGetLastError();
+}
+
+template <int OP>
+cudaError_t product(const OperandMaps& P, const OperandMaps& Q, const Product& p,
+                    cudaStream_t s) {
+  constexpr bool SYM = OP == kGram || OP == kPoly;
+  const long long n = p.n_mats;
+  const long long large = n * Tiles<256, 256, SYM>(p.rowsP, p.rowsQ).count();
+  const long long small = n * Tiles<128, kSmallN, SYM>(p.rowsP, p.rowsQ).count();
+  return large < kPairUnits || 2 * small < 5 * large ? launch_small<OP>(P, Q, p, small, s)
+                                                     : launch_pairs<OP>(P, Q, p, large, s);
 }
 
 int sum_blocks(size_t per_mat) {
   const size_t want = (per_mat + 16383) / 16384;  // 32 elements a thread
   return want < kSumBlocks ? (int)want : kSumBlocks;
+}
+
+// |G|, the scales and the first X in both layouts.
+template <typename T>
+cudaError_t start(const moe_ortho_desc& D, const T* g, const OrthoLayout& L, float* partial,
+                  Scale* scales, int* flags, __half* x, __half* xt, cudaStream_t s) {
+  const size_t per_mat = (size_t)D.rows * D.cols;
+  const int nb = sum_blocks(per_mat);
+  {
+    ProfScope pr("ortho_sumsq", s);
+    (void)launch_kernel(ortho_sumsq_kernel<T>, dim3(nb, D.n_mats), 512, 0, s, g, per_mat, partial,
+                        flags);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool tall = D.rows > D.cols;
+  const int rp = tall ? L.np : L.mp, cp = tall ? L.mp : L.np;
+  ProfScope pr("ortho_start", s);
+  (void)launch_kernel(D.cols % (16 / (int)sizeof(T)) == 0 ? ortho_start_kernel<T, true>
+                                                          : ortho_start_kernel<T, false>,
+                      dim3(cp / 64, rp / 64, D.n_mats), 256, 0, s, g, D.rows, D.cols, rp, cp,
+                      D.eps, partial, nb, scales, tall ? xt : x, tall ? x : xt);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -571,29 +923,18 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 16 + 255) &
                                           ~(uintptr_t)255);
   const int m = D.rows < D.cols ? D.rows : D.cols, n = D.rows < D.cols ? D.cols : D.rows;
-  const int bf16 = D.dtype == MOE_BF16;
-  const size_t per_mat = (size_t)D.rows * D.cols;
   float* partial = reinterpret_cast<float*>(b + L.partial);
   Scale* scales = reinterpret_cast<Scale*>(b + L.scales);
   __half* x = reinterpret_cast<__half*>(b + L.x);
   __half* xt[2] = {reinterpret_cast<__half*>(b + L.xt[0]), reinterpret_cast<__half*>(b + L.xt[1])};
   __half* gram = reinterpret_cast<__half*>(b + L.gram);
   __half* poly = reinterpret_cast<__half*>(b + L.poly);
-  const int nb = sum_blocks(per_mat);
-  {
-    ProfScope pr("ortho_sumsq", s);
-    (void)launch_kernel(ortho_sumsq_kernel, dim3(nb, D.n_mats), 512, 0, s, g, bf16, per_mat,
-                        partial, flags);
-  }
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = D.dtype == MOE_BF16
+                      ? start(D, static_cast<const __nv_bfloat16*>(g), L, partial, scales, flags,
+                              x, xt[0], s)
+                      : start(D, static_cast<const float*>(g), L, partial, scales, flags, x,
+                              xt[0], s);
   if (e != cudaSuccess) return e;
-  {
-    ProfScope pr("ortho_start", s);
-    (void)launch_kernel(ortho_start_kernel, dim3(L.np / 64, L.mp / 64, D.n_mats), 256, 0, s, g,
-                        bf16, D.rows, D.cols, m, n, L.mp, L.np, D.eps, partial, nb, scales, x,
-                        xt[0]);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   Product p{};
   p.n_mats = D.n_mats;
   p.m = m, p.n = n;
@@ -601,18 +942,24 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   p.err = flags;
   p.tall = D.rows > D.cols;
   p.result = static_cast<__nv_bfloat16*>(out);
+  OperandMaps mx, mt[2], mg, mb;
+  const long long rm = (long long)D.n_mats * L.mp, rn = (long long)D.n_mats * L.np;
+  if (!make_maps(&mx, x, L.np, rm) || !make_maps(&mt[0], xt[0], L.mp, rn) ||
+      !make_maps(&mt[1], xt[1], L.mp, rn) || !make_maps(&mg, gram, L.mp, rm) ||
+      !make_maps(&mb, poly, L.mp, rm))
+    return cudaErrorInvalidValue;
   for (int i = 0; i < D.steps; ++i) {
     p.first = i == 0;
     p.K = L.np, p.rowsP = p.rowsQ = L.mp;
     p.out = gram;
-    if ((e = product<kGram>(x, x, p, s)) != cudaSuccess) return e;
+    if ((e = product<kGram>(mx, mx, p, s)) != cudaSuccess) return e;
     p.K = L.mp;
     p.gram = gram, p.out = poly;
-    if ((e = product<kPoly>(gram, gram, p, s)) != cudaSuccess) return e;
+    if ((e = product<kPoly>(mg, mg, p, s)) != cudaSuccess) return e;
     p.rowsQ = L.np;
     p.out = x, p.out_t = xt[(i + 1) & 1];
-    e = i + 1 < D.steps ? product<kApply>(poly, xt[i & 1], p, s)
-                        : product<kLast>(poly, xt[i & 1], p, s);
+    e = i + 1 < D.steps ? product<kApply>(mb, mt[i & 1], p, s)
+                        : product<kLast>(mb, mt[i & 1], p, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
