@@ -207,8 +207,7 @@ cudaError_t launch_norm_backward(const moe_norm_desc& D, const void* dy, const v
 struct OrthoLayout {
   size_t partial;  // partial sums of squares
   size_t scales;
-  size_t x;        // fp16 [n_mats, mp, np]
-  size_t xt[2];    // fp16 [n_mats, np, mp]
+  size_t x[2];     // fp16 [n_mats, mp, np], read and written in turn
   size_t gram;     // fp16 [n_mats, mp, mp]
   size_t poly;     // fp16 [n_mats, mp, mp]
   size_t total;

@@ -19,8 +19,10 @@
 // needs no second pass over X and no cancelling difference of rounded terms.
 //
 // Work.  A and B are symmetric: only the tiles of one triangle are computed and
-// each is written twice, straight and mirrored.  X is kept in both layouts,
-// X [m, n] for X X^T and X^T [n, m] for B X, so every operand is K-major.
+// each is written twice, straight and mirrored.  X [m, n] is the only copy of
+// X: it is K-major in X X^T, and in B X the tensor cores read it MN-major
+// (rows of 64 columns of X, the reduction running down the rows), so no
+// transposed copy is written.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -167,15 +169,14 @@ __device__ Scale matrix_scale(const float* partial, int n, float eps) {
   return r;
 }
 
-// First X in fp16, padded with zeros, in the input's own layout, same
-// [rows, cols] padded to [rp, cp], and transposed, turned [cp, rp]: a 64 x 64
-// tile a block.  A thread loads and stores 8 elements of a row at a time; the
-// transposed copy goes through shared memory.
-template <typename T, bool VEC>
+// First X in fp16, padded with zeros: the input, [rows, cols] padded to
+// [rp, cp], or its transpose [cp, rp] (TURN): a 64 x 64 tile a block.  A thread
+// loads and stores 8 elements of a row at a time; a transposed tile goes
+// through shared memory.
+template <typename T, bool VEC, bool TURN>
 __global__ void __launch_bounds__(256)
     ortho_start_kernel(const T* g, int rows, int cols, int rp, int cp, float eps,
-                       const float* partial, int n_partial, Scale* scales, __half* same,
-                       __half* turned) {
+                       const float* partial, int n_partial, Scale* scales, __half* x) {
   pdl_wait();
   pdl_trigger();
   __shared__ Scale sc;
@@ -226,11 +227,13 @@ __global__ void __launch_bounds__(256)
     for (int j = 0; j < 4; ++j) {
       const __half2 p = __floats2half2_rn(v[h][2 * j] * f1 * f2, v[h][2 * j + 1] * f1 * f2);
       u[j] = *reinterpret_cast<const uint32_t*>(&p);
-      tile[tr + 32 * h][tc / 2 + j] = u[j];
+      if (TURN) tile[tr + 32 * h][tc / 2 + j] = u[j];
     }
-    *reinterpret_cast<uint4*>(same + ((size_t)mat * rp + r0 + tr + 32 * h) * cp + c0 + tc) =
-        make_uint4(u[0], u[1], u[2], u[3]);
+    if (!TURN)
+      *reinterpret_cast<uint4*>(x + ((size_t)mat * rp + r0 + tr + 32 * h) * cp + c0 + tc) =
+          make_uint4(u[0], u[1], u[2], u[3]);
   }
+  if (!TURN) return;
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -241,29 +244,28 @@ __global__ void __launch_bounds__(256)
       const uint32_t a = tile[tc + 2 * j][c / 2], b = tile[tc + 2 * j + 1][c / 2];
       u[j] = c & 1 ? (a >> 16) | (b & 0xffff0000u) : (a & 0xffffu) | (b << 16);
     }
-    *reinterpret_cast<uint4*>(turned + ((size_t)mat * cp + c0 + c) * rp + r0 + tc) =
+    *reinterpret_cast<uint4*>(x + ((size_t)mat * cp + c0 + c) * rp + r0 + tc) =
         make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
 // ---------------------------------------------------------------- products
-// Product P Q^T of the matrices' K-major operands, on pairs of SMs: a unit is
-// (matrix, 256 rows of P, BN rows of Q, all of K).
+// Products of the matrices' operands, on pairs of SMs: a unit is (matrix, 256
+// rows of P, BN columns of the product, all of K).
 //   kGram : A  = X X^T, from P = Q = X             -> out, both triangles
 //   kPoly : B  = a I + b A + c A A, P = Q = A      -> out, both triangles
-//   kApply: X' = B X, P = B, Q = X^T               -> out = X', out_t = X'^T
+//   kApply: X' = B X, P = B, Q = X (MN-major)      -> out
 //   kLast : the same                               -> result in bf16
 enum Op { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
 struct Product {
   int n_mats;
   int K;             // reduction length, a multiple of 64
-  int rowsP, rowsQ;  // padded rows a matrix has in P and in Q: multiples of 64
+  int rowsP, rowsQ;  // padded rows and columns of a product: multiples of 64
   int m, n;          // the matrices' own size
   int first;         // X is the first one: apply rho
   const Scale* scales;
   __half* out;             // [n_mats * rowsP, rowsQ]
-  __half* out_t;           // kApply: [n_mats * rowsQ, rowsP]
   const __half* gram;      // kPoly: A
   __nv_bfloat16* result;   // kLast: [n_mats, m, n], or [n_mats, n, m] if tall
   int tall;
@@ -313,6 +315,20 @@ struct Tiles {
   __device__ bool mirrored(int i, int j) const { return SYM && (j + 1) * BN <= i * BM; }
 };
 
+// Shared-memory descriptor of an MN-major operand written by TMA in boxes of 64
+// columns (128 bytes, 128-byte swizzle) by 64 reduction rows: 8-row groups are
+// 1024 bytes apart, the next 64 columns 8192.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
+  uint64_t desc = 0;
+  desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
+  desc |= static_cast<uint64_t>(8192 >> 4) << 16;          // leading byte offset: 64 columns
+  desc |= static_cast<uint64_t>(1024 >> 4) << 32;          // stride byte offset: 8 rows
+  desc |= static_cast<uint64_t>(1) << 46;                  // descriptor version
+  desc |= static_cast<uint64_t>(2) << 61;                  // 128-byte swizzle
+  return desc;
+}
+constexpr uint32_t kTransposeB = 1u << 16;  // instruction descriptor: B is MN-major
+
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -361,7 +377,7 @@ __device__ __forceinline__ float product_scale(const Product& p, int mat) {
 
 // Accumulators of W columns (8 or 16) of row `row` from column c0 on, already
 // scaled, to the product's outputs: along the row in one 16- or 32-byte store,
-// and column by column (64 bytes a warp) for the mirrored or transposed copy.
+// and column by column (64 bytes a warp) for the mirrored copy.
 template <int OP, int W>
 __device__ __forceinline__ void store_product(const Product& p, int mat, int row, int c0,
                                               bool mirror, float (&v)[W]) {
@@ -401,9 +417,9 @@ __device__ __forceinline__ void store_product(const Product& p, int mat, int row
   } else {
     *reinterpret_cast<uint4*>(p.out + at) = make_uint4(u[0], u[1], u[2], u[3]);
   }
-  if (mirror || OP == kApply) {
-    uint16_t* t = reinterpret_cast<uint16_t*>(OP == kApply ? p.out_t : p.out) +
-                  ((size_t)mat * p.rowsQ + c0) * p.rowsP + row;
+  if (mirror) {  // rowsP == rowsQ
+    uint16_t* t = reinterpret_cast<uint16_t*>(p.out) +
+                  ((size_t)mat * p.rowsP + c0) * p.rowsP + row;
 #pragma unroll
     for (int j = 0; j < W; ++j)
       t[(size_t)j * p.rowsP] = (uint16_t)(j & 1 ? u[j / 2] >> 16 : u[j / 2] & 0xffffu);
@@ -415,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ortho_product_kernel(const __grid_constant__ CUtensorMap tmP,
                          const __grid_constant__ CUtensorMap tmQ, const Product p) {
   using C = Cfg<BN, STAGES>;
-  constexpr bool SYM = OP == kGram || OP == kPoly;
+  constexpr bool SYM = OP == kGram || OP == kPoly;  // else Q is MN-major
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -474,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int i, j;
         tiles.at(u - mat * per_mat, i, j);
         const int prow = mat * p.rowsP + i * 256 + (int)rank * 128;
-        const int qrow = mat * p.rowsQ + j * BN + (int)rank * (BN / 2);
+        const int qcol = j * BN + (int)rank * (BN / 2);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
             ok = false;
@@ -488,7 +504,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t fb = mapa_shared(full_bar(stage), 0);
           const uint32_t s = sbase + stage * C::STAGE_BYTES;
           tma_load_2d_pair(s, &tmP, fb, kb * 64, prow);
-          tma_load_2d_pair(s + C::A_BYTES, &tmQ, fb, kb * 64, qrow);
+          if (SYM) {
+            tma_load_2d_pair(s + C::A_BYTES, &tmQ, fb, kb * 64, mat * p.rowsQ + qcol);
+          } else {
+#pragma unroll
+            for (int c = 0; c < BN / 2; c += 64)
+              tma_load_2d_pair(s + C::A_BYTES + c * 128, &tmQ, fb, qcol + c, mat * p.K + kb * 64);
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -510,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(256, BN);
+      constexpr uint32_t idesc = idesc_f16_f32(256, BN) | (SYM ? 0u : kTransposeB);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool issued = false;
@@ -531,7 +553,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16_pair(d0, smem_desc_sw128(s + kk * 32),
-                           smem_desc_sw128(s + C::A_BYTES + kk * 32), idesc, kb | kk ? 1u : 0u);
+                           SYM ? smem_desc_sw128(s + C::A_BYTES + kk * 32)
+                               : smem_desc_mn128(s + C::A_BYTES + kk * 2048),
+                           idesc, kb | kk ? 1u : 0u);
           issued = true;
           umma_commit_pair_mc(empty_bar(stage), 3);  // both CTAs' stage is free again
           if (++stage == STAGES) {
@@ -672,7 +696,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
-      const int prow = mat * p.rowsP + ti * 128, qrow = mat * p.rowsQ + tj * kSmallN;
+      const int prow = mat * p.rowsP + ti * 128, qcol = tj * kSmallN;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) break;
         mbar_arrive_expect_tx(full_bar(stage), C::STAGE_BYTES);
@@ -680,7 +704,10 @@ __global__ void __launch_bounds__(kSmallThreads)
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         const uint32_t s = sbase + stage * C::STAGE_BYTES;
         tma_load_2d(s, &tmP, full_bar(stage), kb * 64, prow);
-        tma_load_2d(s + C::A_BYTES, &tmQ, full_bar(stage), kb * 64, qrow);
+        if (SYM)
+          tma_load_2d(s + C::A_BYTES, &tmQ, full_bar(stage), kb * 64, mat * p.rowsQ + qcol);
+        else
+          tma_load_2d(s + C::A_BYTES, &tmQ, full_bar(stage), qcol, mat * p.K + kb * 64);
         if (++stage == kSmallStages) {
           stage = 0;
           phase ^= 1u;
@@ -691,7 +718,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(128, kSmallN);
+      constexpr uint32_t idesc = idesc_f16_f32(128, kSmallN) | (SYM ? 0u : kTransposeB);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -702,7 +729,9 @@ __global__ void __launch_bounds__(kSmallThreads)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16(tmem_base, smem_desc_sw128(s + kk * 32),
-                    smem_desc_sw128(s + C::A_BYTES + kk * 32), idesc, kb != kb0 || kk ? 1u : 0u);
+                    SYM ? smem_desc_sw128(s + C::A_BYTES + kk * 32)
+                        : smem_desc_mn128(s + C::A_BYTES + kk * 2048),
+                    idesc, kb != kb0 || kk ? 1u : 0u);
         umma_commit(empty_bar(stage));
         if (++stage == kSmallStages) {
           stage = 0;
@@ -764,7 +793,7 @@ __global__ void __launch_bounds__(kSmallThreads)
 }
 
 // ---------------------------------------------------------------- host
-// Tensor maps of one K-major operand, boxes of 64 columns.
+// Tensor maps of one operand, boxes of 64 columns by 128 or 64 rows.
 struct OperandMaps {
   CUtensorMap rows128, rows64;
 };
@@ -811,7 +840,7 @@ cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, const Produ
   const long long pairs = units < most ? units : most;
   ProfScope pr(kOpName[OP], s);
   (void)launch_kernel(kern, (unsigned)(2 * pairs), kThreads, C::SMEM_TOTAL, s, P.rows128,
-                      Q.rows128, p);
+                      OP == kGram || OP == kPoly ? Q.rows128 : Q.rows64, p);
   return cudaGetLastError();
 }
 
@@ -869,10 +898,10 @@ int sum_blocks(size_t per_mat) {
   return want < kSumBlocks ? (int)want : kSumBlocks;
 }
 
-// |G|, the scales and the first X in both layouts.
+// |G|, the scales and the first X.
 template <typename T>
 cudaError_t start(const moe_ortho_desc& D, const T* g, const OrthoLayout& L, float* partial,
-                  Scale* scales, int* flags, __half* x, __half* xt, cudaStream_t s) {
+                  Scale* scales, int* flags, __half* x, cudaStream_t s) {
   const size_t per_mat = (size_t)D.rows * D.cols;
   const int nb = sum_blocks(per_mat);
   {
@@ -885,10 +914,12 @@ cudaError_t start(const moe_ortho_desc& D, const T* g, const OrthoLayout& L, flo
   const bool tall = D.rows > D.cols;
   const int rp = tall ? L.np : L.mp, cp = tall ? L.mp : L.np;
   ProfScope pr("ortho_start", s);
-  (void)launch_kernel(D.cols % (16 / (int)sizeof(T)) == 0 ? ortho_start_kernel<T, true>
-                                                          : ortho_start_kernel<T, false>,
-                      dim3(cp / 64, rp / 64, D.n_mats), 256, 0, s, g, D.rows, D.cols, rp, cp,
-                      D.eps, partial, nb, scales, tall ? xt : x, tall ? x : xt);
+  const bool vec = D.cols % (16 / (int)sizeof(T)) == 0;
+  auto kern = vec ? (tall ? ortho_start_kernel<T, true, true> : ortho_start_kernel<T, true, false>)
+                  : (tall ? ortho_start_kernel<T, false, true>
+                          : ortho_start_kernel<T, false, false>);
+  (void)launch_kernel(kern, dim3(cp / 64, rp / 64, D.n_mats), 256, 0, s, g, D.rows, D.cols, rp,
+                      cp, D.eps, partial, nb, scales, x);
   return cudaGetLastError();
 }
 
@@ -908,8 +939,7 @@ OrthoLayout ortho_layout(const moe_ortho_desc& D) {
   };
   L.partial = take(n * kSumBlocks * 3 * sizeof(float));
   L.scales = take(n * sizeof(Scale));
-  L.x = take(n * L.mp * L.np * 2);
-  for (size_t& o : L.xt) o = take(n * L.mp * L.np * 2);
+  for (size_t& o : L.x) o = take(n * L.mp * L.np * 2);
   L.gram = take(n * L.mp * L.mp * 2);
   L.poly = take(n * L.mp * L.mp * 2);
   L.total = 512 + off;  // the flags' 16 bytes, then the regions at the next multiple of 256
@@ -925,15 +955,14 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   const int m = D.rows < D.cols ? D.rows : D.cols, n = D.rows < D.cols ? D.cols : D.rows;
   float* partial = reinterpret_cast<float*>(b + L.partial);
   Scale* scales = reinterpret_cast<Scale*>(b + L.scales);
-  __half* x = reinterpret_cast<__half*>(b + L.x);
-  __half* xt[2] = {reinterpret_cast<__half*>(b + L.xt[0]), reinterpret_cast<__half*>(b + L.xt[1])};
+  __half* x[2] = {reinterpret_cast<__half*>(b + L.x[0]), reinterpret_cast<__half*>(b + L.x[1])};
   __half* gram = reinterpret_cast<__half*>(b + L.gram);
   __half* poly = reinterpret_cast<__half*>(b + L.poly);
   cudaError_t e = D.dtype == MOE_BF16
                       ? start(D, static_cast<const __nv_bfloat16*>(g), L, partial, scales, flags,
-                              x, xt[0], s)
-                      : start(D, static_cast<const float*>(g), L, partial, scales, flags, x,
-                              xt[0], s);
+                              x[0], s)
+                      : start(D, static_cast<const float*>(g), L, partial, scales, flags, x[0],
+                              s);
   if (e != cudaSuccess) return e;
   Product p{};
   p.n_mats = D.n_mats;
@@ -942,24 +971,23 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   p.err = flags;
   p.tall = D.rows > D.cols;
   p.result = static_cast<__nv_bfloat16*>(out);
-  OperandMaps mx, mt[2], mg, mb;
-  const long long rm = (long long)D.n_mats * L.mp, rn = (long long)D.n_mats * L.np;
-  if (!make_maps(&mx, x, L.np, rm) || !make_maps(&mt[0], xt[0], L.mp, rn) ||
-      !make_maps(&mt[1], xt[1], L.mp, rn) || !make_maps(&mg, gram, L.mp, rm) ||
-      !make_maps(&mb, poly, L.mp, rm))
+  OperandMaps mx[2], mg, mb;
+  const long long rows = (long long)D.n_mats * L.mp;
+  if (!make_maps(&mx[0], x[0], L.np, rows) || !make_maps(&mx[1], x[1], L.np, rows) ||
+      !make_maps(&mg, gram, L.mp, rows) || !make_maps(&mb, poly, L.mp, rows))
     return cudaErrorInvalidValue;
   for (int i = 0; i < D.steps; ++i) {
     p.first = i == 0;
     p.K = L.np, p.rowsP = p.rowsQ = L.mp;
     p.out = gram;
-    if ((e = product<kGram>(mx, mx, p, s)) != cudaSuccess) return e;
+    if ((e = product<kGram>(mx[i & 1], mx[i & 1], p, s)) != cudaSuccess) return e;
     p.K = L.mp;
     p.gram = gram, p.out = poly;
     if ((e = product<kPoly>(mg, mg, p, s)) != cudaSuccess) return e;
     p.rowsQ = L.np;
-    p.out = x, p.out_t = xt[(i + 1) & 1];
-    e = i + 1 < D.steps ? product<kApply>(mb, mt[i & 1], p, s)
-                        : product<kLast>(mb, mt[i & 1], p, s);
+    p.out = x[(i + 1) & 1];
+    e = i + 1 < D.steps ? product<kApply>(mb, mx[i & 1], p, s)
+                        : product<kLast>(mb, mx[i & 1], p, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
