@@ -70,8 +70,11 @@ __device__ __forceinline__ void load_elems(const T* p, float (&v)[V]) {
 
 constexpr float kBig = 0x1p45f, kSmall = 0x1p-45f, kUp = 0x1p84f, kDown = 0x1p-84f;
 
-// Sums of squares of one matrix, block blockIdx.x of gridDim.x; three sums so
-// that no square over- or underflows: of values above 2^45 times 2^-84, of
+// Sums of squares of one matrix, block blockIdx.x of gridDim.x.  Squares are
+// summed as they are while the block's largest value lies between 2^-45 and
+// 2^45 (what then underflows is below 2^-63, far under the sum's last digit).
+// A block for which it does not reads its values again and keeps three sums in
+// which no square over- or underflows: of values above 2^45 times 2^-84, of
 // values below 2^-45 times 2^84, and of the rest.  A matrix that starts off a
 // 16-byte boundary is read in vectors from the next one on.
 template <typename T>
@@ -80,43 +83,59 @@ __global__ void __launch_bounds__(512)
   pdl_wait();
   pdl_trigger();
   __shared__ float red[3][16];
+  __shared__ float top[16];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flags[0] = 0;
   constexpr int V = 16 / (int)sizeof(T);
   const T* p = g + (size_t)blockIdx.y * per_mat;
-  float s[3] = {0.f, 0.f, 0.f};
-  auto add = [&](float x) {
-    const float ax = fabsf(x);
-    if (ax > kBig) {
-      s[0] = fmaf(x * kDown, x * kDown, s[0]);
-    } else if (ax < kSmall) {
-      s[2] = fmaf(x * kUp, x * kUp, s[2]);
-    } else {
-      s[1] = fmaf(x, x, s[1]);
-    }
-  };
   const size_t tid = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
   const size_t stride = (size_t)gridDim.x * blockDim.x;
   const size_t off = (reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T);
   const size_t head = off ? (V - off < per_mat ? V - off : per_mat) : 0;
   const size_t nv = (per_mat - head) / V, tail = head + nv * V;
-  if (tid < head) add(load_as_f32(p, tid));
-  if (tid < per_mat - tail) add(load_as_f32(p, tail + tid));
-  constexpr int U = 4;  // vectors in flight
-  for (size_t i = tid; i < nv; i += U * stride) {
-    float v[U][V];
+  auto each = [&](auto&& add) {
+    if (tid < head) add(load_as_f32(p, tid));
+    if (tid < per_mat - tail) add(load_as_f32(p, tail + tid));
+    constexpr int U = 4;  // vectors in flight
+    for (size_t i = tid; i < nv; i += U * stride) {
+      float v[U][V];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (i + k * stride < nv) {
-        load_elems<T, V>(p + head + (i + k * stride) * V, v[k]);
-      } else {
+      for (int k = 0; k < U; ++k) {
+        if (i + k * stride < nv) {
+          load_elems<T, V>(p + head + (i + k * stride) * V, v[k]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+          for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+        }
       }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) add(v[k][j]);
     }
+  };
+  float s[3] = {0.f, 0.f, 0.f}, most = 0.f;
+  each([&](float x) {
+    s[1] = fmaf(x, x, s[1]);
+    most = fmaxf(most, fabsf(x));  // a NaN is in the sum
+  });
 #pragma unroll
-    for (int k = 0; k < U; ++k)
+  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = most;
+  __syncthreads();
 #pragma unroll
-      for (int j = 0; j < V; ++j) add(v[k][j]);
+  for (int w = 0; w < 16; ++w) most = fmaxf(most, top[w]);
+  if (most != 0.f && (most > kBig || most < kSmall)) {
+    s[1] = 0.f;
+    each([&](float x) {
+      const float ax = fabsf(x);
+      if (ax > kBig) {
+        s[0] = fmaf(x * kDown, x * kDown, s[0]);
+      } else if (ax < kSmall) {
+        s[2] = fmaf(x * kUp, x * kUp, s[2]);
+      } else {
+        s[1] = fmaf(x, x, s[1]);
+      }
+    });
   }
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
@@ -251,7 +270,9 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- products
 // Products of the matrices' operands, on pairs of SMs: a unit is (matrix, 256
-// rows of P, BN columns of the product, all of K).
+// rows of P, BN columns of the product, all of K).  The tiles that are left for
+// the last round of the pairs are cut along their columns into as many parts as
+// keep every pair to one unit.
 //   kGram : A  = X X^T, from P = Q = X             -> out, both triangles
 //   kPoly : B  = a I + b A + c A A, P = Q = A      -> out, both triangles
 //   kApply: X' = B X, P = B, Q = X (MN-major)      -> out
@@ -264,6 +285,7 @@ struct Product {
   int rowsP, rowsQ;  // padded rows and columns of a product: multiples of 64
   int m, n;          // the matrices' own size
   int first;         // X is the first one: apply rho
+  int whole, cut;    // SM pairs: units that are whole tiles; the rest are cut into `cut` parts
   const Scale* scales;
   __half* out;             // [n_mats * rowsP, rowsQ]
   const __half* gram;      // kPoly: A
@@ -449,8 +471,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int pair = (int)(blockIdx.x >> 1), n_pairs = (int)(gridDim.x >> 1);
   const Tiles<256, BN, SYM> tiles(p.rowsP, p.rowsQ);
-  const int per_mat = tiles.count(), total = per_mat * p.n_mats;
+  const int per_mat = tiles.count(), whole = p.whole;
+  const int total = whole + (per_mat * p.n_mats - whole) * p.cut;
   const int KB = p.K / 64;
+  // unit u -> matrix, row block, first column and width
+  auto unit = [&](int u, int& mat, int& ti, int& col, int& width) {
+    int tile = u, part = 0;
+    width = BN;
+    if (u >= whole) {
+      part = (u - whole) % p.cut;
+      tile = whole + (u - whole) / p.cut;
+      width = BN / p.cut;
+    }
+    mat = tile / per_mat;
+    int tj;
+    tiles.at(tile - mat * per_mat, ti, tj);
+    col = tj * BN + part * width;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -486,29 +523,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
       for (int u = pair; u < total && ok && !*abort_flag; u += n_pairs) {
-        const int mat = u / per_mat;
-        int i, j;
-        tiles.at(u - mat * per_mat, i, j);
-        const int prow = mat * p.rowsP + i * 256 + (int)rank * 128;
-        const int qcol = j * BN + (int)rank * (BN / 2);
+        int mat, ti, col, width;
+        unit(u, mat, ti, col, width);
+        const int prow = mat * p.rowsP + ti * 256 + (int)rank * 128;
+        const int qcol = col + (int)rank * (width / 2);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
           if (rank == 0) {
-            mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
+            mbar_arrive_expect_tx(full_bar(stage), 2 * (C::A_BYTES + (width / 2) * 128));
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           }
           const uint32_t fb = mapa_shared(full_bar(stage), 0);
           const uint32_t s = sbase + stage * C::STAGE_BYTES;
           tma_load_2d_pair(s, &tmP, fb, kb * 64, prow);
-          if (SYM) {
-            tma_load_2d_pair(s + C::A_BYTES, &tmQ, fb, kb * 64, mat * p.rowsQ + qcol);
-          } else {
-#pragma unroll
-            for (int c = 0; c < BN / 2; c += 64)
+          for (int c = 0; c < width / 2; c += 64) {  // boxes of 64 columns of the product
+            if (SYM)
+              tma_load_2d_pair(s + C::A_BYTES + c * 128, &tmQ, fb, kb * 64,
+                               mat * p.rowsQ + qcol + c);
+            else
               tma_load_2d_pair(s + C::A_BYTES + c * 128, &tmQ, fb, qcol + c, mat * p.K + kb * 64);
           }
           if (++stage == STAGES) {
@@ -532,7 +568,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(256, BN) | (SYM ? 0u : kTransposeB);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool issued = false;
@@ -542,6 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         tc_fence_after();
         const uint32_t d0 = tmem_base + (uint32_t)(buf * BN);
+        const uint32_t idesc =
+            idesc_f16_f32(256, u < whole ? BN : BN / p.cut) | (SYM ? 0u : kTransposeB);
         bool ok = true;
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
@@ -575,23 +612,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9, both CTAs)
     // A warp reads its TMEM lane quarter (row = lane); the two warps of a
-    // quarter take one half of the columns each, 16 at a time.
+    // quarter take one half of the unit's columns each, 16 at a time.
     const int q = warp & 3, half = (warp - 2) >> 2;
     int it = 0;
     for (int u = pair; u < total; u += n_pairs, ++it) {
-      const int mat = u / per_mat;
-      int ti, tj;
-      tiles.at(u - mat * per_mat, ti, tj);
+      int mat, ti, col, width;
+      unit(u, mat, ti, col, width);
       const int buf = it & 1;
       if (!tc::mbar_wait_warp(accf0 + 8u * buf, (uint32_t)(it >> 1) & 1u, abort_flag, p.err)) break;
       tc_fence_after();
       const int row = ti * 256 + (int)rank * 128 + q * 32 + lane;
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
       const float alpha = product_scale<OP>(p, mat);
-      const bool mirror = tiles.mirrored(ti, tj);
+      const bool mirror = tiles.mirrored(ti, col / BN);
 #pragma unroll 1
-      for (int cc = half * (BN / 2); cc < (half + 1) * (BN / 2); cc += 16) {
-        const int c0 = tj * BN + cc;
+      for (int cc = half * (width / 2); cc < (half + 1) * (width / 2); cc += 16) {
+        const int c0 = col + cc;
         if (c0 >= p.rowsQ) break;  // warp-uniform
         uint32_t a[16];
         tmem_ld16(tb + cc, a);
@@ -808,8 +844,8 @@ bool make_maps(OperandMaps* o, const void* base, int K, long long rows) {
 constexpr const char* kOpName[] = {"ortho_gram", "ortho_poly", "ortho_apply", "ortho_apply"};
 
 template <int OP>
-cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, const Product& p,
-                         long long units, cudaStream_t s) {
+cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, Product p,
+                         long long tiles, cudaStream_t s) {
   using C = Cfg<256, 6>;
   auto kern = ortho_product_kernel<OP, 256, 6>;
   int dev = 0;
@@ -837,10 +873,14 @@ cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, const Produ
     }
     most = max_clusters[dev];
   }
+  const int rest = (int)(tiles % most);
+  p.cut = 2 * rest <= most ? 2 : 1;
+  p.whole = (int)tiles - (p.cut > 1 ? rest : 0);
+  const long long units = p.whole + (tiles - p.whole) * p.cut;
   const long long pairs = units < most ? units : most;
   ProfScope pr(kOpName[OP], s);
   (void)launch_kernel(kern, (unsigned)(2 * pairs), kThreads, C::SMEM_TOTAL, s, P.rows128,
-                      OP == kGram || OP == kPoly ? Q.rows128 : Q.rows64, p);
+                      Q.rows64, p);
   return cudaGetLastError();
 }
 

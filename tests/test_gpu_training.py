@@ -385,7 +385,8 @@ def check_ortho(got, want):
 @pytest.mark.parametrize("n,rows,cols", [
     (1, 1, 1), (2, 3, 5), (2, 1, 300), (1, 300, 1), (1, 64, 64), (3, 65, 130), (2, 130, 65),
     (1, 257, 1001), (2, 300, 260), (1, 512, 512), (1, 1000, 64), (5, 128, 512), (1, 256, 4096),
-    (40, 100, 90), (1, 520, 776), (2, 1032, 600)])
+    (40, 100, 90), (1, 520, 776), (2, 1032, 600), (9, 1100, 600), (7, 1030, 1100),
+    (3, 1000, 2500), (60, 300, 260)])
 def test_ortho(n, rows, cols, dtype):
     g = rnd((n, rows, cols), rows + cols, DT[dtype], 0.02)
     check_ortho(moe.orthogonalize(g), ref_ortho(g, 5, 1e-7))
@@ -435,6 +436,11 @@ def test_ortho_zero_and_nan_matrices():
         assert not out[1].any() and out[2].isnan().all() and out[3].isnan().all()
         if eps:
             assert torch.equal(out[0], want[0]) and torch.equal(out[4], want[4])
+    # values so large or small that their squares leave fp32, beside ordinary ones
+    wide = rnd((1, 200, 300), 5)
+    wide[0, :, 7] *= 2.0 ** 70
+    wide[0, 9] *= 2.0 ** -80
+    check_ortho(moe.orthogonalize(wide, steps=1), ref_ortho(wide, 1, 1e-7))
 
 
 def test_ortho_workspace_stream_and_graph():
