@@ -14,9 +14,10 @@
 //
 // A row belongs to a group of whole warps that holds it in registers, so it
 // crosses HBM once.  Rows whose bytes are a multiple of 16 move in 16-byte
-// vectors, others element by element.
+// vectors, of 4 in 4-byte ones, others (bf16, odd d) element by element.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -26,67 +27,101 @@ namespace moe {
 namespace {
 
 constexpr int kMaxGroupWarps = 32;
-constexpr int kBwdBlocks = 304;  // most blocks of the backward pass: two per SM
+constexpr int kMaxStages = 8;
+constexpr int kBwdBlocks = 304;  // most blocks of the backward pass: two an SM, or one of
+                                 // more than 256 threads
+constexpr size_t kBwdRingBytes = 104 * 1024;  // shared memory of the rings, two blocks an SM
 
-// VEC consecutive elements of a row as fp32: one 16-byte access, or one element.
+// VEC consecutive elements of a row as they lie in memory (2, 4 or 16 bytes).
 template <typename T, int VEC>
-__device__ __forceinline__ void load_pack(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = load_as_f32(p, 0);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+struct alignas(VEC * sizeof(T)) Raw {
+  T e[VEC];
+};
+template <>
+struct alignas(16) Raw<__nv_bfloat16, 8> {
+  uint32_t w[4];
+};
+template <>
+struct alignas(4) Raw<__nv_bfloat16, 2> {
+  uint32_t w[1];
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float* v) {
+  if constexpr (sizeof(T) == 2 && VEC > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < VEC / 2; ++i) {
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = load_as_f32(r.e, i);
   }
 }
 
 template <typename T, int VEC>
-__device__ __forceinline__ void store_pack(T* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    if constexpr (sizeof(T) == 4)
-      *p = v[0];
-    else
-      *p = __float2bfloat16_rn(v[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    uint32_t u[4];
+__device__ __forceinline__ Raw<T, VEC> pack(const float* v) {
+  Raw<T, VEC> r;
+  if constexpr (sizeof(T) == 2 && VEC > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < VEC / 2; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+      r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      if constexpr (sizeof(T) == 2)
+        r.e[i] = __float2bfloat16_rn(v[i]);
+      else
+        r.e[i] = v[i];
+    }
   }
+  return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
+  if constexpr (VEC * sizeof(T) == 16) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    Raw<T, VEC> r;
+    *reinterpret_cast<uint4*>(&r) = a;
+    return r;
+  } else {
+    return *reinterpret_cast<const Raw<T, VEC>*>(p);
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, VEC>& r) {
+  if constexpr (VEC * sizeof(T) == 16)
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
+  else
+    *reinterpret_cast<Raw<T, VEC>*>(p) = r;
 }
 
 // VEC elements of a parameter vector (fp32 or bf16, whatever the rows are);
 // null stands for `otherwise`.
 template <int VEC>
 __device__ __forceinline__ void load_param(const void* p, bool bf16, int c, float otherwise,
-                                           float (&v)[VEC]) {
+                                           float* v) {
 #pragma unroll
   for (int i = 0; i < VEC; ++i) v[i] = otherwise;
   if (!p) return;
   if (bf16) {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + c;
-    if constexpr (VEC == 8) {
-      load_pack<__nv_bfloat16, 8>(q, v);
+    if constexpr (VEC == 8 || VEC == 2) {
+      unpack<__nv_bfloat16, VEC>(load_raw<__nv_bfloat16, VEC>(q), v);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v[i] = load_as_f32(q, i);
     }
   } else {
     const float* q = static_cast<const float*>(p) + c;
-    if constexpr (VEC == 1) {
-      v[0] = *q;
+    if constexpr (VEC < 4) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = q[i];
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; i += 4) {
@@ -97,175 +132,377 @@ __device__ __forceinline__ void load_param(const void* p, bool bf16, int c, floa
   }
 }
 
+// Two fp32 values in a 64-bit register pair, for the packed fp32 instructions:
+// the kernels below are bound by instruction issue before they are bound by
+// HBM otherwise (the backward pass took 31 instructions an element and 122 us at
+// 16384 x 4096 bf16 with one value an instruction).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(F2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ float both(F2 v) {
+  float a, b;
+  split(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Sums of N values over a group of `warps` warps, the same in every thread.
-// `buf` holds the group's partial sums, [2][N][kMaxGroupWarps]; successive
-// calls take its halves in turn, so one barrier a call is enough.  A group of
-// several warps meets at named barrier 1 + group (at most 8 such groups).
+// The warp's sums of two values: in a lane of the lower half that of a, of the
+// upper half that of b.  Five shuffles for both.
+__device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
+  const bool up = lane & 16;
+  float mine = up ? b : a;
+  const float other = up ? a : b;
+  mine += __shfl_xor_sync(0xffffffffu, other, 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  return mine;
+}
+
+// Sums of N (1 or 2) values over a group of `warps` warps, the same in every
+// thread.  `buf` holds the warps' sums, [2][N][kMaxGroupWarps], zero where the
+// group has no warp; successive calls take its halves in turn, so one barrier a
+// call is enough.  A group of several warps meets at named barrier 1 + group (at
+// most 8 such groups).  Every warp adds the warps' sums in the same order.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], int warps, int warp_in_group, int group,
                                           float* buf, int& turn) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
-  float* b = buf + turn * N * kMaxGroupWarps;
-  turn ^= 1;
   const int lane = threadIdx.x & 31;
-  if (lane == 0) {
+  float mine = N == 2 ? warp_sum2(v[0], v[N - 1], lane) : warp_sum(v[0]);
+  if (warps > 1) {
+    float* b = buf + turn * N * kMaxGroupWarps;
+    turn ^= 1;
+    if ((lane & (N == 2 ? 15 : 31)) == 0) b[(lane >> 4) * kMaxGroupWarps + warp_in_group] = mine;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
+    if constexpr (N == 2) {  // the lower half's lanes add up one value, the upper's the other
+      const float* p = b + (lane >> 4) * kMaxGroupWarps + (lane & 15);
+      mine = p[0] + (warps > 16 ? p[16] : 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[i * kMaxGroupWarps + warp_in_group] = v[i];
+      for (int o = 8; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    } else {
+      mine = warp_sum(b[lane]);
+    }
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? b[i * kMaxGroupWarps + lane] : 0.f);
+  if constexpr (N == 2) v[1] = __shfl_sync(0xffffffffu, mine, 16);
+  v[0] = N == 2 ? __shfl_sync(0xffffffffu, mine, 0) : mine;
+}
+
+// Zeroes the blocks' buffers for group_sum.
+template <int SIZE>
+__device__ __forceinline__ void clear_sums(float (&red)[8][SIZE]) {
+  for (int i = threadIdx.x; i < 8 * SIZE; i += blockDim.x) (&red[0][0])[i] = 0.f;
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------- forward
 // blockDim.x = groups * warps * 32; the groups of a block take successive rows.
+// The row stays packed as it was read, which leaves registers for enough
+// blocks an SM to keep HBM busy.
 template <typename T, int VEC, int VPT, bool RMS>
 __global__ void __launch_bounds__(512)
-    norm_forward_kernel(const T* x, const void* gamma, const void* beta, bool w_bf16,
-                                    int rows, int d, int warps, float eps, T* y, float* mean,
-                                    float* rstd) {
+    norm_forward_kernel(const T* x, const void* gamma, const void* beta, bool w_bf16, int rows,
+                        int d, int warps, float eps, T* y, float* mean, float* rstd) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[8][2 * kMaxGroupWarps];
+  if (warps > 1) clear_sums(red);
   const int gt = warps * 32;
   const int group = threadIdx.x / gt, tid = threadIdx.x - group * gt;
   const int row = blockIdx.x * (blockDim.x / gt) + group;
   if (row >= rows) return;  // a whole group
   const int nv = d / VEC;
   const T* xr = x + (size_t)row * d;
-  float v[VPT][VEC];
-  float s[1] = {0.f};
+  Raw<T, VEC> raw[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = tid + i * gt;
-    if (c < nv) {
-      load_pack<T, VEC>(xr + (size_t)c * VEC, v[i]);
-    } else {
+    raw[i] = Raw<T, VEC>{};
+    if (tid + i * gt < nv) raw[i] = load_raw<T, VEC>(xr + (size_t)(tid + i * gt) * VEC);
+  }
+  constexpr int N = VPT * VEC;
+  const float inv_d = 1.f / (float)d;
+  // the row's values, zero beyond its end
+  auto values = [&](float (&v)[N]) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+    for (int i = 0; i < VPT; ++i) unpack<T, VEC>(raw[i], v + i * VEC);
+  };
+  float s[1];
+  {
+    float v[N];
+    values(v);
+    F2 acc = f2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      const F2 p = f2(v[2 * k], v[2 * k + 1]);
+      acc = RMS ? fma2(p, p, acc) : add2(p, acc);
     }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) s[0] += RMS ? v[i][j] * v[i][j] : v[i][j];
+    s[0] = both(acc);
   }
   int turn = 0;
   float* buf = red[warps == 1 ? 0 : group];
   group_sum<1>(s, warps, tid >> 5, group, buf, turn);
   float mu = 0.f;
   if (!RMS) {
-    mu = s[0] / d;
-    s[0] = 0.f;
+    mu = s[0] * inv_d;
+    float v[N];
+    values(v);
+    const F2 m = f2(-mu, -mu);
+    F2 acc = f2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (tid + i * gt < nv) {
+      if (tid + i * gt < nv) {  // what lies beyond the row is not mu
+        if constexpr (VEC > 1) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float c = v[i][j] - mu;
-          s[0] = fmaf(c, c, s[0]);
+          for (int j = 0; j < VEC; j += 2) {
+            const F2 c = add2(f2(v[i * VEC + j], v[i * VEC + j + 1]), m);
+            acc = fma2(c, c, acc);
+          }
+        } else {
+          const F2 c = f2(v[i] - mu, 0.f);
+          acc = fma2(c, c, acc);
         }
       }
     }
+    s[0] = both(acc);
     group_sum<1>(s, warps, tid >> 5, group, buf, turn);
   }
-  const float r = 1.f / sqrtf(s[0] / d + eps);
+  const float r = 1.f / sqrtf(s[0] * inv_d + eps);
   if (tid == 0) {
     if (mean) mean[row] = mu;
     if (rstd) rstd[row] = r;
   }
   T* yr = y + (size_t)row * d;
+  const F2 m = f2(-mu, -mu), rr = f2(r, r);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * gt;
     if (c >= nv) break;
-    float g[VEC], b[VEC], o[VEC];
+    float v[VEC], g[VEC], b[VEC];
+    unpack<T, VEC>(raw[i], v);
     load_param<VEC>(gamma, w_bf16, c * VEC, 1.f, g);
     load_param<VEC>(RMS ? nullptr : beta, w_bf16, c * VEC, 0.f, b);
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] = fmaf((v[i][j] - mu) * r, g[j], b[j]);
-    store_pack<T, VEC>(yr + (size_t)c * VEC, o);
+      for (int j = 0; j < VEC; j += 2) {
+        const F2 x2 = f2(v[j], v[j + 1]);
+        const F2 h = mul2(RMS ? x2 : add2(x2, m), rr);
+        const F2 g2 = f2(g[j], g[j + 1]);
+        split(RMS ? mul2(h, g2) : fma2(h, g2, f2(b[j], b[j + 1])), v[j], v[j + 1]);
+      }
+    } else {
+      v[0] = fmaf((v[0] - mu) * r, g[0], b[0]);
+    }
+    store_raw<T, VEC>(yr + (size_t)c * VEC, pack<T, VEC>(v));
   }
 }
 
 // ---------------------------------------------------------------- backward
+// `bytes` (a multiple of 16) from global into shared memory, asynchronously;
+// completion is signalled on `bar` as transaction bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // Block b takes rows b * groups + group, + gridDim.x * groups, ...; a thread
 // owns the same columns of every row and keeps their sums of dy h and dy in
-// registers.  At the end the groups' sums are added in group order through
-// shared memory and written to partial [2][gridDim.x][d].
-template <typename T, int VEC, int VPT, bool RMS>
-__global__ void __launch_bounds__(1024)
+// registers.  With RING (rows of 16-byte vectors) each group has a ring of
+// `stages` rows of x and dy in shared memory, filled by bulk copies that one
+// thread requests `stages` rows ahead: HBM latency is hidden without registers
+// and a row's loads cost no instructions but its reads of shared memory.  The
+// barrier of the row's sums also says that every thread has read the stage.
+// Other rows are loaded where they are used.  At the end the groups' sums are
+// added in group order through shared memory and written to
+// partial [2][gridDim.x][d].
+//
+// A wait for a copy is bounded; should one expire, the row's results are NaN
+// and the group requests no more copies.
+template <typename T, int VEC, int VPT, bool RMS, bool RING, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
     norm_backward_kernel(const T* dy, const T* x, const void* gamma, bool w_bf16,
-                         const float* mean, const float* rstd, int rows, int d, int warps, T* dx,
-                         float* partial) {
+                         const float* mean, const float* rstd, int rows, int d, int warps,
+                         int stages, T* dx, float* partial) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float sums[];  // [d] of one quantity, for the groups' sums
+  extern __shared__ __align__(128) uint8_t dyn[];  // the rings, then the groups' sums [d]
   __shared__ float red[8][4 * kMaxGroupWarps];
+  __shared__ __align__(8) uint64_t bars[8][kMaxStages];
+  __shared__ int gave_up;
+  constexpr int N = VPT * VEC;
   const int gt = warps * 32, groups = blockDim.x / gt;
   const int group = threadIdx.x / gt, tid = threadIdx.x - group * gt;
   const int nv = d / VEC;
-  float dg[VPT][VEC], db[VPT][VEC];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) dg[i][j] = db[i][j] = 0.f;
-  int turn = 0;
-  float* buf = red[warps == 1 ? 0 : group];
-  for (int row = blockIdx.x * groups + group; row < rows; row += gridDim.x * groups) {
-    const float mu = RMS ? 0.f : mean[row], r = rstd[row];
-    const size_t base = (size_t)row * d;
-    float h[VPT][VEC], w[VPT][VEC];
-    float s[2] = {0.f, 0.f};
+  const int step = gridDim.x * groups;
+  const uint32_t row_bytes = (uint32_t)d * (uint32_t)sizeof(T);
+  const uint32_t bar0 = smem_u32(&bars[group][0]);
+  uint8_t* ring = dyn + (size_t)group * stages * 2 * row_bytes;
+  if (RING && tid == 0)
+    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8u * s, 1);
+  if (threadIdx.x == 0) gave_up = 0;
+  if (RING) fence_barrier_init();
+  clear_sums(red);
+  auto request = [&](int row, int s) {  // one thread of the group
+    const uint32_t dst = smem_u32(ring) + (uint32_t)s * 2u * row_bytes;
+    mbar_arrive_expect_tx(bar0 + 8u * s, 2u * row_bytes);
+    bulk_load(dst, x + (size_t)row * d, row_bytes, bar0 + 8u * s);
+    bulk_load(dst + row_bytes, dy + (size_t)row * d, row_bytes, bar0 + 8u * s);
+  };
+  int row = blockIdx.x * groups + group;
+  if (RING && tid == 0)
+    for (int s = 0; s < stages && row + s * step < rows; ++s) request(row + s * step, s);
+
+  // pairs of this thread's columns; columns beyond the row's end hold zeros in
+  // dy, so they add nothing to the row's sums, and are never stored
+  F2 g[N / 2], dg[N / 2], db[N / 2];
+  {
+    float gv[N];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = tid + i * gt;
-      if (c < nv) {
-        float g[VEC];
-        load_pack<T, VEC>(x + base + (size_t)c * VEC, h[i]);
-        load_pack<T, VEC>(dy + base + (size_t)c * VEC, w[i]);
-        load_param<VEC>(gamma, w_bf16, c * VEC, 1.f, g);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          h[i][j] = (h[i][j] - mu) * r;
-          dg[i][j] = fmaf(w[i][j], h[i][j], dg[i][j]);
-          if (!RMS) db[i][j] += w[i][j];
-          w[i][j] *= g[j];
-          s[0] = fmaf(w[i][j], h[i][j], s[0]);
-          s[1] += w[i][j];
+      for (int j = 0; j < VEC; ++j) gv[i * VEC + j] = 0.f;
+      if (tid + i * gt < nv) load_param<VEC>(gamma, w_bf16, (tid + i * gt) * VEC, 1.f, gv + i * VEC);
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      g[k] = f2(gv[2 * k], gv[2 * k + 1]);
+      dg[k] = db[k] = f2(0.f, 0.f);
+    }
+  }
+  const float inv_d = -1.f / (float)d;
+  const T* xp = x + (size_t)row * d + (size_t)tid * VEC;
+  const T* dp = dy + (size_t)row * d + (size_t)tid * VEC;
+  T* op = dx + (size_t)row * d + (size_t)tid * VEC;
+  const size_t jump = (size_t)step * d;
+  int turn = 0, stage = 0;
+  uint32_t parity = 0;
+  float* buf = red[warps == 1 ? 0 : group];
+  float mu = 0.f, r = 0.f;
+  if (row < rows) mu = RMS ? 0.f : mean[row], r = rstd[row];
+  for (; row < rows; row += step, xp += jump, dp += jump, op += jump) {
+    float mu2 = 0.f, r2 = 0.f;  // the next row's, loaded ahead
+    if (row + step < rows) mu2 = RMS ? 0.f : mean[row + step], r2 = rstd[row + step];
+    Raw<T, VEC> xr[VPT], dr[VPT];
+    if constexpr (RING) {
+      if (!mbar_wait(bar0 + 8u * stage, parity, &gave_up, nullptr)) r = __int_as_float(0x7fffffff);
+      const uint8_t* src = ring + (size_t)stage * 2 * row_bytes + (size_t)tid * sizeof(Raw<T, VEC>);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        xr[i] = dr[i] = Raw<T, VEC>{};
+        if (tid + i * gt < nv) {
+          const T* p = reinterpret_cast<const T*>(src + (size_t)i * gt * sizeof(Raw<T, VEC>));
+          xr[i] = load_raw<T, VEC>(p);
+          dr[i] = load_raw<T, VEC>(p + d);
+        }
+      }
+      fence_proxy_async_shared();  // before the barrier that hands the stage back
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        xr[i] = dr[i] = Raw<T, VEC>{};
+        if (tid + i * gt < nv) {
+          xr[i] = load_raw<T, VEC>(xp + (size_t)i * gt * VEC);
+          dr[i] = load_raw<T, VEC>(dp + (size_t)i * gt * VEC);
         }
       }
     }
-    group_sum<2>(s, warps, tid >> 5, group, buf, turn);
-    const float c1 = s[0] / d, c2 = RMS ? 0.f : s[1] / d;
+    float xv[N], dv[N];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = tid + i * gt;
-      if (c < nv) {
-        float o[VEC];
+      unpack<T, VEC>(xr[i], xv + i * VEC);
+      unpack<T, VEC>(dr[i], dv + i * VEC);
+    }
+    F2 h[N / 2], w[N / 2];
+    F2 wh = f2(0.f, 0.f), ws = f2(0.f, 0.f);
+    const F2 rr = f2(r, r), m = f2(-mu, -mu);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = (w[i][j] - c2 - h[i][j] * c1) * r;
-        store_pack<T, VEC>(dx + base + (size_t)c * VEC, o);
+    for (int k = 0; k < N / 2; ++k) {
+      const F2 x2 = f2(xv[2 * k], xv[2 * k + 1]), d2 = f2(dv[2 * k], dv[2 * k + 1]);
+      h[k] = mul2(RMS ? x2 : add2(x2, m), rr);
+      dg[k] = fma2(d2, h[k], dg[k]);
+      w[k] = mul2(d2, g[k]);
+      wh = fma2(w[k], h[k], wh);
+      if (!RMS) {
+        db[k] = add2(d2, db[k]);
+        ws = add2(w[k], ws);
       }
     }
+    float s[RMS ? 1 : 2];
+    s[0] = both(wh);
+    if constexpr (!RMS) s[1] = both(ws);
+    if (RING && warps == 1) __syncwarp();
+    group_sum<RMS ? 1 : 2>(s, warps, tid >> 5, group, buf, turn);
+    if (RING && tid == 0 && row + (long long)stages * step < rows &&
+        !*static_cast<volatile int*>(&gave_up))
+      request(row + stages * step, stage);
+    const float c1 = s[0] * inv_d;
+    const F2 n1 = f2(c1, c1);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      F2 t = fma2(h[k], n1, w[k]);
+      if constexpr (!RMS) t = add2(t, f2(s[1] * inv_d, s[1] * inv_d));
+      split(mul2(t, rr), dv[2 * k], dv[2 * k + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (tid + i * gt < nv)
+        store_raw<T, VEC>(op + (size_t)i * gt * VEC, pack<T, VEC>(dv + i * VEC));
+    mu = mu2, r = r2;
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
   }
-  auto flush = [&](float (&acc)[VPT][VEC], float* out) {
-    for (int g = 0; g < groups; ++g) {
+  if (RING && *static_cast<volatile int*>(&gave_up)) {
+    // leave copies that are still on their way a bounded time to land
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000ull) {
+    }
+  }
+  if (!partial) return;
+  float* sums = reinterpret_cast<float*>(dyn);  // every copy has landed and been read
+  auto flush = [&](const F2 (&acc2)[N / 2], float* out) {
+    float acc[N];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) split(acc2[k], acc[2 * k], acc[2 * k + 1]);
+    for (int k = 0; k < groups; ++k) {
       __syncthreads();
-      if (group != g) continue;
+      if (group != k) continue;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * gt;
         if (c < nv) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const float v = g ? sums[c * VEC + j] + acc[i][j] : acc[i][j];
-            if (g == groups - 1)
+            const float v = k ? sums[c * VEC + j] + acc[i * VEC + j] : acc[i * VEC + j];
+            if (k == groups - 1)
               out[c * VEC + j] = v;
             else
               sums[c * VEC + j] = v;
@@ -274,10 +511,8 @@ __global__ void __launch_bounds__(1024)
       }
     }
   };
-  if (partial) {
-    flush(dg, partial + (size_t)blockIdx.x * d);
-    if (!RMS) flush(db, partial + (size_t)(gridDim.x + blockIdx.x) * d);
-  }
+  flush(dg, partial + (size_t)blockIdx.x * d);
+  if (!RMS) flush(db, partial + (size_t)(gridDim.x + blockIdx.x) * d);
 }
 
 // out[c] = sum over the n blocks of partial[q][b][c], q = blockIdx.y: 32
@@ -307,54 +542,63 @@ struct Shape {
   int groups; // rows a block works on at a time
 };
 
-int round_up_pow2(int v, int lo) {
-  int p = lo;
-  while (p < v) p *= 2;
-  return p;
+int vector_of(int d, int es) {
+  const int bytes = d * es;
+  return bytes % 16 == 0 ? 16 / es : bytes % 4 == 0 ? 4 / es : 1;
 }
 
+// Up to 4 vectors or 8 (16 of odd bf16 rows) short accesses a thread while
+// that takes no more than 256 threads, then more.
 Shape forward_shape(int d, int es) {
   Shape s{};
-  s.vec = d * es % 16 == 0 ? 16 / es : 1;
+  s.vec = vector_of(d, es);
   const int nv = d / s.vec;
-  const int least = s.vec == 1 ? 4 : 1;
-  s.vpt = round_up_pow2((nv + 255) / 256, least);
-  if (s.vpt > 8 * least) s.vpt = 8 * least;
+  const bool wide = s.vec * es == 16;
+  s.vpt = wide ? 1 : 4;
+  while (s.vpt < (wide ? 8 : 32) && (nv + s.vpt - 1) / s.vpt > 256) s.vpt *= 2;
   s.warps = (nv + 32 * s.vpt - 1) / (32 * s.vpt);
   s.groups = s.warps >= 5 ? 1 : 8 / s.warps;
   return s;
 }
 
+// 16 columns a thread at most, so that their sums stay in registers.
 Shape backward_shape(int d, int es) {
   Shape s{};
-  s.vec = d * es % 16 == 0 ? 16 / es : 1;
+  s.vec = vector_of(d, es);
   const int nv = d / s.vec;
-  const int most = 16 / s.vec;  // at most 16 columns a thread: their sums stay in registers
-  s.vpt = s.vec == 1 ? 4 : 1;
-  while (s.vpt < most && (nv + s.vpt - 1) / s.vpt > 512) s.vpt *= 2;
+  s.vpt = s.vec * es == 16 ? 1 : 4;
+  while (s.vpt * s.vec < 16 && nv > 32 * s.vpt) s.vpt *= 2;
   s.warps = (nv + 32 * s.vpt - 1) / (32 * s.vpt);
-  s.groups = s.warps >= 9 ? 1 : s.warps == 1 ? 8 : 16 / s.warps > 8 ? 8 : 16 / s.warps;
+  s.groups = s.warps >= 5 ? 1 : 8 / s.warps;
   return s;
 }
 
-template <typename T, bool RMS, typename F>
+// f(elements an access, accesses a thread) as constants.
+template <typename T, typename F>
 cudaError_t by_shape(const Shape& s, const F& f) {
-  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int V = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
   using std::integral_constant;
-  if (s.vec == 1) {
+  if (s.vec == V) {
+    switch (s.vpt) {
+      case 1: return f(integral_constant<int, V>(), integral_constant<int, 1>());
+      case 2: return f(integral_constant<int, V>(), integral_constant<int, 2>());
+      case 4: return f(integral_constant<int, V>(), integral_constant<int, 4>());
+      case 8: return f(integral_constant<int, V>(), integral_constant<int, 8>());
+    }
+  } else if (s.vec == V4) {
+    switch (s.vpt) {
+      case 4: return f(integral_constant<int, V4>(), integral_constant<int, 4>());
+      case 8: return f(integral_constant<int, V4>(), integral_constant<int, 8>());
+      case 16: return f(integral_constant<int, V4>(), integral_constant<int, 16>());
+      case 32: return f(integral_constant<int, V4>(), integral_constant<int, 32>());
+    }
+  } else if constexpr (V4 > 1) {
     switch (s.vpt) {
       case 4: return f(integral_constant<int, 1>(), integral_constant<int, 4>());
       case 8: return f(integral_constant<int, 1>(), integral_constant<int, 8>());
       case 16: return f(integral_constant<int, 1>(), integral_constant<int, 16>());
       case 32: return f(integral_constant<int, 1>(), integral_constant<int, 32>());
     }
-    return cudaErrorInvalidValue;
-  }
-  switch (s.vpt) {
-    case 1: return f(integral_constant<int, V>(), integral_constant<int, 1>());
-    case 2: return f(integral_constant<int, V>(), integral_constant<int, 2>());
-    case 4: return f(integral_constant<int, V>(), integral_constant<int, 4>());
-    case 8: return f(integral_constant<int, V>(), integral_constant<int, 8>());
   }
   return cudaErrorInvalidValue;
 }
@@ -363,7 +607,7 @@ template <typename T, bool RMS>
 cudaError_t forward(const moe_norm_desc& D, const void* x, const void* gamma, const void* beta,
                     void* y, float* mean, float* rstd, cudaStream_t st) {
   const Shape s = forward_shape(D.d, (int)sizeof(T));
-  return by_shape<T, RMS>(s, [&](auto vec, auto vpt) {
+  return by_shape<T>(s, [&](auto vec, auto vpt) {
     (void)launch_kernel(norm_forward_kernel<T, decltype(vec)::value, decltype(vpt)::value, RMS>,
                         (D.T + s.groups - 1) / s.groups, s.groups * s.warps * 32, 0, st,
                         static_cast<const T*>(x), gamma, beta, D.wdtype == MOE_BF16, D.T, D.d,
@@ -372,22 +616,58 @@ cudaError_t forward(const moe_norm_desc& D, const void* x, const void* gamma, co
   });
 }
 
+template <typename T, int VEC, int VPT, bool RMS, int THREADS>
+cudaError_t launch_backward(const moe_norm_desc& D, const Shape& s, const void* dy, const void* x,
+                            const void* gamma, const float* mean, const float* rstd, void* dx,
+                            float* partial, int blocks, cudaStream_t st) {
+  constexpr bool RING = VEC * sizeof(T) == 16;
+  auto kern = norm_backward_kernel<T, VEC, VPT, RMS, RING, THREADS>;
+  const int threads = s.groups * s.warps * 32;
+  const size_t stage = 2 * (size_t)s.groups * D.d * sizeof(T);
+  int stages = 0;
+  if (RING) {  // a block's share of the shared memory of an SM, all of it for one of > 256 threads
+    stages = (int)((threads > 256 ? kBwdRingBytes * 2 : kBwdRingBytes) / stage);
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages < 1) stages = 1;
+  }
+  const size_t sums = s.groups > 1 ? (size_t)D.d * 4 : 0;
+  const size_t smem = stages * stage > sums ? stages * stage : sums;
+  if (smem > 32 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    static std::atomic<bool> configured[64] = {};
+    if (!configured[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(2 * kBwdRingBytes));
+      if (e != cudaSuccess) return e;
+      configured[dev] = true;
+    }
+  }
+  (void)launch_kernel(kern, blocks, threads, smem, st, static_cast<const T*>(dy),
+                      static_cast<const T*>(x), gamma, D.wdtype == MOE_BF16, mean, rstd, D.T,
+                      D.d, s.warps, stages, static_cast<T*>(dx), partial);
+  return cudaGetLastError();
+}
+
 template <typename T, bool RMS>
 cudaError_t backward(const moe_norm_desc& D, const void* dy, const void* x, const void* gamma,
                      const float* mean, const float* rstd, void* dx, float* partial, int blocks,
                      cudaStream_t st) {
   const Shape s = backward_shape(D.d, (int)sizeof(T));
-  return by_shape<T, RMS>(s, [&](auto vec, auto vpt) -> cudaError_t {
-    if constexpr (decltype(vec)::value * decltype(vpt)::value > 16) {
+  return by_shape<T>(s, [&](auto vec, auto vpt) -> cudaError_t {
+    constexpr int VEC = decltype(vec)::value, VPT = decltype(vpt)::value;
+    if constexpr (VEC * VPT > 16) {
       return cudaErrorInvalidValue;
     } else {
-      const size_t smem = partial && s.groups > 1 ? (size_t)D.d * 4 : 0;
-      (void)launch_kernel(
-          norm_backward_kernel<T, decltype(vec)::value, decltype(vpt)::value, RMS>, blocks,
-          s.groups * s.warps * 32, smem, st, static_cast<const T*>(dy), static_cast<const T*>(x),
-          gamma, D.wdtype == MOE_BF16, mean, rstd, D.T, D.d, s.warps, static_cast<T*>(dx),
-          partial);
-      return cudaGetLastError();
+      if constexpr (VEC * VPT == 16) {  // rows of more than 8192 columns: 1024 threads
+        if (s.warps > 16)
+          return launch_backward<T, VEC, VPT, RMS, 1024>(D, s, dy, x, gamma, mean, rstd, dx,
+                                                         partial, blocks, st);
+      }
+      return launch_backward<T, VEC, VPT, RMS, 512>(D, s, dy, x, gamma, mean, rstd, dx, partial,
+                                                    blocks, st);
     }
   });
 }
@@ -397,7 +677,8 @@ cudaError_t backward(const moe_norm_desc& D, const void* dy, const void* x, cons
 int norm_backward_blocks(const moe_norm_desc& D) {
   const Shape s = backward_shape(D.d, (int)dtype_size(D.dtype));
   const int need = (D.T + s.groups - 1) / s.groups;
-  return need < kBwdBlocks ? need : kBwdBlocks;
+  const int most = s.groups * s.warps > 8 ? kBwdBlocks / 2 : kBwdBlocks;
+  return need < most ? need : most;
 }
 
 cudaError_t launch_norm_forward(const moe_norm_desc& D, const void* x, const void* gamma,

@@ -193,21 +193,23 @@ def _p(t, dtype=None, what="tensor"):
     """Device pointer of a contiguous CUDA tensor (None -> NULL)."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (
+            dtype is None or t.dtype is dtype):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % what)
     if t.device.type != "cuda":
         raise ValueError("%s must be a CUDA tensor" % what)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    return t.data_ptr()
+    raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
 
 
 def _stream(stream):
+    """The stream's handle; without one, the current stream of the current device."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _act_dtype(desc):
@@ -220,7 +222,7 @@ def _check(status, what):
 
 
 def _need(t, shape, what):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
 
 
