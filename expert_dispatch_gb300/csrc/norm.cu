@@ -31,6 +31,8 @@ constexpr int kMaxStages = 8;
 constexpr int kBwdBlocks = 304;  // most blocks of the backward pass: two an SM, or one of
                                  // more than 256 threads
 constexpr size_t kBwdRingBytes = 104 * 1024;  // shared memory of the rings, two blocks an SM
+constexpr size_t kFwdRingBytes = 204 * 1024;  // forward: the rings of all blocks of an SM
+constexpr int kFwdRingRows = 608;             // forward: most blocks that take one row a group
 
 // VEC consecutive elements of a row as they lie in memory (2, 4 or 16 bytes).
 template <typename T, int VEC>
@@ -185,10 +187,10 @@ __device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
 }
 
 // Sums of N (1 or 2) values over a group of `warps` warps, the same in every
-// thread.  `buf` holds the warps' sums, [2][N][kMaxGroupWarps], zero where the
-// group has no warp; successive calls take its halves in turn, so one barrier a
-// call is enough.  A group of several warps meets at named barrier 1 + group (at
-// most 8 such groups).  Every warp adds the warps' sums in the same order.
+// thread.  `buf` holds the warps' sums, [2][N][kMaxGroupWarps]; successive calls
+// take its halves in turn, so one barrier a call is enough.  A group of several
+// warps meets at named barrier 1 + group (at most 8 such groups).  Every thread
+// adds the warps' sums in the same order.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], int warps, int warp_in_group, int group,
                                           float* buf, int& turn) {
@@ -199,128 +201,32 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int warps, int warp_in_
     turn ^= 1;
     if ((lane & (N == 2 ? 15 : 31)) == 0) b[(lane >> 4) * kMaxGroupWarps + warp_in_group] = mine;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
+    if (warps <= 8) {  // each thread adds them up: no chain of shuffles
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float4 p = *reinterpret_cast<const float4*>(b + i * kMaxGroupWarps);
+        const float4 q = *reinterpret_cast<const float4*>(b + i * kMaxGroupWarps + 4);
+        const float s01 = p.x + p.y, s23 = (warps > 2 ? p.z : 0.f) + (warps > 3 ? p.w : 0.f);
+        const float s45 = (warps > 4 ? q.x : 0.f) + (warps > 5 ? q.y : 0.f);
+        const float s67 = (warps > 6 ? q.z : 0.f) + (warps > 7 ? q.w : 0.f);
+        v[i] = (s01 + s23) + (s45 + s67);
+      }
+      return;
+    }
     if constexpr (N == 2) {  // the lower half's lanes add up one value, the upper's the other
-      const float* p = b + (lane >> 4) * kMaxGroupWarps + (lane & 15);
-      mine = p[0] + (warps > 16 ? p[16] : 0.f);
+      const float* p = b + (lane >> 4) * kMaxGroupWarps;
+      mine = ((lane & 15) < warps ? p[lane & 15] : 0.f) +
+             ((lane & 15) + 16 < warps ? p[(lane & 15) + 16] : 0.f);
 #pragma unroll
       for (int o = 8; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     } else {
-      mine = warp_sum(b[lane]);
+      mine = warp_sum(lane < warps ? b[lane] : 0.f);
     }
   }
   if constexpr (N == 2) v[1] = __shfl_sync(0xffffffffu, mine, 16);
   v[0] = N == 2 ? __shfl_sync(0xffffffffu, mine, 0) : mine;
 }
 
-// Zeroes the blocks' buffers for group_sum.
-template <int SIZE>
-__device__ __forceinline__ void clear_sums(float (&red)[8][SIZE]) {
-  for (int i = threadIdx.x; i < 8 * SIZE; i += blockDim.x) (&red[0][0])[i] = 0.f;
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------- forward
-// blockDim.x = groups * warps * 32; the groups of a block take successive rows.
-// The row stays packed as it was read, which leaves registers for enough
-// blocks an SM to keep HBM busy.
-template <typename T, int VEC, int VPT, bool RMS>
-__global__ void __launch_bounds__(512)
-    norm_forward_kernel(const T* x, const void* gamma, const void* beta, bool w_bf16, int rows,
-                        int d, int warps, float eps, T* y, float* mean, float* rstd) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ float red[8][2 * kMaxGroupWarps];
-  if (warps > 1) clear_sums(red);
-  const int gt = warps * 32;
-  const int group = threadIdx.x / gt, tid = threadIdx.x - group * gt;
-  const int row = blockIdx.x * (blockDim.x / gt) + group;
-  if (row >= rows) return;  // a whole group
-  const int nv = d / VEC;
-  const T* xr = x + (size_t)row * d;
-  Raw<T, VEC> raw[VPT];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    raw[i] = Raw<T, VEC>{};
-    if (tid + i * gt < nv) raw[i] = load_raw<T, VEC>(xr + (size_t)(tid + i * gt) * VEC);
-  }
-  constexpr int N = VPT * VEC;
-  const float inv_d = 1.f / (float)d;
-  // the row's values, zero beyond its end
-  auto values = [&](float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) unpack<T, VEC>(raw[i], v + i * VEC);
-  };
-  float s[1];
-  {
-    float v[N];
-    values(v);
-    F2 acc = f2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-      const F2 p = f2(v[2 * k], v[2 * k + 1]);
-      acc = RMS ? fma2(p, p, acc) : add2(p, acc);
-    }
-    s[0] = both(acc);
-  }
-  int turn = 0;
-  float* buf = red[warps == 1 ? 0 : group];
-  group_sum<1>(s, warps, tid >> 5, group, buf, turn);
-  float mu = 0.f;
-  if (!RMS) {
-    mu = s[0] * inv_d;
-    float v[N];
-    values(v);
-    const F2 m = f2(-mu, -mu);
-    F2 acc = f2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (tid + i * gt < nv) {  // what lies beyond the row is not mu
-        if constexpr (VEC > 1) {
-#pragma unroll
-          for (int j = 0; j < VEC; j += 2) {
-            const F2 c = add2(f2(v[i * VEC + j], v[i * VEC + j + 1]), m);
-            acc = fma2(c, c, acc);
-          }
-        } else {
-          const F2 c = f2(v[i] - mu, 0.f);
-          acc = fma2(c, c, acc);
-        }
-      }
-    }
-    s[0] = both(acc);
-    group_sum<1>(s, warps, tid >> 5, group, buf, turn);
-  }
-  const float r = 1.f / sqrtf(s[0] * inv_d + eps);
-  if (tid == 0) {
-    if (mean) mean[row] = mu;
-    if (rstd) rstd[row] = r;
-  }
-  T* yr = y + (size_t)row * d;
-  const F2 m = f2(-mu, -mu), rr = f2(r, r);
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = tid + i * gt;
-    if (c >= nv) break;
-    float v[VEC], g[VEC], b[VEC];
-    unpack<T, VEC>(raw[i], v);
-    load_param<VEC>(gamma, w_bf16, c * VEC, 1.f, g);
-    load_param<VEC>(RMS ? nullptr : beta, w_bf16, c * VEC, 0.f, b);
-    if constexpr (VEC > 1) {
-#pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        const F2 x2 = f2(v[j], v[j + 1]);
-        const F2 h = mul2(RMS ? x2 : add2(x2, m), rr);
-        const F2 g2 = f2(g[j], g[j + 1]);
-        split(RMS ? mul2(h, g2) : fma2(h, g2, f2(b[j], b[j + 1])), v[j], v[j + 1]);
-      }
-    } else {
-      v[0] = fmaf((v[0] - mu) * r, g[0], b[0]);
-    }
-    store_raw<T, VEC>(yr + (size_t)c * VEC, pack<T, VEC>(v));
-  }
-}
-
-// ---------------------------------------------------------------- backward
 // `bytes` (a multiple of 16) from global into shared memory, asynchronously;
 // completion is signalled on `bar` as transaction bytes.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -332,19 +238,206 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// A group's ring of rows in shared memory, `streams` rows a stage, filled by
+// bulk copies that one thread of the group requests `stages` rows ahead: HBM
+// latency is hidden without registers, and a row's loads cost no instructions
+// but its reads of shared memory.  Every wait for a copy is bounded; should one
+// expire, the caller makes the row's results NaN and no more copies are
+// requested.
+struct Ring {
+  uint8_t* base;
+  uint32_t bar0, row_bytes;
+  int streams, stages;
+  int stage = 0;
+  uint32_t parity = 0;
+  int* gave_up;
+
+  __device__ __forceinline__ Ring(uint8_t* dyn, uint64_t* bars, int* gave_up_, int group,
+                                  int streams_, int stages_, uint32_t row_bytes_)
+      : base(dyn + (size_t)group * stages_ * streams_ * row_bytes_),
+        bar0(smem_u32(bars)),
+        row_bytes(row_bytes_),
+        streams(streams_),
+        stages(stages_),
+        gave_up(gave_up_) {}
+  // by one thread of the group; a block barrier follows before any use
+  __device__ __forceinline__ void init() const {
+    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8u * s, 1);
+    fence_barrier_init();
+  }
+  // by one thread of the group: the row at a (and at b) into stage s
+  __device__ __forceinline__ void request(int s, const void* a, const void* b) const {
+    const uint32_t dst = smem_u32(base) + (uint32_t)(s * streams) * row_bytes;
+    mbar_arrive_expect_tx(bar0 + 8u * s, (uint32_t)streams * row_bytes);
+    bulk_load(dst, a, row_bytes, bar0 + 8u * s);
+    if (b) bulk_load(dst + row_bytes, b, row_bytes, bar0 + 8u * s);
+  }
+  __device__ __forceinline__ bool wait() const {
+    return mbar_wait(bar0 + 8u * stage, parity, gave_up, nullptr);
+  }
+  __device__ __forceinline__ bool open() const {
+    return !*static_cast<volatile int*>(gave_up);
+  }
+  __device__ __forceinline__ const uint8_t* rows() const {
+    return base + (size_t)stage * streams * row_bytes;
+  }
+  __device__ __forceinline__ void next() {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+  // leaves copies that are still on their way after giving up a bounded time to land
+  __device__ __forceinline__ void close() const {
+    if (open()) return;
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000ull) {
+    }
+  }
+};
+
+// ---------------------------------------------------------------- forward
+// blockDim.x = groups * warps * 32; group g of block b takes the rows
+// b * groups + g, + gridDim.x * groups, ...  With RING they come through a ring
+// and the grid is what fits on the GPU at once; without, each group has one row
+// (of odd length, or one of few: a ring has nothing to run ahead of).  A thread
+// owns the same columns of every row and keeps their gamma and beta.
+template <typename T, int VEC, int VPT, bool RMS, bool RING, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1)
+    norm_forward_kernel(const T* x, const void* gamma, const void* beta, bool w_bf16, int rows,
+                        int d, int warps, int stages, float eps, T* y, float* mean,
+                        float* rstd) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ alignas(16) float red[8][2 * kMaxGroupWarps];
+  __shared__ __align__(8) uint64_t bars[8][kMaxStages];
+  __shared__ int gave_up;
+  constexpr int N = VPT * VEC;
+  const int gt = warps * 32, groups = blockDim.x / gt;
+  const int group = threadIdx.x / gt, tid = threadIdx.x - group * gt;
+  const int step = gridDim.x * groups;
+  const int nv = d / VEC;
+  int row = blockIdx.x * groups + group;
+  Ring ring(dyn, bars[group], &gave_up, group, 1, stages, (uint32_t)d * sizeof(T));
+  if constexpr (RING) {
+    if (threadIdx.x == 0) gave_up = 0;
+    if (tid == 0) ring.init();
+    __syncthreads();
+    if (tid == 0)
+      for (int s = 0; s < stages && row + s * step < rows; ++s)
+        ring.request(s, x + (size_t)(row + s * step) * d, nullptr);
+  }
+  F2 g[N / 2], b[RMS ? 1 : N / 2];
+  auto params = [&](const void* p, float otherwise, F2* out) {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i * VEC + j] = 0.f;
+      if (tid + i * gt < nv)
+        load_param<VEC>(p, w_bf16, (tid + i * gt) * VEC, otherwise, v + i * VEC);
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) out[k] = f2(v[2 * k], v[2 * k + 1]);
+  };
+  params(gamma, 1.f, g);
+  if constexpr (!RMS) params(beta, 0.f, b);
+  const float inv_d = 1.f / (float)d;
+  int turn = 0;
+  float* buf = red[warps == 1 ? 0 : group];
+  for (; row < rows; row += step) {  // the same rows for a whole group
+    bool ok = true;
+    Raw<T, VEC> raw[VPT];  // the row as it was read, zero beyond its end
+    const T* xr = x + (size_t)row * d;
+    if constexpr (RING) {
+      ok = ring.wait();
+      xr = reinterpret_cast<const T*>(ring.rows());
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      raw[i] = Raw<T, VEC>{};
+      if (tid + i * gt < nv) raw[i] = load_raw<T, VEC>(xr + (size_t)(tid + i * gt) * VEC);
+    }
+    if constexpr (RING) {
+      fence_proxy_async_shared();  // before the barrier that hands the stage back
+      if (warps == 1) __syncwarp();
+    }
+    F2 v[N / 2];
+    {
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) unpack<T, VEC>(raw[i], f + i * VEC);
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) v[k] = f2(f[2 * k], f[2 * k + 1]);
+    }
+    F2 acc = f2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) acc = RMS ? fma2(v[k], v[k], acc) : add2(v[k], acc);
+    float s[1] = {both(acc)};
+    group_sum<1>(s, warps, tid >> 5, group, buf, turn);
+    if constexpr (RING) {
+      if (tid == 0 && row + (long long)stages * step < rows && ring.open())
+        ring.request(ring.stage, x + (size_t)(row + stages * step) * d, nullptr);
+      ring.next();
+    }
+    float mu = 0.f;
+    if constexpr (!RMS) {
+      mu = s[0] * inv_d;
+      const F2 m = f2(-mu, -mu);
+      acc = f2(0.f, 0.f);
+      // the columns beyond the row's end would add mu^2 each
+      if (nv == gt * VPT) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+          v[k] = add2(v[k], m);
+          acc = fma2(v[k], v[k], acc);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+          float p, q;
+          split(add2(v[k], m), p, q);
+          v[k] = f2(tid + (2 * k / VEC) * gt < nv ? p : 0.f,
+                    tid + ((2 * k + 1) / VEC) * gt < nv ? q : 0.f);
+          acc = fma2(v[k], v[k], acc);
+        }
+      }
+      s[0] = both(acc);
+      group_sum<1>(s, warps, tid >> 5, group, buf, turn);
+    }
+    const float r = ok ? 1.f / sqrtf(s[0] * inv_d + eps) : __int_as_float(0x7fffffff);
+    if (tid == 0) {
+      if (mean) mean[row] = mu;
+      if (rstd) rstd[row] = r;
+    }
+    const F2 rr = f2(r, r);
+    float o[N];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      const F2 h = mul2(v[k], rr);
+      if constexpr (RMS)
+        split(mul2(h, g[k]), o[2 * k], o[2 * k + 1]);
+      else
+        split(fma2(h, g[k], b[k]), o[2 * k], o[2 * k + 1]);
+    }
+    T* yr = y + (size_t)row * d;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (tid + i * gt < nv)
+        store_raw<T, VEC>(yr + (size_t)(tid + i * gt) * VEC, pack<T, VEC>(o + i * VEC));
+  }
+  if constexpr (RING) ring.close();
+}
+
+// ---------------------------------------------------------------- backward
 // Block b takes rows b * groups + group, + gridDim.x * groups, ...; a thread
 // owns the same columns of every row and keeps their sums of dy h and dy in
-// registers.  With RING (rows of 16-byte vectors) each group has a ring of
-// `stages` rows of x and dy in shared memory, filled by bulk copies that one
-// thread requests `stages` rows ahead: HBM latency is hidden without registers
-// and a row's loads cost no instructions but its reads of shared memory.  The
-// barrier of the row's sums also says that every thread has read the stage.
-// Other rows are loaded where they are used.  At the end the groups' sums are
-// added in group order through shared memory and written to
+// registers.  With RING (rows of 16-byte vectors) x and dy come through a ring;
+// the barrier of the row's sums also says that every thread has read the
+// stage.  Other rows are loaded where they are used.  At the end the groups'
+// sums are added in group order through shared memory and written to
 // partial [2][gridDim.x][d].
-//
-// A wait for a copy is bounded; should one expire, the row's results are NaN
-// and the group requests no more copies.
 template <typename T, int VEC, int VPT, bool RMS, bool RING, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_backward_kernel(const T* dy, const T* x, const void* gamma, bool w_bf16,
@@ -353,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(128) uint8_t dyn[];  // the rings, then the groups' sums [d]
-  __shared__ float red[8][4 * kMaxGroupWarps];
+  __shared__ alignas(16) float red[8][4 * kMaxGroupWarps];
   __shared__ __align__(8) uint64_t bars[8][kMaxStages];
   __shared__ int gave_up;
   constexpr int N = VPT * VEC;
@@ -361,23 +454,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int group = threadIdx.x / gt, tid = threadIdx.x - group * gt;
   const int nv = d / VEC;
   const int step = gridDim.x * groups;
-  const uint32_t row_bytes = (uint32_t)d * (uint32_t)sizeof(T);
-  const uint32_t bar0 = smem_u32(&bars[group][0]);
-  uint8_t* ring = dyn + (size_t)group * stages * 2 * row_bytes;
-  if (RING && tid == 0)
-    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8u * s, 1);
-  if (threadIdx.x == 0) gave_up = 0;
-  if (RING) fence_barrier_init();
-  clear_sums(red);
-  auto request = [&](int row, int s) {  // one thread of the group
-    const uint32_t dst = smem_u32(ring) + (uint32_t)s * 2u * row_bytes;
-    mbar_arrive_expect_tx(bar0 + 8u * s, 2u * row_bytes);
-    bulk_load(dst, x + (size_t)row * d, row_bytes, bar0 + 8u * s);
-    bulk_load(dst + row_bytes, dy + (size_t)row * d, row_bytes, bar0 + 8u * s);
-  };
   int row = blockIdx.x * groups + group;
-  if (RING && tid == 0)
-    for (int s = 0; s < stages && row + s * step < rows; ++s) request(row + s * step, s);
+  Ring ring(dyn, bars[group], &gave_up, group, 2, stages, (uint32_t)d * sizeof(T));
+  if constexpr (RING) {
+    if (threadIdx.x == 0) gave_up = 0;
+    if (tid == 0) ring.init();
+    __syncthreads();
+    if (tid == 0)
+      for (int s = 0; s < stages && row + s * step < rows; ++s)
+        ring.request(s, x + (size_t)(row + s * step) * d, dy + (size_t)(row + s * step) * d);
+  }
 
   // pairs of this thread's columns; columns beyond the row's end hold zeros in
   // dy, so they add nothing to the row's sums, and are never stored
@@ -401,8 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const T* dp = dy + (size_t)row * d + (size_t)tid * VEC;
   T* op = dx + (size_t)row * d + (size_t)tid * VEC;
   const size_t jump = (size_t)step * d;
-  int turn = 0, stage = 0;
-  uint32_t parity = 0;
+  int turn = 0;
   float* buf = red[warps == 1 ? 0 : group];
   float mu = 0.f, r = 0.f;
   if (row < rows) mu = RMS ? 0.f : mean[row], r = rstd[row];
@@ -411,8 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (row + step < rows) mu2 = RMS ? 0.f : mean[row + step], r2 = rstd[row + step];
     Raw<T, VEC> xr[VPT], dr[VPT];
     if constexpr (RING) {
-      if (!mbar_wait(bar0 + 8u * stage, parity, &gave_up, nullptr)) r = __int_as_float(0x7fffffff);
-      const uint8_t* src = ring + (size_t)stage * 2 * row_bytes + (size_t)tid * sizeof(Raw<T, VEC>);
+      if (!ring.wait()) r = __int_as_float(0x7fffffff);
+      const uint8_t* src = ring.rows() + (size_t)tid * sizeof(Raw<T, VEC>);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         xr[i] = dr[i] = Raw<T, VEC>{};
@@ -459,9 +544,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     if constexpr (!RMS) s[1] = both(ws);
     if (RING && warps == 1) __syncwarp();
     group_sum<RMS ? 1 : 2>(s, warps, tid >> 5, group, buf, turn);
-    if (RING && tid == 0 && row + (long long)stages * step < rows &&
-        !*static_cast<volatile int*>(&gave_up))
-      request(row + stages * step, stage);
+    if constexpr (RING) {
+      if (tid == 0 && row + (long long)stages * step < rows && ring.open()) {
+        const size_t at = (size_t)(row + stages * step) * d;
+        ring.request(ring.stage, x + at, dy + at);
+      }
+      ring.next();
+    }
     const float c1 = s[0] * inv_d;
     const F2 n1 = f2(c1, c1);
 #pragma unroll
@@ -475,17 +564,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (tid + i * gt < nv)
         store_raw<T, VEC>(op + (size_t)i * gt * VEC, pack<T, VEC>(dv + i * VEC));
     mu = mu2, r = r2;
-    if (++stage == stages) {
-      stage = 0;
-      parity ^= 1u;
-    }
   }
-  if (RING && *static_cast<volatile int*>(&gave_up)) {
-    // leave copies that are still on their way a bounded time to land
-    const unsigned long long t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 100000ull) {
-    }
-  }
+  if constexpr (RING) ring.close();
   if (!partial) return;
   float* sums = reinterpret_cast<float*>(dyn);  // every copy has landed and been read
   auto flush = [&](const F2 (&acc2)[N / 2], float* out) {
@@ -547,22 +627,9 @@ int vector_of(int d, int es) {
   return bytes % 16 == 0 ? 16 / es : bytes % 4 == 0 ? 4 / es : 1;
 }
 
-// Up to 4 vectors or 8 (16 of odd bf16 rows) short accesses a thread while
-// that takes no more than 256 threads, then more.
-Shape forward_shape(int d, int es) {
-  Shape s{};
-  s.vec = vector_of(d, es);
-  const int nv = d / s.vec;
-  const bool wide = s.vec * es == 16;
-  s.vpt = wide ? 1 : 4;
-  while (s.vpt < (wide ? 8 : 32) && (nv + s.vpt - 1) / s.vpt > 256) s.vpt *= 2;
-  s.warps = (nv + 32 * s.vpt - 1) / (32 * s.vpt);
-  s.groups = s.warps >= 5 ? 1 : 8 / s.warps;
-  return s;
-}
-
-// 16 columns a thread at most, so that their sums stay in registers.
-Shape backward_shape(int d, int es) {
+// 16 columns a thread at most, so that what it keeps of them (parameters, sums)
+// stays in registers.
+Shape row_shape(int d, int es) {
   Shape s{};
   s.vec = vector_of(d, es);
   const int nv = d / s.vec;
@@ -579,40 +646,89 @@ cudaError_t by_shape(const Shape& s, const F& f) {
   constexpr int V = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
   using std::integral_constant;
   if (s.vec == V) {
-    switch (s.vpt) {
-      case 1: return f(integral_constant<int, V>(), integral_constant<int, 1>());
-      case 2: return f(integral_constant<int, V>(), integral_constant<int, 2>());
-      case 4: return f(integral_constant<int, V>(), integral_constant<int, 4>());
-      case 8: return f(integral_constant<int, V>(), integral_constant<int, 8>());
-    }
+    if (s.vpt == 1) return f(integral_constant<int, V>(), integral_constant<int, 1>());
+    if (s.vpt == 2) return f(integral_constant<int, V>(), integral_constant<int, 2>());
+    if constexpr (V == 4)
+      if (s.vpt == 4) return f(integral_constant<int, V>(), integral_constant<int, 4>());
   } else if (s.vec == V4) {
-    switch (s.vpt) {
-      case 4: return f(integral_constant<int, V4>(), integral_constant<int, 4>());
-      case 8: return f(integral_constant<int, V4>(), integral_constant<int, 8>());
-      case 16: return f(integral_constant<int, V4>(), integral_constant<int, 16>());
-      case 32: return f(integral_constant<int, V4>(), integral_constant<int, 32>());
-    }
+    if (s.vpt == 4) return f(integral_constant<int, V4>(), integral_constant<int, 4>());
+    if (s.vpt == 8) return f(integral_constant<int, V4>(), integral_constant<int, 8>());
+    if constexpr (V4 == 1)
+      if (s.vpt == 16) return f(integral_constant<int, V4>(), integral_constant<int, 16>());
   } else if constexpr (V4 > 1) {
-    switch (s.vpt) {
-      case 4: return f(integral_constant<int, 1>(), integral_constant<int, 4>());
-      case 8: return f(integral_constant<int, 1>(), integral_constant<int, 8>());
-      case 16: return f(integral_constant<int, 1>(), integral_constant<int, 16>());
-      case 32: return f(integral_constant<int, 1>(), integral_constant<int, 32>());
-    }
+    if (s.vpt == 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>());
+    if (s.vpt == 8) return f(integral_constant<int, 1>(), integral_constant<int, 8>());
+    if (s.vpt == 16) return f(integral_constant<int, 1>(), integral_constant<int, 16>());
   }
   return cudaErrorInvalidValue;
+}
+
+// Stages of a ring in `room` bytes, at most kMaxStages.
+int ring_stages(size_t room, size_t stage) {
+  const size_t n = room / stage;
+  return n < 1 ? 1 : n > kMaxStages ? kMaxStages : (int)n;
+}
+
+// Dynamic shared memory beyond the default limit, asked for once a device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t most, std::atomic<bool> (&configured)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (configured[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) configured[dev] = true;
+  return e;
+}
+
+template <typename T, int VEC, int VPT, bool RMS, bool RING, int THREADS>
+cudaError_t launch_forward(const moe_norm_desc& D, const Shape& s, const void* x,
+                           const void* gamma, const void* beta, void* y, float* mean, float* rstd,
+                           cudaStream_t st) {
+  auto kern = norm_forward_kernel<T, VEC, VPT, RMS, RING, THREADS>;
+  const int threads = s.groups * s.warps * 32;
+  const size_t stage = (size_t)s.groups * D.d * sizeof(T);
+  int blocks = (D.T + s.groups - 1) / s.groups, stages = 0;
+  if (RING) {
+    static std::atomic<bool> configured[64] = {};
+    const cudaError_t e = allow_smem(kern, kFwdRingBytes, configured);
+    if (e != cudaSuccess) return e;
+    const int per_sm = threads <= 256 ? 4 : threads <= 512 ? 2 : 1;
+    stages = ring_stages(kFwdRingBytes / per_sm, stage);
+    if (blocks > per_sm * num_sms()) blocks = per_sm * num_sms();
+  }
+  (void)launch_kernel(kern, blocks, threads, stages * stage, st, static_cast<const T*>(x), gamma,
+                      beta, D.wdtype == MOE_BF16, D.T, D.d, s.warps, stages, D.eps,
+                      static_cast<T*>(y), mean, rstd);
+  return cudaGetLastError();
+}
+
+// f(elements an access, accesses a thread, the block's largest size): more
+// than 8192 columns take 1024 threads.
+template <typename T, typename F>
+cudaError_t by_threads(const Shape& s, const F& f) {
+  return by_shape<T>(s, [&](auto vec, auto vpt) -> cudaError_t {
+    if constexpr (decltype(vec)::value * decltype(vpt)::value == 16)
+      if (s.warps > 16) return f(vec, vpt, std::integral_constant<int, 1024>());
+    return f(vec, vpt, std::integral_constant<int, 512>());
+  });
 }
 
 template <typename T, bool RMS>
 cudaError_t forward(const moe_norm_desc& D, const void* x, const void* gamma, const void* beta,
                     void* y, float* mean, float* rstd, cudaStream_t st) {
-  const Shape s = forward_shape(D.d, (int)sizeof(T));
-  return by_shape<T>(s, [&](auto vec, auto vpt) {
-    (void)launch_kernel(norm_forward_kernel<T, decltype(vec)::value, decltype(vpt)::value, RMS>,
-                        (D.T + s.groups - 1) / s.groups, s.groups * s.warps * 32, 0, st,
-                        static_cast<const T*>(x), gamma, beta, D.wdtype == MOE_BF16, D.T, D.d,
-                        s.warps, D.eps, static_cast<T*>(y), mean, rstd);
-    return cudaGetLastError();
+  const Shape s = row_shape(D.d, (int)sizeof(T));
+  return by_threads<T>(s, [&](auto vec, auto vpt, auto threads) -> cudaError_t {
+    constexpr int VEC = decltype(vec)::value, VPT = decltype(vpt)::value;
+    constexpr int THREADS = decltype(threads)::value;
+    if constexpr (VEC * sizeof(T) == 16) {
+      if (D.T > kFwdRingRows * s.groups)
+        return launch_forward<T, VEC, VPT, RMS, true, THREADS>(D, s, x, gamma, beta, y, mean,
+                                                               rstd, st);
+    }
+    return launch_forward<T, VEC, VPT, RMS, false, THREADS>(D, s, x, gamma, beta, y, mean, rstd,
+                                                            st);
   });
 }
 
@@ -625,25 +741,14 @@ cudaError_t launch_backward(const moe_norm_desc& D, const Shape& s, const void* 
   const int threads = s.groups * s.warps * 32;
   const size_t stage = 2 * (size_t)s.groups * D.d * sizeof(T);
   int stages = 0;
-  if (RING) {  // a block's share of the shared memory of an SM, all of it for one of > 256 threads
-    stages = (int)((threads > 256 ? kBwdRingBytes * 2 : kBwdRingBytes) / stage);
-    if (stages > kMaxStages) stages = kMaxStages;
-    if (stages < 1) stages = 1;
-  }
+  if (RING)  // a block's share of an SM's shared memory; all of it for one of > 256 threads
+    stages = ring_stages(threads > 256 ? 2 * kBwdRingBytes : kBwdRingBytes, stage);
   const size_t sums = s.groups > 1 ? (size_t)D.d * 4 : 0;
   const size_t smem = stages * stage > sums ? stages * stage : sums;
-  if (smem > 32 * 1024) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64) return cudaErrorInvalidDevice;
+  if (RING) {
     static std::atomic<bool> configured[64] = {};
-    if (!configured[dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(2 * kBwdRingBytes));
-      if (e != cudaSuccess) return e;
-      configured[dev] = true;
-    }
+    const cudaError_t e = allow_smem(kern, 2 * kBwdRingBytes, configured);
+    if (e != cudaSuccess) return e;
   }
   (void)launch_kernel(kern, blocks, threads, smem, st, static_cast<const T*>(dy),
                       static_cast<const T*>(x), gamma, D.wdtype == MOE_BF16, mean, rstd, D.T,
@@ -655,27 +760,18 @@ template <typename T, bool RMS>
 cudaError_t backward(const moe_norm_desc& D, const void* dy, const void* x, const void* gamma,
                      const float* mean, const float* rstd, void* dx, float* partial, int blocks,
                      cudaStream_t st) {
-  const Shape s = backward_shape(D.d, (int)sizeof(T));
-  return by_shape<T>(s, [&](auto vec, auto vpt) -> cudaError_t {
-    constexpr int VEC = decltype(vec)::value, VPT = decltype(vpt)::value;
-    if constexpr (VEC * VPT > 16) {
-      return cudaErrorInvalidValue;
-    } else {
-      if constexpr (VEC * VPT == 16) {  // rows of more than 8192 columns: 1024 threads
-        if (s.warps > 16)
-          return launch_backward<T, VEC, VPT, RMS, 1024>(D, s, dy, x, gamma, mean, rstd, dx,
-                                                         partial, blocks, st);
-      }
-      return launch_backward<T, VEC, VPT, RMS, 512>(D, s, dy, x, gamma, mean, rstd, dx, partial,
-                                                    blocks, st);
-    }
+  const Shape s = row_shape(D.d, (int)sizeof(T));
+  return by_threads<T>(s, [&](auto vec, auto vpt, auto threads) {
+    return launch_backward<T, decltype(vec)::value, decltype(vpt)::value, RMS,
+                           decltype(threads)::value>(D, s, dy, x, gamma, mean, rstd, dx, partial,
+                                                     blocks, st);
   });
 }
 
 }  // namespace
 
 int norm_backward_blocks(const moe_norm_desc& D) {
-  const Shape s = backward_shape(D.d, (int)dtype_size(D.dtype));
+  const Shape s = row_shape(D.d, (int)dtype_size(D.dtype));
   const int need = (D.T + s.groups - 1) / s.groups;
   const int most = s.groups * s.warps > 8 ? kBwdBlocks / 2 : kBwdBlocks;
   return need < most ? need : most;
