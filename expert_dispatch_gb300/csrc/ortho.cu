@@ -397,12 +397,24 @@ __device__ __forceinline__ float product_scale(const Product& p, int mat) {
                         : rho / (kScaleB * kScaleX);
 }
 
+// kPoly: W columns (8 or 16) of A, to be loaded ahead of their use; other kinds
+// have none.
+template <int OP, int W>
+__device__ __forceinline__ void load_gram(const Product& p, int mat, int row, int c0,
+                                          uint4 (&g)[W / 8]) {
+  if (OP != kPoly || row >= p.rowsP) return;
+  const uint4* src =
+      reinterpret_cast<const uint4*>(p.gram + ((size_t)mat * p.rowsP + row) * p.rowsQ + c0);
+#pragma unroll
+  for (int i = 0; i < W / 8; ++i) g[i] = src[i];
+}
+
 // Accumulators of W columns (8 or 16) of row `row` from column c0 on, already
 // scaled, to the product's outputs: along the row in one 16- or 32-byte store,
 // and column by column (64 bytes a warp) for the mirrored copy.
 template <int OP, int W>
 __device__ __forceinline__ void store_product(const Product& p, int mat, int row, int c0,
-                                              bool mirror, float (&v)[W]) {
+                                              bool mirror, const uint4* gram, float (&v)[W]) {
   if (OP == kLast) {
     if (row < p.m) store_result<W>(p, mat, row, c0, v);
     return;
@@ -410,11 +422,9 @@ __device__ __forceinline__ void store_product(const Product& p, int mat, int row
   if (row >= p.rowsP) return;
   const size_t at = ((size_t)mat * p.rowsP + row) * p.rowsQ + c0;
   if (OP == kPoly) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.gram + at);
 #pragma unroll
     for (int i = 0; i < W / 8; ++i) {
-      const uint4 g = src[i];
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+      const uint32_t gw[4] = {gram[i].x, gram[i].y, gram[i].z, gram[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&gw[j]));
@@ -629,13 +639,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int cc = half * (width / 2); cc < (half + 1) * (width / 2); cc += 16) {
         const int c0 = col + cc;
         if (c0 >= p.rowsQ) break;  // warp-uniform
+        uint4 gram[2];
+        load_gram<OP, 16>(p, mat, row, c0, gram);
         uint32_t a[16];
         tmem_ld16(tb + cc, a);
         tmem_ld_wait();
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
-        store_product<OP, 16>(p, mat, row, c0, mirror, v);
+        store_product<OP, 16>(p, mat, row, c0, mirror, gram, v);
         __syncwarp();  // the next tcgen05.ld is the whole warp's
       }
       tc_fence_before();
@@ -660,6 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // barrier each adds up its share of the columns over the cluster in rank order.
 constexpr int kSmallN = 64, kSmallStages = 4, kSmallWarps = 6;  // producer, MMA, 4 epilogue
 constexpr int kSmallThreads = 32 * kSmallWarps;
+constexpr int kMaxSplit = 8;
 
 struct SmallCfg {
   static constexpr int A_BYTES = 128 * 128;
@@ -673,7 +686,7 @@ struct SmallCfg {
 
 __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
 
@@ -778,15 +791,24 @@ __global__ void __launch_bounds__(kSmallThreads)
       umma_commit(drain_bar);  // every MMA has completed before the TMEM is freed
       tc::mbar_wait_drain(drain_bar, 0, p.err);
     }
-  } else if (tc::mbar_wait_warp(accf, 0, abort_flag, p.err)) {
+  } else {
+    // the row's part of A while the products run
+    uint4 gram[kSmallN / 8];
+    if (OP == kPoly && split == 1) {
+#pragma unroll
+      for (int i = 0; i < kSmallN / 16; ++i)
+        load_gram<OP, 16>(p, mat, row, tj * kSmallN + 16 * i,
+                          *reinterpret_cast<uint4(*)[2]>(&gram[2 * i]));
+    }
+    const bool ready = tc::mbar_wait_warp(accf, 0, abort_flag, p.err);
     tc_fence_after();
     const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
     const float alpha = product_scale<OP>(p, mat);
     float* part = reinterpret_cast<float*>(smem);  // [kSmallN][128]
-#pragma unroll 1
-    for (int cc = 0; cc < kSmallN; cc += 16) {
+#pragma unroll
+    for (int cc = 0; cc < kSmallN; cc += 16) {  // rowsQ is a multiple of the tile's width
+      if (!ready) break;
       const int c0 = tj * kSmallN + cc;
-      if (c0 >= p.rowsQ) break;  // warp-uniform
       uint32_t a[16];
       tmem_ld16(tb + cc, a);
       tmem_ld_wait();
@@ -794,7 +816,7 @@ __global__ void __launch_bounds__(kSmallThreads)
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
       if (split == 1) {
-        store_product<OP, 16>(p, mat, row, c0, mirror, v);
+        store_product<OP, 16>(p, mat, row, c0, mirror, &gram[cc / 8], v);
       } else {
         // the stages' last reader was the MMA that this warp waited for
 #pragma unroll
@@ -815,14 +837,27 @@ __global__ void __launch_bounds__(kSmallThreads)
     const int cols = kSmallN / split;
     for (int cc = rank * cols; cc < (rank + 1) * cols; cc += 8) {
       const int c0 = tj * kSmallN + cc;
-      if (c0 >= p.rowsQ) break;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int r = 0; r < split; ++r) {
-        const uint32_t peer = mapa_shared(sbase + (uint32_t)(cc * 128 + q * 32 + lane) * 4u, r);
+      uint4 gram[1];
+      load_gram<OP, 8>(p, mat, row, c0, gram);
+      const uint32_t mine = sbase + (uint32_t)(cc * 128 + q * 32 + lane) * 4u;
+      float part[kMaxSplit][8];  // all loads in flight before the first sum
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += ld_shared_cluster(peer + (uint32_t)j * 512u);
+      for (int r = 0; r < kMaxSplit; ++r) {
+        if (r < split) {
+          const uint32_t peer = mapa_shared(mine, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) part[r][j] = ld_shared_cluster(peer + (uint32_t)j * 512u);
+        }
       }
-      store_product<OP, 8>(p, mat, row, c0, mirror, v);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = part[0][j];
+#pragma unroll
+        for (int r = 1; r < kMaxSplit; ++r)
+          if (r < split) v[j] += part[r][j];
+      }
+      store_product<OP, 8>(p, mat, row, c0, mirror, gram, v);
     }
   }
   cluster_sync();  // a CTA's shared memory stays until its peers have read it
@@ -902,7 +937,7 @@ cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Produ
   // the reduction is shared while that leaves at most two CTAs an SM and each
   // at least four of its blocks
   int split = 1;
-  while (split < 8 && units * split <= num_sms() && p.K / 64 / (2 * split) >= 4) split *= 2;
+  while (split < kMaxSplit && units * split <= num_sms() && p.K / 64 / (2 * split) >= 4) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * split));
   cfg.blockDim = dim3(kSmallThreads);

@@ -550,15 +550,19 @@ def _norm_stat(desc, t, what):
     return _p(t, torch.float32, what)
 
 
+def _norm_forward(desc, x, gamma, beta, y, mean, rstd, stream):
+    """moe_norm_forward with y, mean and rstd as pointers."""
+    st = lib().moe_norm_forward(
+        ctypes.byref(desc), _p(x, _act_dtype(desc), "x"), _norm_param(desc, gamma, "gamma"),
+        _norm_param(desc, beta, "beta"), y, mean, rstd, _stream(stream))
+    _check(st, "moe_norm_forward")
+
+
 def moe_norm_forward(desc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
-    dt = _act_dtype(desc)
     _need(x, (desc.T, desc.d), "x")
     _need(y, (desc.T, desc.d), "y")
-    st = lib().moe_norm_forward(
-        ctypes.byref(desc), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
-        _norm_param(desc, beta, "beta"), _p(y, dt, "y"), _norm_stat(desc, mean, "mean"),
-        _norm_stat(desc, rstd, "rstd"), _stream(stream))
-    _check(st, "moe_norm_forward")
+    _norm_forward(desc, x, gamma, beta, _p(y, _act_dtype(desc), "y"),
+                  _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), stream)
 
 
 def moe_norm_workspace_size(desc: NormDesc) -> int:
@@ -568,20 +572,27 @@ def moe_norm_workspace_size(desc: NormDesc) -> int:
     return n.value
 
 
+def _norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream):
+    """moe_norm_backward with dx, dgamma and dbeta as pointers."""
+    dt = _act_dtype(desc)
+    _need(dy, (desc.T, desc.d), "dy")
+    st = lib().moe_norm_backward(
+        ctypes.byref(desc), _p(dy, dt, "dy"), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
+        _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), dx, dgamma, dbeta,
+        _p(ws, torch.uint8, "workspace"), 0 if ws is None else ws.numel(), _stream(stream))
+    _check(st, "moe_norm_backward")
+
+
 def moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
     """dx, and dgamma / dbeta [d] fp32 unless None (both None: ws may be None)."""
-    dt = _act_dtype(desc)
-    for t, what in ((dy, "dy"), (x, "x"), (dx, "dx")):
-        _need(t, (desc.T, desc.d), what)
+    _need(x, (desc.T, desc.d), "x")
+    _need(dx, (desc.T, desc.d), "dx")
     for t, what in ((dgamma, "dgamma"), (dbeta, "dbeta")):
         if t is not None:
             _need(t, (desc.d,), what)
-    st = lib().moe_norm_backward(
-        ctypes.byref(desc), _p(dy, dt, "dy"), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
-        _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), _p(dx, dt, "dx"),
-        _p(dgamma, torch.float32, "dgamma"), _p(dbeta, torch.float32, "dbeta"),
-        _p(ws, torch.uint8, "workspace"), 0 if ws is None else ws.numel(), _stream(stream))
-    _check(st, "moe_norm_backward")
+    _norm_backward(desc, dy, x, gamma, mean, rstd, _p(dx, _act_dtype(desc), "dx"),
+                   _p(dgamma, torch.float32, "dgamma"), _p(dbeta, torch.float32, "dbeta"), ws,
+                   stream)
 
 
 def norm(x, gamma=None, beta=None, kind=MOE_NORM_LAYER, eps=1e-6, stats=False):
@@ -594,7 +605,8 @@ def norm(x, gamma=None, beta=None, kind=MOE_NORM_LAYER, eps=1e-6, stats=False):
         rstd = torch.empty(desc.T, dtype=torch.float32, device=x.device)
         if kind != MOE_NORM_RMS:
             mean = torch.empty_like(rstd)
-    moe_norm_forward(desc, x, gamma, beta, y, mean, rstd)
+    _norm_forward(desc, x, gamma, beta, y.data_ptr(), None if mean is None else mean.data_ptr(),
+                  None if rstd is None else rstd.data_ptr(), None)
     return y, mean, rstd
 
 
@@ -606,7 +618,8 @@ def norm_backward(dy, x, gamma, mean, rstd, kind=MOE_NORM_LAYER):
     dgamma = torch.empty(desc.d, dtype=torch.float32, device=x.device)
     dbeta = None if kind == MOE_NORM_RMS else torch.empty_like(dgamma)
     ws = torch.empty(moe_norm_workspace_size(desc), dtype=torch.uint8, device=x.device)
-    moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws)
+    _norm_backward(desc, dy, x, gamma, mean, rstd, dx.data_ptr(), dgamma.data_ptr(),
+                   None if dbeta is None else dbeta.data_ptr(), ws, None)
     return dx, dgamma, dbeta
 
 
