@@ -39,7 +39,6 @@ namespace {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 1024.f, kScaleA = 16384.f, kScaleB = 4096.f;
-constexpr int kPairUnits = 48;   // least 256 x 256 tiles for the SM pairs
 constexpr int kSumBlocks = 128;  // most blocks of the norm's sum, per matrix
 
 struct Scale {
@@ -921,7 +920,7 @@ cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, Product p,
 
 template <int OP>
 cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Product& p,
-                         long long units, cudaStream_t s) {
+                         long long units, int split, cudaStream_t s) {
   using C = SmallCfg;
   auto kern = ortho_small_kernel<OP>;
   int dev = 0;
@@ -934,10 +933,6 @@ cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Produ
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  // the reduction is shared while that leaves at most two CTAs an SM and each
-  // at least four of its blocks
-  int split = 1;
-  while (split < kMaxSplit && units * split <= num_sms() && p.K / 64 / (2 * split) >= 4) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * split));
   cfg.blockDim = dim3(kSmallThreads);
@@ -957,15 +952,39 @@ cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Produ
   return cudaGetLastError();
 }
 
+// Whether a product runs in 256 x 256 tiles on SM pairs or in 128 x 64 tiles,
+// and over how many CTAs a small tile's reduction is shared: whatever these
+// times, fitted to graph replays of whole calls (bf16), say is least.  In 10 ns:
+//   pairs: 27 a round of the pairs and 64-column block of the reduction
+//          (512 cycles of the tensor cores), and 550 for a tile's first loads
+//          and its epilogue;
+//   small: 17 a block (24 KB from L2 into an SM) and 125 of prologue and
+//          epilogue for each tile an SM has, and 125 once; a shared reduction
+//          adds 400 for the cluster's launch, barriers and exchange.
+// Measured, us a call: 4 x 512 x 512 98 pairs, 74 small; 2 x 1536 x 4096 340
+// pairs, 516 small; 1 x 512 x 2048 90 with the reductions of 2048 over two
+// CTAs, 84 over four; 1 x 1024 x 1024 130 with 1024 over two, 100 unshared.
 template <int OP>
 cudaError_t product(const OperandMaps& P, const OperandMaps& Q, const Product& p,
                     cudaStream_t s) {
   constexpr bool SYM = OP == kGram || OP == kPoly;
-  const long long n = p.n_mats;
+  const long long n = p.n_mats, sms = num_sms(), blocks = p.K / 64;
   const long long large = n * Tiles<256, 256, SYM>(p.rowsP, p.rowsQ).count();
   const long long small = n * Tiles<128, kSmallN, SYM>(p.rowsP, p.rowsQ).count();
-  return large < kPairUnits || 2 * small < 5 * large ? launch_small<OP>(P, Q, p, small, s)
-                                                     : launch_pairs<OP>(P, Q, p, large, s);
+  const long long pair_cost = (large + sms / 2 - 1) / (sms / 2) * blocks * 27 + 550;
+  long long least = 0;
+  int split = 0;
+  for (int k = 1; k <= kMaxSplit && k <= blocks; k *= 2) {
+    const long long each = 125 + 17 * ((blocks + k - 1) / k);
+    const long long tiles = small * k > sms ? small * k : sms;
+    const long long cost = 125 + each * tiles / sms + (k > 1 ? 400 : 0);
+    if (split == 0 || cost < least) {
+      least = cost;
+      split = k;
+    }
+  }
+  return least < pair_cost ? launch_small<OP>(P, Q, p, small, split, s)
+                           : launch_pairs<OP>(P, Q, p, large, s);
 }
 
 int sum_blocks(size_t per_mat) {
