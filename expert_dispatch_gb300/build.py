@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cu", "simt.cu", "plan.cu", "rows.cu", "tc_gemm.cu", "tc_gemm_q8.cu", "quant.cu",
            "ffn_noalloc.cu", "slot_cache.cu", "tc_gemm_pair.cu",
-           "norm.cu", "row_grads.cu", "ortho.cu"]
+           "norm.cu", "row_grads.cu", "ortho.cu", "ortho_chip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -213,6 +213,11 @@ struct OrthoLayout {
   size_t total;
   int mp, np;
 };
+// Matrices that one cluster of CTAs holds on chip (ortho_chip.cu): one launch,
+// no workspace but the flags.
+bool ortho_fits_chip(const moe_ortho_desc& D);
+cudaError_t launch_ortho_chip(const moe_ortho_desc& D, const void* g, void* out, int* flags,
+                              cudaStream_t s);
 OrthoLayout ortho_layout(const moe_ortho_desc& D);
 cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* out, void* ws,
                                  cudaStream_t s);

@@ -23,6 +23,9 @@
 // X: it is K-major in X X^T, and in B X the tensor cores read it MN-major
 // (rows of 64 columns of X, the reduction running down the rows), so no
 // transposed copy is written.
+//
+// Matrices with m <= 128 and n up to a cluster's shared memory take one launch of
+// the kernel in ortho_chip.cu; what follows here serves the others.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,43 +35,17 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "ortho.cuh"
 #include "tc_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kScaleX = 1024.f, kScaleA = 16384.f, kScaleB = 4096.f;
+using namespace ortho;
+
 constexpr int kSumBlocks = 128;  // most blocks of the norm's sum, per matrix
 
-struct Scale {
-  float f1, f2;  // X = g * f1 * f2, powers of two (one factor could leave fp32's range)
-  float rho;     // what is left of 1 / (|G| + eps), in (1/2, 1]
-  float pad;
-};
-
 // ---------------------------------------------------------------- norm and first X
-// V consecutive elements as fp32: 16 aligned bytes, or one element.
-template <typename T, int V>
-__device__ __forceinline__ void load_elems(const T* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = load_as_f32(p, 0);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  }
-}
-
-constexpr float kBig = 0x1p45f, kSmall = 0x1p-45f, kUp = 0x1p84f, kDown = 0x1p-84f;
-
 // Sums of squares of one matrix, block blockIdx.x of gridDim.x.  Squares are
 // summed as they are while the block's largest value lies between 2^-45 and
 // 2^45 (what then underflows is below 2^-63, far under the sum's last digit).
@@ -148,43 +125,6 @@ __global__ void __launch_bounds__(512)
     for (int w = 0; w < 16; ++w) v += red[threadIdx.x][w];
     partial[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 3 + threadIdx.x] = v;
   }
-}
-
-// The scale of one matrix from its partial sums, added by one warp in a fixed
-// order.
-__device__ Scale matrix_scale(const float* partial, int n, float eps) {
-  float s[3] = {0.f, 0.f, 0.f};
-  for (int i = threadIdx.x & 31; i < n; i += 32)
-#pragma unroll
-    for (int q = 0; q < 3; ++q) s[q] += partial[i * 3 + q];
-#pragma unroll
-  for (int q = 0; q < 3; ++q)
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
-  // |G| + eps = v * 2^off
-  float v;
-  int off = 0;
-  if (s[0] > 0.f || s[0] != s[0]) {
-    v = sqrtf(s[0] + s[1] * kDown * kDown), off = 84;
-  } else if (s[1] > 0.f || s[1] != s[1]) {
-    v = sqrtf(s[1] + s[2] * kDown * kDown) + eps;
-  } else if (eps > 0.f) {
-    v = sqrtf(s[2]) * kDown + eps;
-  } else {
-    v = sqrtf(s[2]), off = -84;
-  }
-  Scale r{0.f, 0.f, 0.f, 0.f};
-  if (v == 0.f) return r;  // a zero matrix, eps = 0: X = 0
-  if (isinf(v) || v != v) {
-    r.f1 = r.f2 = r.rho = __int_as_float(0x7fffffff);
-    return r;
-  }
-  const int e = ilogbf(v);
-  const int k = 10 - e - off;  // X = g * 2^k
-  r.f1 = scalbnf(1.f, k / 2);
-  r.f2 = scalbnf(1.f, k - k / 2);
-  r.rho = 1.f / scalbnf(v, -e);
-  return r;
 }
 
 // First X in fp16, padded with zeros: the input, [rows, cols] padded to
@@ -336,56 +276,6 @@ struct Tiles {
   __device__ bool mirrored(int i, int j) const { return SYM && (j + 1) * BN <= i * BM; }
 };
 
-// Shared-memory descriptor of an MN-major operand written by TMA in boxes of 64
-// columns (128 bytes, 128-byte swizzle) by 64 reduction rows: 8-row groups are
-// 1024 bytes apart, the next 64 columns 8192.
-__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
-  uint64_t desc = 0;
-  desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
-  desc |= static_cast<uint64_t>(8192 >> 4) << 16;          // leading byte offset: 64 columns
-  desc |= static_cast<uint64_t>(1024 >> 4) << 32;          // stride byte offset: 8 rows
-  desc |= static_cast<uint64_t>(1) << 46;                  // descriptor version
-  desc |= static_cast<uint64_t>(2) << 61;                  // 128-byte swizzle
-  return desc;
-}
-constexpr uint32_t kTransposeB = 1u << 16;  // instruction descriptor: B is MN-major
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// W columns of row `row` of the last product, from column c0 on.
-template <int W>
-__device__ __forceinline__ void store_result(const Product& p, int mat, int row, int c0,
-                                             const float (&v)[W]) {
-  __nv_bfloat16* base = p.result + (size_t)mat * p.m * p.n;
-  if (p.tall) {  // [n, m]: a warp's lanes hold consecutive elements
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      if (c0 + j < p.n) base[(size_t)(c0 + j) * p.m + row] = __float2bfloat16_rn(v[j]);
-    return;
-  }
-  __nv_bfloat16* dst = base + (size_t)row * p.n + c0;
-  if (p.n % 8 == 0) {  // 16-byte aligned rows
-#pragma unroll
-    for (int j = 0; j < W; j += 8) {
-      if (c0 + j >= p.n) break;
-      uint32_t w[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * t], v[j + 2 * t + 1]);
-        w[t] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < W; ++j)
-    if (c0 + j < p.n) dst[j] = __float2bfloat16_rn(v[j]);
-}
-
 // The factor of a product's accumulators.
 template <int OP>
 __device__ __forceinline__ float product_scale(const Product& p, int mat) {
@@ -415,7 +305,8 @@ template <int OP, int W>
 __device__ __forceinline__ void store_product(const Product& p, int mat, int row, int c0,
                                               bool mirror, const uint4* gram, float (&v)[W]) {
   if (OP == kLast) {
-    if (row < p.m) store_result<W>(p, mat, row, c0, v);
+    if (row < p.m)
+      store_result<W>(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row, c0, v);
     return;
   }
   if (row >= p.rowsP) return;
@@ -600,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16_pair(d0, smem_desc_sw128(s + kk * 32),
                            SYM ? smem_desc_sw128(s + C::A_BYTES + kk * 32)
-                               : smem_desc_mn128(s + C::A_BYTES + kk * 2048),
+                               : smem_desc_mn128(s + C::A_BYTES + kk * 2048, 8192),
                            idesc, kb | kk ? 1u : 0u);
           issued = true;
           umma_commit_pair_mc(empty_bar(stage), 3);  // both CTAs' stage is free again
@@ -682,12 +573,6 @@ struct SmallCfg {
   static constexpr int SMEM_TOTAL = MISC_OFF + 16 + 1024;
   static_assert(kSmallN * 128 * 4 <= BAR_OFF, "partial sums reuse the stages");
 };
-
-__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
 
 template <int OP>
 __global__ void __launch_bounds__(kSmallThreads)
@@ -778,7 +663,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16(tmem_base, smem_desc_sw128(s + kk * 32),
                     SYM ? smem_desc_sw128(s + C::A_BYTES + kk * 32)
-                        : smem_desc_mn128(s + C::A_BYTES + kk * 2048),
+                        : smem_desc_mn128(s + C::A_BYTES + kk * 2048, 8192),
                     idesc, kb != kb0 || kk ? 1u : 0u);
         umma_commit(empty_bar(stage));
         if (++stage == kSmallStages) {
@@ -1025,6 +910,10 @@ OrthoLayout ortho_layout(const moe_ortho_desc& D) {
   const int m = D.rows < D.cols ? D.rows : D.cols, c = D.rows < D.cols ? D.cols : D.rows;
   L.mp = (m + 63) / 64 * 64;
   L.np = (c + 63) / 64 * 64;
+  if (ortho_fits_chip(D)) {
+    L.total = 256;  // the flags
+    return L;
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -1044,6 +933,7 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
                                  cudaStream_t s) {
   const OrthoLayout L = ortho_layout(D);
   int* flags = static_cast<int*>(ws);
+  if (ortho_fits_chip(D)) return launch_ortho_chip(D, g, out, flags, s);
   uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 16 + 255) &
                                           ~(uintptr_t)255);
   const int m = D.rows < D.cols ? D.rows : D.cols, n = D.rows < D.cols ? D.cols : D.rows;

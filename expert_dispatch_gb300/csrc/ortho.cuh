@@ -1,0 +1,138 @@
+// ortho.cuh -- pieces shared by the kernels of the Newton-Schulz
+// orthogonalisation (ortho.cu, ortho_chip.cu): the polynomial, the fp16 scales
+// (see ortho.cu), the norm's sums and operand helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace ortho {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 1024.f, kScaleA = 16384.f, kScaleB = 4096.f;
+
+struct Scale {
+  float f1, f2;  // X = g * f1 * f2, powers of two (one factor could leave fp32's range)
+  float rho;     // what is left of 1 / (|G| + eps), in (1/2, 1]
+  float pad;
+};
+
+// V consecutive elements as fp32: 16 aligned bytes, or one element.
+template <typename T, int V>
+__device__ __forceinline__ void load_elems(const T* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = load_as_f32(p, 0);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+
+constexpr float kBig = 0x1p45f, kSmall = 0x1p-45f, kUp = 0x1p84f, kDown = 0x1p-84f;
+
+// The scale of one matrix from its partial sums, added by one warp in a fixed
+// order.
+__device__ __forceinline__ Scale matrix_scale(const float* partial, int n, float eps) {
+  float s[3] = {0.f, 0.f, 0.f};
+  for (int i = threadIdx.x & 31; i < n; i += 32)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) s[q] += partial[i * 3 + q];
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
+  // |G| + eps = v * 2^off
+  float v;
+  int off = 0;
+  if (s[0] > 0.f || s[0] != s[0]) {
+    v = sqrtf(s[0] + s[1] * kDown * kDown), off = 84;
+  } else if (s[1] > 0.f || s[1] != s[1]) {
+    v = sqrtf(s[1] + s[2] * kDown * kDown) + eps;
+  } else if (eps > 0.f) {
+    v = sqrtf(s[2]) * kDown + eps;
+  } else {
+    v = sqrtf(s[2]), off = -84;
+  }
+  Scale r{0.f, 0.f, 0.f, 0.f};
+  if (v == 0.f) return r;  // a zero matrix, eps = 0: X = 0
+  if (isinf(v) || v != v) {
+    r.f1 = r.f2 = r.rho = __int_as_float(0x7fffffff);
+    return r;
+  }
+  const int e = ilogbf(v);
+  const int k = 10 - e - off;  // X = g * 2^k
+  r.f1 = scalbnf(1.f, k / 2);
+  r.f2 = scalbnf(1.f, k - k / 2);
+  r.rho = 1.f / scalbnf(v, -e);
+  return r;
+}
+
+// Shared-memory descriptor of an MN-major operand written by TMA in boxes of 64
+// columns (128 bytes, 128-byte swizzle): groups of 8 reduction rows are 1024
+// bytes apart, the next 64 columns `next` bytes.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t next) {
+  uint64_t desc = 0;
+  desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
+  desc |= static_cast<uint64_t>(next >> 4) << 16;          // leading byte offset: 64 columns
+  desc |= static_cast<uint64_t>(1024 >> 4) << 32;          // stride byte offset: 8 rows
+  desc |= static_cast<uint64_t>(1) << 46;                  // descriptor version
+  desc |= static_cast<uint64_t>(2) << 61;                  // 128-byte swizzle
+  return desc;
+}
+constexpr uint32_t kTransposeB = 1u << 16;  // instruction descriptor: B is MN-major
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// W columns of row `row` of one matrix's result, from column c0 on: base is
+// [m, n], or [n, m] if tall.
+template <int W>
+__device__ __forceinline__ void store_result(__nv_bfloat16* base, int m, int n, bool tall, int row,
+                                             int c0, const float (&v)[W]) {
+  if (tall) {  // a warp's lanes hold consecutive elements
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (c0 + j < n) base[(size_t)(c0 + j) * m + row] = __float2bfloat16_rn(v[j]);
+    return;
+  }
+  __nv_bfloat16* dst = base + (size_t)row * n + c0;
+  if (n % 8 == 0) {  // 16-byte aligned rows
+#pragma unroll
+    for (int j = 0; j < W; j += 8) {
+      if (c0 + j >= n) break;
+      uint32_t w[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * t], v[j + 2 * t + 1]);
+        w[t] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+    if (c0 + j < n) dst[j] = __float2bfloat16_rn(v[j]);
+}
+
+}  // namespace ortho
+}  // namespace moe

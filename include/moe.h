@@ -562,7 +562,7 @@ int64_t moe_launch_count(void);
    ffn_gateup_tc_q8, ffn_down_tc_q8, quantize_q8_0, combine, combine_partial,
    missing_pairs, dispatch_rows, dispatch_rows_backward, combine_backward,
    norm_forward, norm_backward, norm_reduce, ortho_sumsq, ortho_start,
-   ortho_gram, ortho_poly, ortho_apply, load_experts (the expert tier's loads of host-resident
+   ortho_gram, ortho_poly, ortho_apply, ortho_chip, load_experts (the expert tier's loads of host-resident
    experts into HBM slots).
    moe_profile_list() gives the named kernel's recorded launches one by one,
    in launch order: the first max_n durations (ms) and the bytes each launch

@@ -386,7 +386,9 @@ def check_ortho(got, want):
     (1, 1, 1), (2, 3, 5), (2, 1, 300), (1, 300, 1), (1, 64, 64), (3, 65, 130), (2, 130, 65),
     (1, 257, 1001), (2, 300, 260), (1, 512, 512), (1, 1000, 64), (5, 128, 512), (1, 256, 4096),
     (40, 100, 90), (1, 520, 776), (2, 1032, 600), (9, 1100, 600), (7, 1030, 1100),
-    (3, 1000, 2500), (60, 300, 260)])
+    (3, 1000, 2500), (60, 300, 260), (1, 16, 16), (3, 128, 128), (2, 128, 257), (1, 100, 512),
+    (2, 513, 128), (1, 128, 2048), (2, 2300, 120), (1, 128, 3008), (1, 128, 3136), (200, 30, 500),
+    (160, 128, 40)])
 def test_ortho(n, rows, cols, dtype):
     g = rnd((n, rows, cols), rows + cols, DT[dtype], 0.02)
     check_ortho(moe.orthogonalize(g), ref_ortho(g, 5, 1e-7))
@@ -409,8 +411,9 @@ def test_ortho_singular_values_meet_one():
     assert 0.6 < float(s.min()) and float(s.max()) < 1.3
 
 
-def test_ortho_scales_by_powers_of_two_change_nothing():
-    g = rnd((3, 90, 140), 1)
+@pytest.mark.parametrize("rows", [90, 190])
+def test_ortho_scales_by_powers_of_two_change_nothing(rows):
+    g = rnd((3, rows, 440), 1)
     want = moe.orthogonalize(g, eps=0.0)
     for e in (-100, -70, 40, 100, 120):
         assert torch.equal(moe.orthogonalize(g * 2.0 ** e, eps=0.0), want), e
@@ -424,27 +427,29 @@ def test_ortho_scales_by_powers_of_two_change_nothing():
     check_ortho(moe.orthogonalize(small, eps=1e-7), ref_ortho(small, 5, 1e-7))
 
 
-def test_ortho_zero_and_nan_matrices():
-    g = rnd((5, 70, 200), 2)
+@pytest.mark.parametrize("rows", [70, 170])
+def test_ortho_zero_and_nan_matrices(rows):
+    g = rnd((5, rows, 300), 2)
     want = moe.orthogonalize(g)
     for eps in (1e-7, 0.0):
         bad = g.clone()
         bad[1] = 0
         bad[2, 3, 4] = float("nan")
-        bad[3, 69, 199] = float("inf")
+        bad[3, rows - 1, 299] = float("inf")
         out = moe.orthogonalize(bad, eps=eps)
         assert not out[1].any() and out[2].isnan().all() and out[3].isnan().all()
         if eps:
             assert torch.equal(out[0], want[0]) and torch.equal(out[4], want[4])
     # values so large or small that their squares leave fp32, beside ordinary ones
-    wide = rnd((1, 200, 300), 5)
+    wide = rnd((1, rows, 300), 5)
     wide[0, :, 7] *= 2.0 ** 70
     wide[0, 9] *= 2.0 ** -80
     check_ortho(moe.orthogonalize(wide, steps=1), ref_ortho(wide, 1, 1e-7))
 
 
-def test_ortho_workspace_stream_and_graph():
-    g = rnd((2, 100, 260), 3, torch.bfloat16)
+@pytest.mark.parametrize("rows", [100, 200])
+def test_ortho_workspace_stream_and_graph(rows):
+    g = rnd((2, rows, 260), 3, torch.bfloat16)
     want = moe.orthogonalize(g)
     desc = moe.make_ortho_desc(g)
     size = moe.moe_ortho_workspace_size(desc)
