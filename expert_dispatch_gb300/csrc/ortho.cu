@@ -246,7 +246,7 @@ struct Cfg {
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM_TOTAL = MISC_OFF + 16 + 1024;
   static_assert(BN == 64 || BN == 128 || BN == 256, "tile");
-  static_assert(SMEM_TOTAL <= 232448, "shared memory");
+  static_assert(SMEM_TOTAL + tc::kEpiWarps * 32 * kRowWords * 4 <= 232448, "shared memory");
 };
 
 // Tiles of BM x BN of one matrix.  Symmetric products take the tiles that meet
@@ -304,11 +304,6 @@ __device__ __forceinline__ void load_gram(const Product& p, int mat, int row, in
 template <int OP, int W>
 __device__ __forceinline__ void store_product(const Product& p, int mat, int row, int c0,
                                               bool mirror, const uint4* gram, float (&v)[W]) {
-  if (OP == kLast) {
-    if (row < p.m)
-      store_result<W>(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row, c0, v);
-    return;
-  }
   if (row >= p.rowsP) return;
   const size_t at = ((size_t)mat * p.rowsP + row) * p.rowsQ + c0;
   if (OP == kPoly) {
@@ -355,6 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   using C = Cfg<BN, STAGES>;
   constexpr bool SYM = OP == kGram || OP == kPoly;  // else Q is MN-major
   extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t scratch[tc::kEpiWarps][OP == kLast ? 32 * kRowWords : 1];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -537,7 +533,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
-        store_product<OP, 16>(p, mat, row, c0, mirror, gram, v);
+        if constexpr (OP == kLast)
+          store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
+                       scratch[warp - 2]);
+        else
+          store_product<OP, 16>(p, mat, row, c0, mirror, gram, v);
         __syncwarp();  // the next tcgen05.ld is the whole warp's
       }
       tc_fence_before();
@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   using C = SmallCfg;
   constexpr bool SYM = OP == kGram || OP == kPoly;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t scratch[4][OP == kLast ? 32 * kRowWords : 1];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -699,7 +700,10 @@ __global__ void __launch_bounds__(kSmallThreads)
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
-      if (split == 1) {
+      if (OP == kLast && split == 1) {
+        store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
+                     scratch[warp - 2]);
+      } else if (split == 1) {
         store_product<OP, 16>(p, mat, row, c0, mirror, &gram[cc / 8], v);
       } else {
         // the stages' last reader was the MMA that this warp waited for
@@ -719,10 +723,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   cluster_sync();  // every CTA's partial sums are in place
   if (warp >= 2) {
     const int cols = kSmallN / split;
-    for (int cc = rank * cols; cc < (rank + 1) * cols; cc += 8) {
-      const int c0 = tj * kSmallN + cc;
-      uint4 gram[1];
-      load_gram<OP, 8>(p, mat, row, c0, gram);
+    auto joined = [&](int cc, float* v) {  // 8 columns of the row over the cluster
       const uint32_t mine = sbase + (uint32_t)(cc * 128 + q * 32 + lane) * 4u;
       float part[kMaxSplit][8];  // all loads in flight before the first sum
 #pragma unroll
@@ -733,7 +734,6 @@ __global__ void __launch_bounds__(kSmallThreads)
           for (int j = 0; j < 8; ++j) part[r][j] = ld_shared_cluster(peer + (uint32_t)j * 512u);
         }
       }
-      float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[j] = part[0][j];
@@ -741,7 +741,22 @@ __global__ void __launch_bounds__(kSmallThreads)
         for (int r = 1; r < kMaxSplit; ++r)
           if (r < split) v[j] += part[r][j];
       }
-      store_product<OP, 8>(p, mat, row, c0, mirror, gram, v);
+    };
+    for (int cc = rank * cols; cc < (rank + 1) * cols; cc += OP == kLast ? 16 : 8) {
+      const int c0 = tj * kSmallN + cc;
+      if constexpr (OP == kLast) {  // its share is 16 columns at least
+        float v[16];
+        joined(cc, v);
+        joined(cc + 8, v + 8);
+        store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
+                     scratch[warp - 2]);
+      } else {
+        uint4 gram[1];
+        load_gram<OP, 8>(p, mat, row, c0, gram);
+        float v[8];
+        joined(cc, v);
+        store_product<OP, 8>(p, mat, row, c0, mirror, gram, v);
+      }
     }
   }
   cluster_sync();  // a CTA's shared memory stays until its peers have read it
@@ -859,7 +874,8 @@ cudaError_t product(const OperandMaps& P, const OperandMaps& Q, const Product& p
   const long long pair_cost = (large + sms / 2 - 1) / (sms / 2) * blocks * 27 + 550;
   long long least = 0;
   int split = 0;
-  for (int k = 1; k <= kMaxSplit && k <= blocks; k *= 2) {
+  const int most = OP == kLast ? kMaxSplit / 2 : kMaxSplit;  // 16 columns a CTA at least
+  for (int k = 1; k <= most && k <= blocks; k *= 2) {
     const long long each = 125 + 17 * ((blocks + k - 1) / k);
     const long long tiles = small * k > sms ? small * k : sms;
     const long long cost = 125 + each * tiles / sms + (k > 1 ? 400 : 0);

@@ -103,35 +103,53 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   return v;
 }
 
-// W columns of row `row` of one matrix's result, from column c0 on: base is
-// [m, n], or [n, m] if tall.
-template <int W>
-__device__ __forceinline__ void store_result(__nv_bfloat16* base, int m, int n, bool tall, int row,
-                                             int c0, const float (&v)[W]) {
-  if (tall) {  // a warp's lanes hold consecutive elements
+constexpr int kRowWords = 9;  // a lane's 16 bf16 values in shared memory, and a pad
+
+// A warp stores 16 columns of 32 rows of one matrix's result: lane l has row
+// row0 + l, columns c0 .. c0 + 15, in v.  base is [m, n], or [n, m] if tall.
+// Rows of a multiple of 16 bytes take two 16-byte stores a lane, columns (tall)
+// lie across the lanes; other rows go through `scratch` (32 kRowWords words of
+// the warp's own), so that 16 lanes store 32 consecutive bytes of a row where
+// each lane's own values would touch 32 rows at once.
+__device__ __forceinline__ void store_result(__nv_bfloat16* base, int m, int n, bool tall,
+                                             int row0, int c0, const float (&v)[16],
+                                             uint32_t* scratch) {
+  const int lane = threadIdx.x & 31, row = row0 + lane;
+  if (tall) {
+    if (row < m) {
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-      if (c0 + j < n) base[(size_t)(c0 + j) * m + row] = __float2bfloat16_rn(v[j]);
+      for (int j = 0; j < 16; ++j)
+        if (c0 + j < n) base[(size_t)(c0 + j) * m + row] = __float2bfloat16_rn(v[j]);
+    }
     return;
   }
-  __nv_bfloat16* dst = base + (size_t)row * n + c0;
-  if (n % 8 == 0) {  // 16-byte aligned rows
+  uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < W; j += 8) {
-      if (c0 + j >= n) break;
-      uint32_t w[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * t], v[j + 2 * t + 1]);
-        w[t] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int t = 0; t < 8; ++t) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * t], v[2 * t + 1]);
+    w[t] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if (n % 8 == 0) {
+    if (row < m) {
+      uint4* dst = reinterpret_cast<uint4*>(base + (size_t)row * n + c0);
+      if (c0 < n) dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      if (c0 + 8 < n) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < W; ++j)
-    if (c0 + j < n) dst[j] = __float2bfloat16_rn(v[j]);
+  for (int t = 0; t < 8; ++t) scratch[lane * kRowWords + t] = w[t];
+  __syncwarp();
+  const int c = lane & 15;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    const uint32_t word = scratch[r * kRowWords + (c >> 1)];
+    if (row0 + r < m && c0 + c < n)
+      reinterpret_cast<uint16_t*>(base)[(size_t)(row0 + r) * n + c0 + c] =
+          (uint16_t)(c & 1 ? word >> 16 : word & 0xffffu);
+  }
+  __syncwarp();
 }
 
 }  // namespace ortho

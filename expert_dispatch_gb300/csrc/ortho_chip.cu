@@ -33,7 +33,9 @@ namespace {
 
 using namespace ortho;
 
-constexpr int kThreads = 256;       // 8 warps: two a TMEM lane quarter
+constexpr int kThreads = 512;       // 16 warps: four a TMEM lane quarter
+constexpr int kWarps = kThreads / 32;
+constexpr int kParts = kWarps / 4;  // warps a quarter
 constexpr int kMaxCluster = 8;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows of 64 fp16 columns
 constexpr int kPartBytes = 128 * 128 * 4;
@@ -65,49 +67,89 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 6) * kBlockBytes + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4));
 }
 
-// f(row, column of the slice, V values) over this CTA's columns c0 .. c0 + w - 1
-// of X = G or G^T, V elements that are consecutive in G at a time (V == 1: any
-// alignment); the values follow each other along X's row, or its column (tall).
-template <typename T, int V, typename F>
-__device__ __forceinline__ void for_slice(const T* __restrict__ g, const ChipArgs& p, int c0,
-                                          int w, F&& f) {
+// The 16 bytes from element `at` (a multiple of their number) of `total`; zeros
+// behind the end.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* __restrict__ g, size_t at, size_t total) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (at + V <= total) return *reinterpret_cast<const uint4*>(g + at);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (at + j >= total) continue;
+    if constexpr (sizeof(T) == 4)
+      w[j] = __float_as_uint(g[at + j]);
+    else
+      w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(g)[at + j] << (16 * (j & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack16(uint4 q, float (&v)[V]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    v[j] = sizeof(T) == 4 ? __uint_as_float(w[j % 4])
+           : j & 1        ? __uint_as_float(w[j / 2] & 0xffff0000u)
+                          : __uint_as_float(w[j / 2] << 16);
+}
+
+// f(line, start, length, V values) over this CTA's columns c0 .. c0 + w - 1 of X =
+// G or G^T.  A line is a row of X, or a column (tall): what is consecutive in G.
+// It is read in aligned 16-byte vectors that may begin before it and end behind
+// it; the values are those of its positions start .. start + V - 1, of which 0 ..
+// length - 1 count.  No vector reaches behind the stack's end.
+template <typename T, typename F>
+__device__ __forceinline__ void for_slice(const T* __restrict__ g, size_t total, const ChipArgs& p,
+                                          int mat, int c0, int w, F&& f) {
+  constexpr int V = 16 / (int)sizeof(T);
   const bool tall = p.rows > p.cols;
   const int wn = min(w, p.n - c0);  // columns that exist
   if (wn <= 0) return;
-  if (!tall) {
-    const int per_row = (wn + V - 1) / V, total = p.m * per_row;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-      const int r = i / per_row, c = (i - r * per_row) * V;
-      float v[V];
-      load_elems<T, V>(g + (size_t)r * p.cols + c0 + c, v);
-      f(r, c, v);
-    }
-  } else {
-    // a warp takes 8 columns by 4 vectors of rows: 64-byte reads, and stores
-    // into X that share a chunk
-    const int nr = (p.m + V - 1) / V, nr4 = (nr + 3) / 4, total = ((wn + 7) / 8) * nr4 * 32;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-      const int t = i >> 5;
-      const int r = ((t % nr4) * 4 + (i & 3)) * V, c = (t / nr4) * 8 + ((i >> 2) & 7);
-      if (r < p.m && c < wn) {
-        float v[V];
-        load_elems<T, V>(g + (size_t)(c0 + c) * p.cols + r, v);
-        f(r, c, v);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lines = tall ? wn : p.m, length = tall ? p.m : wn;
+  const size_t first = (size_t)mat * p.rows * p.cols + (tall ? (size_t)c0 * p.cols : (size_t)c0);
+  // one more where lines begin inside a vector
+  const int vectors = (length + V - 1) / V + (p.cols % V ? 1 : 0);
+  // a warp takes one line by 32 vectors of a row; of a column 8 lines by 4
+  // vectors, so that its stores into X share 16-byte chunks
+  const int wide = tall ? 8 : 1, across = tall ? 4 : 32;
+  const int li = tall ? lane >> 2 : 0, vi = tall ? lane & 3 : lane;
+  constexpr int U = 8;  // vectors in flight: the next lines, or (tall) further along the line
+  const int jl = tall ? 0 : kWarps, jv = tall ? across : 0;
+  for (int l0 = warp * wide + li; l0 < lines; l0 += kWarps * wide * (tall ? 1 : U)) {
+    for (int k0 = vi; k0 < vectors; k0 += across * (tall ? U : 1)) {
+      uint4 raw[U];
+      int start[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int l = l0 + u * jl, k = k0 + u * jv;
+        const size_t e = first + (size_t)l * p.cols;
+        const int shift = (int)(e % V);
+        start[u] = l < lines ? k * V - shift : length;
+        if (start[u] < length) raw[u] = load16(g, e - shift + (size_t)k * V, total);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (start[u] < length) {
+          float v[V];
+          unpack16<T, V>(raw[u], v);
+          f(l0 + u * jl, start[u], length, v);
+        }
     }
   }
 }
 
-template <typename T, int V>
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    ortho_chip_kernel(const T* __restrict__ g_all, const ChipArgs p) {
+    ortho_chip_kernel(const T* __restrict__ g, size_t total, const ChipArgs p) {
+  constexpr int V = 16 / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_s;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
-  __shared__ float red[3][kThreads / 32], top[kThreads / 32];
+  __shared__ float red[3][kWarps], top[kWarps];
   __shared__ float sums[3], all_sums[kMaxCluster * 3];
   __shared__ Scale sc;
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -123,7 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mat = (int)blockIdx.x / C, rank = (int)blockIdx.x - mat * C;
   const int w = p.blocks * 64, c0 = rank * w;
   const bool tall = p.rows > p.cols;
-  const T* g = g_all + (size_t)mat * p.rows * p.cols;
 
   if (tid == 0) {
     mbar_init(bar, 1);
@@ -148,11 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a block's share
   {
     float s[3] = {0.f, 0.f, 0.f}, most = 0.f;
-    for_slice<T, V>(g, p, c0, w, [&](int, int, const float (&v)[V]) {
+    for_slice<T>(g, total, p, mat, c0, w, [&](int, int at, int len, const float (&v)[V]) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        s[1] = fmaf(v[j], v[j], s[1]);
-        most = fmaxf(most, fabsf(v[j]));
+        const float x = at + j >= 0 && at + j < len ? v[j] : 0.f;
+        s[1] = fmaf(x, x, s[1]);
+        most = fmaxf(most, fabsf(x));
       }
     });
 #pragma unroll
@@ -160,19 +202,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) top[warp] = most;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) most = fmaxf(most, top[i]);
+    for (int i = 0; i < kWarps; ++i) most = fmaxf(most, top[i]);
     if (most != 0.f && (most > kBig || most < kSmall)) {
       s[1] = 0.f;
-      for_slice<T, V>(g, p, c0, w, [&](int, int, const float (&v)[V]) {
+      for_slice<T>(g, total, p, mat, c0, w, [&](int, int at, int len, const float (&v)[V]) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float ax = fabsf(v[j]);
+          const float x = at + j >= 0 && at + j < len ? v[j] : 0.f, ax = fabsf(x);
           if (ax > kBig)
-            s[0] = fmaf(v[j] * kDown, v[j] * kDown, s[0]);
+            s[0] = fmaf(x * kDown, x * kDown, s[0]);
           else if (ax < kSmall)
-            s[2] = fmaf(v[j] * kUp, v[j] * kUp, s[2]);
+            s[2] = fmaf(x * kUp, x * kUp, s[2]);
           else
-            s[1] = fmaf(v[j], v[j], s[1]);
+            s[1] = fmaf(x, x, s[1]);
         }
       });
     }
@@ -185,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (tid < 3) {
       float v = 0.f;
-      for (int i = 0; i < kThreads / 32; ++i) v += red[tid][i];
+      for (int i = 0; i < kWarps; ++i) v += red[tid][i];
       sums[tid] = v;
     }
     __syncthreads();
@@ -201,20 +243,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const float f1 = sc.f1, f2 = sc.f2, rho1 = sc.rho;
-  for_slice<T, V>(g, p, c0, w, [&](int r, int c, const float (&v)[V]) {
-    if (!tall && V == 8) {
+  for_slice<T>(g, total, p, mat, c0, w, [&](int line, int at, int len, const float (&v)[V]) {
+    if (!tall && V == 8 && (at & 7) == 0 && at + V <= len) {
       uint32_t u[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         u[j] = pack_half2(v[(2 * j) % V] * f1 * f2, v[(2 * j + 1) % V] * f1 * f2);
-      *reinterpret_cast<uint4*>(xs + chunk_at(r, c)) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
+      *reinterpret_cast<uint4*>(xs + chunk_at(line, at)) = make_uint4(u[0], u[1], u[2], u[3]);
+      return;
+    }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int rr = tall ? r + j : r, cc = tall ? c : c + j;
-        *reinterpret_cast<__half*>(xs + chunk_at(rr, cc & ~7) + (cc & 7) * 2) =
-            __float2half_rn(v[j] * f1 * f2);
-      }
+    for (int j = 0; j < V; ++j) {
+      if (at + j < 0 || at + j >= len) continue;
+      const int r = tall ? at + j : line, c = tall ? line : at + j;
+      *reinterpret_cast<__half*>(xs + chunk_at(r, c & ~7) + (c & 7) * 2) =
+          __float2half_rn(v[j] * f1 * f2);
     }
   });
 
@@ -235,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     parity ^= 1u;
     tc_fence_after();
   };
-  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+  const int q = warp & 3, sub = warp >> 2, row = q * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
 
   for (int step = 0; step < p.steps; ++step) {
@@ -252,29 +295,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     });
     const float alpha = rho * rho * (kScaleA / (kScaleX * kScaleX));
 #pragma unroll 1
-    for (int c = half * 64; c < half * 64 + 64; c += 16) {
-      uint32_t a[16];
-      tmem_ld16(lanes + c, a);
+    for (int c = sub * 32; c < 128; c += 32 * kParts) {
+      uint32_t a[2][16];
+      tmem_ld16(lanes + c, a[0]);
+      tmem_ld16(lanes + c + 16, a[1]);
       tmem_ld_wait();
       if (C == 1) {
-        uint32_t u[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          u[j] = pack_half2(alpha * __uint_as_float(a[2 * j]),
-                            alpha * __uint_as_float(a[2 * j + 1]));
-        *reinterpret_cast<uint4*>(as + chunk_at(row, c)) = make_uint4(u[0], u[1], u[2], u[3]);
-        *reinterpret_cast<uint4*>(as + chunk_at(row, c + 8)) = make_uint4(u[4], u[5], u[6], u[7]);
+        for (int i = 0; i < 4; ++i) {  // 8 columns
+          uint32_t u[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = 8 * i + 2 * j;
+            u[j] = pack_half2(alpha * __uint_as_float(a[k >> 4][k & 15]),
+                              alpha * __uint_as_float(a[k >> 4][(k & 15) + 1]));
+          }
+          *reinterpret_cast<uint4*>(as + chunk_at(row, c + 8 * i)) =
+              make_uint4(u[0], u[1], u[2], u[3]);
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = __uint_as_float(a[j]);
+        for (int j = 0; j < 32; ++j)
+          part[(c + j) * 128 + row] = __uint_as_float(a[j >> 4][j & 15]);
       }
       __syncwarp();
     }
     if (C > 1) {
       __syncthreads();
       cluster_sync();  // every CTA's part is in place; its copy of A is no longer read
-      // 8 columns at a time, dealt out to the cluster and to the warps' halves
-      for (int k = rank + half * C; k < 16; k += 2 * C) {
+      // 8 columns at a time, dealt out to the cluster and to a quarter's warps
+      for (int k = rank + sub * C; k < 16; k += kParts * C) {
         const uint32_t at = smem_u32(part) + (uint32_t)(k * 8 * 128 + row) * 4u;
         float v[8];
 #pragma unroll
@@ -314,31 +364,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     });
 #pragma unroll 1
-    for (int c = half * 64; c < half * 64 + 64; c += 16) {
-      uint32_t a[16];
-      tmem_ld16(lanes + 128 + c, a);
-      uint4 gm[2];
+    for (int c = sub * 32; c < 128; c += 32 * kParts) {
+      uint32_t a[2][16];
+      tmem_ld16(lanes + 128 + c, a[0]);
+      tmem_ld16(lanes + 128 + c + 16, a[1]);
+      uint4 gm[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 4; ++i)
         gm[i] = *reinterpret_cast<const uint4*>(as + chunk_at(row, c + 8 * i));
       tmem_ld_wait();
-      const uint32_t gw[8] = {gm[0].x, gm[0].y, gm[0].z, gm[0].w,
-                              gm[1].x, gm[1].y, gm[1].z, gm[1].w};
-      uint32_t u[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 ga = __half22float2(*reinterpret_cast<const __half2*>(&gw[j]));
-        float v[2];
+      for (int i = 0; i < 4; ++i) {  // 8 columns
+        const uint32_t gw[4] = {gm[i].x, gm[i].y, gm[i].z, gm[i].w};
+        uint32_t u[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          v[t] = fmaf(kB * (kScaleB / kScaleA), t ? ga.y : ga.x,
-                      kC * (kScaleB / (kScaleA * kScaleA)) * __uint_as_float(a[2 * j + t]));
-          if (row == c + 2 * j + t && row < p.m) v[t] += kA * kScaleB;
+        for (int j = 0; j < 4; ++j) {
+          const float2 ga = __half22float2(*reinterpret_cast<const __half2*>(&gw[j]));
+          const int k = 8 * i + 2 * j;
+          float v[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            v[t] = fmaf(kB * (kScaleB / kScaleA), t ? ga.y : ga.x,
+                        kC * (kScaleB / (kScaleA * kScaleA)) *
+                            __uint_as_float(a[k >> 4][(k & 15) + t]));
+            if (row == c + k + t && row < p.m) v[t] += kA * kScaleB;
+          }
+          u[j] = pack_half2(v[0], v[1]);
         }
-        u[j] = pack_half2(v[0], v[1]);
+        *reinterpret_cast<uint4*>(bs + chunk_at(row, c + 8 * i)) =
+            make_uint4(u[0], u[1], u[2], u[3]);
       }
-      *reinterpret_cast<uint4*>(bs + chunk_at(row, c)) = make_uint4(u[0], u[1], u[2], u[3]);
-      *reinterpret_cast<uint4*>(bs + chunk_at(row, c + 8)) = make_uint4(u[4], u[5], u[6], u[7]);
       __syncwarp();
     }
 
@@ -357,22 +412,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool last = step + 1 == p.steps;
     const float beta = last ? rho / (kScaleB * kScaleX) : rho / kScaleB;
 #pragma unroll 1
-    for (int c = half * 16; c < w; c += 32) {
-      uint32_t a[16];
-      tmem_ld16(lanes + c, a);
+    for (int c = sub * 32; c < w; c += 32 * kParts) {  // w is a multiple of 64
+      uint32_t a[2][16];
+      tmem_ld16(lanes + c, a[0]);
+      tmem_ld16(lanes + c + 16, a[1]);
       tmem_ld_wait();
-      float v[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = beta * __uint_as_float(a[j]);
-      if (!last) {
-        uint32_t u[8];
+      for (int h = 0; h < 2; ++h) {
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-        *reinterpret_cast<uint4*>(xs + chunk_at(row, c)) = make_uint4(u[0], u[1], u[2], u[3]);
-        *reinterpret_cast<uint4*>(xs + chunk_at(row, c + 8)) =
-            make_uint4(u[4], u[5], u[6], u[7]);
-      } else if (row < p.m) {
-        store_result<16>(p.out + (size_t)mat * p.m * p.n, p.m, p.n, tall, row, c0 + c, v);
+        for (int j = 0; j < 16; ++j) v[j] = beta * __uint_as_float(a[h][j]);
+        const int cc = c + 16 * h;
+        if (!last) {
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = pack_half2(v[2 * j], v[2 * j + 1]);
+          *reinterpret_cast<uint4*>(xs + chunk_at(row, cc)) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4*>(xs + chunk_at(row, cc + 8)) =
+              make_uint4(u[4], u[5], u[6], u[7]);
+        } else {  // A is done with: the warps' scratch
+          store_result(p.out + (size_t)mat * p.m * p.n, p.m, p.n, tall, q * 32, c0 + cc, v,
+                       reinterpret_cast<uint32_t*>(as) + warp * 32 * kRowWords);
+        }
       }
       __syncwarp();
     }
@@ -386,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the last accesses to a peer's shared memory lie before its last barrier
 }
 
-template <typename T, int V>
+template <typename T>
 cudaError_t launch(const T* g, const ChipArgs& p, int n_mats, cudaStream_t s) {
-  auto kern = ortho_chip_kernel<T, V>;
+  auto kern = ortho_chip_kernel<T>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -415,7 +476,7 @@ cudaError_t launch(const T* g, const ChipArgs& p, int n_mats, cudaStream_t s) {
   cfg.numAttrs = 2;
   ProfScope pr("ortho_chip", s);
   count_launch();
-  (void)cudaLaunchKernelEx(&cfg, kern, g, p);
+  (void)cudaLaunchKernelEx(&cfg, kern, g, (size_t)n_mats * p.rows * p.cols, p);
   return cudaGetLastError();
 }
 
@@ -436,21 +497,15 @@ cudaError_t launch_ortho_chip(const moe_ortho_desc& D, const void* g, void* out,
   p.eps = D.eps;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.err = flags;
-  // four blocks a CTA; up to eight in a CTA alone where the stack fills the GPU
+  // a CTA alone while X fits it (no exchange: about 5 us a step), else four
+  // blocks a CTA, or what eight CTAs need
   const int blocks = (p.n + 63) / 64;
-  p.cluster = (blocks + 3) / 4;
+  p.cluster = blocks <= kMaxBlocksAlone ? 1 : (blocks + 3) / 4;
   if (p.cluster > kMaxCluster) p.cluster = kMaxCluster;
-  if (blocks <= kMaxBlocksAlone && D.n_mats * p.cluster > num_sms()) p.cluster = 1;
   p.blocks = (blocks + p.cluster - 1) / p.cluster;
   p.cluster = (blocks + p.blocks - 1) / p.blocks;  // no CTA without columns
-  if (D.dtype == MOE_BF16) {
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(g);
-    return D.cols % 8 == 0 ? launch<__nv_bfloat16, 8>(x, p, D.n_mats, s)
-                           : launch<__nv_bfloat16, 1>(x, p, D.n_mats, s);
-  }
-  const float* x = static_cast<const float*>(g);
-  return D.cols % 4 == 0 ? launch<float, 4>(x, p, D.n_mats, s)
-                         : launch<float, 1>(x, p, D.n_mats, s);
+  return D.dtype == MOE_BF16 ? launch(static_cast<const __nv_bfloat16*>(g), p, D.n_mats, s)
+                             : launch(static_cast<const float*>(g), p, D.n_mats, s);
 }
 
 }  // namespace moe
