@@ -24,6 +24,17 @@
 // (rows of 64 columns of X, the reduction running down the rows), so no
 // transposed copy is written.
 //
+// Two steps at once.  With B0 the first step's B, A after it is B0 A B0, so that
+// two steps are X = (B1 B0) X with B1 = a I + b A1 + c A1 A1, A1 = (B0 A) B0: five
+// m x m products take the place of one product each of X X^T and of B X.  All
+// of them commute, so they are symmetric and one triangle is enough.  That is
+// fewer operations where n is well above m; measured, 4 x 7168 x 2048 bf16 1438
+// -> 1182 us, 16 x 1536 x 4096 2060 -> 1794 us.  Five steps run as 2 + 1 + 2: X is formed and rounded again before
+// errors of A (which sees the squares of the singular values) have grown; the
+// error of the result is that of five single steps within a few percent, while
+// all five on A alone lose what has small singular values (0.2 where the direct
+// form has 3e-3, singular values falling as 1/k).
+//
 // Matrices with m <= 128 and n up to a cluster's shared memory take one launch of
 // the kernel in ortho_chip.cu; what follows here serves the others.
 #include <cuda.h>
@@ -212,7 +223,8 @@ __global__ void __launch_bounds__(256)
 // rows of P, BN columns of the product, all of K).  The tiles that are left for
 // the last round of the pairs are cut along their columns into as many parts as
 // keep every pair to one unit.
-//   kGram : A  = X X^T, from P = Q = X             -> out, both triangles
+//   kGram : alpha P Q^T, symmetric: A = X X^T, or a product of two of the
+//           m x m matrices                         -> out, both triangles
 //   kPoly : B  = a I + b A + c A A, P = Q = A      -> out, both triangles
 //   kApply: X' = B X, P = B, Q = X (MN-major)      -> out
 //   kLast : the same                               -> result in bf16
@@ -224,6 +236,7 @@ struct Product {
   int rowsP, rowsQ;  // padded rows and columns of a product: multiples of 64
   int m, n;          // the matrices' own size
   int first;         // X is the first one: apply rho
+  float alpha;       // kGram, kApply, kLast: factor of the accumulators
   int whole, cut;    // SM pairs: units that are whole tiles; the rest are cut into `cut` parts
   const Scale* scales;
   __half* out;             // [n_mats * rowsP, rowsQ]
@@ -280,10 +293,9 @@ struct Tiles {
 template <int OP>
 __device__ __forceinline__ float product_scale(const Product& p, int mat) {
   const float rho = p.first ? p.scales[mat].rho : 1.f;
-  return OP == kGram    ? rho * rho * (kScaleA / (kScaleX * kScaleX))
-         : OP == kPoly  ? kC * (kScaleB / (kScaleA * kScaleA))
-         : OP == kApply ? rho / kScaleB
-                        : rho / (kScaleB * kScaleX);
+  return OP == kPoly   ? kC * (kScaleB / (kScaleA * kScaleA))
+         : OP == kGram ? rho * rho * p.alpha
+                       : rho * p.alpha;
 }
 
 // kPoly: W columns (8 or 16) of A, to be loaded ahead of their use; other kinds
@@ -864,28 +876,48 @@ cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Produ
 // Measured, us a call: 4 x 512 x 512 98 pairs, 74 small; 2 x 1536 x 4096 340
 // pairs, 516 small; 1 x 512 x 2048 90 with the reductions of 2048 over two
 // CTAs, 84 over four; 1 x 1024 x 1024 130 with 1024 over two, 100 unshared.
+struct Choice {
+  long long cost;         // 10 ns
+  long long large, small; // tiles of each kind
+  int split;              // small tiles: CTAs a tile; 0: SM pairs
+};
+
 template <int OP>
-cudaError_t product(const OperandMaps& P, const OperandMaps& Q, const Product& p,
-                    cudaStream_t s) {
+Choice choose(int n_mats, int K, int rowsP, int rowsQ) {
   constexpr bool SYM = OP == kGram || OP == kPoly;
-  const long long n = p.n_mats, sms = num_sms(), blocks = p.K / 64;
-  const long long large = n * Tiles<256, 256, SYM>(p.rowsP, p.rowsQ).count();
-  const long long small = n * Tiles<128, kSmallN, SYM>(p.rowsP, p.rowsQ).count();
-  const long long pair_cost = (large + sms / 2 - 1) / (sms / 2) * blocks * 27 + 550;
-  long long least = 0;
-  int split = 0;
+  const long long n = n_mats, sms = num_sms(), blocks = K / 64;
+  Choice c{};
+  c.large = n * Tiles<256, 256, SYM>(rowsP, rowsQ).count();
+  c.small = n * Tiles<128, kSmallN, SYM>(rowsP, rowsQ).count();
+  c.cost = (c.large + sms / 2 - 1) / (sms / 2) * blocks * 27 + 550;
   const int most = OP == kLast ? kMaxSplit / 2 : kMaxSplit;  // 16 columns a CTA at least
   for (int k = 1; k <= most && k <= blocks; k *= 2) {
     const long long each = 125 + 17 * ((blocks + k - 1) / k);
-    const long long tiles = small * k > sms ? small * k : sms;
+    const long long tiles = c.small * k > sms ? c.small * k : sms;
     const long long cost = 125 + each * tiles / sms + (k > 1 ? 400 : 0);
-    if (split == 0 || cost < least) {
-      least = cost;
-      split = k;
+    if (cost < c.cost) {
+      c.cost = cost;
+      c.split = k;
     }
   }
-  return least < pair_cost ? launch_small<OP>(P, Q, p, small, split, s)
-                           : launch_pairs<OP>(P, Q, p, large, s);
+  return c;
+}
+
+template <int OP>
+cudaError_t product(const OperandMaps& P, const OperandMaps& Q, const Product& p,
+                    cudaStream_t s) {
+  const Choice c = choose<OP>(p.n_mats, p.K, p.rowsP, p.rowsQ);
+  return c.split ? launch_small<OP>(P, Q, p, c.small, c.split, s)
+                 : launch_pairs<OP>(P, Q, p, c.large, s);
+}
+
+// Whether two steps at once take less time than one after the other, by a
+// tenth at least (they are one launch more).
+bool pair_steps(int n_mats, int mp, int np) {
+  const long long gram = choose<kGram>(n_mats, np, mp, mp).cost;
+  const long long square = choose<kPoly>(n_mats, mp, mp, mp).cost;
+  const long long apply = choose<kApply>(n_mats, mp, mp, np).cost;
+  return 11 * 5 * square < 10 * (gram + 2 * square + apply);
 }
 
 int sum_blocks(size_t per_mat) {
@@ -941,6 +973,7 @@ OrthoLayout ortho_layout(const moe_ortho_desc& D) {
   for (size_t& o : L.x) o = take(n * L.mp * L.np * 2);
   L.gram = take(n * L.mp * L.mp * 2);
   L.poly = take(n * L.mp * L.mp * 2);
+  if (pair_steps(D.n_mats, L.mp, L.np)) L.mul = take(n * L.mp * L.mp * 2);
   L.total = 512 + off;  // the flags' 16 bytes, then the regions at the next multiple of 256
   return L;
 }
@@ -958,6 +991,7 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   __half* x[2] = {reinterpret_cast<__half*>(b + L.x[0]), reinterpret_cast<__half*>(b + L.x[1])};
   __half* gram = reinterpret_cast<__half*>(b + L.gram);
   __half* poly = reinterpret_cast<__half*>(b + L.poly);
+  __half* mul = reinterpret_cast<__half*>(b + L.mul);
   cudaError_t e = D.dtype == MOE_BF16
                       ? start(D, static_cast<const __nv_bfloat16*>(g), L, partial, scales, flags,
                               x[0], s)
@@ -971,24 +1005,55 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   p.err = flags;
   p.tall = D.rows > D.cols;
   p.result = static_cast<__nv_bfloat16*>(out);
-  OperandMaps mx[2], mg, mb;
+  OperandMaps mx[2], mg, mb, mq;
   const long long rows = (long long)D.n_mats * L.mp;
   if (!make_maps(&mx[0], x[0], L.np, rows) || !make_maps(&mx[1], x[1], L.np, rows) ||
-      !make_maps(&mg, gram, L.mp, rows) || !make_maps(&mb, poly, L.mp, rows))
+      !make_maps(&mg, gram, L.mp, rows) || !make_maps(&mb, poly, L.mp, rows) ||
+      !make_maps(&mq, mul, L.mp, rows))
     return cudaErrorInvalidValue;
-  for (int i = 0; i < D.steps; ++i) {
-    p.first = i == 0;
+  // alpha P Q of m x m matrices
+  auto square = [&](const OperandMaps& P, const OperandMaps& Q, __half* to, float alpha) {
+    p.K = p.rowsP = p.rowsQ = L.mp;
+    p.out = to, p.alpha = alpha;
+    return product<kGram>(P, Q, p, s);
+  };
+  const bool pairs = pair_steps(D.n_mats, L.mp, L.np);
+  int at = 0;  // which x holds X
+  bool paired = false;
+  for (int left = D.steps; left > 0;) {
+    paired = pairs && !paired && left >= 2;
+    p.first = left == D.steps;
+    left -= paired ? 2 : 1;
     p.K = L.np, p.rowsP = p.rowsQ = L.mp;
-    p.out = gram;
-    if ((e = product<kGram>(mx[i & 1], mx[i & 1], p, s)) != cudaSuccess) return e;
+    p.out = gram, p.alpha = kScaleA / (kScaleX * kScaleX);
+    if ((e = product<kGram>(mx[at], mx[at], p, s)) != cudaSuccess) return e;
+    const bool scaled = p.first;
+    p.first = 0;
     p.K = L.mp;
     p.gram = gram, p.out = poly;
     if ((e = product<kPoly>(mg, mg, p, s)) != cudaSuccess) return e;
-    p.rowsQ = L.np;
-    p.out = x[(i + 1) & 1];
-    e = i + 1 < D.steps ? product<kApply>(mb, mx[i & 1], p, s)
-                        : product<kLast>(mb, mx[i & 1], p, s);
+    if (paired) {
+      if ((e = square(mb, mg, mul, kScaleM / (kScaleB * kScaleA))) != cudaSuccess ||  // B0 A
+          (e = square(mq, mb, gram, kScaleA / (kScaleM * kScaleB))) != cudaSuccess)   // A1
+        return e;
+      p.out = mul;
+      if ((e = product<kPoly>(mg, mg, p, s)) != cudaSuccess ||                        // B1
+          (e = square(mq, mb, gram, kScaleQ / (kScaleB * kScaleB))) != cudaSuccess)   // B1 B0
+        return e;
+    }
+    p.first = scaled;
+    p.K = p.rowsP = L.mp, p.rowsQ = L.np;
+    p.out = x[at ^ 1];
+    p.alpha = 1.f / (paired ? kScaleQ : kScaleB);
+    const OperandMaps& by = paired ? mg : mb;
+    if (left > 0) {
+      e = product<kApply>(by, mx[at], p, s);
+    } else {
+      p.alpha /= kScaleX;
+      e = product<kLast>(by, mx[at], p, s);
+    }
     if (e != cudaSuccess) return e;
+    at ^= 1;
   }
   return cudaSuccess;
 }

@@ -13,6 +13,8 @@ namespace ortho {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 1024.f, kScaleA = 16384.f, kScaleB = 4096.f;
+// Two steps at once: of B0 A (up to 1.1) and B1 B0 (up to 3.45^2).
+constexpr float kScaleM = 8192.f, kScaleQ = 1024.f;
 
 struct Scale {
   float f1, f2;  // X = g * f1 * f2, powers of two (one factor could leave fp32's range)
