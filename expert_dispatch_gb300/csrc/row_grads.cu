@@ -56,6 +56,8 @@ __device__ __forceinline__ void store8(void* base, size_t at, const float (&v)[8
   }
 }
 
+constexpr int kSlotsAtOnce = 4;
+
 // Block (token t, 1024-column slice); each thread owns 8 consecutive columns.
 template <bool BF16>
 __global__ void __launch_bounds__(128)
@@ -74,24 +76,33 @@ __global__ void __launch_bounds__(128)
   const int c = blockIdx.y * 1024 + threadIdx.x * 8;
   if (c >= d) return;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < ks; ++j) {
-    const int r = rows_s[j];
-    if (r < 0) continue;
-    float v[8];
-    load8<BF16>(dx_perm, (size_t)r * d + c, v);
+  for (int j0 = 0; j0 < ks; j0 += kSlotsAtOnce) {  // that many slots' loads in flight
+    float v[kSlotsAtOnce][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    for (int u = 0; u < kSlotsAtOnce; ++u) {
+      const int r = j0 + u < ks ? rows_s[j0 + u] : -1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+      if (r >= 0) load8<BF16>(dx_perm, (size_t)r * d + c, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kSlotsAtOnce; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += v[u][i];
   }
   store8<BF16>(dx, (size_t)t * d + c, acc);
 }
 
-// Block per token: for each slot, the row's gradient is written and the dot
-// product with dy[t] summed over the block.  The rows from *total_rows to P
-// that dropped slots leave over are set to zero, each block taking every
-// gridDim.x-th of them.
+// Block per token (256 threads: 353 us at 16384 tokens x 4096 x 8 slots bf16, 6.8
+// TB/s; 128: 384, 512: 417): slot by slot, a thread writes its columns of the row's gradient
+// and adds its part of the dot product with dy[t] (which stays in L1); the warps'
+// sums of all slots meet in shared memory once, at the end.  The rows from
+// *total_rows to P that dropped slots leave over are set to zero, each block
+// taking every gridDim.x-th of them.
 constexpr int kCombineBwdThreads = 256;
+constexpr int kCombineBwdWarps = kCombineBwdThreads / 32;
 
-template <bool BF16>
+template <bool BF16, bool WITH_DW>
 __global__ void __launch_bounds__(kCombineBwdThreads)
     combine_backward_kernel(const float* __restrict__ dy, const void* __restrict__ y_perm,
                             const int32_t* __restrict__ total_rows,
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
   pdl_trigger();
   __shared__ int rows_s[kMaxSlots];
   __shared__ float w_s[kMaxSlots];
-  __shared__ float red[2][kCombineBwdThreads / 32];
+  __shared__ float red[kMaxSlots][kCombineBwdWarps];
   const int t = blockIdx.x, tid = threadIdx.x;
   const int total = min(max(*total_rows, 0), P);
   if (tid < ks) {
@@ -119,7 +130,7 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
       for (int c = tid * 8; c < d; c += kCombineBwdThreads * 8) {
         float g[8], o[8];
         load8<false>(dy, (size_t)t * d + c, g);
-        if (dtopk_w && j < k) {
+        if (WITH_DW && j < k) {
           float v[8];
           load8<BF16>(y_perm, (size_t)r * d + c, v);
 #pragma unroll
@@ -130,16 +141,19 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
         store8<BF16>(dy_perm, (size_t)r * d + c, o);
       }
     }
-    if (dtopk_w && j < k) {
+    if (WITH_DW && j < k) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if ((tid & 31) == 0) red[j & 1][tid >> 5] = dot;
-      __syncthreads();
-      if (tid == 0) {
-        float s = 0.f;
-        for (int i = 0; i < kCombineBwdThreads / 32; ++i) s += red[j & 1][i];
-        dtopk_w[(size_t)t * k + j] = s;
-      }
+      if ((tid & 31) == 0) red[j][tid >> 5] = dot;
+    }
+  }
+  if (WITH_DW) {
+    __syncthreads();
+    if (tid < k) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCombineBwdWarps; ++i) s += red[tid][i];
+      dtopk_w[(size_t)t * k + tid] = s;
     }
   }
   const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -168,9 +182,11 @@ cudaError_t launch_combine_backward(int dtype, const float* dy, const void* y_pe
                                     void* dy_perm, float* dtopk_w, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   ProfScope pr("combine_backward", s);
-  (void)launch_kernel(dtype == MOE_BF16 ? combine_backward_kernel<true>
-                                        : combine_backward_kernel<false>,
-                      T, kCombineBwdThreads, 0, s, dy, y_perm, total_rows, slot_row, topk_w, d, k,
+  auto kern = dtype == MOE_BF16 ? (dtopk_w ? combine_backward_kernel<true, true>
+                                           : combine_backward_kernel<true, false>)
+                                : (dtopk_w ? combine_backward_kernel<false, true>
+                                           : combine_backward_kernel<false, false>);
+  (void)launch_kernel(kern, T, kCombineBwdThreads, 0, s, dy, y_perm, total_rows, slot_row, topk_w, d, k,
                       k + S, T * (k + S), dy_perm, dtopk_w);
   return cudaGetLastError();
 }
