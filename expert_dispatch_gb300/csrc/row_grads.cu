@@ -56,11 +56,17 @@ __device__ __forceinline__ void store8(void* base, size_t at, const float (&v)[8
   }
 }
 
-constexpr int kSlotsAtOnce = 4;
+// Most slots whose loads are in flight, and threads a block: 85 us at 4096 tokens
+// x 7168 x 9 slots bf16 (6.9 TB/s); 3 or 9 slots and 256 threads take 87 to 89,
+// a block for each 1024 columns of a token 93.
+constexpr int kSlotsAtOnce = 5;
+constexpr int kDispatchBwdThreads = 128;
+constexpr int kDispatchBwdBlocks = 1216;  // blocks that keep the GPU busy
 
-// Block (token t, 1024-column slice); each thread owns 8 consecutive columns.
+// Block (token t, slice of 1024-column steps): a slice is the whole row where
+// there are tokens enough; each thread owns 8 consecutive columns of a step.
 template <bool BF16>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kDispatchBwdThreads)
     dispatch_rows_backward_kernel(const void* __restrict__ dx_perm,
                                   const int32_t* __restrict__ slot_row, int d, int ks, int P,
                                   void* __restrict__ dx) {
@@ -73,32 +79,35 @@ __global__ void __launch_bounds__(128)
     rows_s[threadIdx.x] = (r < 0 || r >= P) ? -1 : r;
   }
   __syncthreads();
-  const int c = blockIdx.y * 1024 + threadIdx.x * 8;
-  if (c >= d) return;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 < ks; j0 += kSlotsAtOnce) {  // that many slots' loads in flight
-    float v[kSlotsAtOnce][8];
+  // rounds of about equal size: a last one of a single slot would wait for HBM alone
+  const int rounds = (ks + kSlotsAtOnce - 1) / kSlotsAtOnce, per = (ks + rounds - 1) / rounds;
+  for (int c = (blockIdx.y * kDispatchBwdThreads + threadIdx.x) * 8; c < d;
+       c += gridDim.y * kDispatchBwdThreads * 8) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < ks; j0 += per) {
+      float v[kSlotsAtOnce][8];
 #pragma unroll
-    for (int u = 0; u < kSlotsAtOnce; ++u) {
-      const int r = j0 + u < ks ? rows_s[j0 + u] : -1;
+      for (int u = 0; u < kSlotsAtOnce; ++u) {
+        const int r = u < per && j0 + u < ks ? rows_s[j0 + u] : -1;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-      if (r >= 0) load8<BF16>(dx_perm, (size_t)r * d + c, v[u]);
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        if (r >= 0) load8<BF16>(dx_perm, (size_t)r * d + c, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kSlotsAtOnce; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += v[u][i];
     }
-#pragma unroll
-    for (int u = 0; u < kSlotsAtOnce; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += v[u][i];
+    store8<BF16>(dx, (size_t)t * d + c, acc);
   }
-  store8<BF16>(dx, (size_t)t * d + c, acc);
 }
 
 // Block per token (256 threads: 353 us at 16384 tokens x 4096 x 8 slots bf16, 6.8
-// TB/s; 128: 384, 512: 417): slot by slot, a thread writes its columns of the row's gradient
-// and adds its part of the dot product with dy[t] (which stays in L1); the warps'
-// sums of all slots meet in shared memory once, at the end.  The rows from
-// *total_rows to P that dropped slots leave over are set to zero, each block
-// taking every gridDim.x-th of them.
+// TB/s; 128: 384, 512: 417): slot by slot, a thread writes its columns of the
+// row's gradient and adds its part of the dot product with dy[t] (which stays in
+// L1; held in registers instead, 423); the warps' sums of all slots meet in
+// shared memory once, at the end.  The rows from *total_rows to P that dropped
+// slots leave over are set to zero, each block taking every gridDim.x-th of them.
 constexpr int kCombineBwdThreads = 256;
 constexpr int kCombineBwdWarps = kCombineBwdThreads / 32;
 
@@ -169,10 +178,12 @@ cudaError_t launch_dispatch_rows_backward(int dtype, const void* dx_perm,
                                           void* dx, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   ProfScope pr("dispatch_rows_backward", s);
-  const dim3 grid(T, (d + 1023) / 1024);
+  const int steps = (d + kDispatchBwdThreads * 8 - 1) / (kDispatchBwdThreads * 8);
+  const int want = (kDispatchBwdBlocks + T - 1) / T;
+  const int slices = want < steps ? want : steps;
   (void)launch_kernel(dtype == MOE_BF16 ? dispatch_rows_backward_kernel<true>
                                         : dispatch_rows_backward_kernel<false>,
-                      grid, 128, 0, s, dx_perm, slot_row, d, ks, T * ks, dx);
+                      dim3(T, slices), kDispatchBwdThreads, 0, s, dx_perm, slot_row, d, ks, T * ks, dx);
   return cudaGetLastError();
 }
 
