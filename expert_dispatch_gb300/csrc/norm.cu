@@ -298,12 +298,12 @@ struct Ring {
 
 // ---------------------------------------------------------------- forward
 // blockDim.x = groups * warps * 32; group g of block b takes the rows
-// b * groups + g, + gridDim.x * groups, ...  With RING they come through a ring
-// and the grid is what fits on the GPU at once; without, each group has one row
-// (of odd length, or one of few: a ring has nothing to run ahead of).  A thread
-// owns the same columns of every row and keeps their gamma and beta.
+// b * groups + g, + gridDim.x * groups, ...; the grid is at most what fits on the
+// GPU at once.  With RING they come through a ring; rows of odd length, and few
+// rows (a ring has nothing to run ahead of), are loaded where they are used.  A
+// thread owns the same columns of every row and keeps their gamma and beta.
 template <typename T, int VEC, int VPT, bool RMS, bool RING, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
     norm_forward_kernel(const T* x, const void* gamma, const void* beta, bool w_bf16, int rows,
                         int d, int warps, int stages, float eps, T* y, float* mean,
                         float* rstd) {
@@ -690,14 +690,15 @@ cudaError_t launch_forward(const moe_norm_desc& D, const Shape& s, const void* x
   const int threads = s.groups * s.warps * 32;
   const size_t stage = (size_t)s.groups * D.d * sizeof(T);
   int blocks = (D.T + s.groups - 1) / s.groups, stages = 0;
+  // what the registers allow at once: layer norm keeps beta too
+  const int per_sm = threads <= 256 ? (RMS ? 4 : 2) : threads <= 512 && RMS ? 2 : 1;
   if (RING) {
     static std::atomic<bool> configured[64] = {};
     const cudaError_t e = allow_smem(kern, kFwdRingBytes, configured);
     if (e != cudaSuccess) return e;
-    const int per_sm = threads <= 256 ? 4 : threads <= 512 ? 2 : 1;
     stages = ring_stages(kFwdRingBytes / per_sm, stage);
-    if (blocks > per_sm * num_sms()) blocks = per_sm * num_sms();
   }
+  if (blocks > per_sm * num_sms()) blocks = per_sm * num_sms();
   (void)launch_kernel(kern, blocks, threads, stages * stage, st, static_cast<const T*>(x), gamma,
                       beta, D.wdtype == MOE_BF16, D.T, D.d, s.warps, stages, D.eps,
                       static_cast<T*>(y), mean, rstd);

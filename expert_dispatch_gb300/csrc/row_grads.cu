@@ -11,6 +11,8 @@
 // there are no atomics and the results do not depend on any order of blocks.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -102,16 +104,20 @@ __global__ void __launch_bounds__(kDispatchBwdThreads)
   }
 }
 
-// Block per token (256 threads: 353 us at 16384 tokens x 4096 x 8 slots bf16, 6.8
-// TB/s; 128: 384, 512: 417): slot by slot, a thread writes its columns of the
-// row's gradient and adds its part of the dot product with dy[t] (which stays in
-// L1; held in registers instead, 423); the warps' sums of all slots meet in
-// shared memory once, at the end.  The rows from *total_rows to P that dropped
-// slots leave over are set to zero, each block taking every gridDim.x-th of them.
+// Block (token, share of its slots): all slots where there are tokens enough
+// (dy[t] then crosses HBM once), else one, as a chain of slots costs an HBM latency
+// each.  Up to 256 threads, fewer for short rows.  Slot by slot, a thread writes
+// its columns of the row's gradient and adds its part of the dot product with
+// dy[t]; the warps' sums of all slots meet in shared memory once, at the end.
+// Measured at 16384 tokens x 4096 x 8 slots bf16: 353 us, 6.8 TB/s; with 128
+// threads 384, with 512 417, with dy[t] in registers (it stays in L1 as it is) 423.
+// The rows from *total_rows to P that dropped slots leave over are set to zero,
+// each token's first block taking every gridDim.x-th of them.
 constexpr int kCombineBwdThreads = 256;
 constexpr int kCombineBwdWarps = kCombineBwdThreads / 32;
+constexpr int kCombineBwdTokens = 608;  // tokens that keep the GPU busy with a block each
 
-template <bool BF16, bool WITH_DW>
+template <bool BF16, bool WITH_DW, bool ALL>
 __global__ void __launch_bounds__(kCombineBwdThreads)
     combine_backward_kernel(const float* __restrict__ dy, const void* __restrict__ y_perm,
                             const int32_t* __restrict__ total_rows,
@@ -124,19 +130,26 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
   __shared__ float w_s[kMaxSlots];
   __shared__ float red[kMaxSlots][kCombineBwdWarps];
   const int t = blockIdx.x, tid = threadIdx.x;
+  const int threads = ALL ? kCombineBwdThreads : blockDim.x;
+  const int first = ALL ? 0 : blockIdx.y, step = ALL ? 1 : gridDim.y;
   const int total = min(max(*total_rows, 0), P);
-  if (tid < ks) {
-    const int r = slot_row[(size_t)t * ks + tid];
-    rows_s[tid] = (r < 0 || r >= total) ? -1 : r;
-    w_s[tid] = (tid < k && topk_w) ? topk_w[(size_t)t * k + tid] : 1.f;
+  auto slot = [&](int j) {
+    const int r = slot_row[(size_t)t * ks + j];
+    rows_s[j] = (r < 0 || r >= total) ? -1 : r;
+    w_s[j] = (j < k && topk_w) ? topk_w[(size_t)t * k + j] : 1.f;
+  };
+  if constexpr (ALL) {
+    if (tid < ks) slot(tid);
+  } else {
+    for (int j = tid; j < ks; j += threads) slot(j);
   }
   __syncthreads();
-  for (int j = 0; j < ks; ++j) {
+  for (int j = first; j < ks; j += step) {
     const int r = rows_s[j];
     float dot = 0.f;
     if (r >= 0) {
       const float w = w_s[j];
-      for (int c = tid * 8; c < d; c += kCombineBwdThreads * 8) {
+      for (int c = tid * 8; c < d; c += threads * 8) {
         float g[8], o[8];
         load8<false>(dy, (size_t)t * d + c, g);
         if (WITH_DW && j < k) {
@@ -158,16 +171,25 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
   }
   if (WITH_DW) {
     __syncthreads();
-    if (tid < k) {
-      float s = 0.f;
+    if constexpr (ALL) {
+      if (tid < k) {
+        float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kCombineBwdWarps; ++i) s += red[tid][i];
-      dtopk_w[(size_t)t * k + tid] = s;
+        for (int i = 0; i < kCombineBwdWarps; ++i) s += red[tid][i];
+        dtopk_w[(size_t)t * k + tid] = s;
+      }
+    } else {
+      for (int j = first + step * tid; j < k; j += step * threads) {
+        float s = 0.f;
+        for (int i = 0; i < threads / 32; ++i) s += red[j][i];
+        dtopk_w[(size_t)t * k + j] = s;
+      }
     }
   }
+  if (first) return;
   const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (long long r = (long long)total + t; r < P; r += gridDim.x)
-    for (int c = tid * 8; c < d; c += kCombineBwdThreads * 8)
+    for (int c = tid * 8; c < d; c += threads * 8)
       store8<BF16>(dy_perm, (size_t)r * d + c, zero);
 }
 
@@ -193,12 +215,21 @@ cudaError_t launch_combine_backward(int dtype, const float* dy, const void* y_pe
                                     void* dy_perm, float* dtopk_w, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   ProfScope pr("combine_backward", s);
-  auto kern = dtype == MOE_BF16 ? (dtopk_w ? combine_backward_kernel<true, true>
-                                           : combine_backward_kernel<true, false>)
-                                : (dtopk_w ? combine_backward_kernel<false, true>
-                                           : combine_backward_kernel<false, false>);
-  (void)launch_kernel(kern, T, kCombineBwdThreads, 0, s, dy, y_perm, total_rows, slot_row, topk_w, d, k,
-                      k + S, T * (k + S), dy_perm, dtopk_w);
+  const int ks = k + S, columns = (d / 8 + 31) / 32 * 32;
+  const int threads = columns < kCombineBwdThreads ? columns : kCombineBwdThreads;
+  const bool all = threads == kCombineBwdThreads && T >= kCombineBwdTokens;
+  auto of = [&](auto bf16, auto dw) {
+    constexpr bool B = decltype(bf16)::value, W = decltype(dw)::value;
+    return all ? combine_backward_kernel<B, W, true> : combine_backward_kernel<B, W, false>;
+  };
+  using std::bool_constant;
+  auto kern = dtype == MOE_BF16
+                  ? (dtopk_w ? of(bool_constant<true>(), bool_constant<true>())
+                             : of(bool_constant<true>(), bool_constant<false>()))
+                  : (dtopk_w ? of(bool_constant<false>(), bool_constant<true>())
+                             : of(bool_constant<false>(), bool_constant<false>()));
+  (void)launch_kernel(kern, dim3(T, T < kCombineBwdTokens ? ks : 1), threads, 0, s, dy, y_perm, total_rows, slot_row, topk_w, d, k, ks,
+                      T * ks, dy_perm, dtopk_w);
   return cudaGetLastError();
 }
 
