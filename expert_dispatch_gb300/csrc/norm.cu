@@ -265,12 +265,18 @@ struct Ring {
     for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8u * s, 1);
     fence_barrier_init();
   }
-  // by one thread of the group: the row at a (and at b) into stage s
+  // by one thread of the group: the rows at a and b into stage s
   __device__ __forceinline__ void request(int s, const void* a, const void* b) const {
     const uint32_t dst = smem_u32(base) + (uint32_t)(s * streams) * row_bytes;
-    mbar_arrive_expect_tx(bar0 + 8u * s, (uint32_t)streams * row_bytes);
+    mbar_arrive_expect_tx(bar0 + 8u * s, 2u * row_bytes);
     bulk_load(dst, a, row_bytes, bar0 + 8u * s);
-    if (b) bulk_load(dst + row_bytes, b, row_bytes, bar0 + 8u * s);
+    bulk_load(dst + row_bytes, b, row_bytes, bar0 + 8u * s);
+  }
+  // the same: n consecutive rows at a
+  __device__ __forceinline__ void request_rows(int s, const void* a, int n) const {
+    const uint32_t dst = smem_u32(base) + (uint32_t)(s * streams) * row_bytes;
+    mbar_arrive_expect_tx(bar0 + 8u * s, (uint32_t)n * row_bytes);
+    bulk_load(dst, a, (uint32_t)n * row_bytes, bar0 + 8u * s);
   }
   __device__ __forceinline__ bool wait() const {
     return mbar_wait(bar0 + 8u * stage, parity, gave_up, nullptr);
@@ -297,11 +303,23 @@ struct Ring {
 };
 
 // ---------------------------------------------------------------- forward
-// blockDim.x = groups * warps * 32; group g of block b takes the rows
-// b * groups + g, + gridDim.x * groups, ...; the grid is at most what fits on the
-// GPU at once.  With RING they come through a ring; rows of odd length, and few
-// rows (a ring has nothing to run ahead of), are loaded where they are used.  A
-// thread owns the same columns of every row and keeps their gamma and beta.
+// blockDim.x = groups * warps * 32; group g of block b takes R consecutive rows at
+// a time, the (b * groups + g)-th R, + gridDim.x * groups, ...; the grid is at
+// most what fits on the GPU at once.  With RING they come through a ring; rows of
+// odd length, and few rows (a ring has nothing to run ahead of), are loaded where
+// they are used.  A thread owns the same columns of every row and keeps their
+// gamma and beta.
+//
+// Rows at a time.  A layer norm's bf16 rows are bound by the instructions that a
+// row costs beside its elements (two sums with their barriers, the loop), so they
+// are taken in twos: 16384 x 2048 31.5 -> 26.7 us, 8192 x 8192 65.5 -> 51.2. An RMS
+// norm (one sum; 4096 x 7168 20.3 us alone, 21.6 in twos) and fp32 rows (8192 x 4096
+// 44.0 and 48.2) gain more from the blocks that the registers then allow.
+template <typename T, bool RMS, bool RING, int THREADS>
+__host__ __device__ constexpr int forward_rows() {
+  return RING && !RMS && sizeof(T) == 2 && THREADS == 512 ? 2 : 1;
+}
+
 template <typename T, int VEC, int VPT, bool RMS, bool RING, int THREADS>
 __global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
     norm_forward_kernel(const T* x, const void* gamma, const void* beta, bool w_bf16, int rows,
@@ -310,23 +328,23 @@ __global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ alignas(16) float red[8][2 * kMaxGroupWarps];
+  __shared__ alignas(16) float red[8][4 * kMaxGroupWarps];
   __shared__ __align__(8) uint64_t bars[8][kMaxStages];
   __shared__ int gave_up;
-  constexpr int N = VPT * VEC;
+  constexpr int N = VPT * VEC, R = forward_rows<T, RMS, RING, THREADS>();
   const int gt = warps * 32, groups = blockDim.x / gt;
   const int group = threadIdx.x / gt, tid = threadIdx.x - group * gt;
-  const int step = gridDim.x * groups;
+  const int step = gridDim.x * groups * R;
   const int nv = d / VEC;
-  int row = blockIdx.x * groups + group;
-  Ring ring(dyn, bars[group], &gave_up, group, 1, stages, (uint32_t)d * sizeof(T));
+  int row = (blockIdx.x * groups + group) * R;
+  Ring ring(dyn, bars[group], &gave_up, group, R, stages, (uint32_t)d * sizeof(T));
   if constexpr (RING) {
     if (threadIdx.x == 0) gave_up = 0;
     if (tid == 0) ring.init();
     __syncthreads();
     if (tid == 0)
       for (int s = 0; s < stages && row + s * step < rows; ++s)
-        ring.request(s, x + (size_t)(row + s * step) * d, nullptr);
+        ring.request_rows(s, x + (size_t)(row + s * step) * d, min(R, rows - row - s * step));
   }
   F2 g[N / 2], b[RMS ? 1 : N / 2];
   auto params = [&](const void* p, float otherwise, F2* out) {
@@ -348,84 +366,94 @@ __global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
   float* buf = red[warps == 1 ? 0 : group];
   for (; row < rows; row += step) {  // the same rows for a whole group
     bool ok = true;
-    Raw<T, VEC> raw[VPT];  // the row as it was read, zero beyond its end
+    const int have = min(R, rows - row);
     const T* xr = x + (size_t)row * d;
     if constexpr (RING) {
       ok = ring.wait();
       xr = reinterpret_cast<const T*>(ring.rows());
     }
+    F2 v[R][N / 2];  // zero beyond a row's end
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      raw[i] = Raw<T, VEC>{};
-      if (tid + i * gt < nv) raw[i] = load_raw<T, VEC>(xr + (size_t)(tid + i * gt) * VEC);
+    for (int q = 0; q < R; ++q) {
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        Raw<T, VEC> raw{};
+        if (tid + i * gt < nv && q < have)
+          raw = load_raw<T, VEC>(xr + (size_t)q * d + (size_t)(tid + i * gt) * VEC);
+        unpack<T, VEC>(raw, f + i * VEC);
+      }
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) v[q][k] = f2(f[2 * k], f[2 * k + 1]);
     }
     if constexpr (RING) {
       fence_proxy_async_shared();  // before the barrier that hands the stage back
       if (warps == 1) __syncwarp();
     }
-    F2 v[N / 2];
-    {
-      float f[N];
+    float s[R];
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) unpack<T, VEC>(raw[i], f + i * VEC);
+    for (int q = 0; q < R; ++q) {
+      F2 acc = f2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) v[k] = f2(f[2 * k], f[2 * k + 1]);
+      for (int k = 0; k < N / 2; ++k) acc = RMS ? fma2(v[q][k], v[q][k], acc) : add2(v[q][k], acc);
+      s[q] = both(acc);
     }
-    F2 acc = f2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) acc = RMS ? fma2(v[k], v[k], acc) : add2(v[k], acc);
-    float s[1] = {both(acc)};
-    group_sum<1>(s, warps, tid >> 5, group, buf, turn);
+    group_sum<R>(s, warps, tid >> 5, group, buf, turn);
     if constexpr (RING) {
       if (tid == 0 && row + (long long)stages * step < rows && ring.open())
-        ring.request(ring.stage, x + (size_t)(row + stages * step) * d, nullptr);
+        ring.request_rows(ring.stage, x + (size_t)(row + stages * step) * d,
+                          min(R, rows - row - stages * step));
       ring.next();
     }
-    float mu = 0.f;
+    float mu[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) mu[q] = 0.f;
     if constexpr (!RMS) {
-      mu = s[0] * inv_d;
-      const F2 m = f2(-mu, -mu);
-      acc = f2(0.f, 0.f);
-      // the columns beyond the row's end would add mu^2 each
-      if (nv == gt * VPT) {
+      const bool full = nv == gt * VPT;  // else the columns beyond the end would add mu^2 each
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        mu[q] = s[q] * inv_d;
+        const F2 m = f2(-mu[q], -mu[q]);
+        F2 acc = f2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
-          v[k] = add2(v[k], m);
-          acc = fma2(v[k], v[k], acc);
+          v[q][k] = add2(v[q][k], m);
+          if (!full) {
+            float lo, hi;
+            split(v[q][k], lo, hi);
+            v[q][k] = f2(tid + (2 * k / VEC) * gt < nv ? lo : 0.f,
+                         tid + ((2 * k + 1) / VEC) * gt < nv ? hi : 0.f);
+          }
+          acc = fma2(v[q][k], v[q][k], acc);
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k) {
-          float p, q;
-          split(add2(v[k], m), p, q);
-          v[k] = f2(tid + (2 * k / VEC) * gt < nv ? p : 0.f,
-                    tid + ((2 * k + 1) / VEC) * gt < nv ? q : 0.f);
-          acc = fma2(v[k], v[k], acc);
-        }
+        s[q] = both(acc);
       }
-      s[0] = both(acc);
-      group_sum<1>(s, warps, tid >> 5, group, buf, turn);
+      group_sum<R>(s, warps, tid >> 5, group, buf, turn);
     }
-    const float r = ok ? 1.f / sqrtf(s[0] * inv_d + eps) : __int_as_float(0x7fffffff);
-    if (tid == 0) {
-      if (mean) mean[row] = mu;
-      if (rstd) rstd[row] = r;
-    }
-    const F2 rr = f2(r, r);
-    float o[N];
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-      const F2 h = mul2(v[k], rr);
-      if constexpr (RMS)
-        split(mul2(h, g[k]), o[2 * k], o[2 * k + 1]);
-      else
-        split(fma2(h, g[k], b[k]), o[2 * k], o[2 * k + 1]);
-    }
-    T* yr = y + (size_t)row * d;
+    for (int q = 0; q < R; ++q) {
+      if (q >= have) break;
+      const float r = ok ? 1.f / sqrtf(s[q] * inv_d + eps) : __int_as_float(0x7fffffff);
+      if (tid == 0) {
+        if (mean) mean[row + q] = mu[q];
+        if (rstd) rstd[row + q] = r;
+      }
+      const F2 rr = f2(r, r);
+      float o[N];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (tid + i * gt < nv)
-        store_raw<T, VEC>(yr + (size_t)(tid + i * gt) * VEC, pack<T, VEC>(o + i * VEC));
+      for (int k = 0; k < N / 2; ++k) {
+        const F2 h = mul2(v[q][k], rr);
+        if constexpr (RMS)
+          split(mul2(h, g[k]), o[2 * k], o[2 * k + 1]);
+        else
+          split(fma2(h, g[k], b[k]), o[2 * k], o[2 * k + 1]);
+      }
+      T* yr = y + (size_t)(row + q) * d;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (tid + i * gt < nv)
+          store_raw<T, VEC>(yr + (size_t)(tid + i * gt) * VEC, pack<T, VEC>(o + i * VEC));
+    }
   }
   if constexpr (RING) ring.close();
 }
@@ -688,8 +716,9 @@ cudaError_t launch_forward(const moe_norm_desc& D, const Shape& s, const void* x
                            cudaStream_t st) {
   auto kern = norm_forward_kernel<T, VEC, VPT, RMS, RING, THREADS>;
   const int threads = s.groups * s.warps * 32;
-  const size_t stage = (size_t)s.groups * D.d * sizeof(T);
-  int blocks = (D.T + s.groups - 1) / s.groups, stages = 0;
+  constexpr int R = forward_rows<T, RMS, RING, THREADS>();
+  const size_t stage = (size_t)s.groups * R * D.d * sizeof(T);
+  int blocks = (D.T + s.groups * R - 1) / (s.groups * R), stages = 0;
   // what the registers allow at once: layer norm keeps beta too
   const int per_sm = threads <= 256 ? (RMS ? 4 : 2) : threads <= 512 && RMS ? 2 : 1;
   if (RING) {
