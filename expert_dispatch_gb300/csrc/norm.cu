@@ -610,10 +610,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
             const float v = k ? sums[c * VEC + j] + acc[i * VEC + j] : acc[i * VEC + j];
-            if (k == groups - 1)
-              out[c * VEC + j] = v;
-            else
+            if (k < groups - 1)
               sums[c * VEC + j] = v;
+            else
+              acc[i * VEC + j] = v;
+          }
+          if (k == groups - 1) {
+            if constexpr (VEC >= 4) {
+#pragma unroll
+              for (int j = 0; j < VEC; j += 4)
+                *reinterpret_cast<float4*>(out + c * VEC + j) =
+                    make_float4(acc[i * VEC + j], acc[i * VEC + j + 1], acc[i * VEC + j + 2],
+                                acc[i * VEC + j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) out[c * VEC + j] = acc[i * VEC + j];
+            }
           }
         }
       }
