@@ -520,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9, both CTAs)
     // A warp reads its TMEM lane quarter (row = lane); the two warps of a
-    // quarter take one half of the unit's columns each, 16 at a time.
+    // quarter take one half of the unit's columns each, 32 at a time.
     const int q = warp & 3, half = (warp - 2) >> 2;
     int it = 0;
     for (int u = pair; u < total; u += n_pairs, ++it) {
@@ -534,22 +534,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float alpha = product_scale<OP>(p, mat);
       const bool mirror = tiles.mirrored(ti, col / BN);
 #pragma unroll 1
-      for (int cc = half * (width / 2); cc < (half + 1) * (width / 2); cc += 16) {
-        const int c0 = col + cc;
-        if (c0 >= p.rowsQ) break;  // warp-uniform
-        uint4 gram[2];
-        load_gram<OP, 16>(p, mat, row, c0, gram);
-        uint32_t a[16];
-        tmem_ld16(tb + cc, a);
-        tmem_ld_wait();
-        float v[16];
+      for (int cc = half * (width / 2); cc < (half + 1) * (width / 2); cc += 32) {
+        if (col + cc >= p.rowsQ) break;  // warp-uniform; rowsQ is a multiple of 64
+        uint32_t a[2][16];
+        uint4 gram[2][2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
-        if constexpr (OP == kLast)
-          store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
-                       scratch[warp - 2]);
-        else
-          store_product<OP, 16>(p, mat, row, c0, mirror, gram, v);
+        for (int i = 0; i < 2; ++i) {
+          load_gram<OP, 16>(p, mat, row, col + cc + 16 * i, gram[i]);
+          tmem_ld16(tb + cc + 16 * i, a[i]);
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c0 = col + cc + 16 * i;
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[i][j]);
+          if constexpr (OP == kLast)
+            store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
+                         scratch[warp - 2]);
+          else
+            store_product<OP, 16>(p, mat, row, c0, mirror, gram[i], v);
+        }
         __syncwarp();  // the next tcgen05.ld is the whole warp's
       }
       tc_fence_before();
