@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(256)
   pdl_trigger();
   __shared__ Scale sc;
   __shared__ uint32_t tile[64][33];  // two elements a word
-  const int mat = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  // the last matrices first: the sum before this kernel left them in L2
+  const int mat = gridDim.z - 1 - blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
   const T* src = g + (size_t)mat * rows * cols;
   const int tc = (threadIdx.x & 7) * 8, tr = threadIdx.x >> 3;  // 8 columns of rows tr, tr + 32
   float v[2][8];
@@ -926,9 +927,13 @@ bool pair_steps(int n_mats, int mp, int np) {
   return 11 * 5 * square < 10 * (gram + 2 * square + apply);
 }
 
-int sum_blocks(size_t per_mat) {
-  const size_t want = (per_mat + 16383) / 16384;  // 32 elements a thread
-  return want < kSumBlocks ? (int)want : kSumBlocks;
+// Blocks of the norm's sum for each matrix: four an SM over the stack, 32 elements
+// a thread at least.
+int sum_blocks(size_t per_mat, int n_mats) {
+  const size_t want = (per_mat + 16383) / 16384;
+  const int share = (4 * num_sms() + n_mats - 1) / n_mats;
+  const int most = share < kSumBlocks ? share : kSumBlocks;
+  return want < (size_t)most ? (int)want : most;
 }
 
 // |G|, the scales and the first X.
@@ -936,7 +941,7 @@ template <typename T>
 cudaError_t start(const moe_ortho_desc& D, const T* g, const OrthoLayout& L, float* partial,
                   Scale* scales, int* flags, __half* x, cudaStream_t s) {
   const size_t per_mat = (size_t)D.rows * D.cols;
-  const int nb = sum_blocks(per_mat);
+  const int nb = sum_blocks(per_mat, D.n_mats);
   {
     ProfScope pr("ortho_sumsq", s);
     (void)launch_kernel(ortho_sumsq_kernel<T>, dim3(nb, D.n_mats), 512, 0, s, g, per_mat, partial,
