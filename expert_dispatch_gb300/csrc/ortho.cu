@@ -57,20 +57,15 @@ using namespace ortho;
 constexpr int kSumBlocks = 128;  // most blocks of the norm's sum, per matrix
 
 // ---------------------------------------------------------------- norm and first X
-// Sums of squares of one matrix, block blockIdx.x of gridDim.x.  Squares are
-// summed as they are while the block's largest value lies between 2^-45 and
-// 2^45 (what then underflows is below 2^-63, far under the sum's last digit).
-// A block for which it does not reads its values again and keeps three sums in
-// which no square over- or underflows: of values above 2^45 times 2^-84, of
-// values below 2^-45 times 2^84, and of the rest.  A matrix that starts off a
-// 16-byte boundary is read in vectors from the next one on.
+// Sums of squares of one matrix, block blockIdx.x of gridDim.x: a plain sum, or
+// where that is not good (ortho.cuh) three, over values read again.  A matrix that
+// starts off a 16-byte boundary is read in vectors from the next one on.
 template <typename T>
 __global__ void __launch_bounds__(512)
     ortho_sumsq_kernel(const T* g, size_t per_mat, float* partial, int* flags) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[3][16];
-  __shared__ float top[16];
+  __shared__ float red[16];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flags[0] = 0;
   constexpr int V = 16 / (int)sizeof(T);
   const T* p = g + (size_t)blockIdx.y * per_mat;
@@ -100,42 +95,29 @@ __global__ void __launch_bounds__(512)
         for (int j = 0; j < V; ++j) add(v[k][j]);
     }
   };
-  float s[3] = {0.f, 0.f, 0.f}, most = 0.f;
-  each([&](float x) {
-    s[1] = fmaf(x, x, s[1]);
-    most = fmaxf(most, fabsf(x));  // a NaN is in the sum
-  });
+  auto block_sum = [&](float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = most;
-  __syncthreads();
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) most = fmaxf(most, top[w]);
-  if (most != 0.f && (most > kBig || most < kSmall)) {
+    for (int w = 0; w < 16; ++w) v += red[w];
+    return v;
+  };
+  float s[3] = {0.f, 0.f, 0.f};
+  each([&](float x) { s[1] = fmaf(x, x, s[1]); });
+  s[1] = block_sum(s[1]);
+  if (!plain_sum(s[1])) {
     s[1] = 0.f;
-    each([&](float x) {
-      const float ax = fabsf(x);
-      if (ax > kBig) {
-        s[0] = fmaf(x * kDown, x * kDown, s[0]);
-      } else if (ax < kSmall) {
-        s[2] = fmaf(x * kUp, x * kUp, s[2]);
-      } else {
-        s[1] = fmaf(x, x, s[1]);
-      }
-    });
-  }
+    each([&](float x) { add_square(x, s); });
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
-    if ((threadIdx.x & 31) == 0) red[q][threadIdx.x >> 5] = s[q];
+    for (int q = 0; q < 3; ++q) s[q] = block_sum(s[q]);
   }
-  __syncthreads();
-  if (threadIdx.x < 3) {
-    float v = 0.f;
-    for (int w = 0; w < 16; ++w) v += red[threadIdx.x][w];
-    partial[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 3 + threadIdx.x] = v;
-  }
+  if (threadIdx.x < 3)
+    partial[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 3 + threadIdx.x] =
+        threadIdx.x == 0 ? s[0] : threadIdx.x == 1 ? s[1] : s[2];
 }
 
 // First X in fp16, padded with zeros: the input, [rows, cols] padded to

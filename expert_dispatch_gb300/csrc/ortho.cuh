@@ -41,7 +41,24 @@ __device__ __forceinline__ void load_elems(const T* p, float (&v)[V]) {
   }
 }
 
+// Sums of squares.  A plain sum of squares in fp32 is good while it lies between
+// 2^-80 and 2^100: no square was near overflow, and what underflowed lies 46
+// powers of two below the sum (NaN, infinity and 0 are outside, too).  Otherwise
+// three sums are kept in which no square over- or underflows: of values above
+// 2^45 times 2^-84, of values below 2^-45 times 2^84, and of the rest.
 constexpr float kBig = 0x1p45f, kSmall = 0x1p-45f, kUp = 0x1p84f, kDown = 0x1p-84f;
+
+__device__ __forceinline__ bool plain_sum(float s) { return s >= 0x1p-80f && s <= 0x1p100f; }
+
+__device__ __forceinline__ void add_square(float x, float (&s)[3]) {
+  const float ax = fabsf(x);
+  if (ax > kBig)
+    s[0] = fmaf(x * kDown, x * kDown, s[0]);
+  else if (ax < kSmall)
+    s[2] = fmaf(x * kUp, x * kUp, s[2]);
+  else
+    s[1] = fmaf(x, x, s[1]);
+}
 
 // The scale of one matrix from its partial sums, added by one warp in a fixed
 // order.

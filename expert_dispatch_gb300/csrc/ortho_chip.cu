@@ -7,10 +7,11 @@
 // (fp16, 128 rows, blocks of 64 columns in the 128-byte swizzle) for all steps.
 // The same bytes serve the tensor cores as K-major operand of X X^T and as
 // MN-major operand of B X.  Only A = X X^T couples the slices: each CTA computes
-// its slice's part (128 x 128, fp32), leaves it in shared memory, and after a
-// cluster barrier adds up its share of A's columns over the cluster in rank
-// order, rounds it and stores it into every CTA's copy of A.  B is computed by
-// every CTA for itself.  HBM sees G (twice) and the result.
+// its slice's part (128 x 128, fp32) and stores it into the shared memory of the
+// CTAs that add it up, each its share of A's columns, in rank order; these round
+// their sums and store them into every CTA's copy of A.  (Stores into a partner's
+// shared memory wait for nothing; loading the parts from the partners took 12000
+// cycles a step with 8 CTAs.)  B is computed by every CTA for itself.
 //
 // What bounds it is latency: the chain of 3 products, 3 epilogues and 2 cluster
 // barriers a step.  In launches of single products the same chain costs 17
@@ -46,6 +47,7 @@ constexpr int kMaxBlocks = 6;       // beside a CTA's part of A: shared memory
 // SM: a CTA takes all of the SM's tensor memory, and two clusters that each
 // held it on one SM and waited for it on another would not end.
 constexpr int kLeastSmem = 136 * 1024;
+constexpr int kBlocksWanted = 4;    // blocks a CTA of a cluster, where eight CTAs are enough
 
 struct ChipArgs {
   int rows, cols, m, n;
@@ -61,6 +63,13 @@ __host__ __device__ constexpr int chip_smem(int cluster, int blocks) {
   return need > kLeastSmem ? need : kLeastSmem;
 }
 
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t a, uint32_t b,
+                                                  uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
 // Byte offset of the 16-byte chunk that holds column c (a multiple of 8) of row
 // r, in an operand of 64-column blocks.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
@@ -70,7 +79,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 // The 16 bytes from element `at` (a multiple of their number) of `total`; zeros
 // behind the end.
 template <typename T>
-__device__ __forceinline__ uint4 load16(const T* __restrict__ g, size_t at, size_t total) {
+__device__ __forceinline__ uint4 load16(const T* __restrict__ g, int at, int total) {
   constexpr int V = 16 / (int)sizeof(T);
   if (at + V <= total) return *reinterpret_cast<const uint4*>(g + at);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -95,51 +104,86 @@ __device__ __forceinline__ void unpack16(uint4 q, float (&v)[V]) {
                           : __uint_as_float(w[j / 2] << 16);
 }
 
-// f(line, start, length, V values) over this CTA's columns c0 .. c0 + w - 1 of X =
-// G or G^T.  A line is a row of X, or a column (tall): what is consecutive in G.
-// It is read in aligned 16-byte vectors that may begin before it and end behind
-// it; the values are those of its positions start .. start + V - 1, of which 0 ..
-// length - 1 count.  No vector reaches behind the stack's end.
-template <typename T, typename F>
-__device__ __forceinline__ void for_slice(const T* __restrict__ g, size_t total, const ChipArgs& p,
-                                          int mat, int c0, int w, F&& f) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const bool tall = p.rows > p.cols;
-  const int wn = min(w, p.n - c0);  // columns that exist
-  if (wn <= 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lines = tall ? wn : p.m, length = tall ? p.m : wn;
-  const size_t first = (size_t)mat * p.rows * p.cols + (tall ? (size_t)c0 * p.cols : (size_t)c0);
-  // one more where lines begin inside a vector
-  const int vectors = (length + V - 1) / V + (p.cols % V ? 1 : 0);
-  // a warp takes one line by 32 vectors of a row; of a column 8 lines by 4
-  // vectors, so that its stores into X share 16-byte chunks
-  const int wide = tall ? 8 : 1, across = tall ? 4 : 32;
-  const int li = tall ? lane >> 2 : 0, vi = tall ? lane & 3 : lane;
-  constexpr int U = 8;  // vectors in flight: the next lines, or (tall) further along the line
-  const int jl = tall ? 0 : kWarps, jv = tall ? across : 0;
-  for (int l0 = warp * wide + li; l0 < lines; l0 += kWarps * wide * (tall ? 1 : U)) {
-    for (int k0 = vi; k0 < vectors; k0 += across * (tall ? U : 1)) {
-      uint4 raw[U];
-      int start[U];
+// This CTA's columns c0 .. c0 + w - 1 of X = G or G^T, in the order in which its
+// threads read them.  A line is a row of X, or a column (tall): what is
+// consecutive in G.  It is read in aligned 16-byte vectors that may begin before
+// it and end behind it; a vector's values are the line's positions start ..
+// start + V - 1, of which 0 .. length - 1 count.  No vector reaches behind the
+// stack's end.  A thread takes kSlots vectors at a time, all in flight at once; a
+// slice of one such batch stays in registers, so G crosses into the SM once.
+constexpr int kSlots = 16;
+
+template <typename T>
+struct Slice {
+  static constexpr int V = 16 / (int)sizeof(T);
+  const T* g;      // the vector in which the matrix begins; offsets below count from it
+  int total;       // elements from g to the stack's end, or more than the matrix needs
+  int first;       // the first line's offset
+  int cols, lines, length, line0, vec0, line_step, vec_step, hshift, vec_batches, batches, used;
+
+  __device__ __forceinline__ Slice(const T* stack, size_t stack_total, const ChipArgs& p, int mat,
+                                   int c0, int w)
+      : cols(p.cols) {
+    const bool tall = p.rows > p.cols;
+    const int wn = max(0, min(w, p.n - c0));  // columns that exist
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    lines = tall ? wn : (wn ? p.m : 0);
+    length = tall ? p.m : wn;
+    const size_t begin = (size_t)mat * p.rows * p.cols, aligned = begin / V * V;
+    g = stack + aligned;
+    total = (int)min(stack_total - aligned, (size_t)1 << 30);
+    first = (int)(begin - aligned) + (tall ? c0 * cols : c0);
+    // one vector more where lines begin inside one
+    const int vectors = (length + V - 1) / V + (cols % V ? 1 : 0);
+    // a warp takes one line by 32 vectors of a row; of a column 8 lines by 4
+    // vectors, so that its stores into X share 16-byte chunks
+    line0 = tall ? warp * 8 + (lane >> 2) : warp;
+    vec0 = tall ? lane & 3 : lane;
+    line_step = tall ? kWarps * 8 : kWarps;
+    vec_step = tall ? 4 : 32;
+    // slots: 2^hshift steps along a line by kSlots >> hshift lines
+    const int along = (vectors + vec_step - 1) / vec_step;
+    hshift = 0;
+    while ((1 << hshift) < along && (1 << hshift) < kSlots) ++hshift;
+    const int down = (lines + line_step - 1) / line_step, per = kSlots >> hshift;
+    vec_batches = (along + (1 << hshift) - 1) >> hshift;
+    batches = vec_batches * ((down + per - 1) / per);
+    used = min(down, per) << hshift;  // slots that can hold something
+  }
+  // line and position of slot s of the batch from (line, vector) step (lb, vb) on;
+  // false: none
+  __device__ __forceinline__ bool place(int lb, int vb, int s, int& line, int& start,
+                                        int& at) const {
+    line = line0 + (lb + (s >> hshift)) * line_step;
+    const int k = (vec0 + (vb + (s & ((1 << hshift) - 1))) * vec_step) * V;
+    const int e = first + line * cols, shift = e & (V - 1);
+    start = k - shift;
+    at = e - shift + k;
+    return line < lines && start < length;
+  }
+  template <typename F>
+  __device__ __forceinline__ void slots(int b, F&& f) const {
+    const int vb = b % vec_batches, lb = b / vec_batches;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int l = l0 + u * jl, k = k0 + u * jv;
-        const size_t e = first + (size_t)l * p.cols;
-        const int shift = (int)(e % V);
-        start[u] = l < lines ? k * V - shift : length;
-        if (start[u] < length) raw[u] = load16(g, e - shift + (size_t)k * V, total);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (start[u] < length) {
-          float v[V];
-          unpack16<T, V>(raw[u], v);
-          f(l0 + u * jl, start[u], length, v);
-        }
+    for (int s = 0; s < kSlots; ++s) {
+      if (s >= used) break;  // the same for all threads
+      int line, start, at;
+      if (place(lb * (kSlots >> hshift), vb << hshift, s, line, start, at)) f(s, line, start, at);
     }
   }
-}
+  __device__ __forceinline__ void load(int b, uint4 (&raw)[kSlots]) const {
+    slots(b, [&](int s, int, int, int at) { raw[s] = load16(g, at, total); });
+  }
+  // f(line, start, V values); values outside the line as they lie
+  template <typename F>
+  __device__ __forceinline__ void each(int b, const uint4 (&raw)[kSlots], F&& f) const {
+    slots(b, [&](int s, int line, int start, int) {
+      float v[V];
+      unpack16<T, V>(raw[s], v);
+      f(line, start, v);
+    });
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -149,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_s;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
-  __shared__ float red[3][kWarps], top[kWarps];
+  __shared__ float red[kWarps];
   __shared__ float sums[3], all_sums[kMaxCluster * 3];
   __shared__ Scale sc;
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -157,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* xs = smem;                              // X: blocks
   uint8_t* as = xs + p.blocks * kBlockBytes;       // A: 2 blocks
   uint8_t* bs = as + 2 * kBlockBytes;              // B: 2 blocks
-  float* part = reinterpret_cast<float*>(bs + 2 * kBlockBytes);  // [128 columns][128 rows]
+  uint8_t* part = bs + 2 * kBlockBytes;            // parts of A: [CTA][8-column group][row][8] fp32
   const uint32_t xa = smem_u32(xs), aa = smem_u32(as), ba = smem_u32(bs);
   const uint32_t bar = smem_u32(&bar_s);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -175,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
-  for (int i = tid; i < (p.blocks + 4) * kBlockBytes / 16; i += kThreads)  // X, A and B: zeros
+  for (int i = tid; i < p.blocks * kBlockBytes / 16; i += kThreads)  // X: zeros
     reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc_fence_before();
   __syncthreads();
@@ -185,50 +229,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   if (blockIdx.x == 0 && tid == 0) *p.err = 0;
 
-  // |G|: sums of squares as in ortho_sumsq_kernel, a CTA's slice in the place of
-  // a block's share
-  {
-    float s[3] = {0.f, 0.f, 0.f}, most = 0.f;
-    for_slice<T>(g, total, p, mat, c0, w, [&](int, int at, int len, const float (&v)[V]) {
+  const Slice<T> slice(g, total, p, mat, c0, w);
+  uint4 raw[kSlots];
+  if (slice.batches == 1) slice.load(0, raw);
+  // f over the slice: from the registers, or read again
+  auto over_slice = [&](auto&& f) {
+    if (slice.batches == 1) {
+      slice.each(0, raw, f);
+    } else {
+      for (int b = 0; b < slice.batches; ++b) {
+        slice.load(b, raw);
+        slice.each(b, raw, f);
+      }
+    }
+  };
+  auto block_sum = [&](float v) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float x = at + j >= 0 && at + j < len ? v[j] : 0.f;
-        s[1] = fmaf(x, x, s[1]);
-        most = fmaxf(most, fabsf(x));
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += red[i];
+    return v;
+  };
+
+  // |G|, a CTA's slice in the place of a block's share (ortho_sumsq_kernel)
+  {
+    const int len = slice.length;
+    float s[3] = {0.f, 0.f, 0.f};
+    over_slice([&](int, int at, const float (&v)[V]) {
+      if (at >= 0 && at + V <= len) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[1] = fmaf(v[j], v[j], s[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (at + j >= 0 && at + j < len) s[1] = fmaf(v[j], v[j], s[1]);
       }
     });
-#pragma unroll
-    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (lane == 0) top[warp] = most;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) most = fmaxf(most, top[i]);
-    if (most != 0.f && (most > kBig || most < kSmall)) {
+    s[1] = block_sum(s[1]);
+    if (!plain_sum(s[1])) {
       s[1] = 0.f;
-      for_slice<T>(g, total, p, mat, c0, w, [&](int, int at, int len, const float (&v)[V]) {
+      over_slice([&](int, int at, const float (&v)[V]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float x = at + j >= 0 && at + j < len ? v[j] : 0.f, ax = fabsf(x);
-          if (ax > kBig)
-            s[0] = fmaf(x * kDown, x * kDown, s[0]);
-          else if (ax < kSmall)
-            s[2] = fmaf(x * kUp, x * kUp, s[2]);
-          else
-            s[1] = fmaf(x, x, s[1]);
-        }
+        for (int j = 0; j < V; ++j)
+          if (at + j >= 0 && at + j < len) add_square(v[j], s);
       });
-    }
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
-      if (lane == 0) red[q][warp] = s[q];
+      for (int q = 0; q < 3; ++q) s[q] = block_sum(s[q]);
     }
-    __syncthreads();
-    if (tid < 3) {
-      float v = 0.f;
-      for (int i = 0; i < kWarps; ++i) v += red[tid][i];
-      sums[tid] = v;
+    if (tid == 0) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q) sums[q] = s[q];
     }
     __syncthreads();
     if (C > 1) cluster_sync();
@@ -243,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const float f1 = sc.f1, f2 = sc.f2, rho1 = sc.rho;
-  for_slice<T>(g, total, p, mat, c0, w, [&](int line, int at, int len, const float (&v)[V]) {
+  over_slice([&](int line, int at, const float (&v)[V]) {
+    const int len = slice.length;
     if (!tall && V == 8 && (at & 7) == 0 && at + V <= len) {
       uint32_t u[4];
 #pragma unroll
@@ -314,38 +369,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(u[0], u[1], u[2], u[3]);
         }
       } else {
+        // 8-column group k of A is added up by CTA k % C: there, behind the
+        // groups of the CTAs before this one
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          part[(c + j) * 128 + row] = __uint_as_float(a[j >> 4][j & 15]);
+        for (int i = 0; i < 4; ++i) {
+          const int k = c / 8 + i, owner = k & (C - 1), slot = k / C;
+          const uint32_t to = mapa_shared(
+              smem_u32(part) + (uint32_t)(((rank * (16 / C) + slot) * 128 + row) * 32), owner);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t* u = &a[i >> 1][(i & 1) * 8 + 4 * h];
+            st_shared_cluster(to + 16u * h, u[0], u[1], u[2], u[3]);
+          }
+        }
       }
       __syncwarp();
     }
     if (C > 1) {
       __syncthreads();
-      cluster_sync();  // every CTA's part is in place; its copy of A is no longer read
-      // 8 columns at a time, dealt out to the cluster and to a quarter's warps
-      for (int k = rank + sub * C; k < 16; k += kParts * C) {
-        const uint32_t at = smem_u32(part) + (uint32_t)(k * 8 * 128 + row) * 4u;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          if (r < C) {
-            const uint32_t peer = mapa_shared(at, r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += ld_shared_cluster(peer + (uint32_t)j * 512u);
-          }
+      cluster_sync();  // every CTA's parts are in place; its copy of A is no longer read
+      const int groups = 16 / C;
+      for (int i = tid; i < groups * 128; i += kThreads) {
+        const int slot = i >> 7, r = i & 127;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int src = 0; src < C; ++src) {
+          const float4* f =
+              reinterpret_cast<const float4*>(part + ((src * groups + slot) * 128 + r) * 32);
+          const float4 lo = f[0], hi = f[1];
+          v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+          v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
         }
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = pack_half2(alpha * v[2 * j], alpha * v[2 * j + 1]);
-        const uint32_t to = aa + chunk_at(row, k * 8);
-        for (int r = 0; r < C; ++r)
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           mapa_shared(to, r)),
-                       "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
-                       : "memory");
+        const uint32_t to = aa + chunk_at(r, (slot * C + rank) * 8);
+        for (int k = 0; k < C; ++k)
+          st_shared_cluster(mapa_shared(to, (rank + k) & (C - 1)), u[0], u[1], u[2], u[3]);
       }
       // the stores reach the peers' tensor cores: ordered before this barrier
       // here and after it there (product's fence)
@@ -430,12 +489,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(xs + chunk_at(row, cc)) = make_uint4(u[0], u[1], u[2], u[3]);
           *reinterpret_cast<uint4*>(xs + chunk_at(row, cc + 8)) =
               make_uint4(u[4], u[5], u[6], u[7]);
-        } else {  // A is done with: the warps' scratch
-          store_result(p.out + (size_t)mat * p.m * p.n, p.m, p.n, tall, q * 32, c0 + cc, v,
-                       reinterpret_cast<uint32_t*>(as) + warp * 32 * kRowWords);
+        } else if (tall) {  // a warp's lanes hold consecutive elements of the result
+          if (row < p.m) {
+            __nv_bfloat16* to = p.out + (size_t)mat * p.m * p.n + row;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c0 + cc + j < p.n)
+                to[(size_t)(c0 + cc + j) * p.m] = __float2bfloat16_rn(v[j]);
+          }
+        } else {  // in X's place, to be stored along its rows
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            u[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *reinterpret_cast<uint4*>(xs + chunk_at(row, cc)) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4*>(xs + chunk_at(row, cc + 8)) =
+              make_uint4(u[4], u[5], u[6], u[7]);
         }
       }
       __syncwarp();
+    }
+  }
+  if (!tall) {
+    __syncthreads();
+    const int wn = min(w, p.n - c0);
+    for (int r = warp; r < p.m; r += kWarps) {
+      __nv_bfloat16* to = p.out + ((size_t)mat * p.m + r) * p.n + c0;
+      if (p.n % 8 == 0) {  // 16-byte aligned rows
+        for (int c = lane * 8; c < wn; c += 256)
+          *reinterpret_cast<uint4*>(to + c) =
+              *reinterpret_cast<const uint4*>(xs + chunk_at(r, c));
+      } else {
+        for (int c = lane; c < wn; c += 32)
+          to[c] = *reinterpret_cast<const __nv_bfloat16*>(xs + chunk_at(r, c & ~7) + (c & 7) * 2);
+      }
     }
   }
   tc_fence_before();
@@ -497,13 +586,15 @@ cudaError_t launch_ortho_chip(const moe_ortho_desc& D, const void* g, void* out,
   p.eps = D.eps;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.err = flags;
-  // a CTA alone while X fits it (no exchange: about 5 us a step), else four
-  // blocks a CTA, or what eight CTAs need
+  // a CTA alone while X fits it (no exchange), else the least power of two of
+  // CTAs that hold it
   const int blocks = (p.n + 63) / 64;
-  p.cluster = blocks <= kMaxBlocksAlone ? 1 : (blocks + 3) / 4;
-  if (p.cluster > kMaxCluster) p.cluster = kMaxCluster;
+  p.cluster = 1;
+  if (blocks > kMaxBlocksAlone)
+    for (p.cluster = 2; (blocks + p.cluster - 1) / p.cluster > kBlocksWanted &&
+                        p.cluster < kMaxCluster;)
+      p.cluster *= 2;
   p.blocks = (blocks + p.cluster - 1) / p.cluster;
-  p.cluster = (blocks + p.blocks - 1) / p.blocks;  // no CTA without columns
   return D.dtype == MOE_BF16 ? launch(static_cast<const __nv_bfloat16*>(g), p, D.n_mats, s)
                              : launch(static_cast<const float*>(g), p, D.n_mats, s);
 }
