@@ -210,7 +210,7 @@ struct OrthoLayout {
   size_t x[2];     // fp16 [n_mats, mp, np], read and written in turn
   size_t gram;     // fp16 [n_mats, mp, mp]
   size_t poly;     // fp16 [n_mats, mp, mp]
-  size_t mul;      // fp16 [n_mats, mp, mp], where two steps are taken at once
+  size_t mul;      // fp16 [n_mats, mp, mp], for two steps at once
   size_t total;
   int mp, np;
 };

@@ -874,7 +874,8 @@ struct Choice {
 template <int OP>
 Choice choose(int n_mats, int K, int rowsP, int rowsQ) {
   constexpr bool SYM = OP == kGram || OP == kPoly;
-  const long long n = n_mats, sms = num_sms(), blocks = K / 64;
+  const long long n = n_mats, blocks = K / 64;
+  const long long sms = num_sms() > 2 ? num_sms() : 2;  // 1 where no device answers
   Choice c{};
   c.large = n * Tiles<256, 256, SYM>(rowsP, rowsQ).count();
   c.small = n * Tiles<128, kSmallN, SYM>(rowsP, rowsQ).count();
@@ -966,7 +967,7 @@ OrthoLayout ortho_layout(const moe_ortho_desc& D) {
   for (size_t& o : L.x) o = take(n * L.mp * L.np * 2);
   L.gram = take(n * L.mp * L.mp * 2);
   L.poly = take(n * L.mp * L.mp * 2);
-  if (pair_steps(D.n_mats, L.mp, L.np)) L.mul = take(n * L.mp * L.mp * 2);
+  L.mul = take(n * L.mp * L.mp * 2);
   L.total = 512 + off;  // the flags' 16 bytes, then the regions at the next multiple of 256
   return L;
 }

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* xs = smem;                              // X: blocks
   uint8_t* as = xs + p.blocks * kBlockBytes;       // A: 2 blocks
   uint8_t* bs = as + 2 * kBlockBytes;              // B: 2 blocks
-  uint8_t* part = bs + 2 * kBlockBytes;            // parts of A: [CTA][8-column group][row][8] fp32
+  uint8_t* part = bs + 2 * kBlockBytes;            // parts of A: [CTA][8-column group][half][row][4] fp32
   const uint32_t xa = smem_u32(xs), aa = smem_u32(as), ba = smem_u32(bs);
   const uint32_t bar = smem_u32(&bar_s);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -370,16 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // 8-column group k of A is added up by CTA k % C: there, behind the
-        // groups of the CTAs before this one
+        // groups of the CTAs before this one, [row][4] fp32 of its two halves
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int k = c / 8 + i, owner = k & (C - 1), slot = k / C;
           const uint32_t to = mapa_shared(
-              smem_u32(part) + (uint32_t)(((rank * (16 / C) + slot) * 128 + row) * 32), owner);
+              smem_u32(part) + (uint32_t)(((rank * (16 / C) + slot) * 256 + row) * 16), owner);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {  // 512 consecutive bytes a warp
             const uint32_t* u = &a[i >> 1][(i & 1) * 8 + 4 * h];
-            st_shared_cluster(to + 16u * h, u[0], u[1], u[2], u[3]);
+            st_shared_cluster(to + 2048u * h, u[0], u[1], u[2], u[3]);
           }
         }
       }
@@ -394,23 +394,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int src = 0; src < C; ++src) {
           const float4* f =
-              reinterpret_cast<const float4*>(part + ((src * groups + slot) * 128 + r) * 32);
-          const float4 lo = f[0], hi = f[1];
+              reinterpret_cast<const float4*>(part) + (src * groups + slot) * 256 + r;
+          const float4 lo = f[0], hi = f[128];
           v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
           v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
         }
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = pack_half2(alpha * v[2 * j], alpha * v[2 * j + 1]);
-        const uint32_t to = aa + chunk_at(r, (slot * C + rank) * 8);
+        // by way of B's place, group after group: a warp's stores are consecutive there
+        const uint32_t to = ba + (uint32_t)(((slot * C + rank) * 128 + r) * 16);
         for (int k = 0; k < C; ++k)
           st_shared_cluster(mapa_shared(to, (rank + k) & (C - 1)), u[0], u[1], u[2], u[3]);
       }
-      // the stores reach the peers' tensor cores: ordered before this barrier
-      // here and after it there (product's fence)
-      asm volatile("fence.proxy.async;" ::: "memory");
       __syncthreads();
-      cluster_sync();
+      cluster_sync();  // A's groups are in place
+      for (int i = tid; i < 16 * 128; i += kThreads)
+        *reinterpret_cast<uint4*>(as + chunk_at(i & 127, (i >> 7) * 8)) =
+            reinterpret_cast<const uint4*>(bs)[i];
     }
 
     // ---- B = a I + b A + c A A: TMEM columns 128 .. 255

@@ -169,6 +169,14 @@ def test_ortho_refuses(L):
     assert L.moe_ortho_workspace_size(_ortho(n_mats=0), ctypes.byref(n)) == moe.MOE_OK
     assert n.value == 0
     assert L.moe_ortho_workspace_size(_ortho(), ctypes.byref(n)) == moe.MOE_OK and n.value > 0
+    sizes = []
+    for m, cols in ((128, 2048), (129, 2048), (2048, 129), (1536, 4096)):
+        assert L.moe_ortho_workspace_size(_ortho(rows=m, cols=cols), ctypes.byref(n)) == moe.MOE_OK
+        sizes.append(n.value)
+    # on chip the flags are enough; else two fp16 X and three m x m matrices, padded to 64
+    assert sizes[0] == 256 and sizes[1] == sizes[2]
+    assert sizes[1] > 2 * 2 * 2 * 192 * 2048 and sizes[3] > 2 * 2 * (2 * 1536 * 4096 + 3 * 1536 ** 2)
+    assert L.moe_ortho_workspace_size(_ortho(), ctypes.byref(n)) == moe.MOE_OK
     out, fn = ctypes.c_void_p(0x20000), L.moe_orthogonalize
     for g, o in ((None, out), (FAKE, None), (ODD, out), (FAKE, ODD), (FAKE, FAKE)):
         assert fn(_ortho(), g, o, FAKE, n.value, None) == moe.MOE_ERR_INVALID_ARG
