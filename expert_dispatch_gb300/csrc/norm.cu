@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) gv[i * VEC + j] = 0.f;
-      if (tid + i * gt < nv) load_param<VEC>(gamma, w_bf16, (tid + i * gt) * VEC, 1.f, gv + i * VEC);
+      if (tid + i * gt < nv)
+        load_param<VEC>(gamma, w_bf16, (tid + i * gt) * VEC, 1.f, gv + i * VEC);
     }
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) {

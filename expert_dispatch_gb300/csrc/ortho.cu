@@ -29,11 +29,12 @@
 // m x m products take the place of one product each of X X^T and of B X.  All
 // of them commute, so they are symmetric and one triangle is enough.  That is
 // fewer operations where n is well above m; measured, 4 x 7168 x 2048 bf16 1438
-// -> 1182 us, 16 x 1536 x 4096 2060 -> 1794 us.  Five steps run as 2 + 1 + 2: X is formed and rounded again before
-// errors of A (which sees the squares of the singular values) have grown; the
-// error of the result is that of five single steps within a few percent, while
-// all five on A alone lose what has small singular values (0.2 where the direct
-// form has 3e-3, singular values falling as 1/k).
+// -> 1182 us, 16 x 1536 x 4096 2060 -> 1794 us.  Five steps run as 2 + 1 + 2: X is
+// formed and rounded again before errors of A (which sees the squares of the
+// singular values) have grown; the error of the result is that of five single
+// steps within a few percent, while all five on A alone lose what has small
+// singular values (0.2 where the direct form has 3e-3, singular values falling as
+// 1/k).
 //
 // Matrices with m <= 128 and n up to a cluster's shared memory take one launch of
 // the kernel in ortho_chip.cu; what follows here serves the others.

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* xs = smem;                              // X: blocks
   uint8_t* as = xs + p.blocks * kBlockBytes;       // A: 2 blocks
   uint8_t* bs = as + 2 * kBlockBytes;              // B: 2 blocks
-  uint8_t* part = bs + 2 * kBlockBytes;            // parts of A: [CTA][8-column group][half][row][4] fp32
+  uint8_t* part = bs + 2 * kBlockBytes;  // parts of A: [CTA][8-column group][half][row][4] fp32
   const uint32_t xa = smem_u32(xs), aa = smem_u32(as), ba = smem_u32(bs);
   const uint32_t bar = smem_u32(&bar_s);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

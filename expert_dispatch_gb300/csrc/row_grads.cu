@@ -205,7 +205,8 @@ cudaError_t launch_dispatch_rows_backward(int dtype, const void* dx_perm,
   const int slices = want < steps ? want : steps;
   (void)launch_kernel(dtype == MOE_BF16 ? dispatch_rows_backward_kernel<true>
                                         : dispatch_rows_backward_kernel<false>,
-                      dim3(T, slices), kDispatchBwdThreads, 0, s, dx_perm, slot_row, d, ks, T * ks, dx);
+                      dim3(T, slices), kDispatchBwdThreads, 0, s, dx_perm, slot_row, d, ks, T * ks,
+                      dx);
   return cudaGetLastError();
 }
 
@@ -228,8 +229,8 @@ cudaError_t launch_combine_backward(int dtype, const float* dy, const void* y_pe
                              : of(bool_constant<true>(), bool_constant<false>()))
                   : (dtopk_w ? of(bool_constant<false>(), bool_constant<true>())
                              : of(bool_constant<false>(), bool_constant<false>()));
-  (void)launch_kernel(kern, dim3(T, T < kCombineBwdTokens ? ks : 1), threads, 0, s, dy, y_perm, total_rows, slot_row, topk_w, d, k, ks,
-                      T * ks, dy_perm, dtopk_w);
+  (void)launch_kernel(kern, dim3(T, T < kCombineBwdTokens ? ks : 1), threads, 0, s, dy, y_perm,
+                      total_rows, slot_row, topk_w, d, k, ks, T * ks, dy_perm, dtopk_w);
   return cudaGetLastError();
 }
 

@@ -457,7 +457,8 @@ moe_status moe_combine_backward(const moe_layer_desc* desc, const float* dy, con
                                 void* stream);
 
 /* Row norms.  Any d from 1 to 16384 (beyond: MOE_ERR_UNSUPPORTED) and any
-   T up to 2^30. */
+   T up to 2^30.  Should a bounded wait in their kernels expire, the rows that
+   it served (and the sums over them) are NaN. */
 typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
 typedef struct {
   int32_t T;       /* rows */

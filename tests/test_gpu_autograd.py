@@ -47,8 +47,8 @@ def test_chain_against_torch():
         if lib:
             xp = training.dispatch(training.layer_norm(x, g, b), plan)
             return training.combine(xp * m, w, plan, residual=res)
-        h = (x - x.mean(1, keepdim=True)) / torch.sqrt(x.var(1, unbiased=False, keepdim=True) + 1e-6)
-        h = h * g + b
+        var = x.var(1, unbiased=False, keepdim=True)
+        h = (x - x.mean(1, keepdim=True)) / torch.sqrt(var + 1e-6) * g + b
         at = plan.slot_row.long()
         W = torch.cat([w, torch.ones((T, desc.S), device="cuda", dtype=w.dtype)], 1)
         W = torch.where(at >= 0, W, 0.0)

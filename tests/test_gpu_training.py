@@ -71,11 +71,14 @@ def check_forward(x, g, b, rms, eps=1e-6):
 SIZES = [(1, 1), (1, 7168), (3, 2), (5, 8), (7, 31), (2, 64), (33, 72), (4, 264), (3, 257),
          (19, 1000), (9, 1111), (6, 2048), (5, 4100), (2, 4096), (3, 8191), (2, 8192), (2, 16383),
          (2, 16384)]
+# rows enough that blocks take several, in rings of rows where their bytes allow
+MANY = [(5001, 64), (5000, 40), (2601, 520), (1301, 2048), (3001, 33), (613, 7168), (1300, 8192),
+        (701, 16384), (700, 1111)]
 
 
 @pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,d", SIZES)
+@pytest.mark.parametrize("T,d", SIZES + MANY)
 def test_norm_forward(T, d, dtype, rms):
     x = rnd((T, d), 1, scale=3.0) + 5.0  # a mean larger than the spread
     x = x.to(DT[dtype])
@@ -86,7 +89,7 @@ def test_norm_forward(T, d, dtype, rms):
 
 @pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,d", SIZES + [(700, 520), (1300, 33), (613, 7168), (5000, 64)])
+@pytest.mark.parametrize("T,d", SIZES + MANY + [(700, 520), (1300, 33), (5000, 64), (3000, 4096)])
 def test_norm_backward(T, d, dtype, rms):
     dt = DT[dtype]
     x = (rnd((T, d), 1, scale=2.0) + 1.5).to(dt)
@@ -105,7 +108,8 @@ def test_norm_backward(T, d, dtype, rms):
     a1, a2 = (w * h).abs().mean(1, keepdim=True), w.abs().mean(1, keepdim=True)
     tol = r * U * (8 * w.abs() + 100 * a2 * (not rms) + h.abs() * 110 * a1)
     close(dx, want, H(dt) * want.abs() + tol * (1 + H(dt)))
-    # rows: a thread's chain of T / 304 rows, 8 groups, 304 / 32 blocks and a 5-step tree
+    # rows: a thread's chain of T / 152 rows at most, 8 groups, 304 / 32 blocks and a 5-step
+    # tree: below T / 304 + 40 for the T here
     chain = (T / 304 + 40) * U
     close(dg, (D * h).sum(0), chain * (D * h).abs().sum(0))
     if rms:
@@ -127,7 +131,8 @@ def test_norm_backward_against_differences(rms):
     args = [x.double(), g.double(), b]
 
     def loss(a):
-        return float((ref_norm(a[0], a[1], None if rms else a[2], rms, 1e-6)[0] * dy.double()).sum())
+        y = ref_norm(a[0], a[1], None if rms else a[2], rms, 1e-6)[0]
+        return float((y * dy.double()).sum())
 
     for got, which in ((dx, 0), (dg, 1), (db, 2)):
         if got is None:
@@ -159,6 +164,20 @@ def test_norm_parts_can_be_left_out():
         assert not want_g or torch.equal(b, dg)
         assert not want_b or torch.equal(c, db)
     # in place: y over x, dx over dy
+    xi, di = x.clone(), dy.clone()
+    moe.moe_norm_forward(desc, xi, g, None, xi)
+    moe.moe_norm_backward(desc, di, x, g, mean, rstd, di, None, None, None)
+    assert torch.equal(xi, y) and torch.equal(di, dx)
+
+
+@pytest.mark.parametrize("T,d", [(1301, 2048), (5001, 64), (700, 8192), (700, 1111)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_in_place(T, d, dtype):
+    """y over x and dx over dy, where later rows are already on their way."""
+    x, dy, g = rnd((T, d), 1, DT[dtype]), rnd((T, d), 2, DT[dtype]), rnd((d,), 3)
+    desc = moe.make_norm_desc(x, g)
+    y, mean, rstd = moe.norm(x, g, stats=True)
+    dx, _, _ = moe.norm_backward(dy, x, g, mean, rstd)
     xi, di = x.clone(), dy.clone()
     moe.moe_norm_forward(desc, xi, g, None, xi)
     moe.moe_norm_backward(desc, di, x, g, mean, rstd, di, None, None, None)
@@ -472,6 +491,25 @@ def test_ortho_workspace_stream_and_graph(rows):
     none = torch.empty((0, 8, 8), device="cuda")
     assert moe.orthogonalize(none).shape == (0, 8, 8)
     assert torch.equal(moe.orthogonalize(g[1]), want[1])
+
+
+def test_ortho_calls_on_several_streams_at_once():
+    """Kernels that take tensor memory and clusters of different kinds, side by side."""
+    shapes = [(1, 256, 4096), (2, 128, 2048), (4, 512, 512), (3, 1030, 1100), (20, 100, 400)]
+    gs = [rnd(s, i, torch.bfloat16) for i, s in enumerate(shapes)]
+    want = [moe.orthogonalize(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    descs = [moe.make_ortho_desc(g) for g in gs]
+    ws = [torch.empty(moe.moe_ortho_workspace_size(d), dtype=torch.uint8, device="cuda")
+          for d in descs]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for d, g, o, w, s in zip(descs, gs, outs, ws, streams):
+            moe.moe_orthogonalize(d, g, o, w, s)
+    for o, e, w, s in zip(outs, want, ws, streams):
+        assert moe.moe_get_device_status(w, stream=s) == moe.MOE_OK
+        assert torch.equal(o, e)
 
 
 # ---------------------------------------------------------------- streams and graphs
