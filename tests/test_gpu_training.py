@@ -551,3 +551,59 @@ def test_on_another_stream_and_in_a_graph():
     for n in want:
         assert torch.equal(want[n], other[n]), n
         assert torch.equal(want[n], graphed[n]), n
+
+
+# ---------------------------------------------------------------- offsets beyond 32 bits
+def test_norm_beyond_32_bit_offsets():
+    T, d = 270000, 8192  # 2.2e9 elements
+    x = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    part = rnd((9000, d), 1, torch.bfloat16)
+    for i in range(0, T, 9000):
+        x[i:i + 9000] = part
+    x[-7:] = rnd((7, d), 2, torch.bfloat16)
+    g = rnd((d,), 3)
+    for kind in (moe.MOE_NORM_LAYER, moe.MOE_NORM_RMS):
+        y, mean, rstd = moe.norm(x, g, None, kind=kind, stats=True)
+        few = moe.norm(x[-7:], g, None, kind=kind, stats=True)
+        assert torch.allclose(y[-7:].float(), few[0].float(), rtol=2 ** -7, atol=1e-6)
+        del y
+        dx, _, _ = moe.norm_backward(x, x, g, mean, rstd, kind=kind)
+        m7 = None if mean is None else mean[-7:].clone()
+        few, _, _ = moe.norm_backward(x[-7:], x[-7:], g, m7, rstd[-7:].clone(), kind=kind)
+        assert torch.allclose(dx[-7:].float(), few.float(), rtol=2 ** -7, atol=1e-6)
+        del dx
+
+
+def test_rows_beyond_32_bit_offsets():
+    T, d, E, k = 140000, 4096, 4, 4  # every token goes to every expert: 2.3e9 elements
+    desc = moe.make_desc(T, d, E, k, 128, 0, dtype=moe.MOE_BF16)
+    t = torch.arange(T, device="cuda", dtype=torch.int32)
+    slot = torch.stack([t + e * T for e in range(E)], 1).contiguous()
+    off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * T
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rnd((3, d), 1, torch.bfloat16)
+    xp = torch.empty((T * k, d), dtype=torch.bfloat16, device="cuda")
+    moe.moe_dispatch_rows(desc, x, off, slot, xp)
+    for e in range(E):
+        assert torch.equal(xp[(e + 1) * T - 3:(e + 1) * T], x[-3:])
+    dx = torch.empty_like(x)
+    moe.moe_dispatch_rows_backward(desc, xp, slot, dx)
+    assert torch.equal(dx[-3:].float(), (k * x[-3:].float()).bfloat16().float())
+    w = torch.full((T, k), 0.5, device="cuda")
+    dy = torch.zeros((T, d), device="cuda")
+    dy[-3:] = x[-3:].float()
+    out, dw = torch.empty_like(xp), torch.empty_like(w)
+    moe.moe_combine_backward(desc, dy, xp, off, slot, w, out, dw)
+    assert torch.equal(out[-3:], (0.5 * dy[-3:]).bfloat16())
+    want = dy[-3:].double().square().sum(1)
+    assert torch.allclose(dw[-3:].double(), want[:, None].expand(3, k), rtol=(d / 128 + 32) * U)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(40000, 128, 448), (350, 1536, 4096)])
+def test_ortho_beyond_32_bit_offsets(n, rows, cols):
+    g = torch.empty((n, rows, cols), dtype=torch.bfloat16, device="cuda")
+    g[:] = rnd((rows, cols), 1, torch.bfloat16)
+    g[-1] = rnd((rows, cols), 2, torch.bfloat16)
+    out = moe.orthogonalize(g)
+    for i in (0, n // 2, n - 1):
+        check_ortho(out[i][None], ref_ortho(g[i][None], 5, 1e-7))
