@@ -241,9 +241,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // A group's ring of rows in shared memory, `streams` rows a stage, filled by
 // bulk copies that one thread of the group requests `stages` rows ahead: HBM
 // latency is hidden without registers, and a row's loads cost no instructions
-// but its reads of shared memory.  Every wait for a copy is bounded; should one
-// expire, the caller makes the row's results NaN and no more copies are
-// requested.
+// but its reads of shared memory.  Every wait for a copy is bounded.  The threads
+// of a group wait each for itself, so some may give up on a row that the others
+// still see arrive: one that has given up adds NaN to the sums of that row and of
+// every row after it, which makes NaN of these rows' results in all threads, and
+// waits for nothing more.  No more copies are requested then.
 struct Ring {
   uint8_t* base;
   uint32_t bar0, row_bytes;
@@ -364,12 +366,12 @@ __global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
   const float inv_d = 1.f / (float)d;
   int turn = 0;
   float* buf = red[warps == 1 ? 0 : group];
+  bool ok = true;  // this thread has not given up waiting
   for (; row < rows; row += step) {  // the same rows for a whole group
-    bool ok = true;
     const int have = min(R, rows - row);
     const T* xr = x + (size_t)row * d;
     if constexpr (RING) {
-      ok = ring.wait();
+      ok = ok && ring.wait();
       xr = reinterpret_cast<const T*>(ring.rows());
     }
     F2 v[R][N / 2];  // zero beyond a row's end
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
       F2 acc = f2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) acc = RMS ? fma2(v[q][k], v[q][k], acc) : add2(v[q][k], acc);
-      s[q] = both(acc);
+      s[q] = ok ? both(acc) : quiet_nan();
     }
     group_sum<R>(s, warps, tid >> 5, group, buf, turn);
     if constexpr (RING) {
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, RMS && THREADS == 512 ? 2 : 1)
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       if (q >= have) break;
-      const float r = ok ? 1.f / sqrtf(s[q] * inv_d + eps) : __int_as_float(0x7fffffff);
+      const float r = 1.f / sqrtf(s[q] * inv_d + eps);
       if (tid == 0) {
         if (mean) mean[row + q] = mu[q];
         if (rstd) rstd[row + q] = r;
@@ -518,6 +520,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const size_t jump = (size_t)step * d;
   int turn = 0;
   float* buf = red[warps == 1 ? 0 : group];
+  bool ok = true;  // this thread has not given up waiting
   float mu = 0.f, r = 0.f;
   if (row < rows) mu = RMS ? 0.f : mean[row], r = rstd[row];
   for (; row < rows; row += step, xp += jump, dp += jump, op += jump) {
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (row + step < rows) mu2 = RMS ? 0.f : mean[row + step], r2 = rstd[row + step];
     Raw<T, VEC> xr[VPT], dr[VPT];
     if constexpr (RING) {
-      if (!ring.wait()) r = __int_as_float(0x7fffffff);
+      ok = ok && ring.wait();
       const uint8_t* src = ring.rows() + (size_t)tid * sizeof(Raw<T, VEC>);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     float s[RMS ? 1 : 2];
-    s[0] = both(wh);
+    s[0] = ok ? both(wh) : quiet_nan();
     if constexpr (!RMS) s[1] = both(ws);
     if (RING && warps == 1) __syncwarp();
     group_sum<RMS ? 1 : 2>(s, warps, tid >> 5, group, buf, turn);
@@ -596,6 +599,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if constexpr (RING) ring.close();
   if (!partial) return;
+  if constexpr (RING) {
+    __syncthreads();
+    if (!ring.open()) {  // a thread gave up: the sums hold what was never loaded
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) dg[k] = db[k] = f2(quiet_nan(), quiet_nan());
+    }
+  }
   float* sums = reinterpret_cast<float*>(dyn);  // every copy has landed and been read
   auto flush = [&](const F2 (&acc2)[N / 2], float* out) {
     float acc[N];
