@@ -36,6 +36,11 @@
 // singular values (0.2 where the direct form has 3e-3, singular values falling as
 // 1/k).
 //
+// Waits are bounded (common.cuh).  One that expires leaves a part of a product
+// unwritten and raises the workspace's flag: the last product, which reads the flag
+// once its predecessors are done, then makes every result NaN.  What a wait of the
+// last product itself keeps from being computed is written as NaN.
+//
 // Matrices with m <= 128 and n up to a cluster's shared memory take one launch of
 // the kernel in ortho_chip.cu; what follows here serves the others.
 #include <cuda.h>
@@ -273,6 +278,12 @@ struct Tiles {
   __device__ bool mirrored(int i, int j) const { return SYM && (j + 1) * BN <= i * BM; }
 };
 
+// kLast: whether a wait in one of the call's earlier products expired.
+template <int OP>
+__device__ __forceinline__ bool predecessors_failed(const Product& p) {
+  return OP == kLast && (*static_cast<const volatile int*>(p.err) & kErrTimeout);
+}
+
 // The factor of a product's accumulators.
 template <int OP>
 __device__ __forceinline__ float product_scale(const Product& p, int mat) {
@@ -506,16 +517,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // A warp reads its TMEM lane quarter (row = lane); the two warps of a
     // quarter take one half of the unit's columns each, 32 at a time.
     const int q = warp & 3, half = (warp - 2) >> 2;
+    const bool failed = predecessors_failed<OP>(p);
+    bool ok = true;  // once a wait has expired: NaN for this warp's share of all units left
     int it = 0;
     for (int u = pair; u < total; u += n_pairs, ++it) {
       int mat, ti, col, width;
       unit(u, mat, ti, col, width);
       const int buf = it & 1;
-      if (!tc::mbar_wait_warp(accf0 + 8u * buf, (uint32_t)(it >> 1) & 1u, abort_flag, p.err)) break;
+      ok = ok && tc::mbar_wait_warp(accf0 + 8u * buf, (uint32_t)(it >> 1) & 1u, abort_flag, p.err);
+      if (!ok && OP != kLast) break;
       tc_fence_after();
       const int row = ti * 256 + (int)rank * 128 + q * 32 + lane;
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-      const float alpha = product_scale<OP>(p, mat);
+      const float alpha = ok && !failed ? product_scale<OP>(p, mat) : quiet_nan();
       const bool mirror = tiles.mirrored(ti, col / BN);
 #pragma unroll 1
       for (int cc = half * (width / 2); cc < (half + 1) * (width / 2); cc += 32) {
@@ -544,7 +558,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(acce0 + 8u * buf, 0));
+      // after giving up, no arrival that would count for a warp still reading
+      if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(acce0 + 8u * buf, 0));
     }
   }
 
@@ -687,14 +702,15 @@ __global__ void __launch_bounds__(kSmallThreads)
         load_gram<OP, 16>(p, mat, row, tj * kSmallN + 16 * i,
                           *reinterpret_cast<uint4(*)[2]>(&gram[2 * i]));
     }
+    const bool failed = predecessors_failed<OP>(p);
     const bool ready = tc::mbar_wait_warp(accf, 0, abort_flag, p.err);
     tc_fence_after();
     const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
-    const float alpha = product_scale<OP>(p, mat);
+    const float alpha = ready && !failed ? product_scale<OP>(p, mat) : quiet_nan();
     float* part = reinterpret_cast<float*>(smem);  // [kSmallN][128]
 #pragma unroll
     for (int cc = 0; cc < kSmallN; cc += 16) {  // rowsQ is a multiple of the tile's width
-      if (!ready) break;
+      if (!ready && OP != kLast) break;
       const int c0 = tj * kSmallN + cc;
       uint32_t a[16];
       tmem_ld16(tb + cc, a);

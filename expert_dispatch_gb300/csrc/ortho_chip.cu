@@ -18,8 +18,10 @@
 // launches, about 64 us of host time and 2 to 5 us a launch on the GPU.
 //
 // Every wait is bounded; one that expires raises the CTA's abort flag and the
-// workspace's error flag, and the CTA goes on through the same barriers (its
-// later waits end early), so that no partner is left behind.
+// workspace's error flag, and the warp goes on through the same barriers, so that
+// no partner is left behind.  It waits for no product again and writes NaN in the
+// place of everything that it takes from the accumulators from then on; the next
+// products carry that through the matrix.
 #include <cuda.h>
 
 #include <atomic>
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   });
 
   uint32_t parity = 0;
+  bool ok = true;  // this warp has not given up waiting
   volatile int* abort_flag = &abort_s;
   // Every thread's stores to the operands are in place and every read of the
   // accumulators is done: thread 0 issues the products, all wait for them.
@@ -329,12 +332,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       issue();
       umma_commit(bar);
     }
-    (void)tc::mbar_wait_warp(bar, parity, abort_flag, p.err);
+    ok = ok && tc::mbar_wait_warp(bar, parity, abort_flag, p.err);
     parity ^= 1u;
     tc_fence_after();
   };
   const int q = warp & 3, sub = warp >> 2, row = q * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+  auto load_accumulators = [&](int c, uint32_t (&a)[2][16]) {  // 32 columns
+    tmem_ld16(lanes + c, a[0]);
+    tmem_ld16(lanes + c + 16, a[1]);
+    tmem_ld_wait();
+    if (!ok) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a[0][j] = a[1][j] = 0x7fffffffu;  // NaN
+    }
+  };
 
   for (int step = 0; step < p.steps; ++step) {
     const float rho = step == 0 ? rho1 : 1.f;
@@ -352,9 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int c = sub * 32; c < 128; c += 32 * kParts) {
       uint32_t a[2][16];
-      tmem_ld16(lanes + c, a[0]);
-      tmem_ld16(lanes + c + 16, a[1]);
-      tmem_ld_wait();
+      load_accumulators(c, a);
       if (C == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 8 columns
@@ -426,13 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int c = sub * 32; c < 128; c += 32 * kParts) {
       uint32_t a[2][16];
-      tmem_ld16(lanes + 128 + c, a[0]);
-      tmem_ld16(lanes + 128 + c + 16, a[1]);
       uint4 gm[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         gm[i] = *reinterpret_cast<const uint4*>(as + chunk_at(row, c + 8 * i));
-      tmem_ld_wait();
+      load_accumulators(128 + c, a);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // 8 columns
         const uint32_t gw[4] = {gm[i].x, gm[i].y, gm[i].z, gm[i].w};
@@ -474,9 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int c = sub * 32; c < w; c += 32 * kParts) {  // w is a multiple of 64
       uint32_t a[2][16];
-      tmem_ld16(lanes + c, a[0]);
-      tmem_ld16(lanes + c + 16, a[1]);
-      tmem_ld_wait();
+      load_accumulators(c, a);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[16];

@@ -652,7 +652,7 @@ def moe_orthogonalize(desc, g, out, ws, stream=None):
 
 def orthogonalize(g, steps=5, eps=1e-7):
     """moe_orthogonalize of g [n_mats, rows, cols] or [rows, cols] (fp32 or bf16) into a
-    fresh bf16 tensor, on the current stream."""
+    fresh bf16 tensor, on the current stream.  A bounded wait that expires shows as NaN in it."""
     stack = g if g.dim() == 3 else g.unsqueeze(0)
     desc = make_ortho_desc(stack, steps, eps)
     out = torch.empty(stack.shape, dtype=torch.bfloat16, device=g.device)

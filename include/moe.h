@@ -521,8 +521,9 @@ moe_status moe_ortho_workspace_size(const moe_ortho_desc* desc, size_t* bytes);
    the others of the stack are not touched by it.
    rows and cols from 1 to 65536, n_mats up to 65535 and n_mats * max(rows, cols)
    (rounded up to 64) up to 2^30 (beyond: MOE_ERR_UNSUPPORTED).  out may not
-   be g.  moe_get_device_status(workspace, ...) reports a bounded wait that
-   expired. */
+   be g.  Should a bounded wait expire, the results that it kept from being computed
+   are NaN, and moe_get_device_status(workspace, ...) reports it until the next call
+   on the same workspace: every call clears the workspace's flag when it starts. */
 moe_status moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* out,
                              void* workspace, size_t ws_bytes, void* stream);
 

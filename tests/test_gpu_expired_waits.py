@@ -89,3 +89,34 @@ def test_norm_rows_of_an_expired_wait_are_nan(on_expiring, T, d, dtype, rms):
     gone = nan_rows(dx, back[0])
     assert bool(gone[0]) and int(gone.sum()) < T // 20
     assert dg.isnan().all() and (rms or db.isnan().all())
+
+
+# on chip in one CTA and in a cluster, 128 x 64 tiles whole and shared by a cluster, SM pairs
+@pytest.mark.parametrize("n,rows,cols", [(2, 100, 90), (3, 70, 300), (1, 128, 2048), (1, 200, 330),
+                                         (1, 256, 4096), (9, 600, 1100), (3, 1000, 2500)])
+def test_ortho_results_of_an_expired_wait_are_nan(on_expiring, n, rows, cols):
+    g = rnd((n, rows, cols), 1, torch.bfloat16)
+    want = moe.orthogonalize(g)
+    desc = moe.make_ortho_desc(g)
+    ws = torch.zeros(moe.moe_ortho_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    flags = ws[:16].view(torch.int32)
+
+    def call(expires):
+        flags.copy_(torch.tensor([0, expires, 0, 0], dtype=torch.int32))
+        out = torch.full_like(want, 7.0)
+        on_expiring(lambda: moe.moe_orthogonalize(desc, g, out, ws))
+        return out, moe.moe_get_device_status(ws)
+
+    out, status = call(-1)
+    assert status == moe.MOE_OK and torch.equal(out, want)
+    waits = int(flags[2])  # of one warp: 15 products on chip or in launches, some twice
+    assert waits >= 15
+    for at in (0, 1, 2, waits // 2, waits - 5, waits - 1):
+        out, status = call(at)
+        assert status == moe.MOE_ERR_TIMEOUT
+        assert bool((out.isnan() | (out == want)).all()), at
+        # in the last product only its own share is lost, in whichever matrix that lies
+        assert bool(out.isnan().any() if at == waits - 1 else out[0].isnan().all()), at
+    # the next call on the workspace starts anew
+    out, status = call(-1)
+    assert status == moe.MOE_OK and torch.equal(out, want)
