@@ -527,6 +527,14 @@ def moe_combine_backward(desc, dy, y_perm, expert_offsets, slot_row, topk_w, dy_
 _MOE_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
+def _int32(*sizes):
+    """A record's fields: ctypes would wrap a size that 32 bits do not hold."""
+    for n in sizes:
+        if not -1 << 31 <= n < 1 << 31:
+            raise ValueError("%d does not fit the 32 bits of a record's field" % n)
+    return sizes
+
+
 def make_norm_desc(x, gamma=None, kind=MOE_NORM_LAYER, eps=1e-6) -> NormDesc:
     """The record of a norm over the rows of x [T, d] with gamma's dtype."""
     if x.dim() != 2:
@@ -534,7 +542,7 @@ def make_norm_desc(x, gamma=None, kind=MOE_NORM_LAYER, eps=1e-6) -> NormDesc:
     w = torch.float32 if gamma is None else gamma.dtype
     if x.dtype not in _MOE_DTYPE or w not in _MOE_DTYPE:
         raise TypeError("x and gamma must be fp32 or bf16")
-    return NormDesc(x.shape[0], x.shape[1], kind, _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
+    return NormDesc(*_int32(*x.shape, kind), _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
 
 
 def _norm_param(desc, t, what):
@@ -629,7 +637,7 @@ def make_ortho_desc(g, steps=5, eps=1e-7) -> OrthoDesc:
         raise ValueError("g has shape %s, expected [n_mats, rows, cols]" % (tuple(g.shape),))
     if g.dtype not in _MOE_DTYPE:
         raise TypeError("g must be fp32 or bf16")
-    return OrthoDesc(*g.shape, _MOE_DTYPE[g.dtype], steps, eps)
+    return OrthoDesc(*_int32(*g.shape), _MOE_DTYPE[g.dtype], *_int32(steps), eps)
 
 
 def moe_ortho_workspace_size(desc: OrthoDesc) -> int:

@@ -208,3 +208,18 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="topk_w"):
         moe.moe_combine_backward(d, torch.zeros(4, 64), None, torch.zeros(5), torch.zeros(4, 2),
                                  torch.zeros(4, 3), torch.zeros(8, 64), None)
+
+
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 5])
+def test_sizes_beyond_the_records_fields_are_refused(n):
+    """Not taken modulo 2^32: five rows of 2^32 + 5 would be computed, and no error seen."""
+    x = torch.empty((n, 1), dtype=torch.bfloat16, device="meta")
+    for call in (moe.make_norm_desc, moe.norm, lambda t: moe.norm_backward(t, t, None, None, None)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(x)
+    for shape in ((n, 1, 1), (1, n, 1), (1, 1, n)):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.make_ortho_desc(torch.empty(shape, dtype=torch.bfloat16, device="meta"))
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.make_ortho_desc(x[:4, None], steps=n)
+    assert moe.make_norm_desc(x[:8]).T == 8 and moe.make_ortho_desc(x[:4, None]).n_mats == 4
