@@ -475,6 +475,19 @@ def moe_layer_forward_q8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, residual
 
 
 # ---------------------------------------------------------------- training
+def _here(*tensors):
+    """The training calls launch on the current device: a tensor of another one is refused,
+    where a kernel would read memory that is not its device's."""
+    here = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if here is None:
+                here = torch.cuda.current_device()
+            if t.get_device() != here:
+                raise ValueError("a tensor is on %s, the current device is cuda:%d"
+                                 % (t.device, here))
+
+
 def moe_dispatch_rows(desc, x, expert_offsets, slot_row, x_perm, stream=None):
     """x_perm[slot_row[t, j]] = x[t]; rows left over by dropped pairs are zero."""
     dt = _act_dtype(desc)
@@ -483,6 +496,7 @@ def moe_dispatch_rows(desc, x, expert_offsets, slot_row, x_perm, stream=None):
     _need(expert_offsets, (desc.E + desc.S + 1,), "expert_offsets")
     _need(slot_row, (desc.T, ks), "slot_row")
     _need(x_perm, (desc.T * ks, desc.d), "x_perm")
+    _here(x, expert_offsets, slot_row, x_perm)
     st = lib().moe_dispatch_rows(
         ctypes.byref(desc), _p(x, dt, "x"), _p(expert_offsets, torch.int32, "expert_offsets"),
         _p(slot_row, torch.int32, "slot_row"), _p(x_perm, dt, "x_perm"), _stream(stream))
@@ -496,6 +510,7 @@ def moe_dispatch_rows_backward(desc, dx_perm, slot_row, dx, stream=None):
     _need(dx_perm, (desc.T * ks, desc.d), "dx_perm")
     _need(slot_row, (desc.T, ks), "slot_row")
     _need(dx, (desc.T, desc.d), "dx")
+    _here(dx_perm, slot_row, dx)
     st = lib().moe_dispatch_rows_backward(
         ctypes.byref(desc), _p(dx_perm, dt, "dx_perm"), _p(slot_row, torch.int32, "slot_row"),
         _p(dx, dt, "dx"), _stream(stream))
@@ -516,6 +531,7 @@ def moe_combine_backward(desc, dy, y_perm, expert_offsets, slot_row, topk_w, dy_
     for t, what in ((topk_w, "topk_w"), (dtopk_w, "dtopk_w")):
         if t is not None:
             _need(t, (desc.T, desc.k), what)
+    _here(dy, y_perm, expert_offsets, slot_row, topk_w, dy_perm, dtopk_w)
     st = lib().moe_combine_backward(
         ctypes.byref(desc), _p(dy, torch.float32, "dy"), _p(y_perm, dt, "y_perm"),
         _p(expert_offsets, torch.int32, "expert_offsets"), _p(slot_row, torch.int32, "slot_row"),
@@ -560,6 +576,7 @@ def _norm_stat(desc, t, what):
 
 def _norm_forward(desc, x, gamma, beta, y, mean, rstd, stream):
     """moe_norm_forward with y, mean and rstd as pointers."""
+    _here(x, gamma, beta)
     st = lib().moe_norm_forward(
         ctypes.byref(desc), _p(x, _act_dtype(desc), "x"), _norm_param(desc, gamma, "gamma"),
         _norm_param(desc, beta, "beta"), y, mean, rstd, _stream(stream))
@@ -569,6 +586,7 @@ def _norm_forward(desc, x, gamma, beta, y, mean, rstd, stream):
 def moe_norm_forward(desc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
     _need(x, (desc.T, desc.d), "x")
     _need(y, (desc.T, desc.d), "y")
+    _here(y, mean, rstd)
     _norm_forward(desc, x, gamma, beta, _p(y, _act_dtype(desc), "y"),
                   _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), stream)
 
@@ -584,6 +602,7 @@ def _norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream
     """moe_norm_backward with dx, dgamma and dbeta as pointers."""
     dt = _act_dtype(desc)
     _need(dy, (desc.T, desc.d), "dy")
+    _here(dy, x, gamma, mean, rstd, ws)
     st = lib().moe_norm_backward(
         ctypes.byref(desc), _p(dy, dt, "dy"), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
         _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), dx, dgamma, dbeta,
@@ -598,6 +617,7 @@ def moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, str
     for t, what in ((dgamma, "dgamma"), (dbeta, "dbeta")):
         if t is not None:
             _need(t, (desc.d,), what)
+    _here(dx, dgamma, dbeta)
     _norm_backward(desc, dy, x, gamma, mean, rstd, _p(dx, _act_dtype(desc), "dx"),
                    _p(dgamma, torch.float32, "dgamma"), _p(dbeta, torch.float32, "dbeta"), ws,
                    stream)
@@ -652,6 +672,7 @@ def moe_orthogonalize(desc, g, out, ws, stream=None):
     shape = (desc.n_mats, desc.rows, desc.cols)
     _need(g, shape, "g")
     _need(out, shape, "out")
+    _here(g, out, ws)
     st = lib().moe_orthogonalize(
         ctypes.byref(desc), _p(g, _act_dtype(desc), "g"), _p(out, torch.bfloat16, "out"),
         _p(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream))

@@ -42,6 +42,7 @@ class Plan:
 def make_plan(desc, topk_ids, ws) -> Plan:
     """The plan of topk_ids [T, k] int32 (an id outside [0, E) drops its pair); ws as for
     moe.moe_plan_dispatch."""
+    moe._here(topk_ids, ws)
     new = lambda *s: torch.empty(s, dtype=torch.int32, device=topk_ids.device)  # noqa: E731
     ks = desc.k + desc.S
     p = Plan(desc, new(desc.E + desc.S + 1), new(desc.T * ks), new(desc.T, ks))
@@ -113,6 +114,7 @@ def dispatch(x, plan: Plan):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y_perm, topk_w, residual, plan):
+        moe._here(y_perm, topk_w, residual, plan.slot_row)
         ctx.plan = plan
         ctx.save_for_backward(y_perm, topk_w)
         y = torch.empty((plan.desc.T, plan.desc.d), dtype=torch.float32, device=y_perm.device)

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from expert_dispatch_gb300 import build as moe_build
-from expert_dispatch_gb300 import moe
+from expert_dispatch_gb300 import moe, training
 
 FAKE = ctypes.c_void_p(0x10000)  # never dereferenced: validation fails first
 ODD = ctypes.c_void_p(0x10004)
@@ -223,3 +223,40 @@ def test_sizes_beyond_the_records_fields_are_refused(n):
     with pytest.raises(ValueError, match="32 bits"):
         moe.make_ortho_desc(x[:4, None], steps=n)
     assert moe.make_norm_desc(x[:8]).T == 8 and moe.make_ortho_desc(x[:4, None]).n_mats == 4
+
+
+class _Elsewhere(torch.Tensor):
+    """A CPU tensor that says it lies on another GPU."""
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", 1))
+
+    def get_device(self):
+        return 1
+
+    def data_ptr(self):
+        raise AssertionError("its address was about to be used")
+
+
+def test_tensors_of_another_device_are_refused(L, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(_Elsewhere)
+
+    i32 = torch.int32
+    d = moe.make_desc(4, 64, 4, 2, 64, dtype=moe.MOE_F32)
+    nd = moe.make_norm_desc(torch.zeros(4, 64))
+    od = moe.make_ortho_desc(torch.zeros(1, 4, 64))
+    x, rows, slot, off = t(4, 64), t(8, 64), t(4, 2, dtype=i32), t(5, dtype=i32)
+    ws, s4, s64 = t(1 << 20, dtype=torch.uint8), t(4), t(64)
+    for call in (
+            lambda: moe.moe_dispatch_rows(d, x, off, slot, rows),
+            lambda: moe.moe_dispatch_rows_backward(d, rows, slot, x),
+            lambda: moe.moe_combine_backward(d, x, rows, off, slot, t(4, 2), rows, t(4, 2)),
+            lambda: moe.moe_norm_forward(nd, x, s64, None, x, s4, s4),
+            lambda: moe.moe_norm_backward(nd, x, x, s64, s4, s4, x, s64, s64, ws),
+            lambda: moe.moe_orthogonalize(od, x[None], t(1, 4, 64, dtype=torch.bfloat16), ws),
+            lambda: training.make_plan(d, t(4, 2, dtype=i32), ws),
+            lambda: training.combine(rows, t(4, 2), training.Plan(d, off, None, slot))):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
