@@ -51,6 +51,13 @@ def make_plan(desc, topk_ids, ws) -> Plan:
     return p
 
 
+def _grad(g):
+    """An incoming gradient as the calls take it: contiguous and 16-byte aligned.  Torch passes
+    views on too, where what followed cut or joined rows, and a view may begin anywhere."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, kind, eps):
@@ -73,7 +80,7 @@ class _Norm(torch.autograd.Function):
             ws = torch.empty(moe.moe_norm_workspace_size(desc), dtype=torch.uint8,
                              device=x.device)
         dx = torch.empty_like(x)
-        moe.moe_norm_backward(desc, dy.reshape(x.shape).contiguous(), x, gamma, mean, rstd, dx,
+        moe.moe_norm_backward(desc, _grad(dy.reshape(x.shape)), x, gamma, mean, rstd, dx,
                               dg, db, ws)
         return (dx.view(dy.shape), dg.to(gamma.dtype) if want_g else None,
                 db.to(ctx.beta_dtype) if want_b else None, None, None)
@@ -102,7 +109,7 @@ class _Dispatch(torch.autograd.Function):
     def backward(ctx, dx_perm):
         p = ctx.plan
         dx = torch.empty((p.desc.T, p.desc.d), dtype=dx_perm.dtype, device=dx_perm.device)
-        moe.moe_dispatch_rows_backward(p.desc, dx_perm.contiguous(), p.slot_row, dx)
+        moe.moe_dispatch_rows_backward(p.desc, _grad(dx_perm), p.slot_row, dx)
         return dx, None
 
 
@@ -127,7 +134,7 @@ class _Combine(torch.autograd.Function):
         p = ctx.plan
         y_perm, topk_w = ctx.saved_tensors
         want_rows, want_w, want_res = ctx.needs_input_grad[:3]
-        dy = dy.contiguous()
+        dy = _grad(dy)
         dy_perm = dw = None
         if want_rows or want_w:
             dy_perm = torch.empty_like(y_perm)

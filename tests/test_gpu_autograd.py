@@ -89,6 +89,35 @@ def test_rms_norm_shapes_and_partial_gradients():
         torch.autograd.grad(grad.sum(), v)
 
 
+def _joined(first, y):
+    """torch.cat hands on a gradient that begins behind `first`'s, at an odd address."""
+    return torch.cat([first.view(-1), y.reshape(-1)])
+
+
+def test_gradients_at_any_address():
+    desc, plan = make()
+    x, w, g = rnd((desc.T, 45), 1), rnd((desc.T, desc.k), 2), rnd((45,), 3)
+    h = rnd((desc.T, desc.d), 4)
+    rows = rnd((plan.rows, desc.d), 5)
+    for f, leaves in ((lambda a, b: training.layer_norm(a, b), (x, g)),
+                      (lambda a, b: training.rms_norm(a, b), (x.bfloat16(), g)),
+                      (lambda a: training.dispatch(a, plan), (h,)),
+                      (lambda a, b: training.combine(a, b, plan), (rows, w))):
+        grads = []
+        for joined in (False, True):
+            on = [t.clone().requires_grad_() for t in leaves]
+            y = f(*on)
+            dy = rnd(tuple(y.shape), 6).to(y.dtype)
+            if joined:
+                first = torch.ones(1, dtype=y.dtype, device="cuda", requires_grad=True)
+                _joined(first, y).backward(_joined(first.detach(), dy))
+            else:
+                y.backward(dy)
+            grads.append([t.grad for t in on])
+        for p, q in zip(*grads):
+            assert torch.equal(p, q)
+
+
 def test_on_another_stream():
     desc, plan = make()
     x, w, dy = rnd((desc.T, desc.d), 1), rnd((desc.T, desc.k), 2), rnd((desc.T, desc.d), 3)
