@@ -480,10 +480,11 @@ def _here(*tensors):
     where a kernel would read memory that is not its device's."""
     here = None
     for t in tensors:
-        if t is not None and t.is_cuda:
+        at = -1 if t is None else t.get_device()  # -1: not a CUDA tensor, refused elsewhere
+        if at != here and at >= 0:
             if here is None:
                 here = torch.cuda.current_device()
-            if t.get_device() != here:
+            if at != here:
                 raise ValueError("a tensor is on %s, the current device is cuda:%d"
                                  % (t.device, here))
 
