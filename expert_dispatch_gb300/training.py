@@ -26,7 +26,11 @@ from . import moe
 
 
 class Plan:
-    """moe_plan_dispatch's record of one routing: rows per expert, row of every pair."""
+    """moe_plan_dispatch's record of one routing: rows per expert, row of every pair.
+
+    A backward pass needs the plan that its forward pass took: torch raises if one of the
+    tensors has been written in between by its own operations, and a later
+    moe.moe_plan_dispatch needs tensors of its own."""
 
     def __init__(self, desc, expert_offsets, token_indices, slot_row):
         self.desc = desc
@@ -99,7 +103,8 @@ def rms_norm(x, gamma=None, eps=1e-6):
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, plan):
-        ctx.plan = plan
+        ctx.desc = plan.desc
+        ctx.save_for_backward(plan.slot_row)
         out = torch.empty((plan.rows, plan.desc.d), dtype=x.dtype, device=x.device)
         moe.moe_dispatch_rows(plan.desc, x, plan.expert_offsets, plan.slot_row, out)
         return out
@@ -107,9 +112,10 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dx_perm):
-        p = ctx.plan
-        dx = torch.empty((p.desc.T, p.desc.d), dtype=dx_perm.dtype, device=dx_perm.device)
-        moe.moe_dispatch_rows_backward(p.desc, _grad(dx_perm), p.slot_row, dx)
+        (slot_row,) = ctx.saved_tensors
+        desc = ctx.desc
+        dx = torch.empty((desc.T, desc.d), dtype=dx_perm.dtype, device=dx_perm.device)
+        moe.moe_dispatch_rows_backward(desc, _grad(dx_perm), slot_row, dx)
         return dx, None
 
 
@@ -122,8 +128,8 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y_perm, topk_w, residual, plan):
         moe._here(y_perm, topk_w, residual, plan.slot_row)
-        ctx.plan = plan
-        ctx.save_for_backward(y_perm, topk_w)
+        ctx.desc = plan.desc
+        ctx.save_for_backward(y_perm, topk_w, plan.expert_offsets, plan.slot_row)
         y = torch.empty((plan.desc.T, plan.desc.d), dtype=torch.float32, device=y_perm.device)
         moe.moe_combine(plan.desc, y_perm, plan.slot_row, topk_w, residual, y)
         return y
@@ -131,15 +137,14 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        p = ctx.plan
-        y_perm, topk_w = ctx.saved_tensors
+        y_perm, topk_w, expert_offsets, slot_row = ctx.saved_tensors
         want_rows, want_w, want_res = ctx.needs_input_grad[:3]
         dy = _grad(dy)
         dy_perm = dw = None
         if want_rows or want_w:
             dy_perm = torch.empty_like(y_perm)
             dw = torch.empty_like(topk_w) if want_w else None
-            moe.moe_combine_backward(p.desc, dy, y_perm, p.expert_offsets, p.slot_row, topk_w,
+            moe.moe_combine_backward(ctx.desc, dy, y_perm, expert_offsets, slot_row, topk_w,
                                      dy_perm, dw)
         return dy_perm if want_rows else None, dw, dy if want_res else None, None
 

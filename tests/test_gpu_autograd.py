@@ -118,6 +118,21 @@ def test_gradients_at_any_address():
             assert torch.equal(p, q)
 
 
+def test_a_plan_written_before_the_backward_pass_is_noticed():
+    desc, plan = make()
+    x = rnd((desc.T, desc.d), 1).requires_grad_()
+    rows = rnd((plan.rows, desc.d), 2).requires_grad_()
+    w = rnd((desc.T, desc.k), 3)
+    for f, t in ((lambda: training.dispatch(x, plan), plan.slot_row),
+                 (lambda: training.combine(rows, w, plan), plan.slot_row),
+                 (lambda: training.combine(rows, w, plan), plan.expert_offsets)):
+        f().sum().backward()
+        y = f()
+        t.add_(0)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+
+
 def test_on_another_stream():
     desc, plan = make()
     x, w, dy = rnd((desc.T, desc.d), 1), rnd((desc.T, desc.k), 2), rnd((desc.T, desc.d), 3)
