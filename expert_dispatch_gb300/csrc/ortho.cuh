@@ -75,7 +75,7 @@ __device__ __forceinline__ Scale matrix_scale(const float* partial, int n, float
   float v;
   int off = 0;
   if (s[0] > 0.f || s[0] != s[0]) {
-    v = sqrtf(s[0] + s[1] * kDown * kDown), off = 84;
+    v = sqrtf(s[0] + s[1] * kDown * kDown) + eps * kDown, off = 84;
   } else if (s[1] > 0.f || s[1] != s[1]) {
     v = sqrtf(s[1] + s[2] * kDown * kDown) + eps;
   } else if (eps > 0.f) {

@@ -446,6 +446,15 @@ def test_ortho_scales_by_powers_of_two_change_nothing(rows):
     check_ortho(moe.orthogonalize(small, eps=1e-7), ref_ortho(small, 5, 1e-7))
 
 
+@pytest.mark.parametrize("rows", [90, 190])
+def test_ortho_eps_counts_beside_very_large_matrices(rows):
+    """The norm is about 1.2 times (rows = 90) and 0.9 times eps."""
+    g = rnd((2, rows, 440), 1) * 2.0 ** 60
+    eps = 2.0 ** 67 * (1.3 if rows == 90 else 2.5)
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    check_ortho(moe.orthogonalize(g, eps=eps), ref_ortho(g, 5, eps))
+
+
 @pytest.mark.parametrize("rows", [70, 170])
 def test_ortho_zero_and_nan_matrices(rows):
     g = rnd((5, rows, 300), 2)
