@@ -12,7 +12,7 @@
 // result is off by about 1e-3 with fp16 operands and 1e-2 with bf16 ones (its
 // own rounding to bf16 is 1.7e-3).  fp16's narrow range is met by powers of two:
 // X is stored times 2^10 (entries up to about 1.2, of order 1/sqrt(m n) at the
-// start), A times 2^14 (up to 1.5, and 1/m) and B times 2^12 (up to 3.5).
+// start; where eps outweighs |G|, more: Scale in ortho.cuh), A times 2^14 (up to 1.5, and 1/m) and B times 2^12 (up to 3.5).
 // Because |G|_F is rounded down to a power of two for the first X, a bf16 input
 // is held without error; the remaining factor in (1/2, 1] is applied in fp32 to
 // the first products.  B holds a I + b A + c A A as one matrix, so the update
@@ -224,7 +224,8 @@ struct Product {
   int K;             // reduction length, a multiple of 64
   int rowsP, rowsQ;  // padded rows and columns of a product: multiples of 64
   int m, n;          // the matrices' own size
-  int first;         // X is the first one: apply rho
+  int steps;         // steps behind the X that is read: 0, the first one, takes rho; -1: no X
+  int ahead;         // kApply: steps that the product takes X forward
   float alpha;       // kGram, kApply, kLast: factor of the accumulators
   int whole, cut;    // SM pairs: units that are whole tiles; the rest are cut into `cut` parts
   const Scale* scales;
@@ -287,10 +288,13 @@ __device__ __forceinline__ bool predecessors_failed(const Product& p) {
 // The factor of a product's accumulators.
 template <int OP>
 __device__ __forceinline__ float product_scale(const Product& p, int mat) {
-  const float rho = p.first ? p.scales[mat].rho : 1.f;
-  return OP == kPoly   ? kC * (kScaleB / (kScaleA * kScaleA))
-         : OP == kGram ? rho * rho * p.alpha
-                       : rho * p.alpha;
+  if (OP == kPoly) return kC * (kScaleB / (kScaleA * kScaleA));
+  if (p.steps < 0) return p.alpha;
+  const Scale s = p.scales[mat];
+  const float rho = p.steps == 0 ? s.rho : 1.f;
+  return OP == kGram    ? gram_factor(s, rho * rho * p.alpha, p.steps)
+         : OP == kApply ? apply_factor(s, rho * p.alpha, p.steps, p.ahead)
+                        : last_factor(s, rho * p.alpha, p.steps);
 }
 
 // kPoly: W columns (8 or 16) of A, to be loaded ahead of their use; other kinds
@@ -524,12 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int mat, ti, col, width;
       unit(u, mat, ti, col, width);
       const int buf = it & 1;
+      const float scale = product_scale<OP>(p, mat);
       ok = ok && tc::mbar_wait_warp(accf0 + 8u * buf, (uint32_t)(it >> 1) & 1u, abort_flag, p.err);
       if (!ok && OP != kLast) break;
       tc_fence_after();
       const int row = ti * 256 + (int)rank * 128 + q * 32 + lane;
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-      const float alpha = ok && !failed ? product_scale<OP>(p, mat) : quiet_nan();
+      const float alpha = ok && !failed ? scale : quiet_nan();
       const bool mirror = tiles.mirrored(ti, col / BN);
 #pragma unroll 1
       for (int cc = half * (width / 2); cc < (half + 1) * (width / 2); cc += 32) {
@@ -703,10 +708,11 @@ __global__ void __launch_bounds__(kSmallThreads)
                           *reinterpret_cast<uint4(*)[2]>(&gram[2 * i]));
     }
     const bool failed = predecessors_failed<OP>(p);
+    const float scale = product_scale<OP>(p, mat);
     const bool ready = tc::mbar_wait_warp(accf, 0, abort_flag, p.err);
     tc_fence_after();
     const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
-    const float alpha = ready && !failed ? product_scale<OP>(p, mat) : quiet_nan();
+    const float alpha = ready && !failed ? scale : quiet_nan();
     float* part = reinterpret_cast<float*>(smem);  // [kSmallN][128]
 #pragma unroll
     for (int cc = 0; cc < kSmallN; cc += 16) {  // rowsQ is a multiple of the tile's width
@@ -1030,16 +1036,17 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
   };
   const bool pairs = pair_steps(D.n_mats, L.mp, L.np);
   int at = 0;  // which x holds X
+  int done = 0;
   bool paired = false;
   for (int left = D.steps; left > 0;) {
     paired = pairs && !paired && left >= 2;
-    p.first = left == D.steps;
-    left -= paired ? 2 : 1;
+    p.ahead = paired ? 2 : 1;
+    left -= p.ahead;
+    p.steps = done;
     p.K = L.np, p.rowsP = p.rowsQ = L.mp;
     p.out = gram, p.alpha = kScaleA / (kScaleX * kScaleX);
     if ((e = product<kGram>(mx[at], mx[at], p, s)) != cudaSuccess) return e;
-    const bool scaled = p.first;
-    p.first = 0;
+    p.steps = -1;
     p.K = L.mp;
     p.gram = gram, p.out = poly;
     if ((e = product<kPoly>(mg, mg, p, s)) != cudaSuccess) return e;
@@ -1052,7 +1059,7 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
           (e = square(mq, mb, gram, kScaleQ / (kScaleB * kScaleB))) != cudaSuccess)   // B1 B0
         return e;
     }
-    p.first = scaled;
+    p.steps = done;
     p.K = p.rowsP = L.mp, p.rowsQ = L.np;
     p.out = x[at ^ 1];
     p.alpha = 1.f / (paired ? kScaleQ : kScaleB);
@@ -1065,6 +1072,7 @@ cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* o
     }
     if (e != cudaSuccess) return e;
     at ^= 1;
+    done += p.ahead;
   }
   return cudaSuccess;
 }

@@ -19,8 +19,28 @@ constexpr float kScaleM = 8192.f, kScaleQ = 1024.f;
 struct Scale {
   float f1, f2;  // X = g * f1 * f2, powers of two (one factor could leave fp32's range)
   float rho;     // what is left of 1 / (|G| + eps), in (1/2, 1]
-  float pad;
+  int shift;     // X is held 2^shift larger than its 2^10 says: where eps outweighs |G|
 };
+
+// X is small as long as eps outweighs |G|, and a step makes it 3.4445 times larger
+// at most.  So after `steps` steps it is held 2^(shift - 2 steps) larger than
+// otherwise, and its values stay in fp16's range: without it a matrix of 1e-8 eps
+// came out 38 % off, one of 1e-9 eps as zeros.
+__device__ __forceinline__ int shift_after(const Scale& s, int steps) {
+  return max(s.shift - 2 * steps, 0);
+}
+// The factor of X X^T, and of B X, `ahead` steps further on; f includes rho where
+// X is the first one.
+__device__ __forceinline__ float gram_factor(const Scale& s, float f, int steps) {
+  return s.shift ? scalbnf(f, -2 * shift_after(s, steps)) : f;
+}
+__device__ __forceinline__ float apply_factor(const Scale& s, float f, int steps, int ahead) {
+  return s.shift ? scalbnf(f, shift_after(s, steps + ahead) - shift_after(s, steps)) : f;
+}
+// The same where the result is no longer held larger.
+__device__ __forceinline__ float last_factor(const Scale& s, float f, int steps) {
+  return s.shift ? scalbnf(f, -shift_after(s, steps)) : f;
+}
 
 // V consecutive elements as fp32: 16 aligned bytes, or one element.
 template <typename T, int V>
@@ -71,26 +91,32 @@ __device__ __forceinline__ Scale matrix_scale(const float* partial, int n, float
   for (int q = 0; q < 3; ++q)
 #pragma unroll
     for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
-  // |G| + eps = v * 2^off
-  float v;
-  int off = 0;
+  // |G| = norm * 2^off, |G| + eps = v * 2^off_v
+  float norm, v;
+  int off = 0, off_v = 0;
   if (s[0] > 0.f || s[0] != s[0]) {
-    v = sqrtf(s[0] + s[1] * kDown * kDown) + eps * kDown, off = 84;
+    norm = sqrtf(s[0] + s[1] * kDown * kDown), off = 84;
+    v = norm + eps * kDown, off_v = 84;
   } else if (s[1] > 0.f || s[1] != s[1]) {
-    v = sqrtf(s[1] + s[2] * kDown * kDown) + eps;
-  } else if (eps > 0.f) {
-    v = sqrtf(s[2]) * kDown + eps;
+    norm = sqrtf(s[1] + s[2] * kDown * kDown);
+    v = norm + eps;
   } else {
-    v = sqrtf(s[2]), off = -84;
+    norm = sqrtf(s[2]), off = -84;
+    if (eps > 0.f)
+      v = norm * kDown + eps;
+    else
+      v = norm, off_v = -84;
   }
-  Scale r{0.f, 0.f, 0.f, 0.f};
+  Scale r{0.f, 0.f, 0.f, 0};
   if (v == 0.f) return r;  // a zero matrix, eps = 0: X = 0
   if (isinf(v) || v != v) {
     r.f1 = r.f2 = r.rho = __int_as_float(0x7fffffff);
     return r;
   }
   const int e = ilogbf(v);
-  const int k = 10 - e - off;  // X = g * 2^k
+  // |G| 2^shift stays below 2^(e + off_v), as large as |G| + eps at most
+  if (norm > 0.f) r.shift = max(e + off_v - (ilogbf(norm) + off) - 1, 0);
+  const int k = 10 - e - off_v + r.shift;  // X = g * 2^k
   r.f1 = scalbnf(1.f, k / 2);
   r.f2 = scalbnf(1.f, k - k / 2);
   r.rho = 1.f / scalbnf(v, -e);

@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  const float f1 = sc.f1, f2 = sc.f2, rho1 = sc.rho;
+  const Scale scale = sc;
+  const float f1 = scale.f1, f2 = scale.f2;
   over_slice([&](int line, int at, const float (&v)[V]) {
     const int len = slice.length;
     if (!tall && V == 8 && (at & 7) == 0 && at + V <= len) {
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   for (int step = 0; step < p.steps; ++step) {
-    const float rho = step == 0 ? rho1 : 1.f;
+    const float rho = step == 0 ? scale.rho : 1.f;
     // ---- A = X X^T, this slice's part: TMEM columns 0 .. 127
     product([&] {
       constexpr uint32_t idesc = idesc_f16_f32(128, 128);
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_bf16(tmem, d, d, idesc, b | kk ? 1u : 0u);
         }
     });
-    const float alpha = rho * rho * (kScaleA / (kScaleX * kScaleX));
+    const float alpha = gram_factor(scale, rho * rho * (kScaleA / (kScaleX * kScaleX)), step);
 #pragma unroll 1
     for (int c = sub * 32; c < 128; c += 32 * kParts) {
       uint32_t a[2][16];
@@ -478,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     });
     const bool last = step + 1 == p.steps;
-    const float beta = last ? rho / (kScaleB * kScaleX) : rho / kScaleB;
+    const float beta = last ? last_factor(scale, rho / (kScaleB * kScaleX), step)
+                            : apply_factor(scale, rho / kScaleB, step, 1);
 #pragma unroll 1
     for (int c = sub * 32; c < w; c += 32 * kParts) {  // w is a multiple of 64
       uint32_t a[2][16];

@@ -455,6 +455,22 @@ def test_ortho_eps_counts_beside_very_large_matrices(rows):
     check_ortho(moe.orthogonalize(g, eps=eps), ref_ortho(g, 5, eps))
 
 
+@pytest.mark.parametrize("n,rows,cols", [(2, 90, 440), (1, 128, 2048), (2, 190, 440),
+                                         (3, 1000, 2500)])
+@pytest.mark.parametrize("steps", [1, 5])
+def test_ortho_matrices_far_below_eps(n, rows, cols, steps):
+    """X is then G / eps and small for all steps; its own size decides how it is held."""
+    g = rnd((n, rows, cols), 1)
+    g /= g.double().square().sum((1, 2), keepdim=True).sqrt().float()
+    eps = 2.0 ** -20
+    for e in (-6, -13, -20, -27, -34, -60, -90):  # of the norm, in eps
+        small = g * (eps * 2.0 ** e)
+        check_ortho(moe.orthogonalize(small, steps=steps, eps=eps), ref_ortho(small, steps, eps))
+    # a stack of all these beside ordinary matrices
+    mixed = torch.cat([g, g * (eps * 2.0 ** -34), g * eps])
+    check_ortho(moe.orthogonalize(mixed, steps=steps, eps=eps), ref_ortho(mixed, steps, eps))
+
+
 @pytest.mark.parametrize("rows", [70, 170])
 def test_ortho_zero_and_nan_matrices(rows):
     g = rnd((5, rows, 300), 2)
