@@ -12,7 +12,8 @@
 // result is off by about 1e-3 with fp16 operands and 1e-2 with bf16 ones (its
 // own rounding to bf16 is 1.7e-3).  fp16's narrow range is met by powers of two:
 // X is stored times 2^10 (entries up to about 1.2, of order 1/sqrt(m n) at the
-// start; where eps outweighs |G|, more: Scale in ortho.cuh), A times 2^14 (up to 1.5, and 1/m) and B times 2^12 (up to 3.5).
+// start; where eps outweighs |G|, more: Scale in ortho.cuh), A times 2^14 (up to 1.5,
+// and 1/m) and B times 2^12 (up to 3.5).
 // Because |G|_F is rounded down to a power of two for the first X, a bf16 input
 // is held without error; the remaining factor in (1/2, 1] is applied in fp32 to
 // the first products.  B holds a I + b A + c A A as one matrix, so the update

@@ -418,15 +418,21 @@ moe_status moe_layer_forward_q8_host_pipelined(const moe_layer_desc* desc, int n
 /* ---------------------------------------------------------------- training
    What a training step needs around the expert FFN: the norm in front of the
    router, the row movement as calls of its own, and their gradients.  The
-   pages describe the forward only; these are the derivatives of its formulas. */
+   pages describe the forward only; these are the derivatives of its formulas.
+
+   slot_row is a plan's: every entry is -1 or below expert_offsets[E+S].  These
+   calls and moe_combine skip an entry outside [0, T*(k+S)), like -1.  An entry
+   between expert_offsets[E+S] and T*(k+S) is in no plan, and they differ on it:
+   moe_dispatch_rows and moe_combine_backward skip it, moe_combine and
+   moe_dispatch_rows_backward, which take no expert_offsets, read the row it names,
+   so that for such an entry these are not each other's gradients. */
 
 /* moe_dispatch_rows -- the rows of every batch, from the plan:
      x_perm[slot_row[t, j]] = x[t]   for every pair (t, j), j < k + S.
      expert_offsets [E+S+1], slot_row [T, k+S]: from moe_plan_dispatch.
      x_perm [T*(k+S), d] out, the layer's dtype.  The rows from
                     expert_offsets[E+S] on (left over by dropped pairs, whose
-                    slot_row is -1) are set to zero.
-   A slot_row outside [0, expert_offsets[E+S]) is skipped. */
+                    slot_row is -1) are set to zero. */
 moe_status moe_dispatch_rows(const moe_layer_desc* desc, const void* x,
                              const int32_t* expert_offsets, const int32_t* slot_row,
                              void* x_perm, void* stream);

@@ -367,6 +367,32 @@ def test_rows_outside_the_batches_are_skipped():
         assert torch.equal(a, b)
 
 
+def test_an_entry_in_the_rows_left_over():
+    """No plan has one; what the calls do with it is what their header says."""
+    desc, slot, off, w = rows_case(dict(T=12, d=64, E=4, k=2, S=0, drop=0.4), "f32", 8)
+    total = int(off[-1])
+    assert total < 23
+    t, j = divmod(int(torch.nonzero(slot.view(-1) < 0)[0]), 2)
+    bad = slot.clone()
+    bad[t, j] = total + 1
+    x, g, dy = rnd((12, 64), 1), rnd((24, 64), 2), rnd((12, 64), 3)
+    out = []
+    for s in (slot, bad):
+        xp, dyp = rnd((24, 64), 4), rnd((24, 64), 5)
+        dx, dw, y = torch.empty_like(x), torch.empty_like(w), torch.empty_like(x)
+        moe.moe_dispatch_rows(desc, x, off, s, xp)
+        moe.moe_combine_backward(desc, dy, g, off, s, w, dyp, dw)
+        moe.moe_dispatch_rows_backward(desc, g, s, dx)
+        moe.moe_combine(desc, g, s, w, None, y)
+        out.append((xp, dyp, dw, dx, y))
+    for a, b in list(zip(*out))[:3]:
+        assert torch.equal(a, b)
+    for (a, b), f in zip(list(zip(*out))[3:], (1.0, float(w[t, j]))):
+        assert torch.equal(a[:t], b[:t]) and torch.equal(a[t + 1:], b[t + 1:])
+        want = (a[t].double() + f * g[total + 1].double())[None]
+        close(b[t][None], want, 4 * U * (a[t].abs() + g[total + 1].abs())[None].double())
+
+
 # ---------------------------------------------------------------- orthogonalisation
 # Tolerance: the output's rounding to bf16, 2^-8 of each value, and the products'
 # operands: a step rounds X, A and B to fp16, 2^-11 of each value at most and about a
