@@ -239,8 +239,8 @@ struct Product {
 
 constexpr int kThreads = 32 * (2 + tc::kEpiWarps);  // producer, MMA, epilogue
 
-template <int BN, int STAGES>
-struct Cfg {
+struct PairCfg {
+  static constexpr int BN = 256, STAGES = 6;
   static constexpr int A_BYTES = 128 * 128;       // this CTA's 128 rows of P, 64 columns
   static constexpr int B_BYTES = (BN / 2) * 128;  // this CTA's half of Q's rows
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -249,7 +249,6 @@ struct Cfg {
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM_TOTAL = MISC_OFF + 16 + 1024;
-  static_assert(BN == 64 || BN == 128 || BN == 256, "tile");
   static_assert(SMEM_TOTAL + tc::kEpiWarps * 32 * kRowWords * 4 <= 232448, "shared memory");
 };
 
@@ -298,16 +297,15 @@ __device__ __forceinline__ float product_scale(const Product& p, int mat) {
                         : last_factor(s, rho * p.alpha, p.steps);
 }
 
-// kPoly: W columns (8 or 16) of A, to be loaded ahead of their use; other kinds
-// have none.
-template <int OP, int W>
+// kPoly: 16 columns of A, to be loaded ahead of their use; other kinds have none.
+template <int OP>
 __device__ __forceinline__ void load_gram(const Product& p, int mat, int row, int c0,
-                                          uint4 (&g)[W / 8]) {
+                                          uint4 (&g)[2]) {
   if (OP != kPoly || row >= p.rowsP) return;
   const uint4* src =
       reinterpret_cast<const uint4*>(p.gram + ((size_t)mat * p.rowsP + row) * p.rowsQ + c0);
 #pragma unroll
-  for (int i = 0; i < W / 8; ++i) g[i] = src[i];
+  for (int i = 0; i < 2; ++i) g[i] = src[i];
 }
 
 // Accumulators of W columns (8 or 16) of row `row` from column c0 on, already
@@ -355,11 +353,12 @@ __device__ __forceinline__ void store_product(const Product& p, int mat, int row
   }
 }
 
-template <int OP, int BN, int STAGES>
+template <int OP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ortho_product_kernel(const __grid_constant__ CUtensorMap tmP,
                          const __grid_constant__ CUtensorMap tmQ, const Product p) {
-  using C = Cfg<BN, STAGES>;
+  using C = PairCfg;
+  constexpr int BN = C::BN, STAGES = C::STAGES;
   constexpr bool SYM = OP == kGram || OP == kPoly;  // else Q is MN-major
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t scratch[tc::kEpiWarps][OP == kLast ? 32 * kRowWords : 1];
@@ -544,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint4 gram[2][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_gram<OP, 16>(p, mat, row, col + cc + 16 * i, gram[i]);
+          load_gram<OP>(p, mat, row, col + cc + 16 * i, gram[i]);
           tmem_ld16(tb + cc + 16 * i, a[i]);
         }
         tmem_ld_wait();
@@ -579,10 +578,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// The same products where they have few tiles: one CTA a tile of 128 x 64, or
-// a cluster of `split` CTAs that share the tile's reduction length.  There a
-// CTA leaves its partial sums in its shared memory, and after a cluster
-// barrier each adds up its share of the columns over the cluster in rank order.
+// The same products where they have few tiles: one CTA a tile of 128 x 64, or, for
+// X X^T (kGram) with its long reduction, a cluster of `split` CTAs that share the
+// tile's reduction length.  There a CTA leaves its partial sums in its shared
+// memory, and after a cluster barrier each adds up its share of the columns over
+// the cluster in rank order.
 constexpr int kSmallN = 64, kSmallStages = 4, kSmallWarps = 6;  // producer, MMA, 4 epilogue
 constexpr int kSmallThreads = 32 * kSmallWarps;
 constexpr int kMaxSplit = 8;
@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kSmallThreads)
                        const __grid_constant__ CUtensorMap tmQ, const Product p, int split) {
   using C = SmallCfg;
   constexpr bool SYM = OP == kGram || OP == kPoly;
+  if constexpr (OP != kGram) split = 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t scratch[4][OP == kLast ? 32 * kRowWords : 1];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -702,10 +703,10 @@ __global__ void __launch_bounds__(kSmallThreads)
   } else {
     // the row's part of A while the products run
     uint4 gram[kSmallN / 8];
-    if (OP == kPoly && split == 1) {
+    if (OP == kPoly) {
 #pragma unroll
       for (int i = 0; i < kSmallN / 16; ++i)
-        load_gram<OP, 16>(p, mat, row, tj * kSmallN + 16 * i,
+        load_gram<OP>(p, mat, row, tj * kSmallN + 16 * i,
                           *reinterpret_cast<uint4(*)[2]>(&gram[2 * i]));
     }
     const bool failed = predecessors_failed<OP>(p);
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(kSmallThreads)
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = alpha * __uint_as_float(a[j]);
-      if (OP == kLast && split == 1) {
+      if (OP == kLast) {
         store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
                      scratch[warp - 2]);
       } else if (split == 1) {
@@ -745,46 +746,34 @@ __global__ void __launch_bounds__(kSmallThreads)
     tmem_dealloc(tmem_base, kSmallN);
   }
   if (split == 1) return;
-  cluster_sync();  // every CTA's partial sums are in place
-  if (warp >= 2) {
-    const int cols = kSmallN / split;
-    auto joined = [&](int cc, float* v) {  // 8 columns of the row over the cluster
-      const uint32_t mine = sbase + (uint32_t)(cc * 128 + q * 32 + lane) * 4u;
-      float part[kMaxSplit][8];  // all loads in flight before the first sum
+  if constexpr (OP == kGram) {
+    cluster_sync();  // every CTA's partial sums are in place
+    if (warp >= 2) {
+      const int cols = kSmallN / split;  // 8 at least
+      for (int cc = rank * cols; cc < (rank + 1) * cols; cc += 8) {
+        const uint32_t mine = sbase + (uint32_t)(cc * 128 + q * 32 + lane) * 4u;
+        float part[kMaxSplit][8];  // all loads in flight before the first sum
 #pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r) {
-        if (r < split) {
-          const uint32_t peer = mapa_shared(mine, r);
+        for (int r = 0; r < kMaxSplit; ++r) {
+          if (r < split) {
+            const uint32_t peer = mapa_shared(mine, r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) part[r][j] = ld_shared_cluster(peer + (uint32_t)j * 512u);
+            for (int j = 0; j < 8; ++j) part[r][j] = ld_shared_cluster(peer + (uint32_t)j * 512u);
+          }
         }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = part[0][j];
-#pragma unroll
-        for (int r = 1; r < kMaxSplit; ++r)
-          if (r < split) v[j] += part[r][j];
-      }
-    };
-    for (int cc = rank * cols; cc < (rank + 1) * cols; cc += OP == kLast ? 16 : 8) {
-      const int c0 = tj * kSmallN + cc;
-      if constexpr (OP == kLast) {  // its share is 16 columns at least
-        float v[16];
-        joined(cc, v);
-        joined(cc + 8, v + 8);
-        store_result(p.result + (size_t)mat * p.m * p.n, p.m, p.n, p.tall, row - lane, c0, v,
-                     scratch[warp - 2]);
-      } else {
-        uint4 gram[1];
-        load_gram<OP, 8>(p, mat, row, c0, gram);
         float v[8];
-        joined(cc, v);
-        store_product<OP, 8>(p, mat, row, c0, mirror, gram, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = part[0][j];
+#pragma unroll
+          for (int r = 1; r < kMaxSplit; ++r)
+            if (r < split) v[j] += part[r][j];
+        }
+        store_product<OP, 8>(p, mat, row, tj * kSmallN + cc, mirror, nullptr, v);
       }
     }
+    cluster_sync();  // a CTA's shared memory stays until its peers have read it
   }
-  cluster_sync();  // a CTA's shared memory stays until its peers have read it
 }
 
 // ---------------------------------------------------------------- host
@@ -805,8 +794,8 @@ constexpr const char* kOpName[] = {"ortho_gram", "ortho_poly", "ortho_apply", "o
 template <int OP>
 cudaError_t launch_pairs(const OperandMaps& P, const OperandMaps& Q, Product p,
                          long long tiles, cudaStream_t s) {
-  using C = Cfg<256, 6>;
-  auto kern = ortho_product_kernel<OP, 256, 6>;
+  using C = PairCfg;
+  auto kern = ortho_product_kernel<OP>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -904,7 +893,9 @@ Choice choose(int n_mats, int K, int rowsP, int rowsQ) {
   c.large = n * Tiles<256, 256, SYM>(rowsP, rowsQ).count();
   c.small = n * Tiles<128, kSmallN, SYM>(rowsP, rowsQ).count();
   c.cost = (c.large + sms / 2 - 1) / (sms / 2) * blocks * 27 + 550;
-  const int most = OP == kLast ? kMaxSplit / 2 : kMaxSplit;  // 16 columns a CTA at least
+  // only X X^T has a reduction long enough: over all sizes up to 65536 the rule
+  // takes one CTA a tile for the other products
+  const int most = OP == kGram ? kMaxSplit : 1;
   for (int k = 1; k <= most && k <= blocks; k *= 2) {
     const long long each = 125 + 17 * ((blocks + k - 1) / k);
     const long long tiles = c.small * k > sms ? c.small * k : sms;

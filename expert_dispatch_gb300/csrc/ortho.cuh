@@ -42,12 +42,10 @@ __device__ __forceinline__ float last_factor(const Scale& s, float f, int steps)
   return s.shift ? scalbnf(f, -shift_after(s, steps)) : f;
 }
 
-// V consecutive elements as fp32: 16 aligned bytes, or one element.
+// V consecutive elements as fp32: 16 aligned bytes.
 template <typename T, int V>
 __device__ __forceinline__ void load_elems(const T* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = load_as_f32(p, 0);
-  } else if constexpr (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4) {
     const float4 a = *reinterpret_cast<const float4*>(p);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   } else {
