@@ -306,6 +306,22 @@ def test_combine_backward(c, dtype):
     close(b, want, H(dt) * want.abs())
 
 
+# tokens enough that a block takes all slots of a token (combine backward: 608; with whole rows
+# or short ones) and all columns (dispatch backward: 1216)
+LARGE = [dict(T=700, d=4096, E=16, k=8, S=1, drop=0.3, all_dropped=range(0, 700, 50)),
+         dict(T=700, d=256, E=16, k=8, S=1, drop=0.3, all_dropped=range(0, 700, 50)),
+         dict(T=1300, d=2112, E=60, k=6, S=2, drop=0.3, all_dropped=range(1, 1300, 90)),
+         dict(T=1300, d=320, E=8, k=3, S=0, drop=0.2, all_dropped=range(2, 1300, 90)),
+         dict(T=1217, d=1920, E=9, k=5, S=0), dict(T=609, d=64, E=40, k=30, S=4, drop=0.5)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", LARGE)
+def test_rows_of_large_batches(c, dtype):
+    test_dispatch_and_back(c, dtype)
+    test_combine_backward(c, dtype)
+
+
 def test_combine_backward_is_the_derivative_of_moe_combine():
     """y is linear in the rows and in the weights, so a difference of moe_combine's own
     results is exact up to fp32: <dy, combine(rows + e) - combine(rows)> = <dy_perm, e>."""
@@ -445,6 +461,77 @@ def test_ortho_steps(steps):
     check_ortho(moe.orthogonalize(g, steps=steps), ref_ortho(g, steps, 1e-7))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,cols", [
+    (1, 960, 3264),   # two CTAs share a tile's reduction; two steps at once
+    (1, 576, 2112),   # four
+    (1, 512, 2048),   # eight
+    (1, 2112, 576), (4, 256, 2048)])
+def test_ortho_shared_reductions(n, rows, cols, dtype):
+    g = rnd((n, rows, cols), rows + cols, DT[dtype], 0.02)
+    check_ortho(moe.orthogonalize(g), ref_ortho(g, 5, 1e-7))
+
+
+@pytest.mark.parametrize("n,rows,cols", [(3, 1000, 2500), (1, 960, 3264), (4, 2048, 256)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 8])
+def test_ortho_steps_in_pairs(n, rows, cols, steps):
+    """Two steps at once, where these sizes have them: calls that end on a pair, or on one."""
+    g = rnd((n, rows, cols), steps)
+    check_ortho(moe.orthogonalize(g, steps=steps), ref_ortho(g, steps, 1e-7))
+
+
+def rounded_ortho(g, steps, pairs):
+    """The formula in 64 bits with X, A, B and their products rounded to fp16 as they are held,
+    each times its power of two; `pairs`: two steps at once, then one, in turn."""
+    a, b, c = 3.4445, -4.7750, 2.0315
+    sx, sa, sb, sm, sq = 2.0 ** 10, 2.0 ** 14, 2.0 ** 12, 2.0 ** 13, 2.0 ** 10
+    held = lambda t, scale: (t * scale).half().double() / scale  # noqa: E731
+    eye = torch.eye(g.shape[1], dtype=torch.float64, device="cuda")
+    norm = g.double().square().sum((1, 2), keepdim=True).sqrt()
+    two = torch.exp2(torch.floor(torch.log2(norm)))
+    x, rho, paired, left = held(g.double() / two, sx), two / norm, False, steps
+    poly = lambda t: held(a * eye + b * t + c * t @ t, sb)  # noqa: E731
+    while left:
+        paired = pairs and not paired and left >= 2
+        left -= 2 if paired else 1
+        gram = held(rho * rho * (x @ x.transpose(1, 2)), sa)
+        by = poly(gram)
+        if paired:
+            gram = held(held(by @ gram, sm) @ by, sa)
+            by = held(poly(gram) @ by, sq)
+        x = rho * (by @ x)
+        if left:
+            x = held(x, sx)
+        rho = 1.0
+    return x
+
+
+@pytest.mark.parametrize("spectrum", ["1/k", "1/k^2", 0.1, 0.01, 0.003, 0.001])
+@pytest.mark.parametrize("rows,cols,pairs", [(100, 700, False), (192, 768, False),
+                                             (1000, 2500, True)])
+def test_ortho_where_few_directions_dominate(rows, cols, pairs, spectrum):
+    """Singular values falling as 1/k or 1/k^2, or eight large ones and the rest at the given
+    part of them.  There the roundings to fp16 weigh more than for matrices whose singular
+    values grow together.  Bound: the output's rounding, and twice the error that these
+    roundings alone have in 64 bits (the same roundings meet other fp32 sums); the header's
+    4e-2 of the norm holds as well."""
+    rng = np.random.default_rng(rows)
+    k = np.arange(1, rows + 1)
+    sv = (1.0 / k if spectrum == "1/k" else 1.0 / k ** 2 if spectrum == "1/k^2"
+          else np.where(k <= 8, 1.0, spectrum))
+    q1 = np.linalg.qr(rng.standard_normal((rows, rows)))[0]
+    q2 = np.linalg.qr(rng.standard_normal((cols, rows)))[0]
+    g = torch.from_numpy((q1 * sv) @ q2.T).cuda().float()[None]
+    n = 3 if pairs else 1  # with one matrix of this size the steps stay single
+    got = moe.orthogonalize(g.repeat(n, 1, 1))
+    want = ref_ortho(g, 5, 1e-7)
+    norm = float(want.square().sum().sqrt())
+    alone = float((rounded_ortho(g, 5, pairs) - want).square().sum().sqrt()) / norm
+    for i in range(n):
+        err = float((got[i].double() - want[0]).square().sum().sqrt()) / norm
+        assert err <= 2.0 ** -8 + 2 * alone and err <= 2.0 ** -8 + 4e-2, (err, alone)
+
+
 def test_ortho_singular_values_meet_one():
     """Singular values from 1 down to 0.05 of the largest end between 0.6 and 1.3."""
     q1, q2 = (torch.linalg.qr(rnd((160, 160), s).double())[0] for s in (1, 2))
@@ -561,6 +648,26 @@ def test_ortho_calls_on_several_streams_at_once():
     for o, e, w, s in zip(outs, want, ws, streams):
         assert moe.moe_get_device_status(w, stream=s) == moe.MOE_OK
         assert torch.equal(o, e)
+
+
+def test_ortho_every_call_on_several_streams():
+    """The same with outputs and workspaces of each call's own, so that every call counts."""
+    shapes = [(1, 256, 4096), (2, 128, 2048), (4, 512, 512), (3, 1030, 1100), (20, 100, 400),
+              (3, 1000, 2500)]
+    gs = [rnd(s, i, torch.bfloat16) for i, s in enumerate(shapes)]
+    want = [moe.orthogonalize(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    descs = [moe.make_ortho_desc(g) for g in gs]
+    calls = []
+    for i, s in [(i, s) for _ in range(4) for i, s in enumerate(streams)]:
+        ws = torch.empty(moe.moe_ortho_workspace_size(descs[i]), dtype=torch.uint8, device="cuda")
+        calls.append((i, s, torch.full_like(want[i], float("nan")), ws))
+    torch.cuda.synchronize()
+    for i, s, out, ws in calls:
+        moe.moe_orthogonalize(descs[i], gs[i], out, ws, s)
+    for i, s, out, ws in calls:
+        assert moe.moe_get_device_status(ws, stream=s) == moe.MOE_OK
+        assert torch.equal(out, want[i])
 
 
 # ---------------------------------------------------------------- streams and graphs
