@@ -189,12 +189,13 @@ def lib():
 
 
 # ---------------------------------------------------------------- marshalling helpers
-def _p(t, dtype=None, what="tensor"):
-    """Device pointer of a contiguous CUDA tensor (None -> NULL)."""
+def _p(t, dtype=None, what="tensor", device=None):
+    """Device pointer of a contiguous CUDA tensor (None -> NULL), of the given device if any."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (
-            dtype is None or t.dtype is dtype):
+    if isinstance(t, torch.Tensor) and t.is_contiguous() and (
+            dtype is None or t.dtype is dtype) and (
+            t.is_cuda if device is None else t.get_device() == device):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % what)
@@ -202,13 +203,17 @@ def _p(t, dtype=None, what="tensor"):
         raise ValueError("%s must be a CUDA tensor" % what)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
+    if device is not None and t.get_device() != device:
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d"
+                         % (what, t.get_device(), device))
     raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     """The stream's handle; without one, the current stream of the current device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if device is None else device)
     return stream.cuda_stream
 
 
@@ -475,18 +480,17 @@ def moe_layer_forward_q8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, residual
 
 
 # ---------------------------------------------------------------- training
-def _here(*tensors):
-    """The training calls launch on the current device: a tensor of another one is refused,
-    where a kernel would read memory that is not its device's."""
-    here = None
-    for t in tensors:
-        at = -1 if t is None else t.get_device()  # -1: not a CUDA tensor, refused elsewhere
-        if at != here and at >= 0:
-            if here is None:
-                here = torch.cuda.current_device()
-            if at != here:
-                raise ValueError("a tensor is on %s, the current device is cuda:%d"
-                                 % (t.device, here))
+def _device(t, what):
+    """The current device, which t is on.  The training calls launch there: a tensor of
+    another device (the others are held to this one) is refused, where a kernel would read
+    memory that is not its device's."""
+    at = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if at < 0:
+        _p(t, None, what)  # raises
+    if at != torch.cuda.current_device():
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d"
+                         % (what, at, torch.cuda.current_device()))
+    return at
 
 
 def moe_dispatch_rows(desc, x, expert_offsets, slot_row, x_perm, stream=None):
@@ -497,10 +501,12 @@ def moe_dispatch_rows(desc, x, expert_offsets, slot_row, x_perm, stream=None):
     _need(expert_offsets, (desc.E + desc.S + 1,), "expert_offsets")
     _need(slot_row, (desc.T, ks), "slot_row")
     _need(x_perm, (desc.T * ks, desc.d), "x_perm")
-    _here(x, expert_offsets, slot_row, x_perm)
+    at = _device(x, "x")
     st = lib().moe_dispatch_rows(
-        ctypes.byref(desc), _p(x, dt, "x"), _p(expert_offsets, torch.int32, "expert_offsets"),
-        _p(slot_row, torch.int32, "slot_row"), _p(x_perm, dt, "x_perm"), _stream(stream))
+        ctypes.byref(desc), _p(x, dt, "x", at),
+        _p(expert_offsets, torch.int32, "expert_offsets", at),
+        _p(slot_row, torch.int32, "slot_row", at), _p(x_perm, dt, "x_perm", at),
+        _stream(stream, at))
     _check(st, "moe_dispatch_rows")
 
 
@@ -511,10 +517,10 @@ def moe_dispatch_rows_backward(desc, dx_perm, slot_row, dx, stream=None):
     _need(dx_perm, (desc.T * ks, desc.d), "dx_perm")
     _need(slot_row, (desc.T, ks), "slot_row")
     _need(dx, (desc.T, desc.d), "dx")
-    _here(dx_perm, slot_row, dx)
+    at = _device(dx_perm, "dx_perm")
     st = lib().moe_dispatch_rows_backward(
-        ctypes.byref(desc), _p(dx_perm, dt, "dx_perm"), _p(slot_row, torch.int32, "slot_row"),
-        _p(dx, dt, "dx"), _stream(stream))
+        ctypes.byref(desc), _p(dx_perm, dt, "dx_perm", at),
+        _p(slot_row, torch.int32, "slot_row", at), _p(dx, dt, "dx", at), _stream(stream, at))
     _check(st, "moe_dispatch_rows_backward")
 
 
@@ -532,23 +538,23 @@ def moe_combine_backward(desc, dy, y_perm, expert_offsets, slot_row, topk_w, dy_
     for t, what in ((topk_w, "topk_w"), (dtopk_w, "dtopk_w")):
         if t is not None:
             _need(t, (desc.T, desc.k), what)
-    _here(dy, y_perm, expert_offsets, slot_row, topk_w, dy_perm, dtopk_w)
+    at = _device(dy, "dy")
     st = lib().moe_combine_backward(
-        ctypes.byref(desc), _p(dy, torch.float32, "dy"), _p(y_perm, dt, "y_perm"),
-        _p(expert_offsets, torch.int32, "expert_offsets"), _p(slot_row, torch.int32, "slot_row"),
-        _p(topk_w, torch.float32, "topk_w"), _p(dy_perm, dt, "dy_perm"),
-        _p(dtopk_w, torch.float32, "dtopk_w"), _stream(stream))
+        ctypes.byref(desc), _p(dy, torch.float32, "dy", at), _p(y_perm, dt, "y_perm", at),
+        _p(expert_offsets, torch.int32, "expert_offsets", at),
+        _p(slot_row, torch.int32, "slot_row", at), _p(topk_w, torch.float32, "topk_w", at),
+        _p(dy_perm, dt, "dy_perm", at), _p(dtopk_w, torch.float32, "dtopk_w", at),
+        _stream(stream, at))
     _check(st, "moe_combine_backward")
 
 
 _MOE_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _int32(*sizes):
-    """A record's fields: ctypes would wrap a size that 32 bits do not hold."""
-    for n in sizes:
-        if not -1 << 31 <= n < 1 << 31:
-            raise ValueError("%d does not fit the 32 bits of a record's field" % n)
+def _int32(sizes):
+    """A record's sizes: ctypes would wrap one that 32 bits do not hold."""
+    if max(sizes) >= 1 << 31 or min(sizes) < -1 << 31:
+        raise ValueError("%s does not fit the 32 bits of a record's fields" % (tuple(sizes),))
     return sizes
 
 
@@ -559,37 +565,38 @@ def make_norm_desc(x, gamma=None, kind=MOE_NORM_LAYER, eps=1e-6) -> NormDesc:
     w = torch.float32 if gamma is None else gamma.dtype
     if x.dtype not in _MOE_DTYPE or w not in _MOE_DTYPE:
         raise TypeError("x and gamma must be fp32 or bf16")
-    return NormDesc(*_int32(*x.shape, kind), _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
+    return NormDesc(*_int32(x.shape), kind, _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
 
 
-def _norm_param(desc, t, what):
+def _norm_param(desc, t, what, device):
     if t is None:
         return None
     _need(t, (desc.d,), what)
-    return _p(t, torch.float32 if desc.wdtype == MOE_F32 else torch.bfloat16, what)
+    return _p(t, torch.float32 if desc.wdtype == MOE_F32 else torch.bfloat16, what, device)
 
 
-def _norm_stat(desc, t, what):
+def _norm_stat(desc, t, what, device):
     if t is not None:
         _need(t, (desc.T,), what)
-    return _p(t, torch.float32, what)
+    return _p(t, torch.float32, what, device)
 
 
-def _norm_forward(desc, x, gamma, beta, y, mean, rstd, stream):
-    """moe_norm_forward with y, mean and rstd as pointers."""
-    _here(x, gamma, beta)
+def _norm_forward(desc, x, gamma, beta, y, mean, rstd, stream, at):
+    """moe_norm_forward with y, mean and rstd as pointers, on device `at`."""
     st = lib().moe_norm_forward(
-        ctypes.byref(desc), _p(x, _act_dtype(desc), "x"), _norm_param(desc, gamma, "gamma"),
-        _norm_param(desc, beta, "beta"), y, mean, rstd, _stream(stream))
+        ctypes.byref(desc), _p(x, _act_dtype(desc), "x", at),
+        _norm_param(desc, gamma, "gamma", at), _norm_param(desc, beta, "beta", at), y, mean, rstd,
+        _stream(stream, at))
     _check(st, "moe_norm_forward")
 
 
 def moe_norm_forward(desc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
     _need(x, (desc.T, desc.d), "x")
     _need(y, (desc.T, desc.d), "y")
-    _here(y, mean, rstd)
-    _norm_forward(desc, x, gamma, beta, _p(y, _act_dtype(desc), "y"),
-                  _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), stream)
+    at = _device(x, "x")
+    _norm_forward(desc, x, gamma, beta, _p(y, _act_dtype(desc), "y", at),
+                  _norm_stat(desc, mean, "mean", at), _norm_stat(desc, rstd, "rstd", at), stream,
+                  at)
 
 
 def moe_norm_workspace_size(desc: NormDesc) -> int:
@@ -599,15 +606,16 @@ def moe_norm_workspace_size(desc: NormDesc) -> int:
     return n.value
 
 
-def _norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream):
-    """moe_norm_backward with dx, dgamma and dbeta as pointers."""
+def _norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream, at):
+    """moe_norm_backward with dx, dgamma and dbeta as pointers, on device `at`."""
     dt = _act_dtype(desc)
     _need(dy, (desc.T, desc.d), "dy")
-    _here(dy, x, gamma, mean, rstd, ws)
     st = lib().moe_norm_backward(
-        ctypes.byref(desc), _p(dy, dt, "dy"), _p(x, dt, "x"), _norm_param(desc, gamma, "gamma"),
-        _norm_stat(desc, mean, "mean"), _norm_stat(desc, rstd, "rstd"), dx, dgamma, dbeta,
-        _p(ws, torch.uint8, "workspace"), 0 if ws is None else ws.numel(), _stream(stream))
+        ctypes.byref(desc), _p(dy, dt, "dy", at), _p(x, dt, "x", at),
+        _norm_param(desc, gamma, "gamma", at), _norm_stat(desc, mean, "mean", at),
+        _norm_stat(desc, rstd, "rstd", at), dx, dgamma, dbeta,
+        _p(ws, torch.uint8, "workspace", at), 0 if ws is None else ws.numel(),
+        _stream(stream, at))
     _check(st, "moe_norm_backward")
 
 
@@ -618,16 +626,17 @@ def moe_norm_backward(desc, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, str
     for t, what in ((dgamma, "dgamma"), (dbeta, "dbeta")):
         if t is not None:
             _need(t, (desc.d,), what)
-    _here(dx, dgamma, dbeta)
-    _norm_backward(desc, dy, x, gamma, mean, rstd, _p(dx, _act_dtype(desc), "dx"),
-                   _p(dgamma, torch.float32, "dgamma"), _p(dbeta, torch.float32, "dbeta"), ws,
-                   stream)
+    at = _device(x, "x")
+    _norm_backward(desc, dy, x, gamma, mean, rstd, _p(dx, _act_dtype(desc), "dx", at),
+                   _p(dgamma, torch.float32, "dgamma", at), _p(dbeta, torch.float32, "dbeta", at),
+                   ws, stream, at)
 
 
 def norm(x, gamma=None, beta=None, kind=MOE_NORM_LAYER, eps=1e-6, stats=False):
     """(y, mean, rstd) of moe_norm_forward in fresh tensors, on the current stream;
     mean and rstd are None without stats (mean always for MOE_NORM_RMS)."""
     desc = make_norm_desc(x, gamma if gamma is not None else beta, kind, eps)
+    at = _device(x, "x")
     y = torch.empty_like(x)
     mean = rstd = None
     if stats:
@@ -635,7 +644,7 @@ def norm(x, gamma=None, beta=None, kind=MOE_NORM_LAYER, eps=1e-6, stats=False):
         if kind != MOE_NORM_RMS:
             mean = torch.empty_like(rstd)
     _norm_forward(desc, x, gamma, beta, y.data_ptr(), None if mean is None else mean.data_ptr(),
-                  None if rstd is None else rstd.data_ptr(), None)
+                  None if rstd is None else rstd.data_ptr(), None, at)
     return y, mean, rstd
 
 
@@ -643,12 +652,13 @@ def norm_backward(dy, x, gamma, mean, rstd, kind=MOE_NORM_LAYER):
     """(dx, dgamma, dbeta) of moe_norm_backward in fresh tensors, on the current
     stream; dbeta is None for MOE_NORM_RMS."""
     desc = make_norm_desc(x, gamma, kind)
+    at = _device(x, "x")
     dx = torch.empty_like(x)
     dgamma = torch.empty(desc.d, dtype=torch.float32, device=x.device)
     dbeta = None if kind == MOE_NORM_RMS else torch.empty_like(dgamma)
     ws = torch.empty(moe_norm_workspace_size(desc), dtype=torch.uint8, device=x.device)
     _norm_backward(desc, dy, x, gamma, mean, rstd, dx.data_ptr(), dgamma.data_ptr(),
-                   None if dbeta is None else dbeta.data_ptr(), ws, None)
+                   None if dbeta is None else dbeta.data_ptr(), ws, None, at)
     return dx, dgamma, dbeta
 
 
@@ -658,7 +668,7 @@ def make_ortho_desc(g, steps=5, eps=1e-7) -> OrthoDesc:
         raise ValueError("g has shape %s, expected [n_mats, rows, cols]" % (tuple(g.shape),))
     if g.dtype not in _MOE_DTYPE:
         raise TypeError("g must be fp32 or bf16")
-    return OrthoDesc(*_int32(*g.shape), _MOE_DTYPE[g.dtype], *_int32(steps), eps)
+    return OrthoDesc(*_int32(g.shape), _MOE_DTYPE[g.dtype], *_int32((steps,)), eps)
 
 
 def moe_ortho_workspace_size(desc: OrthoDesc) -> int:
@@ -673,10 +683,10 @@ def moe_orthogonalize(desc, g, out, ws, stream=None):
     shape = (desc.n_mats, desc.rows, desc.cols)
     _need(g, shape, "g")
     _need(out, shape, "out")
-    _here(g, out, ws)
+    at = _device(g, "g")
     st = lib().moe_orthogonalize(
-        ctypes.byref(desc), _p(g, _act_dtype(desc), "g"), _p(out, torch.bfloat16, "out"),
-        _p(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream))
+        ctypes.byref(desc), _p(g, _act_dtype(desc), "g", at), _p(out, torch.bfloat16, "out", at),
+        _p(ws, torch.uint8, "workspace", at), ws.numel(), _stream(stream, at))
     _check(st, "moe_orthogonalize")
 
 
@@ -685,6 +695,7 @@ def orthogonalize(g, steps=5, eps=1e-7):
     fresh bf16 tensor, on the current stream.  A bounded wait that expires shows as NaN in it."""
     stack = g if g.dim() == 3 else g.unsqueeze(0)
     desc = make_ortho_desc(stack, steps, eps)
+    _device(g, "g")
     out = torch.empty(stack.shape, dtype=torch.bfloat16, device=g.device)
     ws = torch.empty(max(moe_ortho_workspace_size(desc), 16), dtype=torch.uint8, device=g.device)
     moe_orthogonalize(desc, stack, out, ws)

@@ -46,7 +46,7 @@ class Plan:
 def make_plan(desc, topk_ids, ws) -> Plan:
     """The plan of topk_ids [T, k] int32 (an id outside [0, E) drops its pair); ws as for
     moe.moe_plan_dispatch."""
-    moe._here(topk_ids, ws)
+    moe._p(ws, torch.uint8, "workspace", moe._device(topk_ids, "topk_ids"))
     new = lambda *s: torch.empty(s, dtype=torch.int32, device=topk_ids.device)  # noqa: E731
     ks = desc.k + desc.S
     p = Plan(desc, new(desc.E + desc.S + 1), new(desc.T * ks), new(desc.T, ks))
@@ -127,7 +127,9 @@ def dispatch(x, plan: Plan):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y_perm, topk_w, residual, plan):
-        moe._here(y_perm, topk_w, residual, plan.slot_row)
+        at = moe._device(y_perm, "y_perm")
+        for t, what in ((topk_w, "topk_w"), (residual, "residual"), (plan.slot_row, "slot_row")):
+            moe._p(t, None, what, at)
         ctx.desc = plan.desc
         ctx.save_for_backward(y_perm, topk_w, plan.expert_offsets, plan.slot_row)
         y = torch.empty((plan.desc.T, plan.desc.d), dtype=torch.float32, device=y_perm.device)

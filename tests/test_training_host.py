@@ -225,10 +225,20 @@ def test_sizes_beyond_the_records_fields_are_refused(n):
     assert moe.make_norm_desc(x[:8]).T == 8 and moe.make_ortho_desc(x[:4, None]).n_mats == 4
 
 
-class _Elsewhere(torch.Tensor):
-    """A CPU tensor that says it lies on another GPU."""
+class _Here(torch.Tensor):
+    """A CPU tensor that says it lies on the current GPU."""
     is_cuda = property(lambda self: True)
-    device = property(lambda self: torch.device("cuda", 1))
+    device = property(lambda self: torch.device("cuda", self.get_device()))
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 0x10000
+
+
+class _Elsewhere(_Here):
+    """And one on another, whose address is not to be used."""
 
     def get_device(self):
         return 1
@@ -239,24 +249,29 @@ class _Elsewhere(torch.Tensor):
 
 def test_tensors_of_another_device_are_refused(L, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-
-    def t(*shape, dtype=torch.float32):
-        return torch.zeros(shape, dtype=dtype).as_subclass(_Elsewhere)
-
-    i32 = torch.int32
+    i32, u8, f32, bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
     d = moe.make_desc(4, 64, 4, 2, 64, dtype=moe.MOE_F32)
     nd = moe.make_norm_desc(torch.zeros(4, 64))
     od = moe.make_ortho_desc(torch.zeros(1, 4, 64))
-    x, rows, slot, off = t(4, 64), t(8, 64), t(4, 2, dtype=i32), t(5, dtype=i32)
-    ws, s4, s64 = t(1 << 20, dtype=torch.uint8), t(4), t(64)
-    for call in (
-            lambda: moe.moe_dispatch_rows(d, x, off, slot, rows),
-            lambda: moe.moe_dispatch_rows_backward(d, rows, slot, x),
-            lambda: moe.moe_combine_backward(d, x, rows, off, slot, t(4, 2), rows, t(4, 2)),
-            lambda: moe.moe_norm_forward(nd, x, s64, None, x, s4, s4),
-            lambda: moe.moe_norm_backward(nd, x, x, s64, s4, s4, x, s64, s64, ws),
-            lambda: moe.moe_orthogonalize(od, x[None], t(1, 4, 64, dtype=torch.bfloat16), ws),
-            lambda: training.make_plan(d, t(4, 2, dtype=i32), ws),
-            lambda: training.combine(rows, t(4, 2), training.Plan(d, off, None, slot))):
-        with pytest.raises(ValueError, match="current device is cuda:0"):
-            call()
+    x, rows, slot, off = ((4, 64), f32), ((8, 64), f32), ((4, 2), i32), ((5,), i32)
+    w, s4, s64, ws = ((4, 2), f32), ((4,), f32), ((64,), f32), ((1 << 20,), u8)
+    calls = [
+        (lambda *a: moe.moe_dispatch_rows(d, *a), (x, off, slot, rows)),
+        (lambda *a: moe.moe_dispatch_rows_backward(d, *a), (rows, slot, x)),
+        (lambda *a: moe.moe_combine_backward(d, *a), (x, rows, off, slot, w, rows, w)),
+        (lambda *a: moe.moe_norm_forward(nd, *a), (x, s64, s64, x, s4, s4)),
+        (lambda *a: moe.moe_norm_backward(nd, *a), (x, x, s64, s4, s4, x, s64, s64, ws)),
+        (lambda *a: moe.moe_orthogonalize(od, *a), (((1, 4, 64), f32), ((1, 4, 64), bf16), ws)),
+        (lambda *a: moe.norm(*a), (x, s64, s64)),
+        (lambda *a: moe.orthogonalize(*a), (x,)),
+        (lambda *a: training.make_plan(d, *a), (((4, 2), i32), ws)),
+        (lambda r, w, o, s, e: training.combine(r, w, training.Plan(d, o, None, s), e),
+         (rows, w, off, slot, x))]
+    for call, shapes in calls:
+        for i in range(len(shapes)):
+            if call is calls[-1][0] and i == 2:
+                continue  # the forward combine takes no offsets
+            args = [torch.zeros(sh, dtype=t).as_subclass(_Elsewhere if j == i else _Here)
+                    for j, (sh, t) in enumerate(shapes)]
+            with pytest.raises(ValueError, match="current device is cuda:0"):
+                call(*args)
