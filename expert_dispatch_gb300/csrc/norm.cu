@@ -244,8 +244,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // but its reads of shared memory.  Every wait for a copy is bounded.  The threads
 // of a group wait each for itself, so some may give up on a row that the others
 // still see arrive: one that has given up adds NaN to the sums of that row and of
-// every row after it, which makes NaN of these rows' results in all threads, and
-// waits for nothing more.  No more copies are requested then.
+// every row after it (backward: by its gamma), which makes NaN of these rows'
+// results in all threads.  No more copies are requested then, and nobody waits for
+// one that has not come.
 struct Ring {
   uint8_t* base;
   uint32_t bar0, row_bytes;
@@ -281,7 +282,8 @@ struct Ring {
     bulk_load(dst, a, (uint32_t)n * row_bytes, bar0 + 8u * s);
   }
   __device__ __forceinline__ bool wait() const {
-    return mbar_wait(bar0 + 8u * stage, parity, gave_up, nullptr);
+    const uint32_t bar = bar0 + 8u * stage;
+    return mbar_try_wait(bar, parity) || (open() && mbar_wait(bar, parity, gave_up, nullptr));
   }
   __device__ __forceinline__ bool open() const {
     return !*static_cast<volatile int*>(gave_up);
@@ -520,7 +522,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const size_t jump = (size_t)step * d;
   int turn = 0;
   float* buf = red[warps == 1 ? 0 : group];
-  bool ok = true;  // this thread has not given up waiting
   float mu = 0.f, r = 0.f;
   if (row < rows) mu = RMS ? 0.f : mean[row], r = rstd[row];
   for (; row < rows; row += step, xp += jump, dp += jump, op += jump) {
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (row + step < rows) mu2 = RMS ? 0.f : mean[row + step], r2 = rstd[row + step];
     Raw<T, VEC> xr[VPT], dr[VPT];
     if constexpr (RING) {
-      ok = ok && ring.wait();
+      if (!ring.wait()) g[0] = f2(quiet_nan(), quiet_nan());
       const uint8_t* src = ring.rows() + (size_t)tid * sizeof(Raw<T, VEC>);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     float s[RMS ? 1 : 2];
-    s[0] = ok ? both(wh) : quiet_nan();
+    s[0] = both(wh);
     if constexpr (!RMS) s[1] = both(ws);
     if (RING && warps == 1) __syncwarp();
     group_sum<RMS ? 1 : 2>(s, warps, tid >> 5, group, buf, turn);
@@ -599,18 +600,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if constexpr (RING) ring.close();
   if (!partial) return;
+  bool lost = false;
   if constexpr (RING) {
     __syncthreads();
-    if (!ring.open()) {  // a thread gave up: the sums hold what was never loaded
-#pragma unroll
-      for (int k = 0; k < N / 2; ++k) dg[k] = db[k] = f2(quiet_nan(), quiet_nan());
-    }
+    lost = !ring.open();
   }
   float* sums = reinterpret_cast<float*>(dyn);  // every copy has landed and been read
   auto flush = [&](const F2 (&acc2)[N / 2], float* out) {
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) split(acc2[k], acc[2 * k], acc[2 * k + 1]);
+    if (lost) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] = quiet_nan();
+    }
     for (int k = 0; k < groups; ++k) {
       __syncthreads();
       if (group != k) continue;
