@@ -323,8 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;  // this warp has not given up waiting
   volatile int* abort_flag = &abort_s;
   // Every thread's stores to the operands are in place and every read of the
-  // accumulators is done: thread 0 issues the products, all wait for them.
-  auto product = [&](auto&& issue) {
+  // accumulators is done: thread 0 issues the products, all run `meanwhile` and wait
+  // for them.
+  auto product = [&](auto&& issue, auto&& meanwhile) {
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
@@ -333,24 +334,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       issue();
       umma_commit(bar);
     }
+    meanwhile();
     ok = ok && tc::mbar_wait_warp(bar, parity, abort_flag, p.err);
     parity ^= 1u;
     tc_fence_after();
   };
   const int q = warp & 3, sub = warp >> 2, row = q * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-  auto load_accumulators = [&](int c, uint32_t (&a)[2][16]) {  // 32 columns
-    tmem_ld16(lanes + c, a[0]);
-    tmem_ld16(lanes + c + 16, a[1]);
-    tmem_ld_wait();
-    if (!ok) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) a[0][j] = a[1][j] = 0x7fffffffu;  // NaN
-    }
-  };
 
   for (int step = 0; step < p.steps; ++step) {
     const float rho = step == 0 ? scale.rho : 1.f;
+    const bool last = step + 1 == p.steps;
+    float alpha, beta;
     // ---- A = X X^T, this slice's part: TMEM columns 0 .. 127
     product([&] {
       constexpr uint32_t idesc = idesc_f16_f32(128, 128);
@@ -360,12 +355,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t d = smem_desc_sw128(xa + b * kBlockBytes + kk * 32);
           umma_bf16(tmem, d, d, idesc, b | kk ? 1u : 0u);
         }
+    }, [&] {
+      alpha = gram_factor(scale, rho * rho * (kScaleA / (kScaleX * kScaleX)), step);
+      beta = last ? last_factor(scale, rho / (kScaleB * kScaleX), step)
+                  : apply_factor(scale, rho / kScaleB, step, 1);
     });
-    const float alpha = gram_factor(scale, rho * rho * (kScaleA / (kScaleX * kScaleX)), step);
+    const float alpha1 = ok ? alpha : quiet_nan();
 #pragma unroll 1
     for (int c = sub * 32; c < 128; c += 32 * kParts) {
       uint32_t a[2][16];
-      load_accumulators(c, a);
+      tmem_ld16(lanes + c, a[0]);
+      tmem_ld16(lanes + c + 16, a[1]);
+      tmem_ld_wait();
       if (C == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 8 columns
@@ -373,13 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int k = 8 * i + 2 * j;
-            u[j] = pack_half2(alpha * __uint_as_float(a[k >> 4][k & 15]),
-                              alpha * __uint_as_float(a[k >> 4][(k & 15) + 1]));
+            u[j] = pack_half2(alpha1 * __uint_as_float(a[k >> 4][k & 15]),
+                              alpha1 * __uint_as_float(a[k >> 4][(k & 15) + 1]));
           }
           *reinterpret_cast<uint4*>(as + chunk_at(row, c + 8 * i)) =
               make_uint4(u[0], u[1], u[2], u[3]);
         }
       } else {
+        // one NaN in each of the warp's rows of A: products with A spread it over the matrix
+        if (!ok) a[0][0] = __float_as_uint(quiet_nan());
         // 8-column group k of A is added up by CTA k % C: there, behind the
         // groups of the CTAs before this one, [row][4] fp32 of its two halves
 #pragma unroll
@@ -433,15 +436,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t d = smem_desc_sw128(aa + (k >> 2) * kBlockBytes + (k & 3) * 32);
         umma_bf16(tmem + 128, d, d, idesc, k ? 1u : 0u);
       }
-    });
+    }, [] {});
+    const float gamma1 = ok ? kC * (kScaleB / (kScaleA * kScaleA)) : quiet_nan();
 #pragma unroll 1
     for (int c = sub * 32; c < 128; c += 32 * kParts) {
       uint32_t a[2][16];
+      tmem_ld16(lanes + 128 + c, a[0]);
+      tmem_ld16(lanes + 128 + c + 16, a[1]);
       uint4 gm[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         gm[i] = *reinterpret_cast<const uint4*>(as + chunk_at(row, c + 8 * i));
-      load_accumulators(128 + c, a);
+      tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // 8 columns
         const uint32_t gw[4] = {gm[i].x, gm[i].y, gm[i].z, gm[i].w};
@@ -454,8 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             v[t] = fmaf(kB * (kScaleB / kScaleA), t ? ga.y : ga.x,
-                        kC * (kScaleB / (kScaleA * kScaleA)) *
-                            __uint_as_float(a[k >> 4][(k & 15) + t]));
+                        gamma1 * __uint_as_float(a[k >> 4][(k & 15) + t]));
             if (row == c + k + t && row < p.m) v[t] += kA * kScaleB;
           }
           u[j] = pack_half2(v[0], v[1]);
@@ -477,19 +482,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     smem_desc_mn128(xa + b * kBlockBytes + k * 2048, kBlockBytes), idesc,
                     k ? 1u : 0u);
       }
-    });
-    const bool last = step + 1 == p.steps;
-    const float beta = last ? last_factor(scale, rho / (kScaleB * kScaleX), step)
-                            : apply_factor(scale, rho / kScaleB, step, 1);
+    }, [] {});
+    const float beta1 = ok ? beta : quiet_nan();
 #pragma unroll 1
     for (int c = sub * 32; c < w; c += 32 * kParts) {  // w is a multiple of 64
       uint32_t a[2][16];
-      load_accumulators(c, a);
+      tmem_ld16(lanes + c, a[0]);
+      tmem_ld16(lanes + c + 16, a[1]);
+      tmem_ld_wait();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = beta * __uint_as_float(a[h][j]);
+        for (int j = 0; j < 16; ++j) v[j] = beta1 * __uint_as_float(a[h][j]);
         const int cc = c + 16 * h;
         if (!last) {
           uint32_t u[8];
