@@ -551,11 +551,9 @@ def moe_combine_backward(desc, dy, y_perm, expert_offsets, slot_row, topk_w, dy_
 _MOE_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _int32(sizes):
-    """A record's sizes: ctypes would wrap one that 32 bits do not hold."""
-    if max(sizes) >= 1 << 31 or min(sizes) < -1 << 31:
-        raise ValueError("%s does not fit the 32 bits of a record's fields" % (tuple(sizes),))
-    return sizes
+def _too_large(*sizes):
+    """A record's size that 32 bits do not hold: ctypes would wrap it."""
+    return ValueError("one of %s does not fit the 32 bits of a record's field" % (sizes,))
 
 
 def make_norm_desc(x, gamma=None, kind=MOE_NORM_LAYER, eps=1e-6) -> NormDesc:
@@ -565,7 +563,10 @@ def make_norm_desc(x, gamma=None, kind=MOE_NORM_LAYER, eps=1e-6) -> NormDesc:
     w = torch.float32 if gamma is None else gamma.dtype
     if x.dtype not in _MOE_DTYPE or w not in _MOE_DTYPE:
         raise TypeError("x and gamma must be fp32 or bf16")
-    return NormDesc(*_int32(x.shape), kind, _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
+    rows, d = x.shape
+    if (rows | d) >> 31:
+        raise _too_large(rows, d)
+    return NormDesc(rows, d, kind, _MOE_DTYPE[x.dtype], _MOE_DTYPE[w], eps)
 
 
 def _norm_param(desc, t, what, device):
@@ -668,7 +669,10 @@ def make_ortho_desc(g, steps=5, eps=1e-7) -> OrthoDesc:
         raise ValueError("g has shape %s, expected [n_mats, rows, cols]" % (tuple(g.shape),))
     if g.dtype not in _MOE_DTYPE:
         raise TypeError("g must be fp32 or bf16")
-    return OrthoDesc(*_int32(g.shape), _MOE_DTYPE[g.dtype], *_int32((steps,)), eps)
+    n, rows, cols = g.shape
+    if (n | rows | cols | max(steps, 0)) >> 31:
+        raise _too_large(n, rows, cols, steps)
+    return OrthoDesc(n, rows, cols, _MOE_DTYPE[g.dtype], steps, eps)
 
 
 def moe_ortho_workspace_size(desc: OrthoDesc) -> int:
