@@ -136,7 +136,7 @@ __device__ __forceinline__ void load_param(const void* p, bool bf16, int c, floa
 
 // Two fp32 values in a 64-bit register pair, for the packed fp32 instructions:
 // the kernels below are bound by instruction issue before they are bound by
-// HBM otherwise (the backward pass took 31 instructions an element and 122 us at
+// HBM otherwise (the backward pass took 31 instructions an element and 116 us at
 // 16384 x 4096 bf16 with one value an instruction).
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float a, float b) {
@@ -316,9 +316,11 @@ struct Ring {
 //
 // Rows at a time.  A layer norm's bf16 rows are bound by the instructions that a
 // row costs beside its elements (two sums with their barriers, the loop), so they
-// are taken in twos: 16384 x 2048 31.5 -> 26.7 us, 8192 x 8192 65.5 -> 51.2. An RMS
-// norm (one sum; 4096 x 7168 20.3 us alone, 21.6 in twos) and fp32 rows (8192 x 4096
-// 44.0 and 48.2) gain more from the blocks that the registers then allow.
+// are taken in twos: 16384 x 2048 31.5 -> 26.9 us, 8192 x 8192 65.5 -> 50.0.  An RMS
+// norm has one sum and gains more from the blocks that the registers then allow:
+// one row at a time against two, bf16 4096 x 7168 20.1 and 22.5 us (16384 x 4096, the
+// other way round, 49.8 and 45.1), fp32 8192 x 4096 46.3 and 52.4.  For a layer norm of
+// fp32 rows both take 48.7 there.
 template <typename T, bool RMS, bool RING, int THREADS>
 __host__ __device__ constexpr int forward_rows() {
   return RING && !RMS && sizeof(T) == 2 && THREADS == 512 ? 2 : 1;

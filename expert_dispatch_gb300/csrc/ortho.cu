@@ -8,9 +8,15 @@
 // singular value of X (all in (0, 1] at the start) towards 1.
 //
 // Precision.  The products run on the tensor cores with fp16 operands and fp32
-// accumulators.  fp16 keeps 11 bits where bf16 keeps 8: on the same inputs the
-// result is off by about 1e-3 with fp16 operands and 1e-2 with bf16 ones (its
-// own rounding to bf16 is 1.7e-3).  fp16's narrow range is met by powers of two:
+// accumulators, for fp32 matrices too: the output is bf16, whose rounding alone is
+// 1.7e-3 of its norm, and operands split into two fp16 parts would take three products
+// for each.  fp16 keeps 11 bits where bf16 keeps 8: on the same inputs the
+// result is off by about 1e-3 with fp16 operands and 1e-2 with bf16 ones, where the
+// singular values grow together.  Where a few directions hold almost all of the
+// norm, the roundings of A and B (relative to those) weigh on the others until they
+// have grown: 2e-2 for singular values falling as 1/k^2, up to 4e-2 where all but
+// eight are 0.1 % of the largest; the tests hold the kernels to twice what these
+// roundings alone give in 64 bits.  fp16's narrow range is met by powers of two:
 // X is stored times 2^10 (entries up to about 1.2, of order 1/sqrt(m n) at the
 // start; where eps outweighs |G|, more: Scale in ortho.cuh), A times 2^14 (up to 1.5,
 // and 1/m) and B times 2^12 (up to 3.5).
@@ -879,8 +885,11 @@ cudaError_t launch_small(const OperandMaps& P, const OperandMaps& Q, const Produ
 //          epilogue for each tile an SM has, and 125 once; a shared reduction
 //          adds 400 for the cluster's launch, barriers and exchange.
 // Measured, us a call: 4 x 512 x 512 98 pairs, 74 small; 2 x 1536 x 4096 340
-// pairs, 516 small; 1 x 512 x 2048 90 with the reductions of 2048 over two
-// CTAs, 84 over four; 1 x 1024 x 1024 130 with 1024 over two, 100 unshared.
+// pairs, 516 small; 1 x 1024 x 1024 130 with 1024 over two CTAs, 100 unshared.
+// With X X^T over 1, 2, 4 and 8 CTAs, what the rule takes in brackets:
+// 1 x 512 x 2048 95.7, 87.6, 81.7, [82.7]; 1 x 256 x 4096 120.5, 94.7, 77.4, [70.5];
+// 1 x 576 x 2112 103.3, 96.8, [87.4], 91.6; 1 x 960 x 3264 143.7, [135.8], 135.4,
+// 157.5.
 struct Choice {
   long long cost;         // 10 ns
   long long large, small; // tiles of each kind
