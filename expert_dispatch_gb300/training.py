@@ -91,12 +91,12 @@ class _Norm(torch.autograd.Function):
 
 
 def layer_norm(x, gamma=None, beta=None, eps=1e-6):
-    """Layer norm over the last dimension of x (contiguous, fp32 or bf16)."""
+    """Layer norm over the last dimension of x (contiguous, 16-byte aligned, fp32 or bf16)."""
     return _Norm.apply(x, gamma, beta, moe.MOE_NORM_LAYER, eps)
 
 
 def rms_norm(x, gamma=None, eps=1e-6):
-    """RMS norm over the last dimension of x (contiguous, fp32 or bf16)."""
+    """RMS norm over the last dimension of x (contiguous, 16-byte aligned, fp32 or bf16)."""
     return _Norm.apply(x, gamma, None, moe.MOE_NORM_RMS, eps)
 
 

@@ -525,7 +525,11 @@ moe_status moe_ortho_workspace_size(const moe_ortho_desc* desc, size_t* bytes);
    factor of 10 of each other, and by more where a few directions hold almost all
    of the norm: 2e-3 to 4e-3 for singular values falling as 1/k, 2e-2 as 1/k^2;
    with eight equal ones 2e-3 to 7e-3 where the others have 1 % of them, 6e-3 to
-   2e-2 at 0.3 %, 2e-2 to 4e-2 at 0.1 % (100 to 1000 rows, five steps).
+   2e-2 at 0.3 %, 2e-2 to 4e-2 at 0.1 % (100 to 1000 rows, five steps).  Singular
+   values that are all alike (few rows, or few beside the columns) can pass the
+   polynomial's steep parts together, which carries an error on enlarged: 3e-3 at
+   32 x 1000 and up to 6e-3 at 4 x 200 after five steps, 6e-3 and 1e-2 after eight,
+   2e-2 at 2 x 40.
    A zero matrix gives zeros; one that holds a NaN or an infinity gives NaNs,
    the others of the stack are not touched by it.
    rows and cols from 1 to 65536, n_mats up to 65535 and n_mats * max(rows, cols)

@@ -506,6 +506,23 @@ def rounded_ortho(g, steps, pairs):
     return x
 
 
+@pytest.mark.parametrize("n,rows,cols", [(40, 2, 40), (40, 4, 200), (10, 16, 600), (6, 32, 1000),
+                                         (6, 1000, 32), (4, 45, 1600)])
+@pytest.mark.parametrize("steps", [5, 8])
+def test_ortho_singular_values_all_alike(n, rows, cols, steps):
+    """They pass the polynomial's steep parts together, so roundings are carried on enlarged.
+    Bound: the output's rounding, and twice the largest error in the stack that the roundings
+    to fp16 have in 64 bits."""
+    g = rnd((n, rows, cols), rows)
+    want = ref_ortho(g, steps, 1e-7)
+    wide = g.transpose(1, 2).contiguous() if rows > cols else g
+    alone = rounded_ortho(wide, steps, False) - (want.transpose(1, 2) if rows > cols else want)
+    norm = want.square().sum((1, 2)).sqrt()
+    alone = float((alone.square().sum((1, 2)).sqrt() / norm).max())
+    err = (moe.orthogonalize(g, steps=steps).double() - want).square().sum((1, 2)).sqrt() / norm
+    assert bool((err <= 2.0 ** -8 + 2 * alone).all()), (float(err.max()), alone)
+
+
 @pytest.mark.parametrize("spectrum", ["1/k", "1/k^2", 0.1, 0.01, 0.003, 0.001])
 @pytest.mark.parametrize("rows,cols,pairs", [(100, 700, False), (192, 768, False),
                                              (1000, 2500, True)])
