@@ -3,8 +3,9 @@
     python examples/train_layer.py [--steps 30] [--dtype bf16|f32]
 
 The layer is residual + combine(experts(dispatch(rms_norm(x)))): the norm, the routing and
-its plan, the row movement and all their gradients are the library's; the experts'
-products, which the library has forward only, are torch's here.  The matrices are updated
+its plan, the gate weights and the balance loss, the row movement, the activation (its
+inputs kept in 8 bits) and all their gradients are the library's; the experts' products,
+which the library has forward only, are torch's here.  The matrices are updated
 by their averaged gradients made orthogonal (moe.orthogonalize, the Muon optimiser's
 update), the norm's weight by plain descent.  It fits the layer to a fixed random target
 and prints the loss; a GB300 is needed.
@@ -23,12 +24,12 @@ from expert_dispatch_gb300 import moe, training  # noqa: E402
 def experts(x_perm, plan, Wg, Wu, Wd):
     """SwiGLU of every expert on its rows; rows behind the last batch stay zero."""
     bounds = plan.expert_offsets.tolist()
-    out = []
-    for e in range(len(bounds) - 1):
-        r = x_perm[bounds[e]:bounds[e + 1]]
-        out.append((torch.nn.functional.silu(r @ Wg[e].T) * (r @ Wu[e].T)) @ Wd[e].T)
-    out.append(torch.zeros_like(x_perm[bounds[-1]:]))
-    return torch.cat(out)
+
+    def each(rows, W):
+        out = [rows[lo:hi] @ W[e].T for e, (lo, hi) in enumerate(zip(bounds, bounds[1:]))]
+        return torch.cat(out + [rows.new_zeros(len(rows) - bounds[-1], W.shape[1])])
+
+    return each(training.swiglu(each(x_perm, Wg), each(x_perm, Wu)), Wd)
 
 
 def forward(desc, ws, x, p):
@@ -36,12 +37,11 @@ def forward(desc, ws, x, p):
     ids = torch.empty((desc.T, desc.k), dtype=torch.int32, device=x.device)
     w = torch.empty((desc.T, desc.k), device=x.device)
     moe.moe_route(desc, h.detach(), p["Wr"].detach(), None, None, ids, w, ws)
-    # the gate weights again, from the same logits, for autograd
-    probs = torch.softmax(h.float() @ p["Wr"].float().T, 1)
-    w = probs.gather(1, ids.long())
+    # the gate weights again, from the same logits, for autograd, and the balance loss
+    w, balance, _, _ = training.gate(h.float() @ p["Wr"].float().T, ids, desc)
     plan = training.make_plan(desc, ids, ws)
     y_perm = experts(training.dispatch(h, plan), plan, p["Wg"], p["Wu"], p["Wd"])
-    return training.combine(y_perm, w.contiguous(), plan, residual=x.float())
+    return training.combine(y_perm, w, plan, residual=x.float()), balance
 
 
 def train(steps=30, dtype=torch.bfloat16, T=256, d=256, E=8, k=2, I=128, S=1, seed=0):
@@ -60,8 +60,9 @@ def train(steps=30, dtype=torch.bfloat16, T=256, d=256, E=8, k=2, I=128, S=1, se
     for _ in range(steps):
         p = {n: (t if n == "gamma" else t.to(dtype)).detach().requires_grad_()
              for n, t in master.items()}
-        loss = (forward(desc, ws, x, p) - target).square().mean()
-        loss.backward()
+        y, balance = forward(desc, ws, x, p)
+        loss = (y - target).square().mean()
+        (loss + 0.01 * balance).backward()
         for n, t in master.items():
             averaged[n].mul_(0.9).add_(p[n].grad.float())
             if n == "gamma":

@@ -243,6 +243,32 @@ moe_status do_ffn_q8(const moe_layer_desc* D, const void* x, const int32_t* offs
                                       dn, slot_w, W.h, y_perm, W.flags, s));
 }
 
+// The same with 8-bit projections and products: x_perm and h hold codes, their
+// scales behind them (d + 4 ceil(d / 128) bytes a row fit the 2 d of bf16 rows).
+moe_status do_ffn_fp8(const moe_layer_desc* D, const void* x, const int32_t* offsets,
+                      const int32_t* tok_idx, const float* slot_w, const moe_fp8_weight* Wg,
+                      const moe_fp8_weight* Wu, const moe_fp8_weight* Wd, void* y_perm,
+                      const Ws& W, cudaStream_t s) {
+  const int P = D->T * (D->k + D->S);
+  const int nE = D->E + D->S;
+  const size_t cap = (size_t)tc_row_capacity(P);
+  auto scales = [&](void* rows, int n) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(rows) + align256(cap * (size_t)n));
+  };
+  float* xs = scales(W.x_perm, D->d);
+  float* hs = scales(W.h, D->I);
+  if (launch_gather_rows_fp8(x, tok_idx, offsets + nE, P, D->T, D->d, W.x_perm, xs, W.flags, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  const Fp8Weight g{Wg->q, Wg->scale}, u{Wu->q, Wu->scale}, dn{Wd->q, Wd->scale};
+  return cuda_status(launch_ffn_fp8(W.x_perm, xs, offsets, nE, P, D->d, D->I, g, u, dn, slot_w,
+                                    W.h, hs, y_perm, W.flags, s));
+}
+
+bool fp8_ok(const moe_fp8_weight* w) {
+  return w && w->q && w->scale && aligned16(w->q) && aligned16(w->scale);
+}
+
 bool q8_ok(const moe_q8_weight* w) {
   return w && w->q && w->scale && aligned16(w->q) && aligned16(w->scale);
 }
@@ -801,6 +827,184 @@ moe_status moe_layer_forward_q8(const moe_layer_desc* desc, const void* x, const
                                     desc->d, desc->k, desc->S, y, s));
 }
 
+moe_status moe_quantize_fp8(int n_mats, int rows, int K, int src_dtype, const void* w, void* q,
+                            float* scale, void* stream) {
+  const NvtxRange nvtx("moe_quantize_fp8");
+  if (n_mats < 0 || rows <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (src_dtype != MOE_F32 && src_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (n_mats == 0) return MOE_OK;
+  const long long tiles = (((long long)rows + 127) / 128) * (((long long)K + 127) / 128);
+  if (tiles > 0x7fffffffll / n_mats) return MOE_ERR_UNSUPPORTED;
+  if (!w || !q || !scale || !aligned16(w) || !aligned16(q) || !aligned16(scale))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_fp8(src_dtype, w, n_mats, rows, K, q, scale,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_expert_ffn_fp8(const moe_layer_desc* desc, const void* x,
+                              const int32_t* expert_offsets, const int32_t* token_indices,
+                              const float* slot_w, const moe_fp8_weight* Wg,
+                              const moe_fp8_weight* Wu, const moe_fp8_weight* Wd, void* y_perm,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  const NvtxRange nvtx("moe_expert_ffn_fp8");
+  moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (desc->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (desc->T == 0) return MOE_OK;
+  if (!x || !expert_offsets || !token_indices || !y_perm || !fp8_ok(Wg) || !fp8_ok(Wu) ||
+      !fp8_ok(Wd))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(expert_offsets) || !aligned16(token_indices) ||
+      !aligned16(slot_w) || !aligned16(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(desc, workspace, ws_bytes)) != MOE_OK) return st;
+  const Ws W = carve(workspace, ws_layout(*desc));
+  return do_ffn_fp8(desc, x, expert_offsets, token_indices, slot_w, Wg, Wu, Wd, y_perm, W,
+                    static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_layer_forward_fp8(const moe_layer_desc* desc, const void* x, const void* Wr,
+                                 const float* logit_bias, const float* sel_bias,
+                                 const moe_fp8_weight* Wg, const moe_fp8_weight* Wu,
+                                 const moe_fp8_weight* Wd, const float* residual, float* y,
+                                 int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  const NvtxRange nvtx("moe_layer_forward_fp8");
+  moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (desc->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (desc->T == 0) return MOE_OK;
+  if (!x || !Wr || !y || !fp8_ok(Wg) || !fp8_ok(Wu) || !fp8_ok(Wd)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(Wr) || !aligned16(y) || !aligned16(residual) ||
+      !aligned16(topk_ids_out) || !aligned16(topk_w_out))
+    return MOE_ERR_INVALID_ARG;
+  if (sel_bias && desc->gate != MOE_GATE_SIGMOID_BIAS) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(desc, workspace, ws_bytes)) != MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Ws W = carve(workspace, ws_layout(*desc));
+  int32_t* ids = topk_ids_out ? topk_ids_out : W.topk_ids;
+  float* w = topk_w_out ? topk_w_out : W.topk_w;
+  if (cudaMemsetAsync(W.flags, 0, 16, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((st = route_and_plan(desc, x, Wr, logit_bias, sel_bias, ids, w, W, s)) != MOE_OK) return st;
+  if ((st = do_ffn_fp8(desc, x, W.offsets, W.tok_idx, nullptr, Wg, Wu, Wd, W.y_perm, W, s)) !=
+      MOE_OK)
+    return st;
+  return cuda_status(launch_combine(desc->dtype, W.y_perm, W.slot_row, w, residual, desc->T,
+                                    desc->d, desc->k, desc->S, y, s));
+}
+
+moe_status moe_gate_workspace_size(const moe_layer_desc* desc, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  *bytes = align256(gate_workspace_bytes(*desc));
+  return MOE_OK;
+}
+
+moe_status moe_gate_forward(const moe_layer_desc* desc, int logits_dtype, const void* logits,
+                            const int32_t* topk_ids, float* topk_w, int32_t* counts, float* prob,
+                            float* loss, void* workspace, size_t ws_bytes, void* stream) {
+  const NvtxRange nvtx("moe_gate_forward");
+  const moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (logits_dtype != MOE_F32 && logits_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(topk_w) || !aligned16(counts) || !aligned16(prob) || !aligned16(loss))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (desc->T == 0) {  // sums over no tokens
+    if ((counts && cudaMemsetAsync(counts, 0, ((size_t)desc->E + 1) * 4, s) != cudaSuccess) ||
+        (prob && cudaMemsetAsync(prob, 0, (size_t)desc->E * 4, s) != cudaSuccess) ||
+        (loss && cudaMemsetAsync(loss, 0, 4, s) != cudaSuccess))
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!logits || !topk_ids || !aligned16(logits) || !aligned16(topk_ids))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || ws_bytes < gate_workspace_bytes(*desc))
+    return MOE_ERR_WORKSPACE;
+  return cuda_status(launch_gate_forward(*desc, logits_dtype, logits, topk_ids, topk_w, counts,
+                                         prob, loss, workspace, s));
+}
+
+moe_status moe_gate_backward(const moe_layer_desc* desc, int logits_dtype, const void* logits,
+                             const int32_t* topk_ids, const int32_t* counts,
+                             const float* dtopk_w, const float* dloss, void* dlogits,
+                             void* stream) {
+  const NvtxRange nvtx("moe_gate_backward");
+  const moe_status st = check_desc(desc);
+  if (st != MOE_OK) return st;
+  if (logits_dtype != MOE_F32 && logits_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (desc->T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !dlogits || logits == dlogits || (dloss && !counts))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(counts) || !aligned16(dtopk_w) ||
+      !aligned16(dloss) || !aligned16(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_gate_backward(*desc, logits_dtype, logits, topk_ids, counts, dtopk_w,
+                                          dloss, dlogits, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_pack_rows(int rows, int n, int dtype, const void* x, void* q, float* scale,
+                         void* stream) {
+  const NvtxRange nvtx("moe_pack_rows");
+  if (rows < 0 || n <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale || x == q || !aligned16(x) || !aligned16(q) || !aligned16(scale))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(
+      launch_pack_rows(dtype, x, rows, n, q, scale, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpack_rows(int rows, int n, int dtype, const void* q, const float* scale, void* x,
+                           void* stream) {
+  const NvtxRange nvtx("moe_unpack_rows");
+  if (rows < 0 || n <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale || x == q || !aligned16(x) || !aligned16(q) || !aligned16(scale))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(
+      launch_unpack_rows(dtype, q, scale, rows, n, x, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_swiglu_forward(int rows, int n, int dtype, const void* gate, const void* up, void* h,
+                              void* gate8, float* gate_scale, void* up8, float* up_scale,
+                              void* stream) {
+  const NvtxRange nvtx("moe_swiglu_forward");
+  if (rows < 0 || n <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  const bool pack = gate8 != nullptr;
+  if (pack != (gate_scale != nullptr) || pack != (up8 != nullptr) ||
+      pack != (up_scale != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!gate || !up || !h || h == gate || h == up) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {gate, up, (const void*)h, (const void*)gate8, (const void*)gate_scale,
+                        (const void*)up8, (const void*)up_scale})
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_swiglu_forward(dtype, gate, up, rows, n, h, gate8, gate_scale, up8,
+                                           up_scale, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_swiglu_backward(int rows, int n, int dtype, const void* dh, const void* gate,
+                               const void* up, const void* gate8, const float* gate_scale,
+                               const void* up8, const float* up_scale, void* dgate, void* dup,
+                               void* h, void* stream) {
+  const NvtxRange nvtx("moe_swiglu_backward");
+  if (rows < 0 || n <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const bool packed = gate8 && gate_scale && up8 && up_scale && !gate && !up;
+  const bool plain = gate && up && !gate8 && !gate_scale && !up8 && !up_scale;
+  if (!dh || !dgate || !dup || (!packed && !plain)) return MOE_ERR_INVALID_ARG;
+  if (dgate == dup || h == dgate || h == dup) return MOE_ERR_INVALID_ARG;
+  for (const void* in : {dh, gate, up})
+    if (in && (in == dgate || in == dup || in == h)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {dh, gate, up, gate8, (const void*)gate_scale, up8, (const void*)up_scale,
+                        (const void*)dgate, (const void*)dup, (const void*)h})
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_swiglu_backward(dtype, dh, gate, up, gate8, gate_scale, up8, up_scale,
+                                            rows, n, dgate, dup, h,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
 // The layer call with host buffers: x_host -> the workspace's x rows, the
 // layer on the device, its y rows -> y_host; all on `stream`.
 static moe_status forward_host_common(const moe_layer_desc* desc, const void* x_host,
@@ -862,6 +1066,26 @@ moe_status moe_layer_forward_q8_host(const moe_layer_desc* desc, const void* x_h
   return copy_y_to_host(desc, y, y_host, stream);
 }
 
+moe_status moe_layer_forward_fp8_host(const moe_layer_desc* desc, const void* x_host,
+                                      const void* Wr, const float* logit_bias,
+                                      const float* sel_bias, const moe_fp8_weight* Wg,
+                                      const moe_fp8_weight* Wu, const moe_fp8_weight* Wd,
+                                      const float* residual, float* y_host,
+                                      int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  const NvtxRange nvtx("moe_layer_forward_fp8_host");
+  if (desc && desc->T == 0 && check_desc(desc) == MOE_OK) return MOE_OK;
+  const void* x = nullptr;
+  float* y = nullptr;
+  moe_status st = forward_host_common(desc, x_host, y_host, workspace, ws_bytes, stream, &x, &y);
+  if (st != MOE_OK) return st;
+  if ((st = moe_layer_forward_fp8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, residual, y,
+                                  topk_ids_out, topk_w_out, workspace, ws_bytes, stream)) !=
+      MOE_OK)
+    return st;
+  return copy_y_to_host(desc, y, y_host, stream);
+}
+
 moe_status moe_layer_forward_host_pipelined(const moe_layer_desc* desc, int n_steps,
                                             const void* const* x_host, const void* Wr,
                                             const float* logit_bias, const float* sel_bias,
@@ -889,6 +1113,22 @@ moe_status moe_layer_forward_q8_host_pipelined(const moe_layer_desc* desc, int n
       [&](const void* x, float* y) {
         return moe_layer_forward_q8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, nullptr, y,
                                     nullptr, nullptr, workspace, ws_bytes, stream);
+      });
+}
+
+moe_status moe_layer_forward_fp8_host_pipelined(const moe_layer_desc* desc, int n_steps,
+                                                const void* const* x_host, const void* Wr,
+                                                const float* logit_bias, const float* sel_bias,
+                                                const moe_fp8_weight* Wg,
+                                                const moe_fp8_weight* Wu,
+                                                const moe_fp8_weight* Wd, float* const* y_host,
+                                                void* workspace, size_t ws_bytes, void* stream) {
+  const NvtxRange nvtx("moe_layer_forward_fp8_host_pipelined");
+  return forward_host_pipelined(
+      desc, n_steps, x_host, y_host, workspace, ws_bytes, stream,
+      [&](const void* x, float* y) {
+        return moe_layer_forward_fp8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, nullptr, y,
+                                     nullptr, nullptr, workspace, ws_bytes, stream);
       });
 }
 

@@ -1,0 +1,483 @@
+// fp8_gemm.cu -- the expert FFN's grouped products with 8-bit operands (format:
+// fp8.cuh) on the 5th-generation tensor cores ("Distributed MoE" (tenzro docs),
+// expert-host-runtime and compute-seam paragraphs: SwiGLU experts, every
+// projection Y = X * W^T with W stored [out, in]).
+//
+//   gate/up : h[r, n] = silu(g) u,  g = sum_b sx[r, b] sg[n / 128, b] <x8[r, b], Wg[n, b]>
+//             (u likewise), then h's row into 8 bits, 128 columns a scale
+//   down    : y[r, m] = slot_w[r] sum_b sh[r, b] sd[m / 128, b] <h8[r, b], Wd[m, b]>
+// for every batch row r of expert e (rows offsets[e] .. offsets[e+1]); b runs over
+// the blocks of 128 along the reduction, whose products are summed exactly as
+// codes and scaled once a block.
+//
+// Design (sm_103a, one CTA an SM, persistent):
+//   * A unit is (expert, 256 weight rows, up to 128 token rows): 128 rows of gate
+//     and the same 128 of up, or 256 rows of down.  Token rows are the MMA's M
+//     side (the lanes of TMEM), weight rows its N side.  A thread of the epilogue
+//     then has one token row: that row's scale times the block's weight scale is
+//     one factor for all its columns, a column block of h is one thread's (and its
+//     partner's), and outputs are written along rows.
+//   * A block of 128 along K is one 128-byte swizzled row per operand row: four
+//     tcgen05.mma (kind::f8f6f4, K = 32) into one of two TMEM buffers of 256
+//     columns.  The epilogue's warps add each block's products into registers with
+//     their scales while the next block's MMAs fill the other buffer.
+//   * Warp 0 lane 0 issues TMA loads into a ring of stages, warp 1 lane 0 the
+//     MMAs, warps 2-9 the epilogue: two warps a TMEM lane quarter, each with half
+//     of the columns (64 of gate and the same 64 of up, or 128 of down).
+//   * Every wait is bounded (tc_common.cuh).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "internal.h"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace {
+
+using tc::MODE_DOWN;
+using tc::MODE_GATEUP;
+using tc::Unit;
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kRows = 128;  // token rows of a unit
+constexpr int kCols = 256;  // weight rows of a unit
+constexpr int kBK = 128;    // bytes (= elements) along K of a stage
+
+struct F8Params {
+  tc::Params b;       // offsets, groups, Mg, K, row_scale, err, max_rows
+  const float* xs;    // [rows, KB] scales of the token rows
+  const float* ws0;   // [groups, MB, KB] weight scales (gate, or down)
+  const float* ws1;   // up
+  uint8_t* hq;        // gate/up: h's codes [rows, Mg] and scales [rows, MB]
+  float* hs;
+  __nv_bfloat16* y;   // down: [rows, Mg]
+};
+
+// acc += {lo, hi} * f, two fp32 fused multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t f) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
+}
+__device__ __forceinline__ uint64_t pair_of(float f) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "r"(__float_as_uint(f)));
+  return v;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulate, one CTA.
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0, K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int STAGES>
+struct Cfg {
+  static constexpr int A_BYTES = kRows * kBK;
+  static constexpr int B_BYTES = kCols * kBK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  // full, empty; TMEM buffers full, empty; four meetings of the warps of a quarter; wind-down
+  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 1;
+  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int TOP_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // [2][2][128] row maxima
+  static constexpr int PREFIX_OFF = TOP_OFF + 2 * 2 * kRows * 4;
+  static constexpr int GSTART_OFF = PREFIX_OFF + 4 * (tc::kMaxGroups + 1);
+  static constexpr int SMEM_TOTAL = GSTART_OFF + 4 * (tc::kMaxGroups + 1) + 1024;
+  static_assert(SMEM_TOTAL <= 232448, "shared memory");
+};
+
+template <int MODE, int STAGES>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_grouped_gemm(const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ CUtensorMap tmXfull,
+                     const __grid_constant__ CUtensorMap tmW0,
+                     const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
+  using C = Cfg<STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::BAR_OFF;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  const uint32_t accf0 = bar0 + 8u * (2 * STAGES);
+  const uint32_t acce0 = accf0 + 16;
+  const uint32_t meet0 = acce0 + 16;
+  const uint32_t drain_bar = meet0 + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  volatile uint32_t* top = reinterpret_cast<volatile uint32_t*>(smem + C::TOP_OFF);
+  int* prefix = reinterpret_cast<int*>(smem + C::PREFIX_OFF);
+  int* gstart = reinterpret_cast<int*>(smem + C::GSTART_OFF);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kUnitRows = MODE == MODE_GATEUP ? 128 : kCols;  // of one weight matrix
+  const int m_tiles = (p.b.Mg + kUnitRows - 1) / kUnitRows;
+  const int KB = (p.b.K + kBK - 1) / kBK;
+  const int MB = fp8::blocks_of(p.b.Mg);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf0 + 8u * b, 1);
+      mbar_init(acce0 + 8u * b, kEpiWarps);
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(meet0 + 8u * q, 2);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmXfull);
+    tma_prefetch_desc(&tmW0);
+    if (MODE == MODE_GATEUP) tma_prefetch_desc(&tmW1);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) tc::build_schedule<MODE, kRows>(p.b, m_tiles, prefix, gstart);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = prefix[p.b.n_groups];
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      auto load_weights = [&](int s, const Unit& t, int kb) {
+        const uint32_t sB = sbase + s * C::STAGE_BYTES + C::A_BYTES;
+        const int row = t.g * p.b.Mg + t.mt * kUnitRows;
+        tma_load_2d(sB, &tmW0, full_bar(s), kb * kBK, row);
+        if (MODE == MODE_GATEUP)
+          tma_load_2d(sB + C::B_BYTES / 2, &tmW1, full_bar(s), kb * kBK, row);
+      };
+      auto unit_bytes = [&](const Unit& t) {
+        return (uint32_t)(C::B_BYTES + (t.nt + 31) / 32 * 32 * kBK);
+      };
+      // The first unit's weight tiles are requested before waiting for the
+      // predecessor grid: no kernel of the sequence writes weights, and the
+      // schedule comes from a grid two launches back.
+      int n_pre = 0;
+      if ((int)blockIdx.x < total) {
+        const Unit t = tc::decode_unit<MODE, kRows>(blockIdx.x, prefix, gstart, p.b.n_groups,
+                                                    m_tiles, KB, p.b);
+        n_pre = min(STAGES, KB);
+        for (int i = 0; i < n_pre; ++i) {
+          mbar_arrive_expect_tx(full_bar(i), unit_bytes(t));
+          armed |= 1u << i;
+          load_weights(i, t, i);
+        }
+      }
+      pdl_wait();
+      bool first = true;
+      for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
+        if (u + (int)gridDim.x >= total) pdl_trigger();  // this CTA's last unit
+        const Unit t =
+            tc::decode_unit<MODE, kRows>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
+        const int chunks = (t.nt + 31) / 32;
+        bool ok = true;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!(first && kb < n_pre)) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.b.err)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(full_bar(stage), unit_bytes(t));
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            load_weights(stage, t, kb);
+          }
+          const uint32_t sA = sbase + stage * C::STAGE_BYTES;
+          if (chunks == 4)
+            tma_load_2d(sA, &tmXfull, full_bar(stage), kb * kBK, t.r0);
+          else
+            for (int c = 0; c < chunks; ++c)
+              tma_load_2d(sA + c * 32 * kBK, &tmX, full_bar(stage), kb * kBK, t.r0 + c * 32);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        first = false;
+        if (!ok) break;
+      }
+      if ((int)blockIdx.x >= total) pdl_trigger();
+      // wind down: every copy this thread started has landed before exit
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) tc::mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.b.err);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kCols);
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      bool issued = false, ok = true;
+      for (int u = blockIdx.x; ok && u < total && !*abort_flag; u += gridDim.x) {
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const uint32_t buf = it & 1u;
+          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.b.err) ||
+              !mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sA = sbase + stage * C::STAGE_BYTES;
+          const uint32_t sB = sA + C::A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_e4m3(tmem_base + buf * kCols, smem_desc_sw128(sA + kk * 32),
+                      smem_desc_sw128(sB + kk * 32), idesc, kk != 0);
+          issued = true;
+          umma_commit(empty_bar(stage));
+          umma_commit(accf0 + 8u * buf);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // wind down: every MMA this thread issued has completed before TMEM is freed
+      if (issued) {
+        umma_commit(drain_bar);
+        tc::mbar_wait_drain(drain_bar, 0, p.b.err);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (warps 2..9)
+    pdl_wait();  // the token rows' scales are the predecessor's
+    const int q = warp & 3;            // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;  // its half of the columns
+    uint32_t it = 0, met = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+      const Unit t =
+          tc::decode_unit<MODE, kRows>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
+      const int lrow = q * 32 + lane;
+      const bool warp_live = q * 32 < t.nt, live = lrow < t.nt;
+      const size_t row = (size_t)(t.r0 + (live ? lrow : 0));
+      const float* xs = p.xs + row * KB;
+      // this thread's weight scales: its 64 columns of gate and up, or its 128 of down
+      const int wb = MODE == MODE_GATEUP ? t.mt : min(2 * t.mt + half, MB - 1);
+      const size_t wrow = ((size_t)t.g * MB + wb) * KB;
+      const float* ws0 = p.ws0 + wrow;
+      const float* ws1 = p.ws1 + wrow;
+      uint64_t acc[64];  // 128 sums, two a register pair
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      float sx = warp_live ? xs[0] : 0.f, s0 = ws0[0], s1 = MODE == MODE_GATEUP ? ws1[0] : 0.f;
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const uint32_t buf = it & 1u;
+        const uint64_t f0 = pair_of(sx * s0);
+        const uint64_t f1 = MODE == MODE_GATEUP ? pair_of(sx * s1) : f0;
+        if (kb + 1 < KB) {  // the next block's scales, while this one is waited for
+          if (warp_live) sx = xs[kb + 1];
+          s0 = ws0[kb + 1];
+          if (MODE == MODE_GATEUP) s1 = ws1[kb + 1];
+        }
+        if (!tc::mbar_wait_warp(accf0 + 8u * buf, (it >> 1) & 1u, abort_flag, p.b.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (warp_live) {
+          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kCols;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // gate's 64 columns then up's, or down's 128
+            const uint32_t col = MODE == MODE_GATEUP ? (c >> 1) * 128 + half * 64 + (c & 1) * 32
+                                                     : half * 128 + c * 32;
+            uint32_t v[32];
+            tmem_ld32(tb + col, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              fma2(acc[c * 16 + i], v[2 * i], v[2 * i + 1], c < 2 ? f0 : f1);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acce0 + 8u * buf);
+      }
+      if (!ok) break;
+      if constexpr (MODE == MODE_GATEUP) {
+        // columns of h: t.mt * 128 + half * 64 .. + 63 (Mg is a multiple of 64)
+        const int c0 = t.mt * 128 + half * 64;
+        const bool cols = c0 < p.b.Mg;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float a = silu_fast(lo_of(acc[i])) * lo_of(acc[32 + i]);
+          const float b = silu_fast(hi_of(acc[i])) * hi_of(acc[32 + i]);
+          m = max(m, max(fp8::abs_bits(a), fp8::abs_bits(b)));
+          asm("mov.b64 %0, {%1, %2};"
+              : "=l"(acc[i])
+              : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+        }
+        if (!cols) m = 0;
+        if (warp_live) {
+          // the other half's largest, through shared memory.  Two sets of maxima in
+          // turn: a set is written again only after a meeting that its reader came to.
+          volatile uint32_t* mine = top + ((met & 1) * 2 + half) * kRows + lrow;
+          *mine = m;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(meet0 + 8u * q);
+          if (!tc::mbar_wait_warp(meet0 + 8u * q, met & 1u, abort_flag, p.b.err)) break;
+          m = max(m, top[((met & 1) * 2 + (half ^ 1)) * kRows + lrow]);
+          ++met;
+          const fp8::Scale sc = fp8::scale_of(m);
+          if (live && cols) {
+            uint4* dst = reinterpret_cast<uint4*>(p.hq + row * p.b.Mg + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint64_t a = acc[i * 8 + j * 2], b = acc[i * 8 + j * 2 + 1];
+                w[j] = fp8::codes4(lo_of(a) * sc.inv, hi_of(a) * sc.inv, lo_of(b) * sc.inv,
+                                   hi_of(b) * sc.inv);
+              }
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (half == 0) p.hs[row * MB + t.mt] = sc.scale;
+          }
+        }
+      } else {
+        if (live) {
+          const float f = p.b.row_scale ? p.b.row_scale[row] : 1.0f;
+          const int c0 = t.mt * 256 + half * 128;
+          uint4* dst = reinterpret_cast<uint4*>(p.y + row * p.b.Mg + c0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c0 + (i / 8) * 64 < p.b.Mg) {  // Mg is a multiple of 64
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint64_t a = acc[i * 4 + j];
+                const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * f, hi_of(a) * f);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// e4m3 matrix [rows, inner] (row-major), boxes of box_rows x 128, 128-byte swizzle;
+// columns and rows beyond it are read as zero
+bool make_tmap_f8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows,
+                  uint32_t box_rows) {
+  return make_tmap_2d(tm, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, inner, rows, kBK, box_rows,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int MODE, int STAGES>
+cudaError_t launch_f8(const CUtensorMap& x, const CUtensorMap& xfull, const CUtensorMap& w0,
+                      const CUtensorMap& w1, const F8Params& p, long long max_units,
+                      const char* name, cudaStream_t s) {
+  using C = Cfg<STAGES>;
+  auto kern = fp8_grouped_gemm<MODE, STAGES>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::mutex mu;
+  static bool configured[64] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !configured[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) configured[dev] = true;
+    }
+  }
+  const long long grid = max_units < num_sms() ? max_units : num_sms();
+  if (grid <= 0) return cudaSuccess;
+  ProfScope pr(name, s);
+  (void)launch_kernel(kern, (unsigned)grid, kThreads, C::SMEM_TOTAL, s, x, xfull, w0, w1, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
+                           int P, int d, int I, const Fp8Weight& Wg, const Fp8Weight& Wu,
+                           const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
+                           void* y_perm, int* err, cudaStream_t s) {
+  if (P == 0) return cudaSuccess;
+  const uint64_t cap = (uint64_t)tc_row_capacity(P);
+  CUtensorMap tx, txf, th, thf, tg, tu, td;
+  if (!make_tmap_f8(&tx, x8, d, cap, 32) || !make_tmap_f8(&txf, x8, d, cap, 128) ||
+      !make_tmap_f8(&th, h8, I, cap, 32) || !make_tmap_f8(&thf, h8, I, cap, 128) ||
+      !make_tmap_f8(&tg, Wg.q, d, (uint64_t)n_groups * I, 128) ||
+      !make_tmap_f8(&tu, Wu.q, d, (uint64_t)n_groups * I, 128) ||
+      !make_tmap_f8(&td, Wd.q, I, (uint64_t)n_groups * d, 256))
+    return cudaErrorInvalidValue;
+  F8Params p1{}, p2{};
+  p1.b.offsets = p2.b.offsets = offsets;
+  p1.b.n_groups = p2.b.n_groups = n_groups;
+  p1.b.max_rows = p2.b.max_rows = P;
+  p1.b.err = p2.b.err = err;
+  p1.b.Mg = I, p1.b.K = d;
+  p1.xs = xs, p1.ws0 = Wg.scale, p1.ws1 = Wu.scale;
+  p1.hq = static_cast<uint8_t*>(h8), p1.hs = hs;
+  p2.b.Mg = d, p2.b.K = I;
+  p2.b.row_scale = slot_w;
+  p2.xs = hs, p2.ws0 = p2.ws1 = Wd.scale;
+  p2.y = static_cast<__nv_bfloat16*>(y_perm);
+  const long long tiles = (long long)(P + kRows - 1) / kRows + n_groups;
+  const cudaError_t e = launch_f8<MODE_GATEUP, 4>(tx, txf, tg, tu, p1, (I + 127) / 128 * tiles,
+                                                  "ffn_gateup_fp8", s);
+  if (e != cudaSuccess) return e;
+  return launch_f8<MODE_DOWN, 4>(th, thf, td, td, p2, (d + 255) / 256 * tiles, "ffn_down_fp8", s);
+}
+
+}  // namespace moe

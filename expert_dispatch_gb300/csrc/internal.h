@@ -223,6 +223,46 @@ OrthoLayout ortho_layout(const moe_ortho_desc& D);
 cudaError_t launch_orthogonalize(const moe_ortho_desc& D, const void* g, void* out, void* ws,
                                  cudaStream_t s);
 
+// 8-bit floating point (fp8_rows.cu, fp8_gemm.cu; format: fp8.cuh): codes and fp32
+// scales, e4m3 [E+S, R, K] and [E+S, ceil(R/128), ceil(K/128)].
+struct Fp8Weight {
+  const void* q;
+  const float* scale;
+};
+cudaError_t launch_quantize_fp8(int dtype, const void* w, int n_mats, int rows, int K, void* q,
+                                float* scale, cudaStream_t s);
+cudaError_t launch_pack_rows(int dtype, const void* x, long long rows, int n, void* q,
+                             float* scale, cudaStream_t s);
+cudaError_t launch_unpack_rows(int dtype, const void* q, const float* scale, long long rows, int n,
+                               void* x, cudaStream_t s);
+// bf16 rows gathered by tok_idx and put into 8 bits
+cudaError_t launch_gather_rows_fp8(const void* x, const int32_t* tok_idx,
+                                   const int32_t* total_rows, int P, int T, int d, void* q,
+                                   float* scale, int* flags, cudaStream_t s);
+// x8 [cap, d] with scales xs, h8 [cap, I] with scales hs, cap = tc_row_capacity(P)
+cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
+                           int P, int d, int I, const Fp8Weight& Wg, const Fp8Weight& Wu,
+                           const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
+                           void* y_perm, int* err, cudaStream_t s);
+
+// The activation between the products, its inputs kept in 8 bits (swiglu.cu).
+cudaError_t launch_swiglu_forward(int dtype, const void* gate, const void* up, long long rows,
+                                  int I, void* h, void* gate8, float* gate_scale, void* up8,
+                                  float* up_scale, cudaStream_t s);
+cudaError_t launch_swiglu_backward(int dtype, const void* dh, const void* gate, const void* up,
+                                   const void* gate8, const float* gate_scale, const void* up8,
+                                   const float* up_scale, long long rows, int I, void* dgate,
+                                   void* dup, void* h, cudaStream_t s);
+
+// Gate weights, counts and balance loss from logits, and their gradient (gate.cu).
+size_t gate_workspace_bytes(const moe_layer_desc& D);
+cudaError_t launch_gate_forward(const moe_layer_desc& D, int dtype, const void* logits,
+                                const int32_t* ids, float* w, int32_t* counts, float* prob,
+                                float* loss, void* ws, cudaStream_t s);
+cudaError_t launch_gate_backward(const moe_layer_desc& D, int dtype, const void* logits,
+                                 const int32_t* ids, const int32_t* counts, const float* dw,
+                                 const float* dloss, void* dlogits, cudaStream_t s);
+
 int num_sms();
 
 // Expert residency in a bounded set of device slots (slot_cache.cu).

@@ -10,8 +10,10 @@ Entry points carry the C names: moe_workspace_size, moe_workspace_init,
 moe_route, moe_plan_dispatch, moe_expert_ffn, moe_combine, moe_layer_forward,
 moe_get_device_status, moe_status_string, moe_launch_count,
 moe_profile_enable, moe_profile_query, moe_profile_list, the Q8_0 and no-alloc variants, the
-slot cache (moe_slot_cache_*), the expert tier (moe_tier_*) and the training operators
-(moe_dispatch_rows, moe_norm_* and the gradients moe_*_backward).
+slot cache (moe_slot_cache_*), the expert tier (moe_tier_*), the 8-bit floating point layer
+(moe_quantize_fp8, moe_expert_ffn_fp8, moe_layer_forward_fp8*) and the training operators
+(moe_dispatch_rows, moe_norm_*, moe_swiglu_*, moe_gate_*, moe_pack_rows and the gradients
+moe_*_backward).
 """
 from __future__ import annotations
 
@@ -53,7 +55,10 @@ EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_plan_d
             "moe_layer_forward_q8_host_pipelined", "moe_dispatch_rows",
             "moe_dispatch_rows_backward", "moe_combine_backward", "moe_norm_forward",
             "moe_norm_workspace_size", "moe_norm_backward", "moe_ortho_workspace_size",
-            "moe_orthogonalize")
+            "moe_orthogonalize", "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_layer_forward_fp8",
+            "moe_layer_forward_fp8_host", "moe_layer_forward_fp8_host_pipelined",
+            "moe_gate_workspace_size", "moe_gate_forward", "moe_gate_backward",
+            "moe_pack_rows", "moe_unpack_rows", "moe_swiglu_forward", "moe_swiglu_backward")
 
 
 class MoeError(RuntimeError):
@@ -72,6 +77,11 @@ class LayerDesc(ctypes.Structure):
 
 class Q8WeightStruct(ctypes.Structure):
     """moe_q8_weight"""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class Fp8WeightStruct(ctypes.Structure):
+    """moe_fp8_weight"""
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
@@ -161,6 +171,20 @@ def lib():
     O = ctypes.POINTER(OrthoDesc)
     L.moe_ortho_workspace_size.argtypes = [O, ctypes.POINTER(sz)]
     L.moe_orthogonalize.argtypes = [O, vp, vp, vp, sz, vp]
+    F = ctypes.POINTER(Fp8WeightStruct)
+    L.moe_quantize_fp8.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+    L.moe_expert_ffn_fp8.argtypes = [D, vp, vp, vp, vp, F, F, F, vp, vp, sz, vp]
+    L.moe_layer_forward_fp8.argtypes = [D, vp, vp, vp, vp, F, F, F, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_layer_forward_fp8_host.argtypes = L.moe_layer_forward_fp8.argtypes
+    L.moe_layer_forward_fp8_host_pipelined.argtypes = [D, i32, vp, vp, vp, vp, F, F, F, vp, vp,
+                                                       sz, vp]
+    L.moe_gate_workspace_size.argtypes = [D, ctypes.POINTER(sz)]
+    L.moe_gate_forward.argtypes = [D, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_gate_backward.argtypes = [D, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_pack_rows.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+    L.moe_unpack_rows.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+    L.moe_swiglu_forward.argtypes = [i32, i32, i32] + [vp] * 8
+    L.moe_swiglu_backward.argtypes = [i32, i32, i32] + [vp] * 11
     vpp = ctypes.POINTER(ctypes.c_void_p)
     ip = ctypes.POINTER(ctypes.c_int32)
     TS = ctypes.POINTER(TierStats)
@@ -479,6 +503,140 @@ def moe_layer_forward_q8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, residual
     _check(st, "moe_layer_forward_q8")
 
 
+# ---------------------------------------------------------------- 8-bit floating point
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+class Fp8Weight:
+    """A projection in 8 bits on the device: e4m3 codes [n, rows, K] and fp32 scales of
+    tiles of 128 x 128, [n, ceil(rows/128), ceil(K/128)]."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        if q.dtype != FP8 or scale.dtype != torch.float32:
+            raise TypeError("codes must be float8_e4m3fn and scales float32")
+        if q.dim() != 3:
+            raise ValueError("q has shape %s, expected [n, rows, K]" % (tuple(q.shape),))
+        n, rows, K = q.shape
+        _need(scale, (n, _blocks(rows), _blocks(K)), "scale")
+        self.q, self.scale = q, scale
+
+    def struct(self, device=None):
+        return Fp8WeightStruct(_p(self.q, FP8, "q", device),
+                               _p(self.scale, torch.float32, "scale", device))
+
+    @property
+    def shape(self):
+        return tuple(self.q.shape)
+
+
+class Rows8:
+    """Rows in 8 bits: e4m3 codes [rows, n] and fp32 scales of blocks of 128 columns,
+    [rows, ceil(n/128)]."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        if q.dtype is not FP8 or scale.dtype is not torch.float32:
+            raise TypeError("codes must be float8_e4m3fn and scales float32")
+        if q.dim() != 2:
+            raise ValueError("q has shape %s, expected [rows, n]" % (tuple(q.shape),))
+        rows, n = q.shape
+        if scale.shape != (rows, -(-n // FP8_BLOCK)):
+            raise ValueError("scale has shape %s, expected %s"
+                             % (tuple(scale.shape), (rows, _blocks(n))))
+        self.q, self.scale = q, scale
+
+    @property
+    def shape(self):
+        return tuple(self.q.shape)
+
+
+def moe_quantize_fp8(w, q, scale, stream=None):
+    """Codes and scales of w [n, rows, K] (fp32 or bf16), a scale a tile of 128 x 128."""
+    if w.dim() != 3:
+        raise ValueError("w has shape %s, expected [n, rows, K]" % (tuple(w.shape),))
+    n, rows, K = w.shape
+    if w.dtype not in _MOE_DTYPE:
+        raise TypeError("w must be fp32 or bf16")
+    if (n | rows | K) >> 31:
+        raise _too_large(n, rows, K)
+    _need(q, (n, rows, K), "q")
+    _need(scale, (n, _blocks(rows), _blocks(K)), "scale")
+    at = _device(w, "w")
+    st = lib().moe_quantize_fp8(n, rows, K, _MOE_DTYPE[w.dtype], _p(w, w.dtype, "w", at),
+                                _p(q, FP8, "q", at), _p(scale, torch.float32, "scale", at),
+                                _stream(stream, at))
+    _check(st, "moe_quantize_fp8")
+
+
+def quantize_fp8(w, stream=None) -> Fp8Weight:
+    """w [n, rows, K] (fp32 or bf16) as an Fp8Weight of its own memory."""
+    n, rows, K = w.shape
+    q = torch.empty((n, rows, K), dtype=FP8, device=w.device)
+    s = torch.empty((n, _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    moe_quantize_fp8(w, q, s, stream)
+    return Fp8Weight(q, s)
+
+
+def _fp8_structs(desc, Wg, Wu, Wd, device):
+    nE = desc.E + desc.S
+    for name, W, shape in (("Wg", Wg, (nE, desc.I, desc.d)), ("Wu", Wu, (nE, desc.I, desc.d)),
+                           ("Wd", Wd, (nE, desc.d, desc.I))):
+        if not isinstance(W, Fp8Weight) or W.shape != shape:
+            raise ValueError("%s must be an Fp8Weight of shape %s" % (name, shape))
+    return [ctypes.byref(W.struct(device)) for W in (Wg, Wu, Wd)]
+
+
+def moe_expert_ffn_fp8(desc, x, expert_offsets, token_indices, slot_w, Wg, Wu, Wd, y_perm, ws,
+                       stream=None):
+    """moe_expert_ffn with Fp8Weight projections and 8-bit products (bf16 layers)."""
+    P = desc.T * (desc.k + desc.S)
+    _need(x, (desc.T, desc.d), "x")
+    _need(expert_offsets, (desc.E + desc.S + 1,), "expert_offsets")
+    _need(token_indices, (P,), "token_indices")
+    _need(y_perm, (P, desc.d), "y_perm")
+    if slot_w is not None:
+        _need(slot_w, (P,), "slot_w")
+    at = _device(x, "x")
+    g, u, d = _fp8_structs(desc, Wg, Wu, Wd, at)
+    st = lib().moe_expert_ffn_fp8(
+        ctypes.byref(desc), _p(x, torch.bfloat16, "x", at),
+        _p(expert_offsets, torch.int32, "expert_offsets", at),
+        _p(token_indices, torch.int32, "token_indices", at),
+        _p(slot_w, torch.float32, "slot_w", at), g, u, d,
+        _p(y_perm, torch.bfloat16, "y_perm", at), _p(ws, torch.uint8, "workspace", at),
+        ws.numel(), _stream(stream, at))
+    _check(st, "moe_expert_ffn_fp8")
+
+
+def moe_layer_forward_fp8(desc, x, Wr, logit_bias, sel_bias, Wg, Wu, Wd, residual, y,
+                          topk_ids_out, topk_w_out, ws, stream=None):
+    """moe_layer_forward with Fp8Weight projections and 8-bit products (bf16 layers)."""
+    _need(x, (desc.T, desc.d), "x")
+    _need(Wr, (desc.E, desc.d), "Wr")
+    _need(y, (desc.T, desc.d), "y")
+    for t, shape, what in ((logit_bias, (desc.E,), "logit_bias"), (sel_bias, (desc.E,), "sel_bias"),
+                           (residual, (desc.T, desc.d), "residual"),
+                           (topk_ids_out, (desc.T, desc.k), "topk_ids_out"),
+                           (topk_w_out, (desc.T, desc.k), "topk_w_out")):
+        if t is not None:
+            _need(t, shape, what)
+    at = _device(x, "x")
+    g, u, d = _fp8_structs(desc, Wg, Wu, Wd, at)
+    st = lib().moe_layer_forward_fp8(
+        ctypes.byref(desc), _p(x, torch.bfloat16, "x", at), _p(Wr, torch.bfloat16, "Wr", at),
+        _p(logit_bias, torch.float32, "logit_bias", at),
+        _p(sel_bias, torch.float32, "sel_bias", at), g, u, d,
+        _p(residual, torch.float32, "residual", at), _p(y, torch.float32, "y", at),
+        _p(topk_ids_out, torch.int32, "topk_ids_out", at),
+        _p(topk_w_out, torch.float32, "topk_w_out", at), _p(ws, torch.uint8, "workspace", at),
+        ws.numel(), _stream(stream, at))
+    _check(st, "moe_layer_forward_fp8")
+
+
 # ---------------------------------------------------------------- training
 def _device(t, what):
     """The current device, which t is on.  The training calls launch there: a tensor of
@@ -706,6 +864,155 @@ def orthogonalize(g, steps=5, eps=1e-7):
     return out.view(g.shape)
 
 
+def _rows_args(t, what):
+    """(rows, n, dtype code) of a tensor of rows."""
+    if t.dim() != 2:
+        raise ValueError("%s has shape %s, expected [rows, n]" % (what, tuple(t.shape)))
+    if t.dtype not in _MOE_DTYPE:
+        raise TypeError("%s must be fp32 or bf16" % what)
+    rows, n = t.shape
+    if (rows | n) >> 31:
+        raise _too_large(rows, n)
+    return rows, n, _MOE_DTYPE[t.dtype]
+
+
+def _new_rows8(rows, n, device):
+    return Rows8(torch.empty((rows, n), dtype=FP8, device=device),
+                 torch.empty((rows, _blocks(n)), dtype=torch.float32, device=device))
+
+
+def _rows8_p(r, shape, what, device):
+    if not isinstance(r, Rows8):
+        raise TypeError("%s must be a Rows8" % what)
+    _need(r.q, shape, what)
+    return _p(r.q, FP8, what, device), _p(r.scale, torch.float32, what + "'s scale", device)
+
+
+def pack_rows(x, stream=None) -> Rows8:
+    """x [rows, n] (fp32 or bf16) in 8 bits (moe_pack_rows), in fresh tensors."""
+    rows, n, dt = _rows_args(x, "x")
+    at = _device(x, "x")
+    out = _new_rows8(rows, n, x.device)
+    _check(lib().moe_pack_rows(rows, n, dt, _p(x, x.dtype, "x", at), out.q.data_ptr(),
+                               out.scale.data_ptr(), _stream(stream, at)), "moe_pack_rows")
+    return out
+
+
+def unpack_rows(r: Rows8, dtype=torch.bfloat16, stream=None):
+    """The values of 8-bit rows (moe_unpack_rows) in a fresh fp32 or bf16 tensor."""
+    at = _device(r.q, "q")
+    q, scale = _rows8_p(r, r.q.shape, "q", at)
+    out = torch.empty(r.shape, dtype=dtype, device=r.q.device)
+    rows, n, dt = _rows_args(out, "out")
+    _check(lib().moe_unpack_rows(rows, n, dt, q, scale, out.data_ptr(), _stream(stream, at)),
+           "moe_unpack_rows")
+    return out
+
+
+def swiglu(gate, up, pack=False, stream=None):
+    """silu(gate) * up of rows [rows, n] (moe_swiglu_forward) in a fresh tensor; with pack
+    (h, gate, up), the last two as Rows8 for swiglu_backward."""
+    rows, n, dt = _rows_args(gate, "gate")
+    _need(up, gate.shape, "up")
+    at = _device(gate, "gate")
+    h = torch.empty_like(gate)
+    args = [rows, n, dt, _p(gate, gate.dtype, "gate", at), _p(up, gate.dtype, "up", at),
+            h.data_ptr()]
+    if not pack:
+        _check(lib().moe_swiglu_forward(*args, None, None, None, None, _stream(stream, at)),
+               "moe_swiglu_forward")
+        return h
+    g8, u8 = _new_rows8(rows, n, gate.device), _new_rows8(rows, n, gate.device)
+    _check(lib().moe_swiglu_forward(*args, g8.q.data_ptr(), g8.scale.data_ptr(), u8.q.data_ptr(),
+                                    u8.scale.data_ptr(), _stream(stream, at)),
+           "moe_swiglu_forward")
+    return h, g8, u8
+
+
+def swiglu_backward(dh, gate, up, want_h=False, stream=None):
+    """(dgate, dup, h) of moe_swiglu_backward in fresh tensors of dh's type; gate and up are
+    tensors of that type, or both Rows8.  h is None unless wanted."""
+    rows, n, dt = _rows_args(dh, "dh")
+    at = _device(dh, "dh")
+    if isinstance(gate, Rows8):
+        ins = [None, None, *_rows8_p(gate, dh.shape, "gate", at), *_rows8_p(up, dh.shape, "up", at)]
+    else:
+        _need(gate, dh.shape, "gate")
+        _need(up, dh.shape, "up")
+        ins = [_p(gate, dh.dtype, "gate", at), _p(up, dh.dtype, "up", at), None, None, None, None]
+    dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
+    h = torch.empty_like(dh) if want_h else None
+    _check(lib().moe_swiglu_backward(rows, n, dt, _p(dh, dh.dtype, "dh", at), *ins,
+                                     dgate.data_ptr(), dup.data_ptr(),
+                                     None if h is None else h.data_ptr(), _stream(stream, at)),
+           "moe_swiglu_backward")
+    return dgate, dup, h
+
+
+def moe_gate_workspace_size(desc: LayerDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_gate_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "moe_gate_workspace_size")
+    return n.value
+
+
+def _gate_in(desc, logits, topk_ids):
+    _need(logits, (desc.T, desc.E), "logits")
+    _need(topk_ids, (desc.T, desc.k), "topk_ids")
+    if logits.dtype not in _MOE_DTYPE:
+        raise TypeError("logits must be fp32 or bf16")
+    at = _device(logits, "logits")
+    return at, (_MOE_DTYPE[logits.dtype], _p(logits, logits.dtype, "logits", at),
+                _p(topk_ids, torch.int32, "topk_ids", at))
+
+
+def moe_gate_forward(desc, logits, topk_ids, topk_w, counts, prob, loss, ws, stream=None):
+    """Gate weights [T, k], counts [E+1] int32, prob [E] and loss [1] of the slots topk_ids,
+    each unless None."""
+    for t, shape, what in ((topk_w, (desc.T, desc.k), "topk_w"), (counts, (desc.E + 1,), "counts"),
+                           (prob, (desc.E,), "prob"), (loss, (1,), "loss")):
+        if t is not None:
+            _need(t, shape, what)
+    at, head = _gate_in(desc, logits, topk_ids)
+    st = lib().moe_gate_forward(
+        ctypes.byref(desc), *head, _p(topk_w, torch.float32, "topk_w", at),
+        _p(counts, torch.int32, "counts", at), _p(prob, torch.float32, "prob", at),
+        _p(loss, torch.float32, "loss", at), _p(ws, torch.uint8, "workspace", at),
+        0 if ws is None else ws.numel(), _stream(stream, at))
+    _check(st, "moe_gate_forward")
+
+
+def moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits, stream=None):
+    """dlogits [T, E] from dtopk_w [T, k] and dloss [1], each unless None."""
+    for t, shape, what in ((counts, (desc.E + 1,), "counts"), (dtopk_w, (desc.T, desc.k), "dtopk_w"),
+                           (dloss, (1,), "dloss"), (dlogits, (desc.T, desc.E), "dlogits")):
+        if t is not None:
+            _need(t, shape, what)
+    at, head = _gate_in(desc, logits, topk_ids)
+    st = lib().moe_gate_backward(
+        ctypes.byref(desc), *head, _p(counts, torch.int32, "counts", at),
+        _p(dtopk_w, torch.float32, "dtopk_w", at), _p(dloss, torch.float32, "dloss", at),
+        _p(dlogits, logits.dtype, "dlogits", at), _stream(stream, at))
+    _check(st, "moe_gate_backward")
+
+
+def gate(desc, logits, topk_ids, stream=None):
+    """(topk_w, counts, prob, loss) of moe_gate_forward in fresh tensors."""
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
+    w, counts = new((desc.T, desc.k), torch.float32), new((desc.E + 1,), torch.int32)
+    prob, loss = new((desc.E,), torch.float32), new((1,), torch.float32)
+    ws = new((max(moe_gate_workspace_size(desc), 16),), torch.uint8)
+    moe_gate_forward(desc, logits, topk_ids, w, counts, prob, loss, ws, stream)
+    return w, counts, prob, loss
+
+
+def gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, stream=None):
+    """dlogits of moe_gate_backward in a fresh tensor."""
+    dlogits = torch.empty_like(logits)
+    moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits, stream)
+    return dlogits
+
+
 def moe_get_device_status(ws, clear=False, stream=None) -> int:
     """Synchronizes the stream and returns the workspace's sticky device status."""
     return lib().moe_get_device_status(_p(ws, torch.uint8, "workspace"), ws.numel(),
@@ -903,10 +1210,11 @@ class MoeLayer:
     moe_layer_forward.  Weights are used in place (no copies)."""
 
     def __init__(self, desc: LayerDesc, Wr, Wg, Wu, Wd, logit_bias=None, sel_bias=None):
-        """Wg/Wu/Wd are bf16/fp32 tensors, or Q8Weight (Q8_0 experts, bf16 layers)."""
+        """Wg/Wu/Wd are bf16/fp32 tensors, or Q8Weight or Fp8Weight (bf16 layers)."""
         self.desc = desc
         self.Wr, self.Wg, self.Wu, self.Wd = Wr, Wg, Wu, Wd
         self.q8 = isinstance(Wg, Q8Weight)
+        self.fp8 = isinstance(Wg, Fp8Weight)
         self.logit_bias, self.sel_bias = logit_bias, sel_bias
         self.ws = alloc_workspace(desc, device=Wr.device)
 
@@ -914,7 +1222,8 @@ class MoeLayer:
         d = self.desc
         if y is None:
             y = torch.empty((d.T, d.d), dtype=torch.float32, device=x.device)
-        fwd = moe_layer_forward_q8 if self.q8 else moe_layer_forward
+        fwd = (moe_layer_forward_q8 if self.q8 else
+               moe_layer_forward_fp8 if self.fp8 else moe_layer_forward)
         fwd(d, x, self.Wr, self.logit_bias, self.sel_bias, self.Wg, self.Wu, self.Wd, residual, y,
             topk_ids, topk_w, self.ws, stream)
         return y
@@ -943,6 +1252,10 @@ class MoeLayer:
             st = lib().moe_layer_forward_q8_host(*common, ctypes.byref(g), ctypes.byref(u),
                                                  ctypes.byref(w), *tail)
             _check(st, "moe_layer_forward_q8_host")
+        elif self.fp8:
+            st = lib().moe_layer_forward_fp8_host(
+                *common, *_fp8_structs(d, self.Wg, self.Wu, self.Wd, None), *tail)
+            _check(st, "moe_layer_forward_fp8_host")
         else:
             st = lib().moe_layer_forward_host(*common, _p(self.Wg, None, "Wg"),
                                               _p(self.Wu, None, "Wu"), _p(self.Wd, None, "Wd"),
@@ -981,6 +1294,10 @@ class MoeLayer:
                                                            ctypes.byref(u), ctypes.byref(w),
                                                            *tail)
             _check(st, "moe_layer_forward_q8_host_pipelined")
+        elif self.fp8:
+            st = lib().moe_layer_forward_fp8_host_pipelined(
+                *head, *_fp8_structs(d, self.Wg, self.Wu, self.Wd, None), *tail)
+            _check(st, "moe_layer_forward_fp8_host_pipelined")
         else:
             st = lib().moe_layer_forward_host_pipelined(*head, _p(self.Wg, None, "Wg"),
                                                         _p(self.Wu, None, "Wu"),

@@ -11,6 +11,9 @@ wrapper: it works on gradients.
     y_perm = ...                                        # the experts, on plan.expert_offsets
     y = training.combine(y_perm, topk_w, plan, residual=x)
 
+    topk_w, balance, counts, prob = training.gate(logits, topk_ids, desc)  # the router's side
+    a = training.swiglu(gate, up)     # between the experts' products, its inputs kept in 8 bits
+
 Second derivatives are not provided: they raise.
 
 Capturing a backward pass into a CUDA graph follows torch's own rules: warm up on the
@@ -155,3 +158,60 @@ def combine(y_perm, topk_w, plan: Plan, residual=None):
     """The experts' rows back per token, [T, d] fp32: weighted by topk_w [T, k] fp32 (None:
     by 1), plus the shared slots and the fp32 residual [T, d]."""
     return _Combine.apply(y_perm, topk_w, residual, plan)
+
+
+class _Swiglu(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, up, packed):
+        rows = (gate.reshape(-1, gate.shape[-1]), up.reshape(-1, up.shape[-1]))
+        ctx.packed = packed
+        if packed:
+            h, g8, u8 = moe.swiglu(*rows, pack=True)
+            ctx.save_for_backward(g8.q, g8.scale, u8.q, u8.scale)
+        else:
+            h = moe.swiglu(*rows)
+            ctx.save_for_backward(*rows)
+        return h.view(gate.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        t = ctx.saved_tensors
+        gate, up = (moe.Rows8(*t[:2]), moe.Rows8(*t[2:])) if ctx.packed else t
+        dgate, dup, _ = moe.swiglu_backward(_grad(dh.reshape(-1, dh.shape[-1])), gate, up)
+        return dgate.view(dh.shape), dup.view(dh.shape), None
+
+
+def swiglu(gate, up, packed=True):
+    """silu(gate) * up (contiguous, 16-byte aligned, fp32 or bf16).  packed: the backward pass
+    reads gate and up from 8 bits (e4m3, a scale a block of 128 columns: up to 2^-4 off),
+    half of bf16's memory; else from gate and up themselves."""
+    return _Swiglu.apply(gate, up, packed)
+
+
+class _Gate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_ids, desc):
+        w, counts, prob, loss = moe.gate(desc, logits, topk_ids)
+        ctx.desc = desc
+        ctx.save_for_backward(logits, topk_ids, counts)
+        ctx.mark_non_differentiable(counts, prob)
+        ctx.set_materialize_grads(False)
+        return w, loss.view(()), counts, prob
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dw, dloss, _counts, _prob):
+        if dw is None and dloss is None:
+            return None, None, None
+        logits, topk_ids, counts = ctx.saved_tensors
+        return moe.gate_backward(ctx.desc, logits, topk_ids, counts,
+                                 None if dw is None else _grad(dw),
+                                 None if dloss is None else _grad(dloss.reshape(1))), None, None
+
+
+def gate(logits, topk_ids, desc):
+    """(topk_w [T, k], balance loss [], counts [E+1] int32, prob [E]) of the slots topk_ids
+    [T, k] int32 (an id outside [0, E): a dropped slot, or padding) from router logits [T, E]
+    (fp32 or bf16); the first two have gradients, both by one pass over the logits."""
+    return _Gate.apply(logits, topk_ids, desc)

@@ -276,6 +276,53 @@ moe_status moe_layer_forward_q8(const moe_layer_desc* desc, const void* x, const
                                 int32_t* topk_ids_out, float* topk_w_out, void* workspace,
                                 size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- 8-bit floating point
+   e4m3 codes with one fp32 scale for each block of 128.
+     rows     [R, n]: a scale for 128 columns of a row: q e4m3 [R, n], scale
+              [R, ceil(n/128)]; the last block of a row may be shorter.
+     weights  [n_mats, rows, K]: a scale for a tile of 128 x 128: q e4m3
+              [n_mats, rows, K], scale [n_mats, ceil(rows/128), ceil(K/128)].
+   What the library writes has scales that are powers of two:
+     scale = 2^ceil(log2(max|v| / 448)), at least 2^-126;  q = e4m3(v / scale), to
+     nearest, ties to even (v / scale is exact, so v is rounded once: by 2^-4 of
+     its value at most, or by 2^-10 of the scale where v is below 2^-6 of it).
+   A block that holds a NaN or an infinity gets a NaN scale and NaN codes.
+   The products take any fp32 scales.  (The pages name block quantization of the
+   experts' projections, Q8_0 among others; this is the form with 8-bit floating
+   point products.) */
+typedef struct {
+  const void* q;       /* e4m3 [E+S, rows, K] */
+  const float* scale;  /* fp32 [E+S, ceil(rows/128), ceil(K/128)] */
+} moe_fp8_weight;
+
+/* moe_quantize_fp8 -- n_mats row-major [rows, K] matrices (fp32 or bf16, src_dtype
+   a moe_dtype) in tiles of 128 x 128.  q and scale are device outputs sized as
+   above; any rows, K > 0 (at most 2^31 - 1 tiles, beyond: MOE_ERR_UNSUPPORTED). */
+moe_status moe_quantize_fp8(int n_mats, int rows, int K, int src_dtype, const void* w, void* q,
+                            float* scale, void* stream);
+
+/* moe_expert_ffn_fp8 / moe_layer_forward_fp8 -- moe_expert_ffn and
+   moe_layer_forward with 8-bit expert projections and 8-bit products (router
+   weights stay in the layer's dtype; desc->dtype must be MOE_BF16).  Batch rows
+   are put into 8 bits as above, so is h = silu(Wg x) * (Wu x), formed in fp32; each
+   block of 128 along the reduction is summed over codes in fp32 and scaled by the
+   row's and the tile's scale; y_perm is rounded once to bf16.  Wg/Wu have rows = I
+   and K = d; Wd has rows = d, K = I.  y_perm rows from expert_offsets[E+S] on are
+   left as they were; a token index outside [0, T) sets MOE_ERR_DEVICE_INPUT and its
+   row is that of a zero token.  The _host and _host_pipelined forms are those of
+   moe_layer_forward. */
+moe_status moe_expert_ffn_fp8(const moe_layer_desc* desc, const void* x,
+                              const int32_t* expert_offsets, const int32_t* token_indices,
+                              const float* slot_w, const moe_fp8_weight* Wg,
+                              const moe_fp8_weight* Wu, const moe_fp8_weight* Wd, void* y_perm,
+                              void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_layer_forward_fp8(const moe_layer_desc* desc, const void* x, const void* Wr,
+                                 const float* logit_bias, const float* sel_bias,
+                                 const moe_fp8_weight* Wg, const moe_fp8_weight* Wu,
+                                 const moe_fp8_weight* Wd, const float* residual, float* y,
+                                 int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- expert tier in host memory
    ("Distributed MoE", expert-residency paragraph: experts are kept in a
    byte-bounded, least-recently-used memory tier over a colder tier, and
@@ -384,6 +431,13 @@ moe_status moe_layer_forward_q8_host(const moe_layer_desc* desc, const void* x_h
                                      const float* residual, float* y_host,
                                      int32_t* topk_ids_out, float* topk_w_out, void* workspace,
                                      size_t ws_bytes, void* stream);
+moe_status moe_layer_forward_fp8_host(const moe_layer_desc* desc, const void* x_host,
+                                      const void* Wr, const float* logit_bias,
+                                      const float* sel_bias, const moe_fp8_weight* Wg,
+                                      const moe_fp8_weight* Wu, const moe_fp8_weight* Wd,
+                                      const float* residual, float* y_host,
+                                      int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                                      size_t ws_bytes, void* stream);
 
 /* A run of n_steps layer calls with host buffers, the copies overlapped with
    the neighbouring steps' compute (a serving loop over batches of T tokens
@@ -414,6 +468,13 @@ moe_status moe_layer_forward_q8_host_pipelined(const moe_layer_desc* desc, int n
                                                const moe_q8_weight* Wg, const moe_q8_weight* Wu,
                                                const moe_q8_weight* Wd, float* const* y_host,
                                                void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_layer_forward_fp8_host_pipelined(const moe_layer_desc* desc, int n_steps,
+                                                const void* const* x_host, const void* Wr,
+                                                const float* logit_bias, const float* sel_bias,
+                                                const moe_fp8_weight* Wg,
+                                                const moe_fp8_weight* Wu,
+                                                const moe_fp8_weight* Wd, float* const* y_host,
+                                                void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- training
    What a training step needs around the expert FFN: the norm in front of the
@@ -540,6 +601,68 @@ moe_status moe_ortho_workspace_size(const moe_ortho_desc* desc, size_t* bytes);
 moe_status moe_orthogonalize(const moe_ortho_desc* desc, const void* g, void* out,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* The gate in training: what moe_route's choice gives a loss.  desc: T, E, k, gate,
+   norm_topk and routed_scaling; logits [T, E] in logits_dtype (a moe_dtype), as
+   moe_route ranks them, biases added; topk_ids [T, k] int32, the slots' experts.  A
+   slot whose id is outside [0, E) is dropped: it has no weight, no count and no
+   gradient; a token without any other slot (padding) takes no part at all.  An id
+   may come twice in a token. */
+
+/* Bytes of workspace moe_gate_forward needs (0 when T == 0). */
+moe_status moe_gate_workspace_size(const moe_layer_desc* desc, size_t* bytes);
+
+/* moe_gate_forward -- with p[t] = softmax(logits[t]) (MOE_GATE_SOFTMAX_TOPK) or
+   sigmoid(logits[t]) over its sum (MOE_GATE_SIGMOID_BIAS), n the tokens that take part:
+     topk_w [T, k] fp32 out: the gate weights of the given slots, by moe_route's rule
+            (norm_topk: over the slots that are not dropped).
+     counts [E+1] int32 out: the slots at every expert, and n.
+     prob   [E] fp32 out: the mean of p over those tokens (0 when n == 0).
+     loss   [1] fp32 out: the balance loss E / (k n) * sum_e counts[e] * prob[e], which
+            is 1 where slots and probability are spread evenly (0 when n == 0).
+   Each may be NULL.  fp32 throughout, sums in a fixed order.  T == 0 sets counts,
+   prob and loss to zero. */
+moe_status moe_gate_forward(const moe_layer_desc* desc, int logits_dtype, const void* logits,
+                            const int32_t* topk_ids, float* topk_w, int32_t* counts, float* prob,
+                            float* loss, void* workspace, size_t ws_bytes, void* stream);
+
+/* moe_gate_backward -- the gradient of topk_w and of the loss with respect to the
+   logits (the counts are constants of the loss):
+     counts  [E+1] as moe_gate_forward wrote them (NULL without dloss).
+     dtopk_w [T, k] fp32, or NULL: no gradient by the weights.
+     dloss   [1] fp32 on the device, or NULL: no gradient by the loss.
+     dlogits [T, E] out, logits_dtype, rounded once; zero for tokens that take no
+             part.  Not the logits. */
+moe_status moe_gate_backward(const moe_layer_desc* desc, int logits_dtype, const void* logits,
+                             const int32_t* topk_ids, const int32_t* counts,
+                             const float* dtopk_w, const float* dloss, void* dlogits,
+                             void* stream);
+
+/* Activations kept in 8 bits for the backward pass ("8-bit floating point" above, rows).
+   moe_pack_rows: q, scale from x [rows, n] in dtype (a moe_dtype); moe_unpack_rows: the
+   values again, rounded once.  Any n > 0; rows == 0 is a valid no-op. */
+moe_status moe_pack_rows(int rows, int n, int dtype, const void* x, void* q, float* scale,
+                         void* stream);
+moe_status moe_unpack_rows(int rows, int n, int dtype, const void* q, const float* scale, void* x,
+                           void* stream);
+
+/* moe_swiglu_forward -- h = silu(gate) * up, [rows, n] each in dtype, formed in fp32 and
+   rounded once; with gate8, gate_scale, up8, up_scale (all four or none) also gate
+   and up in 8 bits, as moe_pack_rows writes them, in the same pass.
+   moe_swiglu_backward -- its gradient, from gate and up [rows, n] in dtype, or from
+   their 8-bit form (gate8 .. up_scale; then gate and up are NULL), whose values it
+   takes for gate and up:
+     dgate = dh * up * sigma * (1 + gate * (1 - sigma)),  sigma = sigmoid(gate)
+     dup   = dh * silu(gate)
+     h     [rows, n] out, or NULL: silu(gate) * up again.
+   No output may be an input.  Any n > 0; rows == 0 is a valid no-op. */
+moe_status moe_swiglu_forward(int rows, int n, int dtype, const void* gate, const void* up, void* h,
+                              void* gate8, float* gate_scale, void* up8, float* up_scale,
+                              void* stream);
+moe_status moe_swiglu_backward(int rows, int n, int dtype, const void* dh, const void* gate,
+                               const void* up, const void* gate8, const float* gate_scale,
+                               const void* up8, const float* up_scale, void* dgate, void* dup,
+                               void* h, void* stream);
+
 /* Synchronizes `stream`, then reports the sticky device flag held in the
    workspace: MOE_OK, MOE_ERR_DEVICE_INPUT or MOE_ERR_TIMEOUT (MOE_ERR_CUDA if
    the copy itself fails).  clear != 0 resets the flag afterwards.          */
@@ -577,8 +700,10 @@ int64_t moe_launch_count(void);
    ffn_gateup_tc_q8, ffn_down_tc_q8, quantize_q8_0, combine, combine_partial,
    missing_pairs, dispatch_rows, dispatch_rows_backward, combine_backward,
    norm_forward, norm_backward, norm_reduce, ortho_sumsq, ortho_start,
-   ortho_gram, ortho_poly, ortho_apply, ortho_chip, load_experts (the expert tier's loads of host-resident
-   experts into HBM slots).
+   ortho_gram, ortho_poly, ortho_apply, ortho_chip, gather_rows_fp8, ffn_gateup_fp8,
+   ffn_down_fp8, quantize_fp8, pack_rows, unpack_rows, swiglu_forward, swiglu_backward,
+   gate_forward, gate_finish, gate_backward, load_experts (the expert tier's loads of
+   host-resident experts into HBM slots).
    moe_profile_list() gives the named kernel's recorded launches one by one,
    in launch order: the first max_n durations (ms) and the bytes each launch
    moves where its launcher states them (load_experts: the experts' three

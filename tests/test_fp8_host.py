@@ -1,0 +1,223 @@
+"""Argument checks of the 8-bit, SwiGLU and gate calls that need no GPU: every refusal comes
+back before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+from expert_dispatch_gb300 import build as moe_build
+from expert_dispatch_gb300 import moe
+from tests.test_training_host import FAKE, ODD, _Elsewhere, _Here
+
+BAD, UNSUP, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_OK
+
+
+@pytest.fixture(scope="module")
+def L():
+    moe_build.build()
+    return moe.lib()
+
+
+def _layer(**kw):
+    base = dict(T=8, d=64, E=4, k=2, I=64, S=1, dtype=moe.MOE_BF16)
+    base.update(kw)
+    return moe.make_desc(**base)
+
+
+def _w(q=FAKE, scale=FAKE):
+    return ctypes.byref(moe.Fp8WeightStruct(q, scale))
+
+
+def each_bad(args, needed, optional=()):
+    """args with one pointer missing or misaligned."""
+    for i in needed + tuple(optional):
+        for bad in (None, ODD):
+            if bad is None and i in optional:
+                continue
+            yield [bad if j == i else a for j, a in enumerate(args)]
+
+
+def test_quantize_fp8_refuses(L):
+    fn = L.moe_quantize_fp8
+    for n, r, k, dt in ((-1, 4, 4, 0), (1, 0, 4, 0), (1, 4, 0, 0), (1, 4, 4, 2)):
+        assert fn(n, r, k, dt, FAKE, FAKE, FAKE, None) == BAD
+    for args in each_bad([FAKE] * 3, (0, 1, 2)):
+        assert fn(1, 4, 4, 0, *args, None) == BAD
+    assert fn(1 << 20, 1 << 20, 128, 0, FAKE, FAKE, FAKE, None) == UNSUP
+    assert fn((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, 0, FAKE, FAKE, FAKE, None) == UNSUP
+    assert fn(0, 4, 4, 0, None, None, None, None) == OK
+
+
+def test_expert_ffn_and_layer_refuse(L):
+    d = _layer()
+    n = moe.moe_workspace_size(d)
+    by = ctypes.byref(d)
+    ptrs = [FAKE] * 4  # x, offsets, token_indices, slot_w
+    call = lambda p, w=(_w(), _w(), _w()), y=FAKE, ws=FAKE, b=n, desc=by: \
+        L.moe_expert_ffn_fp8(desc, *p, *w, y, ws, b, None)  # noqa: E731
+    for p in each_bad(ptrs, (0, 1, 2), (3,)):
+        assert call(p) == BAD
+    for i in range(3):
+        for bad in (None, _w(None), _w(FAKE, None), _w(ODD), _w(FAKE, ODD)):
+            assert call(ptrs, [bad if j == i else _w() for j in range(3)]) == BAD
+    assert call(ptrs, y=None) == BAD and call(ptrs, y=ODD) == BAD
+    assert call(ptrs, ws=None) == moe.MOE_ERR_WORKSPACE
+    assert call(ptrs, b=n - 1) == moe.MOE_ERR_WORKSPACE
+    assert call(ptrs, desc=ctypes.byref(_layer(dtype=moe.MOE_F32))) == UNSUP
+    assert call(ptrs, desc=ctypes.byref(_layer(d=96))) == UNSUP
+    assert call(ptrs, desc=None) == BAD
+    assert call([None] * 4, [None] * 3, None, None, 0, ctypes.byref(_layer(T=0))) == OK
+
+    def fwd(x=FAKE, wr=FAKE, lb=None, sb=None, w=None, res=None, y=FAKE, ids=None, tw=None,
+            desc=by, b=n):
+        w = w or [_w()] * 3
+        return L.moe_layer_forward_fp8(desc, x, wr, lb, sb, *w, res, y, ids, tw, FAKE, b, None)
+
+    for kw in (dict(x=None), dict(x=ODD), dict(wr=None), dict(wr=ODD), dict(y=None), dict(y=ODD),
+               dict(res=ODD), dict(ids=ODD), dict(tw=ODD), dict(sb=FAKE),
+               dict(w=[_w(), None, _w()])):
+        assert fwd(**kw) == BAD, kw
+    assert fwd(b=n - 1) == moe.MOE_ERR_WORKSPACE
+    assert fwd(desc=ctypes.byref(_layer(dtype=moe.MOE_F32))) == UNSUP
+    for fn in (L.moe_layer_forward_fp8_host,):
+        assert fn(by, None, FAKE, None, None, _w(), _w(), _w(), None, FAKE, None, None, FAKE, n,
+                  None) == BAD
+    assert L.moe_layer_forward_fp8_host_pipelined(by, -1, FAKE, FAKE, None, None, _w(), _w(), _w(),
+                                                  FAKE, FAKE, n, None) == BAD
+
+
+def test_rows_and_swiglu_refuse(L):
+    for fn in (L.moe_pack_rows, L.moe_unpack_rows):
+        ptrs = [FAKE, ctypes.c_void_p(0x20000), ctypes.c_void_p(0x30000)]
+        for r, n, dt in ((-1, 4, 0), (4, 0, 0), (4, 4, 3)):
+            assert fn(r, n, dt, *ptrs, None) == BAD
+        for args in each_bad(ptrs, (0, 1, 2)):
+            assert fn(4, 4, 0, *args, None) == BAD
+        assert fn(0, 4, 0, None, None, None, None) == OK
+    p = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(10)]
+    fwd, bwd = L.moe_swiglu_forward, L.moe_swiglu_backward
+    for r, n, dt in ((-1, 4, 0), (4, 0, 0), (4, 4, 3)):
+        assert fwd(r, n, dt, *p[:7], None) == BAD and bwd(r, n, dt, *p, None) == BAD
+    for args in each_bad(p[:7], (0, 1, 2, 3, 4, 5, 6)):  # a part of the 8-bit outputs is refused
+        assert fwd(4, 4, 0, *args, None) == BAD
+    for args in ([p[0], p[1], p[0]], [p[0], p[1], p[1]]):  # h over an input
+        assert fwd(4, 4, 0, *args, None, None, None, None, None) == BAD
+    # dh, gate, up, gate8, gate_scale, up8, up_scale, dgate, dup, h
+    plain = [p[0], p[1], p[2], None, None, None, None, p[7], p[8], p[9]]
+    packed = [p[0], None, None, p[3], p[4], p[5], p[6], p[7], p[8], p[9]]
+    for args in each_bad(plain, (0, 1, 2, 7, 8), (9,)):
+        assert bwd(4, 4, 0, *args, None) == BAD
+    for args in each_bad(packed, (0, 3, 4, 5, 6, 7, 8), (9,)):
+        assert bwd(4, 4, 0, *args, None) == BAD
+    assert bwd(4, 4, 0, *p, None) == BAD  # both forms at once
+    for i, j in ((7, 8), (9, 7), (9, 8), (7, 0), (8, 1), (9, 2)):  # outputs over one another
+        args = list(plain)
+        args[i] = args[j]
+        assert bwd(4, 4, 0, *args, None) == BAD
+    assert bwd(0, 4, 0, *[None] * 10, None) == OK
+    assert fwd(0, 4, 0, *[None] * 7, None) == OK
+
+
+def test_gate_refuses(L):
+    n = ctypes.c_size_t(0)
+    d = _layer()
+    by = ctypes.byref(d)
+    assert L.moe_gate_workspace_size(by, None) == BAD
+    assert L.moe_gate_workspace_size(ctypes.byref(_layer(k=9)), ctypes.byref(n)) == BAD
+    assert L.moe_gate_workspace_size(ctypes.byref(_layer(T=0)), ctypes.byref(n)) == OK
+    assert n.value == 0
+    assert L.moe_gate_workspace_size(by, ctypes.byref(n)) == OK and n.value % 256 == 0
+    fwd, bwd = L.moe_gate_forward, L.moe_gate_backward
+    ok = [FAKE] * 6  # logits, ids, w, counts, prob, loss
+    for args in each_bad(ok, (0, 1), (2, 3, 4, 5)):
+        assert fwd(by, 0, *args, FAKE, n.value, None) == BAD
+    assert fwd(by, 2, *ok, FAKE, n.value, None) == BAD
+    assert fwd(None, 0, *ok, FAKE, n.value, None) == BAD
+    for ws, b in ((None, n.value), (ODD, n.value), (FAKE, 16)):
+        assert fwd(by, 0, *ok, ws, b, None) == moe.MOE_ERR_WORKSPACE
+    assert fwd(ctypes.byref(_layer(T=0)), 0, *[None] * 6, None, 0, None) == OK
+    out = ctypes.c_void_p(0x90000)
+    ok = [FAKE] * 5 + [out]  # logits, ids, counts, dw, dloss, dlogits
+    for args in each_bad(ok, (0, 1, 5), (2, 3, 4)):
+        assert bwd(by, 0, *args, None) == BAD
+    assert bwd(by, 0, FAKE, FAKE, None, FAKE, FAKE, out, None) == BAD  # a loss without counts
+    assert bwd(by, 0, out, FAKE, FAKE, FAKE, FAKE, out, None) == BAD   # over the logits
+    assert bwd(by, 5, *ok, None) == BAD
+    assert bwd(ctypes.byref(_layer(T=0)), 0, *[None] * 6, None) == OK
+
+
+def test_binding_checks(monkeypatch):
+    x, q = torch.zeros(4, 130), torch.zeros(4, 130, dtype=moe.FP8)
+    s = torch.zeros(4, 2)
+    r = moe.Rows8(q, s)
+    assert r.shape == (4, 130)
+    for bad in ((x, s), (q, s.double()), (q, s[:, :1]), (q[0], s)):
+        with pytest.raises((TypeError, ValueError)):
+            moe.Rows8(*bad)
+    for bad in ((q, s), (q[None], s), (q[None], s[None].half())):
+        with pytest.raises((TypeError, ValueError)):
+            moe.Fp8Weight(*bad)
+    assert moe.Fp8Weight(q[None], torch.zeros(1, 1, 2)).shape == (1, 4, 130)
+    for call in (lambda: moe.pack_rows(x), lambda: moe.unpack_rows(r), lambda: moe.swiglu(x, x),
+                 lambda: moe.swiglu_backward(x, x, x), lambda: moe.quantize_fp8(x[None])):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError):
+        moe.pack_rows(x.half())
+    with pytest.raises(ValueError, match="shape"):
+        moe.pack_rows(x[0])
+    with pytest.raises(ValueError, match="up"):
+        moe.swiglu(x, x[:2])
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.pack_rows(torch.empty((1 << 32, 1), dtype=torch.bfloat16, device="meta"))
+    d = moe.make_desc(4, 64, 4, 2, 64)
+    with pytest.raises(ValueError, match="logits"):
+        moe.gate(d, x, torch.zeros(4, 2, dtype=torch.int32))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="Fp8Weight"):
+        moe.moe_expert_ffn_fp8(d, _here((4, 64), torch.bfloat16), _here((5,), torch.int32),
+                               _here((8,), torch.int32), None, x, x, x,
+                               _here((8, 64), torch.bfloat16), None)
+
+
+def _here(shape, dtype, cls=_Here):
+    return torch.zeros(shape, dtype=dtype).as_subclass(cls)
+
+
+def test_tensors_of_another_device_are_refused(L, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    i32, u8, f32, bf16, f8 = torch.int32, torch.uint8, torch.float32, torch.bfloat16, moe.FP8
+    d = moe.make_desc(4, 64, 4, 2, 64)
+    ws = ((1 << 20,), u8)
+    w3, s3 = ((4, 64, 64), f8), ((4, 1, 1), f32)
+    x, rows = ((4, 64), bf16), ((8, 64), bf16)
+    r8, rs = ((4, 64), f8), ((4, 1), f32)
+    lg, ids, tw = ((4, 4), f32), ((4, 2), i32), ((4, 2), f32)
+
+    def ffn(x, off, tok, sw, a, b, c, e, f, g, y, w):
+        W = moe.Fp8Weight
+        moe.moe_expert_ffn_fp8(d, x, off, tok, sw, W(a, b), W(c, e), W(f, g), y, w)
+
+    def fwd(x, wr, a, b, c, e, f, g, res, y, i, t, w):
+        W = moe.Fp8Weight
+        moe.moe_layer_forward_fp8(d, x, wr, None, None, W(a, b), W(c, e), W(f, g), res, y, i, t, w)
+
+    calls = [
+        (ffn, (x, ((5,), i32), ((8,), i32), ((8,), f32), w3, s3, w3, s3, w3, s3, rows, ws)),
+        (fwd, (x, x, w3, s3, w3, s3, w3, s3, ((4, 64), f32), ((4, 64), f32), ids, tw, ws)),
+        (moe.moe_quantize_fp8, (((1, 4, 64), f32), ((1, 4, 64), f8), ((1, 1, 1), f32))),
+        (lambda t: moe.pack_rows(t), (x,)),
+        (lambda q, s: moe.unpack_rows(moe.Rows8(q, s)), (r8, rs)),
+        (lambda a, b: moe.swiglu(a, b), (x, x)),
+        (lambda a, b, c: moe.swiglu_backward(a, b, c), (x, x, x)),
+        (lambda h, a, b, c, e: moe.swiglu_backward(h, moe.Rows8(a, b), moe.Rows8(c, e)),
+         (x, r8, rs, r8, rs)),
+        (lambda *a: moe.moe_gate_forward(d, *a), (lg, ids, tw, ((5,), i32), ((4,), f32),
+                                                  ((1,), f32), ws)),
+        (lambda *a: moe.moe_gate_backward(d, *a), (lg, ids, ((5,), i32), tw, ((1,), f32), lg))]
+    for call, shapes in calls:
+        for i in range(len(shapes)):
+            args = [_here(sh, t, _Elsewhere if j == i else _Here)
+                    for j, (sh, t) in enumerate(shapes)]
+            with pytest.raises(ValueError, match="current device is cuda:0"):
+                call(*args)
