@@ -244,7 +244,8 @@ moe_status do_ffn_q8(const moe_layer_desc* D, const void* x, const int32_t* offs
 }
 
 // The same with 8-bit projections and products: x_perm and h hold codes, their
-// scales behind them (d + 4 ceil(d / 128) bytes a row fit the 2 d of bf16 rows).
+// scales behind them (d + 4 fp8_scale_pitch(d) bytes a row, d >= 64, fit the 2 d of
+// bf16 rows and leave what aligning takes).
 moe_status do_ffn_fp8(const moe_layer_desc* D, const void* x, const int32_t* offsets,
                       const int32_t* tok_idx, const float* slot_w, const moe_fp8_weight* Wg,
                       const moe_fp8_weight* Wu, const moe_fp8_weight* Wd, void* y_perm,
@@ -261,8 +262,8 @@ moe_status do_ffn_fp8(const moe_layer_desc* D, const void* x, const int32_t* off
       cudaSuccess)
     return MOE_ERR_CUDA;
   const Fp8Weight g{Wg->q, Wg->scale}, u{Wu->q, Wu->scale}, dn{Wd->q, Wd->scale};
-  return cuda_status(launch_ffn_fp8(W.x_perm, xs, offsets, nE, P, D->d, D->I, g, u, dn, slot_w,
-                                    W.h, hs, y_perm, W.flags, s));
+  return cuda_status(launch_ffn_fp8(W.x_perm, xs, offsets, nE, P, D->d, D->I, (double)P / nE, g, u,
+                                    dn, slot_w, W.h, hs, y_perm, W.flags, s));
 }
 
 bool fp8_ok(const moe_fp8_weight* w) {

@@ -11,8 +11,8 @@
 // codes and scaled once a block.
 //
 // Design (sm_103a, one CTA an SM, persistent):
-//   * A unit is (expert, 256 weight rows, up to 128 token rows): 128 rows of gate
-//     and the same 128 of up, or 256 rows of down.  Token rows are the MMA's M
+//   * A unit is (expert, 256 weight rows, up to 128 token rows, or 256 on an SM
+//     pair): 128 rows of gate and the same 128 of up, or 256 rows of down.  Token rows are the MMA's M
 //     side (the lanes of TMEM), weight rows its N side.  A thread of the epilogue
 //     then has one token row: that row's scale times the block's weight scale is
 //     one factor for all its columns, a column block of h is one thread's (and its
@@ -22,8 +22,14 @@
 //     columns.  The epilogue's warps add each block's products into registers with
 //     their scales while the next block's MMAs fill the other buffer.
 //   * Warp 0 lane 0 issues TMA loads into a ring of stages, warp 1 lane 0 the
-//     MMAs, warps 2-9 the epilogue: two warps a TMEM lane quarter, each with half
-//     of the columns (64 of gate and the same 64 of up, or 128 of down).
+//     MMAs, warps 4-11 the epilogue: two warps a TMEM lane quarter, each with half
+//     of the columns (64 of gate and the same 64 of up, or 128 of down).  A thread
+//     holds 128 sums, so the registers are split unevenly (setmaxnreg).
+//   * Scales never wait on memory: a row's come four blocks at a time, the next
+//     four under way; the tiles' lie across a warp's lanes, 32 blocks at a time.
+//   * Large batches run on SM pairs (cta_group::2, M = 256): each CTA has 128 of the
+//     token rows and brings half of the weight rows, so that an SM is fed 32 KB a
+//     block instead of 48.
 //   * Every wait is bounded (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -42,35 +48,28 @@ using tc::MODE_DOWN;
 using tc::MODE_GATEUP;
 using tc::Unit;
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kRows = 128;  // token rows of a unit
+constexpr int kEpiWarps = 8, kEpiWarp0 = 4;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+// Registers a thread: 384 threads are launched with 168 each; 4 warps give up what 8 take:
+// 128 x 56 + 256 x 224 = 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsEpi = 224;
+static_assert(128 * kRegsIssue + 256 * kRegsEpi == kThreads * kRegsLaunch, "register split");
+constexpr int kRows = 128;  // token rows of a CTA's unit
 constexpr int kCols = 256;  // weight rows of a unit
 constexpr int kBK = 128;    // bytes (= elements) along K of a stage
 
+// Scales of a row lie pitch_of(n) apart, so that four blocks' are one 16-byte load.
+__device__ __forceinline__ int pitch_of(int n) { return fp8_scale_pitch(n); }
+
 struct F8Params {
   tc::Params b;       // offsets, groups, Mg, K, row_scale, err, max_rows
-  const float* xs;    // [rows, KB] scales of the token rows
+  const float* xs;    // [rows, pitch_of(K)] scales of the token rows
   const float* ws0;   // [groups, MB, KB] weight scales (gate, or down)
   const float* ws1;   // up
-  uint8_t* hq;        // gate/up: h's codes [rows, Mg] and scales [rows, MB]
+  uint8_t* hq;        // gate/up: h's codes [rows, Mg] and scales [rows, pitch_of(Mg)]
   float* hs;
   __nv_bfloat16* y;   // down: [rows, Mg]
 };
-
-// acc += {lo, hi} * f, two fp32 fused multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t f) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
-}
-__device__ __forceinline__ uint64_t pair_of(float f) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "r"(__float_as_uint(f)));
-  return v;
-}
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -97,15 +96,35 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// D (+)= A * B^T over an SM pair (M = 256), e4m3 inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0, K-major), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <int STAGES>
+template <int STAGES, bool PAIR>
 struct Cfg {
   static constexpr int A_BYTES = kRows * kBK;
-  static constexpr int B_BYTES = kCols * kBK;
+  static constexpr int B_BYTES = (PAIR ? kCols / 2 : kCols) * kBK;  // a pair's CTA: its half
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   // full, empty; TMEM buffers full, empty; four meetings of the warps of a quarter; wind-down
   static constexpr int NBARS = 2 * STAGES + 4 + 4 + 1;
@@ -118,13 +137,12 @@ struct Cfg {
   static_assert(SMEM_TOTAL <= 232448, "shared memory");
 };
 
-template <int MODE, int STAGES>
-__global__ void __launch_bounds__(kThreads, 1)
-    fp8_grouped_gemm(const __grid_constant__ CUtensorMap tmX,
-                     const __grid_constant__ CUtensorMap tmXfull,
-                     const __grid_constant__ CUtensorMap tmW0,
-                     const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
-  using C = Cfg<STAGES>;
+template <int MODE, int STAGES, bool PAIR>
+__device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUtensorMap& tmXfull,
+                                             const CUtensorMap& tmW0, const CUtensorMap& tmW1,
+                                             const F8Params& p) {
+  using C = Cfg<STAGES, PAIR>;
+  constexpr int kTile = PAIR ? 2 * kRows : kRows;  // token rows of a unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -147,6 +165,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int m_tiles = (p.b.Mg + kUnitRows - 1) / kUnitRows;
   const int KB = (p.b.K + kBK - 1) / kBK;
   const int MB = fp8::blocks_of(p.b.Mg);
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int u0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int ustep = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -155,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8u * b, 1);
-      mbar_init(acce0 + 8u * b, kEpiWarps);
+      mbar_init(acce0 + 8u * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(meet0 + 8u * q, 2);
     mbar_init(drain_bar, 1);
@@ -164,178 +185,264 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmXfull);
     tma_prefetch_desc(&tmW0);
-    if (MODE == MODE_GATEUP) tma_prefetch_desc(&tmW1);
+    tma_prefetch_desc(&tmW1);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
   }
-  if (warp == 2) tc::build_schedule<MODE, kRows>(p.b, m_tiles, prefix, gstart);
+  if (warp == 3) tc::build_schedule<MODE, kTile>(p.b, m_tiles, prefix, gstart);
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = prefix[p.b.n_groups];
+  auto unit = [&](int u) {
+    return tc::decode_unit<MODE, kTile>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
+  };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      auto load_weights = [&](int s, const Unit& t, int kb) {
-        const uint32_t sB = sbase + s * C::STAGE_BYTES + C::A_BYTES;
-        const int row = t.g * p.b.Mg + t.mt * kUnitRows;
-        tma_load_2d(sB, &tmW0, full_bar(s), kb * kBK, row);
-        if (MODE == MODE_GATEUP)
-          tma_load_2d(sB + C::B_BYTES / 2, &tmW1, full_bar(s), kb * kBK, row);
-      };
-      auto unit_bytes = [&](const Unit& t) {
-        return (uint32_t)(C::B_BYTES + (t.nt + 31) / 32 * 32 * kBK);
-      };
-      // The first unit's weight tiles are requested before waiting for the
-      // predecessor grid: no kernel of the sequence writes weights, and the
-      // schedule comes from a grid two launches back.
-      int n_pre = 0;
-      if ((int)blockIdx.x < total) {
-        const Unit t = tc::decode_unit<MODE, kRows>(blockIdx.x, prefix, gstart, p.b.n_groups,
-                                                    m_tiles, KB, p.b);
-        n_pre = min(STAGES, KB);
-        for (int i = 0; i < n_pre; ++i) {
-          mbar_arrive_expect_tx(full_bar(i), unit_bytes(t));
-          armed |= 1u << i;
-          load_weights(i, t, i);
+  if (warp < kEpiWarp0) {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        // Of a pair both CTAs' copies complete on the even CTA's barrier.
+        auto load = [&](int s, uint32_t dst, const CUtensorMap& tm, int kb, int row) {
+          if (PAIR)
+            tma_load_2d_pair(dst, &tm, mapa_shared(full_bar(s), 0), kb * kBK, row);
+          else
+            tma_load_2d(dst, &tm, full_bar(s), kb * kBK, row);
+        };
+        // The unit's 256 weight rows: 128 of gate and of up, or of down twice; a pair's
+        // CTA brings the first or the second 128.
+        auto load_weights = [&](int s, const Unit& t, int kb) {
+          const uint32_t sB = sbase + s * C::STAGE_BYTES + C::A_BYTES;
+          const int row = t.g * p.b.Mg + t.mt * kUnitRows;
+          const int second = MODE == MODE_GATEUP ? row : row + 128;
+          if (PAIR) {
+            if (rank == 0)
+              load(s, sB, tmW0, kb, row);
+            else
+              load(s, sB, tmW1, kb, second);
+          } else {
+            load(s, sB, tmW0, kb, row);
+            load(s, sB + C::B_BYTES / 2, tmW1, kb, second);
+          }
+        };
+        auto arm = [&](int s, const Unit& t) {  // all CTAs' weight and token bytes
+          if (rank != 0) return;
+          const int chunks = (t.nt + 31) / 32;
+          mbar_arrive_expect_tx(full_bar(s), kCols * kBK + chunks * 32 * kBK);
+          armed |= 1u << s;
+        };
+        // The first unit's weight tiles are requested before waiting for the
+        // predecessor grid: no kernel of the sequence writes weights, and the
+        // schedule comes from a grid two launches back.
+        int n_pre = 0;
+        if (u0 < total) {
+          const Unit t = unit(u0);
+          n_pre = min(STAGES, KB);
+          for (int i = 0; i < n_pre; ++i) {
+            arm(i, t);
+            load_weights(i, t, i);
+          }
+        }
+        pdl_wait();
+        bool first = true;
+        for (int u = u0; u < total && !*abort_flag; u += ustep) {
+          if (u + ustep >= total) pdl_trigger();  // this CTA's last unit
+          const Unit t = unit(u);
+          const int mine = min(max(t.nt - rank * kRows, 0), kRows);
+          const int chunks = (mine + 31) / 32, row = t.r0 + rank * kRows;
+          bool ok = true;
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!(first && kb < n_pre)) {
+              if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.b.err)) {
+                ok = false;
+                break;
+              }
+              arm(stage, t);
+              armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+              load_weights(stage, t, kb);
+            }
+            const uint32_t sA = sbase + stage * C::STAGE_BYTES;
+            if (chunks == 4)
+              load(stage, sA, tmXfull, kb, row);
+            else
+              for (int c = 0; c < chunks; ++c)
+                load(stage, sA + c * 32 * kBK, tmX, kb, row + c * 32);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          first = false;
+          if (!ok) break;
+        }
+        if (u0 >= total) pdl_trigger();
+        if (rank == 0) {
+          // wind down: every copy that completes here has landed before exit
+          for (int s = 0; s < STAGES; ++s)
+            if (armed & (1u << s))
+              tc::mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.b.err);
+        } else if (*abort_flag) {
+          // this CTA's copies complete on its partner's barriers: after giving up, leave
+          // them a bounded time to land before the shared memory goes
+          const unsigned long long t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 100000ull) {
+          }
         }
       }
-      pdl_wait();
-      bool first = true;
-      for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
-        if (u + (int)gridDim.x >= total) pdl_trigger();  // this CTA's last unit
-        const Unit t =
-            tc::decode_unit<MODE, kRows>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
-        const int chunks = (t.nt + 31) / 32;
-        bool ok = true;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!(first && kb < n_pre)) {
-            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.b.err)) {
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer (a pair's even CTA)
+      if (lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(kTile, kCols);
+        int stage = 0;
+        uint32_t phase = 0, it = 0;
+        bool issued = false, ok = true;
+        auto commit = [&](uint32_t bar) {
+          if (PAIR)
+            umma_commit_pair_mc(bar, 3);
+          else
+            umma_commit(bar);
+        };
+        for (int u = u0; ok && u < total && !*abort_flag; u += ustep) {
+          for (int kb = 0; kb < KB; ++kb, ++it) {
+            const uint32_t buf = it & 1u;
+            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.b.err) ||
+                !mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(full_bar(stage), unit_bytes(t));
-            armed |= 1u << stage;
-            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-            load_weights(stage, t, kb);
-          }
-          const uint32_t sA = sbase + stage * C::STAGE_BYTES;
-          if (chunks == 4)
-            tma_load_2d(sA, &tmXfull, full_bar(stage), kb * kBK, t.r0);
-          else
-            for (int c = 0; c < chunks; ++c)
-              tma_load_2d(sA + c * 32 * kBK, &tmX, full_bar(stage), kb * kBK, t.r0 + c * 32);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        first = false;
-        if (!ok) break;
-      }
-      if ((int)blockIdx.x >= total) pdl_trigger();
-      // wind down: every copy this thread started has landed before exit
-      for (int s = 0; s < STAGES; ++s)
-        if (armed & (1u << s)) tc::mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.b.err);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kCols);
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
-      bool issued = false, ok = true;
-      for (int u = blockIdx.x; ok && u < total && !*abort_flag; u += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const uint32_t buf = it & 1u;
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.b.err) ||
-              !mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sA = sbase + stage * C::STAGE_BYTES;
-          const uint32_t sB = sA + C::A_BYTES;
+            tc_fence_after();
+            const uint32_t sA = sbase + stage * C::STAGE_BYTES;
+            const uint32_t sB = sA + C::A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_e4m3(tmem_base + buf * kCols, smem_desc_sw128(sA + kk * 32),
-                      smem_desc_sw128(sB + kk * 32), idesc, kk != 0);
-          issued = true;
-          umma_commit(empty_bar(stage));
-          umma_commit(accf0 + 8u * buf);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t a = smem_desc_sw128(sA + kk * 32), b = smem_desc_sw128(sB + kk * 32);
+              if (PAIR)
+                umma_e4m3_pair(tmem_base + buf * kCols, a, b, idesc, kk != 0);
+              else
+                umma_e4m3(tmem_base + buf * kCols, a, b, idesc, kk != 0);
+            }
+            issued = true;
+            commit(empty_bar(stage));
+            commit(accf0 + 8u * buf);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
-      }
-      // wind down: every MMA this thread issued has completed before TMEM is freed
-      if (issued) {
-        umma_commit(drain_bar);
-        tc::mbar_wait_drain(drain_bar, 0, p.b.err);
+        // wind down: every MMA this thread issued has completed before TMEM is freed
+        if (issued) {
+          if (PAIR)
+            umma_commit_pair_mc(drain_bar, 1);
+          else
+            umma_commit(drain_bar);
+          tc::mbar_wait_drain(drain_bar, 0, p.b.err);
+        }
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..9)
+    // ------------------------------------------------------------ epilogue (warps 4..11)
+    setmaxnreg_inc<kRegsEpi>();
     pdl_wait();  // the token rows' scales are the predecessor's
-    const int q = warp & 3;            // TMEM lane quarter this warp may access
-    const int half = (warp - 2) >> 2;  // its half of the columns
+    const int q = warp & 3;                    // TMEM lane quarter this warp may access
+    const int half = (warp - kEpiWarp0) >> 2;  // its half of the columns
+    const int pitch = pitch_of(p.b.K);
     uint32_t it = 0, met = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-      const Unit t =
-          tc::decode_unit<MODE, kRows>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
-      const int lrow = q * 32 + lane;
-      const bool warp_live = q * 32 < t.nt, live = lrow < t.nt;
-      const size_t row = (size_t)(t.r0 + (live ? lrow : 0));
-      const float* xs = p.xs + row * KB;
-      // this thread's weight scales: its 64 columns of gate and up, or its 128 of down
+    for (int u = u0; ok && u < total; u += ustep) {
+      const Unit t = unit(u);
+      const int lrow = q * 32 + lane, mine = t.nt - rank * kRows;
+      const bool warp_live = q * 32 < mine, live = lrow < mine;
+      const size_t row = (size_t)(t.r0 + (live ? rank * kRows + lrow : 0));
+      const float4* xs = reinterpret_cast<const float4*>(p.xs + row * pitch);
+      // this warp's weight scales: its 64 columns of gate and up, or its 128 of down
       const int wb = MODE == MODE_GATEUP ? t.mt : min(2 * t.mt + half, MB - 1);
       const size_t wrow = ((size_t)t.g * MB + wb) * KB;
       const float* ws0 = p.ws0 + wrow;
       const float* ws1 = p.ws1 + wrow;
-      uint64_t acc[64];  // 128 sums, two a register pair
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float sx = warp_live ? xs[0] : 0.f, s0 = ws0[0], s1 = MODE == MODE_GATEUP ? ws1[0] : 0.f;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      float4 sx{}, nx{};
+      float w0 = 0.f, w1 = 0.f, n0 = 0.f, n1 = 0.f;
+      if (warp_live) {
+        nx = xs[0];
+        if (lane < KB) {
+          n0 = ws0[lane];
+          if (MODE == MODE_GATEUP) n1 = ws1[lane];
+        }
+      }
+#pragma unroll 1
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const uint32_t buf = it & 1u;
-        const uint64_t f0 = pair_of(sx * s0);
-        const uint64_t f1 = MODE == MODE_GATEUP ? pair_of(sx * s1) : f0;
-        if (kb + 1 < KB) {  // the next block's scales, while this one is waited for
-          if (warp_live) sx = xs[kb + 1];
-          s0 = ws0[kb + 1];
-          if (MODE == MODE_GATEUP) s1 = ws1[kb + 1];
+        if (warp_live) {
+          if ((kb & 3) == 0) {
+            sx = nx;
+            if (kb + 4 < KB) nx = xs[kb / 4 + 1];
+          }
+          if ((kb & 31) == 0) {
+            w0 = n0, w1 = n1;
+            if (kb + 32 + lane < KB) {
+              n0 = ws0[kb + 32 + lane];
+              if (MODE == MODE_GATEUP) n1 = ws1[kb + 32 + lane];
+            }
+          }
         }
+        const float s = (kb & 2) ? ((kb & 1) ? sx.w : sx.z) : ((kb & 1) ? sx.y : sx.x);
+        const float f0 = s * __shfl_sync(0xffffffffu, w0, kb & 31);
+        const float f1 = MODE == MODE_GATEUP ? s * __shfl_sync(0xffffffffu, w1, kb & 31) : f0;
         if (!tc::mbar_wait_warp(accf0 + 8u * buf, (it >> 1) & 1u, abort_flag, p.b.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (warp_live) {
-          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kCols;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // gate's 64 columns then up's, or down's 128
-            const uint32_t col = MODE == MODE_GATEUP ? (c >> 1) * 128 + half * 64 + (c & 1) * 32
-                                                     : half * 128 + c * 32;
-            uint32_t v[32];
-            tmem_ld32(tb + col, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              fma2(acc[c * 16 + i], v[2 * i], v[2 * i + 1], c < 2 ? f0 : f1);
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR)
+              mbar_arrive_cluster(mapa_shared(acce0 + 8u * buf, 0));
+            else
+              mbar_arrive(acce0 + 8u * buf);
           }
+        };
+        if (!warp_live) {
+          release();
+          continue;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acce0 + 8u * buf);
+        // gate's 64 columns then up's, or down's 128: 32 at a time, two loads under way
+        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kCols +
+                            (MODE == MODE_GATEUP ? half * 64 : half * 128);
+        constexpr uint32_t kSecond = MODE == MODE_GATEUP ? 128 : 64;
+        auto add = [&](int c, const uint32_t (&v)[32], float f) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            acc[c * 32 + i] = fmaf(__uint_as_float(v[i]), f, acc[c * 32 + i]);
+        };
+        uint32_t va[32], vb[32];
+        tmem_ld32(tb, va);
+        tmem_ld32(tb + 32, vb);
+        tmem_ld_wait();
+        add(0, va, f0);
+        tmem_ld32(tb + kSecond, va);
+        add(1, vb, f0);
+        tmem_ld32(tb + kSecond + 32, vb);
+        tmem_ld_wait();
+        release();  // everything is in registers: the next MMAs may have the buffer
+        add(2, va, f1);
+        add(3, vb, f1);
       }
       if (!ok) break;
       if constexpr (MODE == MODE_GATEUP) {
@@ -344,13 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool cols = c0 < p.b.Mg;
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = silu_fast(lo_of(acc[i])) * lo_of(acc[32 + i]);
-          const float b = silu_fast(hi_of(acc[i])) * hi_of(acc[32 + i]);
-          m = max(m, max(fp8::abs_bits(a), fp8::abs_bits(b)));
-          asm("mov.b64 %0, {%1, %2};"
-              : "=l"(acc[i])
-              : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = silu_fast(acc[i]) * acc[64 + i];
+          m = max(m, fp8::abs_bits(acc[i]));
         }
         if (!cols) m = 0;
         if (warp_live) {
@@ -371,13 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint64_t a = acc[i * 8 + j * 2], b = acc[i * 8 + j * 2 + 1];
-                w[j] = fp8::codes4(lo_of(a) * sc.inv, hi_of(a) * sc.inv, lo_of(b) * sc.inv,
-                                   hi_of(b) * sc.inv);
+                const float* a = acc + i * 16 + j * 4;
+                w[j] = fp8::codes4(a[0] * sc.inv, a[1] * sc.inv, a[2] * sc.inv, a[3] * sc.inv);
               }
               dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (half == 0) p.hs[row * MB + t.mt] = sc.scale;
+            if (half == 0) p.hs[row * pitch_of(p.b.Mg) + t.mt] = sc.scale;
           }
         }
       } else {
@@ -391,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint64_t a = acc[i * 4 + j];
-                const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * f, hi_of(a) * f);
+                const float* a = acc + i * 8 + j * 2;
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a[0] * f, a[1] * f);
                 w[j] = *reinterpret_cast<const uint32_t*>(&h);
               }
               dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -405,11 +507,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // the partner is done with this CTA's shared memory and TMEM
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
   }
+}
+
+template <int MODE, int STAGES>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_grouped_gemm(const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ CUtensorMap tmXfull,
+                     const __grid_constant__ CUtensorMap tmW0,
+                     const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
+  grouped_gemm<MODE, STAGES, false>(tmX, tmXfull, tmW0, tmW1, p);
+}
+
+template <int MODE, int STAGES>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp8_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmX,
+                          const __grid_constant__ CUtensorMap tmXfull,
+                          const __grid_constant__ CUtensorMap tmW0,
+                          const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
+  grouped_gemm<MODE, STAGES, true>(tmX, tmXfull, tmW0, tmW1, p);
 }
 
 // e4m3 matrix [rows, inner] (row-major), boxes of box_rows x 128, 128-byte swizzle;
@@ -420,37 +544,55 @@ bool make_tmap_f8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t ro
                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE, int STAGES>
+// The grid is what runs at once: one CTA an SM, or of a pair kernel two for each cluster
+// that fits (an SM pair must share a GPC).
+template <int MODE, int STAGES, bool PAIR>
 cudaError_t launch_f8(const CUtensorMap& x, const CUtensorMap& xfull, const CUtensorMap& w0,
                       const CUtensorMap& w1, const F8Params& p, long long max_units,
                       const char* name, cudaStream_t s) {
-  using C = Cfg<STAGES>;
-  auto kern = fp8_grouped_gemm<MODE, STAGES>;
+  using C = Cfg<STAGES, PAIR>;
+  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, F8Params);
+  if constexpr (PAIR)
+    kern = fp8_grouped_gemm_pair<MODE, STAGES>;
+  else
+    kern = fp8_grouped_gemm<MODE, STAGES>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
   static std::mutex mu;
-  static bool configured[64] = {};
+  static int at_once[64] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (dev >= 64 || !configured[dev]) {
+    if (at_once[dev] == 0) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
       if (e != cudaSuccess) return e;
-      if (dev < 64) configured[dev] = true;
+      int n = num_sms();
+      if (PAIR) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (unsigned)(num_sms() / 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::SMEM_TOTAL;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+      }
+      at_once[dev] = n;
     }
   }
-  const long long grid = max_units < num_sms() ? max_units : num_sms();
-  if (grid <= 0) return cudaSuccess;
+  const long long n = max_units < at_once[dev] ? max_units : at_once[dev];
+  if (n <= 0) return cudaSuccess;
   ProfScope pr(name, s);
-  (void)launch_kernel(kern, (unsigned)grid, kThreads, C::SMEM_TOTAL, s, x, xfull, w0, w1, p);
+  (void)launch_kernel(kern, (unsigned)(PAIR ? 2 * n : n), kThreads, C::SMEM_TOTAL, s, x, xfull, w0,
+                      w1, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
-                           int P, int d, int I, const Fp8Weight& Wg, const Fp8Weight& Wu,
-                           const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
+                           int P, int d, int I, double mean_rows, const Fp8Weight& Wg,
+                           const Fp8Weight& Wu, const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
                            void* y_perm, int* err, cudaStream_t s) {
   if (P == 0) return cudaSuccess;
   const uint64_t cap = (uint64_t)tc_row_capacity(P);
@@ -459,7 +601,7 @@ cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offse
       !make_tmap_f8(&th, h8, I, cap, 32) || !make_tmap_f8(&thf, h8, I, cap, 128) ||
       !make_tmap_f8(&tg, Wg.q, d, (uint64_t)n_groups * I, 128) ||
       !make_tmap_f8(&tu, Wu.q, d, (uint64_t)n_groups * I, 128) ||
-      !make_tmap_f8(&td, Wd.q, I, (uint64_t)n_groups * d, 256))
+      !make_tmap_f8(&td, Wd.q, I, (uint64_t)n_groups * d, 128))
     return cudaErrorInvalidValue;
   F8Params p1{}, p2{};
   p1.b.offsets = p2.b.offsets = offsets;
@@ -473,11 +615,16 @@ cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offse
   p2.b.row_scale = slot_w;
   p2.xs = hs, p2.ws0 = p2.ws1 = Wd.scale;
   p2.y = static_cast<__nv_bfloat16*>(y_perm);
-  const long long tiles = (long long)(P + kRows - 1) / kRows + n_groups;
-  const cudaError_t e = launch_f8<MODE_GATEUP, 4>(tx, txf, tg, tu, p1, (I + 127) / 128 * tiles,
-                                                  "ffn_gateup_fp8", s);
+  const bool pair = mean_rows > 512.0;
+  const int rows = pair ? 2 * kRows : kRows;
+  const long long tiles = (long long)(P + rows - 1) / rows + n_groups;
+  const long long u1 = (I + 127) / 128 * tiles, u2 = (d + 255) / 256 * tiles;
+  const char *n1 = "ffn_gateup_fp8", *n2 = "ffn_down_fp8";
+  const cudaError_t e = pair ? launch_f8<MODE_GATEUP, 6, true>(tx, txf, tg, tu, p1, u1, n1, s)
+                             : launch_f8<MODE_GATEUP, 4, false>(tx, txf, tg, tu, p1, u1, n1, s);
   if (e != cudaSuccess) return e;
-  return launch_f8<MODE_DOWN, 4>(th, thf, td, td, p2, (d + 255) / 256 * tiles, "ffn_down_fp8", s);
+  return pair ? launch_f8<MODE_DOWN, 6, true>(th, thf, td, td, p2, u2, n2, s)
+              : launch_f8<MODE_DOWN, 4, false>(th, thf, td, td, p2, u2, n2, s);
 }
 
 }  // namespace moe

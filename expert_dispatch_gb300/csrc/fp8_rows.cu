@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) gather_rows_fp8_kernel(
     const fp8::Scale sc = fp8::scale_of(amax16(v));
     if (b < nb) {
       store8<true>(q + (size_t)r * d + (size_t)b * fp8::kBlock, lane, width, v, sc.inv);
-      if (lane == 0) scale[(size_t)r * nb + b] = sc.scale;
+      if (lane == 0) scale[(size_t)r * fp8_scale_pitch(d) + b] = sc.scale;
     }
   }
 }

@@ -235,14 +235,16 @@ cudaError_t launch_pack_rows(int dtype, const void* x, long long rows, int n, vo
                              float* scale, cudaStream_t s);
 cudaError_t launch_unpack_rows(int dtype, const void* q, const float* scale, long long rows, int n,
                                void* x, cudaStream_t s);
-// bf16 rows gathered by tok_idx and put into 8 bits
+// The FFN's own rows: scales of a row of n columns lie this many floats apart.
+__host__ __device__ constexpr int fp8_scale_pitch(int n) { return (n + 511) / 512 * 4; }
+// bf16 rows gathered by tok_idx and put into 8 bits, scales fp8_scale_pitch(d) apart
 cudaError_t launch_gather_rows_fp8(const void* x, const int32_t* tok_idx,
                                    const int32_t* total_rows, int P, int T, int d, void* q,
                                    float* scale, int* flags, cudaStream_t s);
 // x8 [cap, d] with scales xs, h8 [cap, I] with scales hs, cap = tc_row_capacity(P)
 cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
-                           int P, int d, int I, const Fp8Weight& Wg, const Fp8Weight& Wu,
-                           const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
+                           int P, int d, int I, double mean_rows, const Fp8Weight& Wg,
+                           const Fp8Weight& Wu, const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
                            void* y_perm, int* err, cudaStream_t s);
 
 // The activation between the products, its inputs kept in 8 bits (swiglu.cu).
