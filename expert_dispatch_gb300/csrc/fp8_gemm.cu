@@ -21,8 +21,11 @@
 //     tcgen05.mma (kind::f8f6f4, K = 32) into one of two TMEM buffers of 256
 //     columns.  The epilogue's warps add each block's products into registers with
 //     their scales while the next block's MMAs fill the other buffer.
-//   * Warp 0 lane 0 issues TMA loads into a ring of stages, warp 1 lane 0 the
-//     MMAs, warps 4-11 the epilogue: two warps a TMEM lane quarter, each with half
+//   * Warp 0 lane 0 issues TMA loads into a ring of stages, lane 0 of warps 1 and 2
+//     the MMAs of even and odd blocks (a block's products go to a TMEM buffer of
+//     their own, so the two need no order, and one waits for its stage and buffer
+//     while the other's MMAs run: one issuing thread left the tensor cores idle for
+//     300 of 800 cycles a block), warps 4-11 the epilogue: two warps a TMEM lane quarter, each with half
 //     of the columns (64 of gate and the same 64 of up, or 128 of down).  A thread
 //     holds 128 sums, so the registers are split unevenly (setmaxnreg).
 //   * Scales never wait on memory: a row's come four blocks at a time, the next
@@ -107,6 +110,25 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
+// acc += {lo, hi} * f, two fp32 fused multiply-adds in one instruction (128 x 256 sums a
+// block by 8 warps: 270 cycles, 350 one by one).  Volatile: the products of a load stay
+// before the next load into the same registers, which would otherwise be copied.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t f) {
+  asm volatile(
+      "{\n\t.reg .b64 v;\n\t"
+      "mov.b64 v, {%1, %2};\n\t"
+      "fma.rn.f32x2 %0, v, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(f));
+}
+__device__ __forceinline__ uint64_t pair_of(float f) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "r"(__float_as_uint(f)));
+  return v;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -126,8 +148,8 @@ struct Cfg {
   static constexpr int A_BYTES = kRows * kBK;
   static constexpr int B_BYTES = (PAIR ? kCols / 2 : kCols) * kBK;  // a pair's CTA: its half
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // full, empty; TMEM buffers full, empty; four meetings of the warps of a quarter; wind-down
-  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 1;
+  // full, empty; TMEM buffers full, empty; four meetings of the warps of a quarter; wind-downs
+  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2;
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int TOP_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // [2][2][128] row maxima
@@ -179,7 +201,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
       mbar_init(acce0 + 8u * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(meet0 + 8u * q, 2);
-    mbar_init(drain_bar, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(drain_bar + 8u * i, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmX);
@@ -301,10 +323,11 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           }
         }
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer (a pair's even CTA)
+    } else if (warp <= 2) {
+      // ---------------------------------------------------------- MMA issuers (a pair's even CTA)
       if (lane == 0 && rank == 0) {
         constexpr uint32_t idesc = idesc_e4m3_f32(kTile, kCols);
+        const uint32_t buf = warp - 1;  // even blocks of this CTA's sequence, or odd ones
         int stage = 0;
         uint32_t phase = 0, it = 0;
         bool issued = false, ok = true;
@@ -316,26 +339,28 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         };
         for (int u = u0; ok && u < total && !*abort_flag; u += ustep) {
           for (int kb = 0; kb < KB; ++kb, ++it) {
-            const uint32_t buf = it & 1u;
-            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.b.err) ||
-                !mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sA = sbase + stage * C::STAGE_BYTES;
-            const uint32_t sB = sA + C::A_BYTES;
+            if ((it & 1u) == buf) {
+              if (!mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err) ||
+                  !mbar_wait(full_bar(stage), phase, abort_flag, p.b.err)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sA = sbase + stage * C::STAGE_BYTES;
+              const uint32_t sB = sA + C::A_BYTES;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = smem_desc_sw128(sA + kk * 32), b = smem_desc_sw128(sB + kk * 32);
-              if (PAIR)
-                umma_e4m3_pair(tmem_base + buf * kCols, a, b, idesc, kk != 0);
-              else
-                umma_e4m3(tmem_base + buf * kCols, a, b, idesc, kk != 0);
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a = smem_desc_sw128(sA + kk * 32);
+                const uint64_t b = smem_desc_sw128(sB + kk * 32);
+                if (PAIR)
+                  umma_e4m3_pair(tmem_base + buf * kCols, a, b, idesc, kk != 0);
+                else
+                  umma_e4m3(tmem_base + buf * kCols, a, b, idesc, kk != 0);
+              }
+              issued = true;
+              commit(accf0 + 8u * buf);
+              commit(empty_bar(stage));
             }
-            issued = true;
-            commit(empty_bar(stage));
-            commit(accf0 + 8u * buf);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -345,10 +370,10 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         // wind down: every MMA this thread issued has completed before TMEM is freed
         if (issued) {
           if (PAIR)
-            umma_commit_pair_mc(drain_bar, 1);
+            umma_commit_pair_mc(drain_bar + 8u * buf, 1);
           else
-            umma_commit(drain_bar);
-          tc::mbar_wait_drain(drain_bar, 0, p.b.err);
+            umma_commit(drain_bar + 8u * buf);
+          tc::mbar_wait_drain(drain_bar + 8u * buf, 0, p.b.err);
         }
       }
     }
@@ -359,6 +384,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
     const int q = warp & 3;                    // TMEM lane quarter this warp may access
     const int half = (warp - kEpiWarp0) >> 2;  // its half of the columns
     const int pitch = pitch_of(p.b.K);
+    const uint32_t acce_even = PAIR ? mapa_shared(acce0, 0) : acce0;
     uint32_t it = 0, met = 0;
     bool ok = true;
     for (int u = u0; ok && u < total; u += ustep) {
@@ -372,9 +398,9 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
       const size_t wrow = ((size_t)t.g * MB + wb) * KB;
       const float* ws0 = p.ws0 + wrow;
       const float* ws1 = p.ws1 + wrow;
-      float acc[128];
+      uint64_t sum[64];  // this thread's 128 columns, two a register pair
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
       float4 sx{}, nx{};
       float w0 = 0.f, w1 = 0.f, n0 = 0.f, n1 = 0.f;
       if (warp_live) {
@@ -384,10 +410,39 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           if (MODE == MODE_GATEUP) n1 = ws1[lane];
         }
       }
+      auto release = [&](uint32_t buf) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(acce_even + 8u * buf);
+          else
+            mbar_arrive(acce0 + 8u * buf);
+        }
+      };
+      auto wait = [&]() {
+        const bool there = tc::mbar_wait_warp(accf0 + 8u * (it & 1u), (it >> 1) & 1u, abort_flag,
+                                              p.b.err);
+        if (there) tc_fence_after();
+        return there;
+      };
+      if (!warp_live) {
+        for (int kb = 0; kb < KB && (ok = wait()); ++kb, ++it) release(it & 1u);
+      } else if ((ok = wait())) {
+        // gate's 64 columns then up's, or down's 128: 32 at a time, the next 32 loaded
+        // while these are added, also across blocks
+        const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) +
+                            (MODE == MODE_GATEUP ? half * 64 : half * 128);
+        constexpr uint32_t kSecond = MODE == MODE_GATEUP ? 128 : 64;
+        auto add = [&](int c, const uint32_t (&v)[32], uint64_t f) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fma2(sum[c * 16 + i], v[2 * i], v[2 * i + 1], f);
+        };
+        uint32_t va[32], vb[32];
+        tmem_ld32(tq + (it & 1u) * kCols, va);
 #pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const uint32_t buf = it & 1u;
-        if (warp_live) {
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint32_t buf = it & 1u, tb = tq + buf * kCols;
           if ((kb & 3) == 0) {
             sx = nx;
             if (kb + 4 < KB) nx = xs[kb / 4 + 1];
@@ -399,50 +454,28 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
               if (MODE == MODE_GATEUP) n1 = ws1[kb + 32 + lane];
             }
           }
-        }
-        const float s = (kb & 2) ? ((kb & 1) ? sx.w : sx.z) : ((kb & 1) ? sx.y : sx.x);
-        const float f0 = s * __shfl_sync(0xffffffffu, w0, kb & 31);
-        const float f1 = MODE == MODE_GATEUP ? s * __shfl_sync(0xffffffffu, w1, kb & 31) : f0;
-        if (!tc::mbar_wait_warp(accf0 + 8u * buf, (it >> 1) & 1u, abort_flag, p.b.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        auto release = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR)
-              mbar_arrive_cluster(mapa_shared(acce0 + 8u * buf, 0));
-            else
-              mbar_arrive(acce0 + 8u * buf);
+          const float s = (kb & 2) ? ((kb & 1) ? sx.w : sx.z) : ((kb & 1) ? sx.y : sx.x);
+          const uint64_t f0 = pair_of(s * __shfl_sync(0xffffffffu, w0, kb & 31));
+          const uint64_t f1 =
+              MODE == MODE_GATEUP ? pair_of(s * __shfl_sync(0xffffffffu, w1, kb & 31)) : f0;
+          tmem_ld_wait();
+          tmem_ld32(tb + 32, vb);
+          add(0, va, f0);
+          tmem_ld_wait();
+          tmem_ld32(tb + kSecond, va);
+          add(1, vb, f0);
+          tmem_ld_wait();
+          tmem_ld32(tb + kSecond + 32, vb);
+          add(2, va, f1);
+          tmem_ld_wait();
+          release(buf);  // everything is in registers: the next MMAs may have the buffer
+          ++it;
+          if (kb + 1 < KB) {
+            if (!(ok = wait())) break;
+            tmem_ld32(tq + (it & 1u) * kCols, va);
           }
-        };
-        if (!warp_live) {
-          release();
-          continue;
+          add(3, vb, f1);
         }
-        // gate's 64 columns then up's, or down's 128: 32 at a time, two loads under way
-        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kCols +
-                            (MODE == MODE_GATEUP ? half * 64 : half * 128);
-        constexpr uint32_t kSecond = MODE == MODE_GATEUP ? 128 : 64;
-        auto add = [&](int c, const uint32_t (&v)[32], float f) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            acc[c * 32 + i] = fmaf(__uint_as_float(v[i]), f, acc[c * 32 + i]);
-        };
-        uint32_t va[32], vb[32];
-        tmem_ld32(tb, va);
-        tmem_ld32(tb + 32, vb);
-        tmem_ld_wait();
-        add(0, va, f0);
-        tmem_ld32(tb + kSecond, va);
-        add(1, vb, f0);
-        tmem_ld32(tb + kSecond + 32, vb);
-        tmem_ld_wait();
-        release();  // everything is in registers: the next MMAs may have the buffer
-        add(2, va, f1);
-        add(3, vb, f1);
       }
       if (!ok) break;
       if constexpr (MODE == MODE_GATEUP) {
@@ -450,10 +483,12 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         const int c0 = t.mt * 128 + half * 64;
         const bool cols = c0 < p.b.Mg;
         uint32_t m = 0;
+        float acc[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          acc[i] = silu_fast(acc[i]) * acc[64 + i];
-          m = max(m, fp8::abs_bits(acc[i]));
+        for (int i = 0; i < 32; ++i) {
+          acc[2 * i] = silu_fast(lo_of(sum[i])) * lo_of(sum[32 + i]);
+          acc[2 * i + 1] = silu_fast(hi_of(sum[i])) * hi_of(sum[32 + i]);
+          m = max(m, max(fp8::abs_bits(acc[2 * i]), fp8::abs_bits(acc[2 * i + 1])));
         }
         if (!cols) m = 0;
         if (warp_live) {
@@ -493,8 +528,8 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
               uint32_t w[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const float* a = acc + i * 8 + j * 2;
-                const __nv_bfloat162 h = __floats2bfloat162_rn(a[0] * f, a[1] * f);
+                const uint64_t a = sum[i * 4 + j];
+                const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * f, hi_of(a) * f);
                 w[j] = *reinterpret_cast<const uint32_t*>(&h);
               }
               dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
