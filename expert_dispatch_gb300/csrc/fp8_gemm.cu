@@ -28,8 +28,10 @@
 //     300 of 800 cycles a block), warps 4-11 the epilogue: two warps a TMEM lane quarter, each with half
 //     of the columns (64 of gate and the same 64 of up, or 128 of down).  A thread
 //     holds 128 sums, so the registers are split unevenly (setmaxnreg).
-//   * Scales never wait on memory: a row's come four blocks at a time, the next
-//     four under way; the tiles' lie across a warp's lanes, 32 blocks at a time.
+//   * Warp 3 turns scales into factors, row's times tile's, two for each of the 128
+//     rows (gate's and up's, or those of down's two tiles), a block ahead: they lie in
+//     shared memory before a block's products are announced, and cost the epilogue's
+//     warps one load a block (formed there they took a tenth of the time).
 //   * Large batches run on SM pairs (cta_group::2, M = 256): each CTA has 128 of the
 //     token rows and brings half of the weight rows, so that an SM is fed 32 KB a
 //     block instead of 48.
@@ -54,8 +56,8 @@ using tc::Unit;
 constexpr int kEpiWarps = 8, kEpiWarp0 = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 // Registers a thread: 384 threads are launched with 168 each; 4 warps give up what 8 take:
-// 128 x 56 + 256 x 224 = 384 x 168.
-constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsEpi = 224;
+// 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsEpi = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsEpi == kThreads * kRegsLaunch, "register split");
 constexpr int kRows = 128;  // token rows of a CTA's unit
 constexpr int kCols = 256;  // weight rows of a unit
@@ -129,6 +131,37 @@ __device__ __forceinline__ uint64_t pair_of(float f) {
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
+// Arrive on a barrier of either CTA of a pair (mbar_arrive_cluster), without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar_cluster, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar_cluster),
+      "r"((uint32_t)on)
+      : "memory");
+}
+
+// A copy of `bytes` (a multiple of 16) from shared memory by this thread, and waits for all
+// of its copies: their sources have been read, or they are done.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(dst),
+      "r"(src), "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t a, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -143,16 +176,24 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <int STAGES, bool PAIR>
+template <int MODE, int STAGES, bool PAIR>
 struct Cfg {
   static constexpr int A_BYTES = kRows * kBK;
   static constexpr int B_BYTES = (PAIR ? kCols / 2 : kCols) * kBK;  // a pair's CTA: its half
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   // full, empty; TMEM buffers full, empty; four meetings of the warps of a quarter; wind-downs
-  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2;
-  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  // (and two for the factors' buffers of a pair's CTA)
+  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2 + 2;
+  // Down on pairs: finished rows go out through shared memory, 256 bytes of a thread's row
+  // (and 16 that keep the banks apart) by one copy; stored straight, 16 bytes of 32 rows an
+  // instruction, they took 4000 cycles a unit.
+  static constexpr bool STAGED = MODE == MODE_DOWN && PAIR;
+  static constexpr int ROW_PITCH = 256 + 16;
+  static constexpr int ROWS_OFF = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFF = ROWS_OFF + (STAGED ? kEpiWarps * 32 * ROW_PITCH : 0);
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int TOP_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // [2][2][128] row maxima
+  static constexpr int FAC_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // [2][128] pairs of factors
+  static constexpr int TOP_OFF = FAC_OFF + 2 * kRows * 8;         // [2][2][128] row maxima
   static constexpr int PREFIX_OFF = TOP_OFF + 2 * 2 * kRows * 4;
   static constexpr int GSTART_OFF = PREFIX_OFF + 4 * (tc::kMaxGroups + 1);
   static constexpr int SMEM_TOTAL = GSTART_OFF + 4 * (tc::kMaxGroups + 1) + 1024;
@@ -163,7 +204,7 @@ template <int MODE, int STAGES, bool PAIR>
 __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUtensorMap& tmXfull,
                                              const CUtensorMap& tmW0, const CUtensorMap& tmW1,
                                              const F8Params& p) {
-  using C = Cfg<STAGES, PAIR>;
+  using C = Cfg<MODE, STAGES, PAIR>;
   constexpr int kTile = PAIR ? 2 * kRows : kRows;  // token rows of a unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -176,8 +217,10 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
   const uint32_t acce0 = accf0 + 16;
   const uint32_t meet0 = acce0 + 16;
   const uint32_t drain_bar = meet0 + 32;
+  const uint32_t facfree0 = drain_bar + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  float2* fac = reinterpret_cast<float2*>(smem + C::FAC_OFF);
   volatile uint32_t* top = reinterpret_cast<volatile uint32_t*>(smem + C::TOP_OFF);
   int* prefix = reinterpret_cast<int*>(smem + C::PREFIX_OFF);
   int* gstart = reinterpret_cast<int*>(smem + C::GSTART_OFF);
@@ -197,7 +240,8 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(accf0 + 8u * b, 1);
+      mbar_init(accf0 + 8u * b, 2);  // the products, the factors
+      mbar_init(facfree0 + 8u * b, kEpiWarps);
       mbar_init(acce0 + 8u * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(meet0 + 8u * q, 2);
@@ -340,8 +384,8 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         for (int u = u0; ok && u < total && !*abort_flag; u += ustep) {
           for (int kb = 0; kb < KB; ++kb, ++it) {
             if ((it & 1u) == buf) {
-              if (!mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err) ||
-                  !mbar_wait(full_bar(stage), phase, abort_flag, p.b.err)) {
+              if (!mbar_wait(full_bar(stage), phase, abort_flag, p.b.err) ||
+                  !mbar_wait(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err)) {
                 ok = false;
                 break;
               }
@@ -377,48 +421,92 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         }
       }
     }
+    else {
+      // ---------------------------------------------------------- factors (warp 3)
+      pdl_wait();  // the token rows' scales are the predecessor's
+      const int pitch = pitch_of(p.b.K);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = u0; ok && u < total; u += ustep) {
+        const Unit t = unit(u);
+        const int mine = min(t.nt - rank * kRows, kRows);
+        const size_t row0 = (size_t)(t.r0 + rank * kRows) * pitch;
+        // the tiles of gate and up, or of down's first and second 128 rows
+        const size_t w0 = ((size_t)t.g * MB + (MODE == MODE_GATEUP ? t.mt : 2 * t.mt)) * KB;
+        const size_t w1 =
+            MODE == MODE_GATEUP ? w0 : ((size_t)t.g * MB + min(2 * t.mt + 1, MB - 1)) * KB;
+        float2 x[4], nx[4];  // two blocks' scales of rows lane, lane + 32, ...; the next two's
+        float s0 = 0.f, s1 = 0.f, n0 = 0.f, n1 = 0.f;  // 32 blocks' across the lanes; the next's
+        auto ask_rows = [&](int kb) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < mine)
+              nx[i] = *reinterpret_cast<const float2*>(p.xs + row0 +
+                                                       (size_t)(lane + 32 * i) * pitch + kb);
+        };
+        auto ask_tiles = [&](int kb) {
+          if (kb + lane < KB) {
+            n0 = p.ws0[w0 + kb + lane];
+            n1 = p.ws1[w1 + kb + lane];
+          }
+        };
+        ask_rows(0);
+        ask_tiles(0);
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const uint32_t buf = it & 1u;
+          if ((kb & 1) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = nx[i];
+            if (kb + 2 < KB) ask_rows(kb + 2);
+          }
+          if ((kb & 31) == 0) {
+            s0 = n0, s1 = n1;
+            ask_tiles(kb + 32);
+          }
+          const float a = __shfl_sync(0xffffffffu, s0, kb & 31);
+          const float b = __shfl_sync(0xffffffffu, s1, kb & 31);
+          // free once this CTA's epilogue has let go of the block before the last
+          if (!tc::mbar_wait_warp((PAIR ? facfree0 : acce0) + 8u * buf, ((it >> 1) & 1u) ^ 1u,
+                                  abort_flag, p.b.err)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float s = (kb & 1) ? x[i].y : x[i].x;
+            if (lane + 32 * i < mine) fac[buf * kRows + lane + 32 * i] = make_float2(s * a, s * b);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(accf0 + 8u * buf);
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue (warps 4..11)
     setmaxnreg_inc<kRegsEpi>();
-    pdl_wait();  // the token rows' scales are the predecessor's
+    pdl_wait();  // what is written here the predecessor may still read
     const int q = warp & 3;                    // TMEM lane quarter this warp may access
     const int half = (warp - kEpiWarp0) >> 2;  // its half of the columns
-    const int pitch = pitch_of(p.b.K);
-    const uint32_t acce_even = PAIR ? mapa_shared(acce0, 0) : acce0;
+    const int lrow = q * 32 + lane;
+    // lane 0 lets go of a TMEM buffer (of a pair on the even CTA), lane 1 of a pair's factors
+    const uint32_t free_bar = lane == 0 ? mapa_shared(acce0, PAIR ? 0 : cluster_rank())
+                                        : mapa_shared(facfree0, cluster_rank());
     uint32_t it = 0, met = 0;
     bool ok = true;
+    float slot_w = 1.0f;
     for (int u = u0; ok && u < total; u += ustep) {
       const Unit t = unit(u);
-      const int lrow = q * 32 + lane, mine = t.nt - rank * kRows;
+      const int mine = t.nt - rank * kRows, tile = t.mt;
       const bool warp_live = q * 32 < mine, live = lrow < mine;
-      const size_t row = (size_t)(t.r0 + (live ? rank * kRows + lrow : 0));
-      const float4* xs = reinterpret_cast<const float4*>(p.xs + row * pitch);
-      // this warp's weight scales: its 64 columns of gate and up, or its 128 of down
-      const int wb = MODE == MODE_GATEUP ? t.mt : min(2 * t.mt + half, MB - 1);
-      const size_t wrow = ((size_t)t.g * MB + wb) * KB;
-      const float* ws0 = p.ws0 + wrow;
-      const float* ws1 = p.ws1 + wrow;
+      const int out_row = t.r0 + (live ? rank * kRows + lrow : 0);
+      if (MODE == MODE_DOWN && p.b.row_scale && live) slot_w = p.b.row_scale[out_row];
       uint64_t sum[64];  // this thread's 128 columns, two a register pair
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      float4 sx{}, nx{};
-      float w0 = 0.f, w1 = 0.f, n0 = 0.f, n1 = 0.f;
-      if (warp_live) {
-        nx = xs[0];
-        if (lane < KB) {
-          n0 = ws0[lane];
-          if (MODE == MODE_GATEUP) n1 = ws1[lane];
-        }
-      }
       auto release = [&](uint32_t buf) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (PAIR)
-            mbar_arrive_cluster(acce_even + 8u * buf);
-          else
-            mbar_arrive(acce0 + 8u * buf);
-        }
+        mbar_arrive_if(free_bar + 8u * buf, lane < (PAIR ? 2 : 1));
       };
       auto wait = [&]() {
         const bool there = tc::mbar_wait_warp(accf0 + 8u * (it & 1u), (it >> 1) & 1u, abort_flag,
@@ -434,30 +522,19 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) +
                             (MODE == MODE_GATEUP ? half * 64 : half * 128);
         constexpr uint32_t kSecond = MODE == MODE_GATEUP ? 128 : 64;
-        auto add = [&](int c, const uint32_t (&v)[32], uint64_t f) {
+        auto add = [&](int c, const uint32_t (&v)[32], float f) {
+          const uint64_t ff = pair_of(f);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(sum[c * 16 + i], v[2 * i], v[2 * i + 1], f);
+          for (int i = 0; i < 16; ++i) fma2(sum[c * 16 + i], v[2 * i], v[2 * i + 1], ff);
         };
         uint32_t va[32], vb[32];
         tmem_ld32(tq + (it & 1u) * kCols, va);
+        float2 f = fac[(it & 1u) * kRows + lrow];
 #pragma unroll 1
         for (int kb = 0; kb < KB; ++kb) {
           const uint32_t buf = it & 1u, tb = tq + buf * kCols;
-          if ((kb & 3) == 0) {
-            sx = nx;
-            if (kb + 4 < KB) nx = xs[kb / 4 + 1];
-          }
-          if ((kb & 31) == 0) {
-            w0 = n0, w1 = n1;
-            if (kb + 32 + lane < KB) {
-              n0 = ws0[kb + 32 + lane];
-              if (MODE == MODE_GATEUP) n1 = ws1[kb + 32 + lane];
-            }
-          }
-          const float s = (kb & 2) ? ((kb & 1) ? sx.w : sx.z) : ((kb & 1) ? sx.y : sx.x);
-          const uint64_t f0 = pair_of(s * __shfl_sync(0xffffffffu, w0, kb & 31));
-          const uint64_t f1 =
-              MODE == MODE_GATEUP ? pair_of(s * __shfl_sync(0xffffffffu, w1, kb & 31)) : f0;
+          const float f0 = MODE == MODE_GATEUP || half == 0 ? f.x : f.y;
+          const float f1 = MODE == MODE_GATEUP || half == 1 ? f.y : f.x;
           tmem_ld_wait();
           tmem_ld32(tb + 32, vb);
           add(0, va, f0);
@@ -473,14 +550,15 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           if (kb + 1 < KB) {
             if (!(ok = wait())) break;
             tmem_ld32(tq + (it & 1u) * kCols, va);
+            f = fac[(it & 1u) * kRows + lrow];
           }
           add(3, vb, f1);
         }
       }
       if (!ok) break;
       if constexpr (MODE == MODE_GATEUP) {
-        // columns of h: t.mt * 128 + half * 64 .. + 63 (Mg is a multiple of 64)
-        const int c0 = t.mt * 128 + half * 64;
+        // columns of h: tile * 128 + half * 64 .. + 63 (Mg is a multiple of 64)
+        const int c0 = tile * 128 + half * 64;
         const bool cols = c0 < p.b.Mg;
         uint32_t m = 0;
         float acc[64];
@@ -503,7 +581,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           ++met;
           const fp8::Scale sc = fp8::scale_of(m);
           if (live && cols) {
-            uint4* dst = reinterpret_cast<uint4*>(p.hq + row * p.b.Mg + c0);
+            uint4* dst = reinterpret_cast<uint4*>(p.hq + (size_t)out_row * p.b.Mg + c0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
@@ -514,30 +592,38 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
               }
               dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (half == 0) p.hs[row * pitch_of(p.b.Mg) + t.mt] = sc.scale;
+            if (half == 0) p.hs[(size_t)out_row * pitch_of(p.b.Mg) + tile] = sc.scale;
           }
         }
       } else {
         if (live) {
-          const float f = p.b.row_scale ? p.b.row_scale[row] : 1.0f;
-          const int c0 = t.mt * 256 + half * 128;
-          uint4* dst = reinterpret_cast<uint4*>(p.y + row * p.b.Mg + c0);
+          const int c0 = tile * 256 + half * 128, cols = min(p.b.Mg - c0, 128);  // 0 or less: none
+          __nv_bfloat16* dst = p.y + (size_t)out_row * p.b.Mg + c0;
+          const uint32_t mine8 =
+              sbase + C::ROWS_OFF + ((warp - kEpiWarp0) * 32 + lane) * C::ROW_PITCH;
+          if (C::STAGED) bulk_wait_read();  // the last unit's copy has read this row
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (c0 + (i / 8) * 64 < p.b.Mg) {  // Mg is a multiple of 64
-              uint32_t w[4];
+            uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint64_t a = sum[i * 4 + j];
-                const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * f, hi_of(a) * f);
-                w[j] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t a = sum[i * 4 + j];
+              const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * slot_w, hi_of(a) * slot_w);
+              w[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
+            if (C::STAGED)
+              st_shared_v4(mine8 + 16 * i, w);
+            else if (8 * i < cols)  // Mg is a multiple of 64
+              reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (C::STAGED && cols > 0) {
+            fence_proxy_async_shared();
+            bulk_store(dst, mine8, 2 * cols);
           }
         }
       }
     }
+    if (C::STAGED) bulk_wait();
   }
 
   tc_fence_before();
@@ -585,7 +671,7 @@ template <int MODE, int STAGES, bool PAIR>
 cudaError_t launch_f8(const CUtensorMap& x, const CUtensorMap& xfull, const CUtensorMap& w0,
                       const CUtensorMap& w1, const F8Params& p, long long max_units,
                       const char* name, cudaStream_t s) {
-  using C = Cfg<STAGES, PAIR>;
+  using C = Cfg<MODE, STAGES, PAIR>;
   void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, F8Params);
   if constexpr (PAIR)
     kern = fp8_grouped_gemm_pair<MODE, STAGES>;
@@ -658,7 +744,7 @@ cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offse
   const cudaError_t e = pair ? launch_f8<MODE_GATEUP, 6, true>(tx, txf, tg, tu, p1, u1, n1, s)
                              : launch_f8<MODE_GATEUP, 4, false>(tx, txf, tg, tu, p1, u1, n1, s);
   if (e != cudaSuccess) return e;
-  return pair ? launch_f8<MODE_DOWN, 6, true>(th, thf, td, td, p2, u2, n2, s)
+  return pair ? launch_f8<MODE_DOWN, 4, true>(th, thf, td, td, p2, u2, n2, s)
               : launch_f8<MODE_DOWN, 4, false>(th, thf, td, td, p2, u2, n2, s);
 }
 
