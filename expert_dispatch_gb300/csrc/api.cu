@@ -243,23 +243,27 @@ moe_status do_ffn_q8(const moe_layer_desc* D, const void* x, const int32_t* offs
                                       dn, slot_w, W.h, y_perm, W.flags, s));
 }
 
-// The same with 8-bit projections and products: x_perm and h hold codes, their
-// scales behind them (d + 4 fp8_scale_pitch(d) bytes a row, d >= 64, fit the 2 d of
-// bf16 rows and leave what aligning takes).
+// The same with 8-bit projections and products.  The workspace's x_perm [cap, d] and h
+// [cap, I] hold codes, then scales: d + 4 fp8_scale_pitch(d) bytes a row, at most 1.25 d
+// of the 2 d of bf16 rows (d >= 64).  The tokens' own rows, where there are two batch rows
+// or more a token, take another 0.625 d of cap rows behind x_perm's, and aligning fits the
+// last eighth (cap >= 288).
 moe_status do_ffn_fp8(const moe_layer_desc* D, const void* x, const int32_t* offsets,
                       const int32_t* tok_idx, const float* slot_w, const moe_fp8_weight* Wg,
                       const moe_fp8_weight* Wu, const moe_fp8_weight* Wd, void* y_perm,
                       const Ws& W, cudaStream_t s) {
   const int P = D->T * (D->k + D->S);
   const int nE = D->E + D->S;
-  const size_t cap = (size_t)tc_row_capacity(P);
-  auto scales = [&](void* rows, int n) {
-    return reinterpret_cast<float*>(static_cast<uint8_t*>(rows) + align256(cap * (size_t)n));
-  };
-  float* xs = scales(W.x_perm, D->d);
-  float* hs = scales(W.h, D->I);
-  if (launch_gather_rows_fp8(x, tok_idx, offsets + nE, P, D->T, D->d, W.x_perm, xs, W.flags, s) !=
-      cudaSuccess)
+  const size_t cap = (size_t)tc_row_capacity(P), T = (size_t)D->T;
+  auto codes = [&](void* base, size_t skip) { return static_cast<uint8_t*>(base) + skip; };
+  const size_t x_bytes = align256(cap * D->d), t_bytes = align256(T * D->d);
+  const size_t xs_bytes = align256(cap * fp8_scale_pitch(D->d) * 4);
+  float* xs = reinterpret_cast<float*>(codes(W.x_perm, x_bytes));
+  uint8_t* x1 = codes(W.x_perm, x_bytes + xs_bytes);
+  float* xs1 = reinterpret_cast<float*>(x1 + t_bytes);
+  float* hs = reinterpret_cast<float*>(codes(W.h, align256(cap * D->I)));
+  if (launch_gather_rows_fp8(x, tok_idx, offsets + nE, P, D->T, D->d, W.x_perm, xs, x1, xs1,
+                             W.flags, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   const Fp8Weight g{Wg->q, Wg->scale}, u{Wu->q, Wu->scale}, dn{Wd->q, Wd->scale};
   return cuda_status(launch_ffn_fp8(W.x_perm, xs, offsets, nE, P, D->d, D->I, (double)P / nE, g, u,

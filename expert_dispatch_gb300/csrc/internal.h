@@ -237,10 +237,12 @@ cudaError_t launch_unpack_rows(int dtype, const void* q, const float* scale, lon
                                void* x, cudaStream_t s);
 // The FFN's own rows: scales of a row of n columns lie this many floats apart.
 __host__ __device__ constexpr int fp8_scale_pitch(int n) { return (n + 511) / 512 * 4; }
-// bf16 rows gathered by tok_idx and put into 8 bits, scales fp8_scale_pitch(d) apart
+// bf16 rows gathered by tok_idx and put into 8 bits, scales fp8_scale_pitch(d) apart;
+// q1 [T, d], scale1: scratch, used where P >= 2 T
 cudaError_t launch_gather_rows_fp8(const void* x, const int32_t* tok_idx,
                                    const int32_t* total_rows, int P, int T, int d, void* q,
-                                   float* scale, int* flags, cudaStream_t s);
+                                   float* scale, void* q1, float* scale1, int* flags,
+                                   cudaStream_t s);
 // x8 [cap, d] with scales xs, h8 [cap, I] with scales hs, cap = tc_row_capacity(P)
 cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
                            int P, int d, int I, double mean_rows, const Fp8Weight& Wg,
