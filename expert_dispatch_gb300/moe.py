@@ -18,6 +18,7 @@ moe_*_backward).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -877,8 +878,10 @@ def _rows_args(t, what):
 
 
 def _new_rows8(rows, n, device):
-    return Rows8(torch.empty((rows, n), dtype=FP8, device=device),
-                 torch.empty((rows, _blocks(n)), dtype=torch.float32, device=device))
+    r = Rows8.__new__(Rows8)  # nothing to check
+    r.q = torch.empty((rows, n), dtype=FP8, device=device)
+    r.scale = torch.empty((rows, -(-n // FP8_BLOCK)), dtype=torch.float32, device=device)
+    return r
 
 
 def _rows8_p(r, shape, what, device):
@@ -996,13 +999,25 @@ def moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits, s
     _check(st, "moe_gate_backward")
 
 
+@functools.lru_cache(maxsize=256)
+def _gate_workspace(T, E, k):
+    """moe_gate_workspace_size of any record with these sizes."""
+    return max(moe_gate_workspace_size(make_desc(T, 128, E, k, 128)), 16)
+
+
 def gate(desc, logits, topk_ids, stream=None):
     """(topk_w, counts, prob, loss) of moe_gate_forward in fresh tensors."""
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
-    w, counts = new((desc.T, desc.k), torch.float32), new((desc.E + 1,), torch.int32)
-    prob, loss = new((desc.E,), torch.float32), new((1,), torch.float32)
-    ws = new((max(moe_gate_workspace_size(desc), 16),), torch.uint8)
-    moe_gate_forward(desc, logits, topk_ids, w, counts, prob, loss, ws, stream)
+    at, head = _gate_in(desc, logits, topk_ids)
+    T, E, k, dev = desc.T, desc.E, desc.k, logits.device
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    prob = torch.empty(E, dtype=torch.float32, device=dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    n = _gate_workspace(T, E, k)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib().moe_gate_forward(ctypes.byref(desc), *head, w.data_ptr(), counts.data_ptr(),
+                                  prob.data_ptr(), loss.data_ptr(), ws.data_ptr(), n,
+                                  _stream(stream, at)), "moe_gate_forward")
     return w, counts, prob, loss
 
 
