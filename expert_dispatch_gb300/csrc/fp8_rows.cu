@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) copy_rows_fp8_kernel(
 }
 
 unsigned seg_grid(long long segs) {
-  const long long most = (long long)num_sms() * 8, need = (segs + kSegs - 1) / kSegs;
+  const long long most = (long long)num_sms() * 32, need = (segs + kSegs - 1) / kSegs;
   return (unsigned)(need < most ? need : most);
 }
 
