@@ -156,9 +156,16 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
-__device__ __forceinline__ void st_shared_v4(uint32_t a, const uint32_t (&w)[4]) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3])
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 
@@ -198,6 +205,10 @@ struct Cfg {
   static constexpr int GSTART_OFF = PREFIX_OFF + 4 * (tc::kMaxGroups + 1);
   static constexpr int SMEM_TOTAL = GSTART_OFF + 4 * (tc::kMaxGroups + 1) + 1024;
   static_assert(SMEM_TOTAL <= 232448, "shared memory");
+  // The issuers take alternate blocks.  With an even number of stages a stage is always the
+  // same one's, which has seen every phase of its barrier; else one could find it two phases
+  // behind and take the old parity for the one it waits for.
+  static_assert(STAGES % 2 == 0, "a stage belongs to one MMA issuer");
 };
 
 template <int MODE, int STAGES, bool PAIR>
@@ -508,6 +519,17 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         __syncwarp();
         mbar_arrive_if(free_bar + 8u * buf, lane < (PAIR ? 2 : 1));
       };
+      auto ready = [&]() {
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(r)
+            : "r"(accf0 + 8u * (it & 1u)), "r"((it >> 1) & 1u)
+            : "memory");
+        return __all_sync(0xffffffffu, r);
+      };
       auto wait = [&]() {
         const bool there = tc::mbar_wait_warp(accf0 + 8u * (it & 1u), (it >> 1) & 1u, abort_flag,
                                               p.b.err);
@@ -547,12 +569,19 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           tmem_ld_wait();
           release(buf);  // everything is in registers: the next MMAs may have the buffer
           ++it;
-          if (kb + 1 < KB) {
+          if (kb + 1 < KB && !ready()) {  // nothing to load yet: add first
+            add(3, vb, f1);
             if (!(ok = wait())) break;
             tmem_ld32(tq + (it & 1u) * kCols, va);
             f = fac[(it & 1u) * kRows + lrow];
+          } else {
+            if (kb + 1 < KB) {
+              tc_fence_after();
+              tmem_ld32(tq + (it & 1u) * kCols, va);
+              f = fac[(it & 1u) * kRows + lrow];
+            }
+            add(3, vb, f1);
           }
-          add(3, vb, f1);
         }
       }
       if (!ok) break;
@@ -602,19 +631,27 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           const uint32_t mine8 =
               sbase + C::ROWS_OFF + ((warp - kEpiWarp0) * 32 + lane) * C::ROW_PITCH;
           if (C::STAGED) bulk_wait_read();  // the last unit's copy has read this row
+          const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31u) == 0;  // rows are: d % 64 == 0
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint64_t a = sum[i * 4 + j];
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t a = sum[i * 8 + j];
               const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * slot_w, hi_of(a) * slot_w);
               w[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            if (C::STAGED)
-              st_shared_v4(mine8 + 16 * i, w);
-            else if (8 * i < cols)  // Mg is a multiple of 64
-              reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (C::STAGED) {
+              st_shared_v4(mine8 + 32 * i, w[0], w[1], w[2], w[3]);
+              st_shared_v4(mine8 + 32 * i + 16, w[4], w[5], w[6], w[7]);
+            } else if (16 * i < cols) {  // Mg is a multiple of 64
+              if (wide) {
+                st_global_v8(dst + 16 * i, w);
+              } else {
+                reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
           }
           if (C::STAGED && cols > 0) {
             fence_proxy_async_shared();
