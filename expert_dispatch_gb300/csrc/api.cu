@@ -266,8 +266,8 @@ moe_status do_ffn_fp8(const moe_layer_desc* D, const void* x, const int32_t* off
                              W.flags, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   const Fp8Weight g{Wg->q, Wg->scale}, u{Wu->q, Wu->scale}, dn{Wd->q, Wd->scale};
-  return cuda_status(launch_ffn_fp8(W.x_perm, xs, offsets, nE, P, D->d, D->I, (double)P / nE, g, u,
-                                    dn, slot_w, W.h, hs, y_perm, W.flags, s));
+  return cuda_status(launch_ffn_fp8(W.x_perm, xs, offsets, nE, P, D->d, D->I, g, u, dn, slot_w,
+                                    W.h, hs, y_perm, W.flags, s));
 }
 
 bool fp8_ok(const moe_fp8_weight* w) {

@@ -11,8 +11,8 @@
 // codes and scaled once a block.
 //
 // Design (sm_103a, one CTA an SM, persistent):
-//   * A unit is (expert, 256 weight rows, up to 128 token rows, or 256 on an SM
-//     pair): 128 rows of gate and the same 128 of up, or 256 rows of down.  Token rows are the MMA's M
+//   * A unit is (expert, 256 weight rows, up to 128 token rows): 128 rows of gate
+//     and the same 128 of up, or 256 rows of down.  Token rows are the MMA's M
 //     side (the lanes of TMEM), weight rows its N side.  A thread of the epilogue
 //     then has one token row: that row's scale times the block's weight scale is
 //     one factor for all its columns, a column block of h is one thread's (and its
@@ -32,9 +32,10 @@
 //     rows (gate's and up's, or those of down's two tiles), a block ahead: they lie in
 //     shared memory before a block's products are announced, and cost the epilogue's
 //     warps one load a block (formed there they took a tenth of the time).
-//   * Large batches run on SM pairs (cta_group::2, M = 256): each CTA has 128 of the
-//     token rows and brings half of the weight rows, so that an SM is fed 32 KB a
-//     block instead of 48.
+//   * SM pairs (cta_group::2, 256 token rows, half of the weight rows to a CTA) were
+//     built and dropped: the tensor cores wait for the additions, not for operands
+//     (8192 tokens x 8, 4096 x 1536, 32 experts: 1.5 % faster; 600 rows an expert 14 %
+//     slower, for its larger tiles).
 //   * Every wait is bounded (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -101,17 +102,6 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// D (+)= A * B^T over an SM pair (M = 256), e4m3 inputs, fp32 accumulate.
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // acc += {lo, hi} * f, two fp32 fused multiply-adds in one instruction (128 x 256 sums a
 // block by 8 warps: 270 cycles, 350 one by one).  Volatile: the products of a load stay
 // before the next load into the same registers, which would otherwise be copied.
@@ -130,38 +120,6 @@ __device__ __forceinline__ uint64_t pair_of(float f) {
 }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-
-// Arrive on a barrier of either CTA of a pair (mbar_arrive_cluster), without a branch.
-__device__ __forceinline__ void mbar_arrive_if(uint32_t bar_cluster, bool on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar_cluster),
-      "r"((uint32_t)on)
-      : "memory");
-}
-
-// A copy of `bytes` (a multiple of 16) from shared memory by this thread, and waits for all
-// of its copies: their sources have been read, or they are done.
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile(
-      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
-      "cp.async.bulk.commit_group;" ::"l"(dst),
-      "r"(src), "r"(bytes)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
-}
 
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
@@ -183,21 +141,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <int MODE, int STAGES, bool PAIR>
+template <int STAGES>
 struct Cfg {
   static constexpr int A_BYTES = kRows * kBK;
-  static constexpr int B_BYTES = (PAIR ? kCols / 2 : kCols) * kBK;  // a pair's CTA: its half
+  static constexpr int B_BYTES = kCols * kBK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   // full, empty; TMEM buffers full, empty; four meetings of the warps of a quarter; wind-downs
-  // (and two for the factors' buffers of a pair's CTA)
-  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2 + 2;
-  // Down on pairs: finished rows go out through shared memory, 256 bytes of a thread's row
-  // (and 16 that keep the banks apart) by one copy; stored straight, 16 bytes of 32 rows an
-  // instruction, they took 4000 cycles a unit.
-  static constexpr bool STAGED = MODE == MODE_DOWN && PAIR;
-  static constexpr int ROW_PITCH = 256 + 16;
-  static constexpr int ROWS_OFF = STAGES * STAGE_BYTES;
-  static constexpr int BAR_OFF = ROWS_OFF + (STAGED ? kEpiWarps * 32 * ROW_PITCH : 0);
+  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2;
+  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int FAC_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // [2][128] pairs of factors
   static constexpr int TOP_OFF = FAC_OFF + 2 * kRows * 8;         // [2][2][128] row maxima
@@ -211,12 +162,13 @@ struct Cfg {
   static_assert(STAGES % 2 == 0, "a stage belongs to one MMA issuer");
 };
 
-template <int MODE, int STAGES, bool PAIR>
-__device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUtensorMap& tmXfull,
-                                             const CUtensorMap& tmW0, const CUtensorMap& tmW1,
-                                             const F8Params& p) {
-  using C = Cfg<MODE, STAGES, PAIR>;
-  constexpr int kTile = PAIR ? 2 * kRows : kRows;  // token rows of a unit
+template <int MODE, int STAGES>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_grouped_gemm(const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ CUtensorMap tmXfull,
+                     const __grid_constant__ CUtensorMap tmW0,
+                     const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
+  using C = Cfg<STAGES>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -228,7 +180,6 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
   const uint32_t acce0 = accf0 + 16;
   const uint32_t meet0 = acce0 + 16;
   const uint32_t drain_bar = meet0 + 32;
-  const uint32_t facfree0 = drain_bar + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   float2* fac = reinterpret_cast<float2*>(smem + C::FAC_OFF);
@@ -241,10 +192,6 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
   const int m_tiles = (p.b.Mg + kUnitRows - 1) / kUnitRows;
   const int KB = (p.b.K + kBK - 1) / kBK;
   const int MB = fp8::blocks_of(p.b.Mg);
-  const int rank = PAIR ? (int)cluster_rank() : 0;
-  const int u0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int ustep = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -252,8 +199,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8u * b, 2);  // the products, the factors
-      mbar_init(facfree0 + 8u * b, kEpiWarps);
-      mbar_init(acce0 + 8u * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
+      mbar_init(acce0 + 8u * b, kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(meet0 + 8u * q, 2);
     for (int i = 0; i < 2; ++i) mbar_init(drain_bar + 8u * i, 1);
@@ -265,23 +211,17 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
     tma_prefetch_desc(&tmW1);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(smem_u32(tmem_slot), 512);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(tmem_slot), 512);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
   }
-  if (warp == 3) tc::build_schedule<MODE, kTile>(p.b, m_tiles, prefix, gstart);
+  if (warp == 3) tc::build_schedule<MODE, kRows>(p.b, m_tiles, prefix, gstart);
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = prefix[p.b.n_groups];
   auto unit = [&](int u) {
-    return tc::decode_unit<MODE, kTile>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
+    return tc::decode_unit<MODE, kRows>(u, prefix, gstart, p.b.n_groups, m_tiles, KB, p.b);
   };
 
   if (warp < kEpiWarp0) {
@@ -291,41 +231,25 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
       if (lane == 0) {
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
-        // Of a pair both CTAs' copies complete on the even CTA's barrier.
-        auto load = [&](int s, uint32_t dst, const CUtensorMap& tm, int kb, int row) {
-          if (PAIR)
-            tma_load_2d_pair(dst, &tm, mapa_shared(full_bar(s), 0), kb * kBK, row);
-          else
-            tma_load_2d(dst, &tm, full_bar(s), kb * kBK, row);
-        };
-        // The unit's 256 weight rows: 128 of gate and of up, or of down twice; a pair's
-        // CTA brings the first or the second 128.
+        // The unit's 256 weight rows: 128 of gate and of up, or of down twice.
         auto load_weights = [&](int s, const Unit& t, int kb) {
           const uint32_t sB = sbase + s * C::STAGE_BYTES + C::A_BYTES;
           const int row = t.g * p.b.Mg + t.mt * kUnitRows;
-          const int second = MODE == MODE_GATEUP ? row : row + 128;
-          if (PAIR) {
-            if (rank == 0)
-              load(s, sB, tmW0, kb, row);
-            else
-              load(s, sB, tmW1, kb, second);
-          } else {
-            load(s, sB, tmW0, kb, row);
-            load(s, sB + C::B_BYTES / 2, tmW1, kb, second);
-          }
+          tma_load_2d(sB, &tmW0, full_bar(s), kb * kBK, row);
+          tma_load_2d(sB + C::B_BYTES / 2, &tmW1, full_bar(s), kb * kBK,
+                      MODE == MODE_GATEUP ? row : row + 128);
         };
-        auto arm = [&](int s, const Unit& t) {  // all CTAs' weight and token bytes
-          if (rank != 0) return;
+        auto arm = [&](int s, const Unit& t) {
           const int chunks = (t.nt + 31) / 32;
-          mbar_arrive_expect_tx(full_bar(s), kCols * kBK + chunks * 32 * kBK);
+          mbar_arrive_expect_tx(full_bar(s), C::B_BYTES + chunks * 32 * kBK);
           armed |= 1u << s;
         };
         // The first unit's weight tiles are requested before waiting for the
         // predecessor grid: no kernel of the sequence writes weights, and the
         // schedule comes from a grid two launches back.
         int n_pre = 0;
-        if (u0 < total) {
-          const Unit t = unit(u0);
+        if ((int)blockIdx.x < total) {
+          const Unit t = unit(blockIdx.x);
           n_pre = min(STAGES, KB);
           for (int i = 0; i < n_pre; ++i) {
             arm(i, t);
@@ -334,11 +258,10 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         }
         pdl_wait();
         bool first = true;
-        for (int u = u0; u < total && !*abort_flag; u += ustep) {
-          if (u + ustep >= total) pdl_trigger();  // this CTA's last unit
+        for (int u = blockIdx.x; u < total && !*abort_flag; u += gridDim.x) {
+          if (u + (int)gridDim.x >= total) pdl_trigger();  // this CTA's last unit
           const Unit t = unit(u);
-          const int mine = min(max(t.nt - rank * kRows, 0), kRows);
-          const int chunks = (mine + 31) / 32, row = t.r0 + rank * kRows;
+          const int chunks = (t.nt + 31) / 32;
           bool ok = true;
           for (int kb = 0; kb < KB; ++kb) {
             if (!(first && kb < n_pre)) {
@@ -352,10 +275,10 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
             }
             const uint32_t sA = sbase + stage * C::STAGE_BYTES;
             if (chunks == 4)
-              load(stage, sA, tmXfull, kb, row);
+              tma_load_2d(sA, &tmXfull, full_bar(stage), kb * kBK, t.r0);
             else
               for (int c = 0; c < chunks; ++c)
-                load(stage, sA + c * 32 * kBK, tmX, kb, row + c * 32);
+                tma_load_2d(sA + c * 32 * kBK, &tmX, full_bar(stage), kb * kBK, t.r0 + c * 32);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -364,35 +287,21 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           first = false;
           if (!ok) break;
         }
-        if (u0 >= total) pdl_trigger();
-        if (rank == 0) {
-          // wind down: every copy that completes here has landed before exit
-          for (int s = 0; s < STAGES; ++s)
-            if (armed & (1u << s))
-              tc::mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.b.err);
-        } else if (*abort_flag) {
-          // this CTA's copies complete on its partner's barriers: after giving up, leave
-          // them a bounded time to land before the shared memory goes
-          const unsigned long long t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 100000ull) {
-          }
-        }
+        if ((int)blockIdx.x >= total) pdl_trigger();
+        // wind down: every copy this thread started has landed before exit
+        for (int s = 0; s < STAGES; ++s)
+          if (armed & (1u << s))
+            tc::mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.b.err);
       }
     } else if (warp <= 2) {
-      // ---------------------------------------------------------- MMA issuers (a pair's even CTA)
-      if (lane == 0 && rank == 0) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(kTile, kCols);
+      // ---------------------------------------------------------- MMA issuers
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kCols);
         const uint32_t buf = warp - 1;  // even blocks of this CTA's sequence, or odd ones
         int stage = 0;
         uint32_t phase = 0, it = 0;
         bool issued = false, ok = true;
-        auto commit = [&](uint32_t bar) {
-          if (PAIR)
-            umma_commit_pair_mc(bar, 3);
-          else
-            umma_commit(bar);
-        };
-        for (int u = u0; ok && u < total && !*abort_flag; u += ustep) {
+        for (int u = blockIdx.x; ok && u < total && !*abort_flag; u += gridDim.x) {
           for (int kb = 0; kb < KB; ++kb, ++it) {
             if ((it & 1u) == buf) {
               if (!mbar_wait(full_bar(stage), phase, abort_flag, p.b.err) ||
@@ -407,14 +316,11 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
               for (int kk = 0; kk < 4; ++kk) {
                 const uint64_t a = smem_desc_sw128(sA + kk * 32);
                 const uint64_t b = smem_desc_sw128(sB + kk * 32);
-                if (PAIR)
-                  umma_e4m3_pair(tmem_base + buf * kCols, a, b, idesc, kk != 0);
-                else
-                  umma_e4m3(tmem_base + buf * kCols, a, b, idesc, kk != 0);
+                umma_e4m3(tmem_base + buf * kCols, a, b, idesc, kk != 0);
               }
               issued = true;
-              commit(accf0 + 8u * buf);
-              commit(empty_bar(stage));
+              umma_commit(accf0 + 8u * buf);
+              umma_commit(empty_bar(stage));
             }
             if (++stage == STAGES) {
               stage = 0;
@@ -424,10 +330,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         }
         // wind down: every MMA this thread issued has completed before TMEM is freed
         if (issued) {
-          if (PAIR)
-            umma_commit_pair_mc(drain_bar + 8u * buf, 1);
-          else
-            umma_commit(drain_bar + 8u * buf);
+          umma_commit(drain_bar + 8u * buf);
           tc::mbar_wait_drain(drain_bar + 8u * buf, 0, p.b.err);
         }
       }
@@ -438,10 +341,10 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
       const int pitch = pitch_of(p.b.K);
       uint32_t it = 0;
       bool ok = true;
-      for (int u = u0; ok && u < total; u += ustep) {
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         const Unit t = unit(u);
-        const int mine = min(t.nt - rank * kRows, kRows);
-        const size_t row0 = (size_t)(t.r0 + rank * kRows) * pitch;
+        const int mine = t.nt;
+        const size_t row0 = (size_t)t.r0 * pitch;
         // the tiles of gate and up, or of down's first and second 128 rows
         const size_t w0 = ((size_t)t.g * MB + (MODE == MODE_GATEUP ? t.mt : 2 * t.mt)) * KB;
         const size_t w1 =
@@ -476,9 +379,8 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
           }
           const float a = __shfl_sync(0xffffffffu, s0, kb & 31);
           const float b = __shfl_sync(0xffffffffu, s1, kb & 31);
-          // free once this CTA's epilogue has let go of the block before the last
-          if (!tc::mbar_wait_warp((PAIR ? facfree0 : acce0) + 8u * buf, ((it >> 1) & 1u) ^ 1u,
-                                  abort_flag, p.b.err)) {
+          // free once the epilogue has let go of the block before the last
+          if (!tc::mbar_wait_warp(acce0 + 8u * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, p.b.err)) {
             ok = false;
             break;
           }
@@ -499,17 +401,14 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
     const int q = warp & 3;                    // TMEM lane quarter this warp may access
     const int half = (warp - kEpiWarp0) >> 2;  // its half of the columns
     const int lrow = q * 32 + lane;
-    // lane 0 lets go of a TMEM buffer (of a pair on the even CTA), lane 1 of a pair's factors
-    const uint32_t free_bar = lane == 0 ? mapa_shared(acce0, PAIR ? 0 : cluster_rank())
-                                        : mapa_shared(facfree0, cluster_rank());
     uint32_t it = 0, met = 0;
     bool ok = true;
     float slot_w = 1.0f;
-    for (int u = u0; ok && u < total; u += ustep) {
+    for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
       const Unit t = unit(u);
-      const int mine = t.nt - rank * kRows, tile = t.mt;
+      const int mine = t.nt, tile = t.mt;
       const bool warp_live = q * 32 < mine, live = lrow < mine;
-      const int out_row = t.r0 + (live ? rank * kRows + lrow : 0);
+      const int out_row = t.r0 + (live ? lrow : 0);
       if (MODE == MODE_DOWN && p.b.row_scale && live) slot_w = p.b.row_scale[out_row];
       uint64_t sum[64];  // this thread's 128 columns, two a register pair
 #pragma unroll
@@ -517,7 +416,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
       auto release = [&](uint32_t buf) {
         tc_fence_before();
         __syncwarp();
-        mbar_arrive_if(free_bar + 8u * buf, lane < (PAIR ? 2 : 1));
+        if (lane == 0) mbar_arrive(acce0 + 8u * buf);
       };
       auto ready = [&]() {
         uint32_t r;
@@ -552,7 +451,9 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         uint32_t va[32], vb[32];
         tmem_ld32(tq + (it & 1u) * kCols, va);
         float2 f = fac[(it & 1u) * kRows + lrow];
-#pragma unroll 1
+// 1, 2, 4 blocks a turn: gate/up 686, 672, 638 us (8192 x 8 rows, 4096 x 1536, 32
+// experts), down 454, 429, 432
+#pragma unroll(MODE == MODE_GATEUP ? 4 : 2)
         for (int kb = 0; kb < KB; ++kb) {
           const uint32_t buf = it & 1u, tb = tq + buf * kCols;
           const float f0 = MODE == MODE_GATEUP || half == 0 ? f.x : f.y;
@@ -628,9 +529,6 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
         if (live) {
           const int c0 = tile * 256 + half * 128, cols = min(p.b.Mg - c0, 128);  // 0 or less: none
           __nv_bfloat16* dst = p.y + (size_t)out_row * p.b.Mg + c0;
-          const uint32_t mine8 =
-              sbase + C::ROWS_OFF + ((warp - kEpiWarp0) * 32 + lane) * C::ROW_PITCH;
-          if (C::STAGED) bulk_wait_read();  // the last unit's copy has read this row
           const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31u) == 0;  // rows are: d % 64 == 0
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -641,10 +539,7 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
               const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(a) * slot_w, hi_of(a) * slot_w);
               w[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            if (C::STAGED) {
-              st_shared_v4(mine8 + 32 * i, w[0], w[1], w[2], w[3]);
-              st_shared_v4(mine8 + 32 * i + 16, w[4], w[5], w[6], w[7]);
-            } else if (16 * i < cols) {  // Mg is a multiple of 64
+            if (16 * i < cols) {  // Mg is a multiple of 64
               if (wide) {
                 st_global_v8(dst + 16 * i, w);
               } else {
@@ -653,45 +548,18 @@ __device__ __forceinline__ void grouped_gemm(const CUtensorMap& tmX, const CUten
               }
             }
           }
-          if (C::STAGED && cols > 0) {
-            fence_proxy_async_shared();
-            bulk_store(dst, mine8, 2 * cols);
-          }
         }
       }
     }
-    if (C::STAGED) bulk_wait();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();  // the partner is done with this CTA's shared memory and TMEM
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    if (PAIR)
-      tmem_dealloc_pair(tmem_base, 512);
-    else
-      tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(tmem_base, 512);
   }
-}
-
-template <int MODE, int STAGES>
-__global__ void __launch_bounds__(kThreads, 1)
-    fp8_grouped_gemm(const __grid_constant__ CUtensorMap tmX,
-                     const __grid_constant__ CUtensorMap tmXfull,
-                     const __grid_constant__ CUtensorMap tmW0,
-                     const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
-  grouped_gemm<MODE, STAGES, false>(tmX, tmXfull, tmW0, tmW1, p);
-}
-
-template <int MODE, int STAGES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    fp8_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmX,
-                          const __grid_constant__ CUtensorMap tmXfull,
-                          const __grid_constant__ CUtensorMap tmW0,
-                          const __grid_constant__ CUtensorMap tmW1, const F8Params p) {
-  grouped_gemm<MODE, STAGES, true>(tmX, tmXfull, tmW0, tmW1, p);
 }
 
 // e4m3 matrix [rows, inner] (row-major), boxes of box_rows x 128, 128-byte swizzle;
@@ -702,55 +570,38 @@ bool make_tmap_f8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t ro
                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The grid is what runs at once: one CTA an SM, or of a pair kernel two for each cluster
-// that fits (an SM pair must share a GPC).
-template <int MODE, int STAGES, bool PAIR>
+template <int MODE, int STAGES>
 cudaError_t launch_f8(const CUtensorMap& x, const CUtensorMap& xfull, const CUtensorMap& w0,
                       const CUtensorMap& w1, const F8Params& p, long long max_units,
                       const char* name, cudaStream_t s) {
-  using C = Cfg<MODE, STAGES, PAIR>;
-  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, F8Params);
-  if constexpr (PAIR)
-    kern = fp8_grouped_gemm_pair<MODE, STAGES>;
-  else
-    kern = fp8_grouped_gemm<MODE, STAGES>;
+  using C = Cfg<STAGES>;
+  auto kern = fp8_grouped_gemm<MODE, STAGES>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64) return cudaErrorInvalidDevice;
   static std::mutex mu;
-  static int at_once[64] = {};
+  static bool configured[64] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (at_once[dev] == 0) {
+    if (!configured[dev]) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
       if (e != cudaSuccess) return e;
-      int n = num_sms();
-      if (PAIR) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (unsigned)(num_sms() / 2));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = C::SMEM_TOTAL;
-        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-        if (e != cudaSuccess) return e;
-        if (n <= 0) return cudaErrorInvalidConfiguration;
-      }
-      at_once[dev] = n;
+      configured[dev] = true;
     }
   }
-  const long long n = max_units < at_once[dev] ? max_units : at_once[dev];
-  if (n <= 0) return cudaSuccess;
+  const long long grid = max_units < num_sms() ? max_units : num_sms();
+  if (grid <= 0) return cudaSuccess;
   ProfScope pr(name, s);
-  (void)launch_kernel(kern, (unsigned)(PAIR ? 2 * n : n), kThreads, C::SMEM_TOTAL, s, x, xfull, w0,
-                      w1, p);
+  (void)launch_kernel(kern, (unsigned)grid, kThreads, C::SMEM_TOTAL, s, x, xfull, w0, w1, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
-                           int P, int d, int I, double mean_rows, const Fp8Weight& Wg,
-                           const Fp8Weight& Wu, const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
+                           int P, int d, int I, const Fp8Weight& Wg, const Fp8Weight& Wu,
+                           const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
                            void* y_perm, int* err, cudaStream_t s) {
   if (P == 0) return cudaSuccess;
   const uint64_t cap = (uint64_t)tc_row_capacity(P);
@@ -773,16 +624,11 @@ cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offse
   p2.b.row_scale = slot_w;
   p2.xs = hs, p2.ws0 = p2.ws1 = Wd.scale;
   p2.y = static_cast<__nv_bfloat16*>(y_perm);
-  const bool pair = mean_rows > 512.0;
-  const int rows = pair ? 2 * kRows : kRows;
-  const long long tiles = (long long)(P + rows - 1) / rows + n_groups;
-  const long long u1 = (I + 127) / 128 * tiles, u2 = (d + 255) / 256 * tiles;
-  const char *n1 = "ffn_gateup_fp8", *n2 = "ffn_down_fp8";
-  const cudaError_t e = pair ? launch_f8<MODE_GATEUP, 6, true>(tx, txf, tg, tu, p1, u1, n1, s)
-                             : launch_f8<MODE_GATEUP, 4, false>(tx, txf, tg, tu, p1, u1, n1, s);
+  const long long tiles = (long long)(P + kRows - 1) / kRows + n_groups;
+  const cudaError_t e = launch_f8<MODE_GATEUP, 4>(tx, txf, tg, tu, p1, (I + 127) / 128 * tiles,
+                                                  "ffn_gateup_fp8", s);
   if (e != cudaSuccess) return e;
-  return pair ? launch_f8<MODE_DOWN, 4, true>(th, thf, td, td, p2, u2, n2, s)
-              : launch_f8<MODE_DOWN, 4, false>(th, thf, td, td, p2, u2, n2, s);
+  return launch_f8<MODE_DOWN, 4>(th, thf, td, td, p2, (d + 255) / 256 * tiles, "ffn_down_fp8", s);
 }
 
 }  // namespace moe

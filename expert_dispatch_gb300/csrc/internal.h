@@ -245,8 +245,8 @@ cudaError_t launch_gather_rows_fp8(const void* x, const int32_t* tok_idx,
                                    cudaStream_t s);
 // x8 [cap, d] with scales xs, h8 [cap, I] with scales hs, cap = tc_row_capacity(P)
 cudaError_t launch_ffn_fp8(const void* x8, const float* xs, const int32_t* offsets, int n_groups,
-                           int P, int d, int I, double mean_rows, const Fp8Weight& Wg,
-                           const Fp8Weight& Wu, const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
+                           int P, int d, int I, const Fp8Weight& Wg, const Fp8Weight& Wu,
+                           const Fp8Weight& Wd, const float* slot_w, void* h8, float* hs,
                            void* y_perm, int* err, cudaStream_t s);
 
 // The activation between the products, its inputs kept in 8 bits (swiglu.cu).
