@@ -7,8 +7,8 @@
 //             (u likewise), then h's row into 8 bits, 128 columns a scale
 //   down    : y[r, m] = slot_w[r] sum_b sh[r, b] sd[m / 128, b] <h8[r, b], Wd[m, b]>
 // for every batch row r of expert e (rows offsets[e] .. offsets[e+1]); b runs over
-// the blocks of 128 along the reduction, whose products are summed exactly as
-// codes and scaled once a block.
+// the blocks of 128 along the reduction: a block's products are summed over codes in
+// fp32, then scaled and added in fp32.
 //
 // Design (sm_103a, one CTA an SM, persistent):
 //   * A unit is (expert, 256 weight rows, up to 128 token rows): 128 rows of gate
@@ -18,16 +18,19 @@
 //     one factor for all its columns, a column block of h is one thread's (and its
 //     partner's), and outputs are written along rows.
 //   * A block of 128 along K is one 128-byte swizzled row per operand row: four
-//     tcgen05.mma (kind::f8f6f4, K = 32) into one of two TMEM buffers of 256
-//     columns.  The epilogue's warps add each block's products into registers with
-//     their scales while the next block's MMAs fill the other buffer.
+//     tcgen05.mma (kind::f8f6f4, K = 32, N = 256; 128 cycles each) into one of two
+//     TMEM buffers of 256 columns.  The epilogue's warps add each block's products
+//     into registers with their factors while the next block's MMAs fill the other
+//     buffer.
 //   * Warp 0 lane 0 issues TMA loads into a ring of stages, lane 0 of warps 1 and 2
-//     the MMAs of even and odd blocks (a block's products go to a TMEM buffer of
-//     their own, so the two need no order, and one waits for its stage and buffer
-//     while the other's MMAs run: one issuing thread left the tensor cores idle for
-//     300 of 800 cycles a block), warps 4-11 the epilogue: two warps a TMEM lane quarter, each with half
-//     of the columns (64 of gate and the same 64 of up, or 128 of down).  A thread
-//     holds 128 sums, so the registers are split unevenly (setmaxnreg).
+//     the MMAs of even and odd blocks.  A block's products go to a buffer of their
+//     own, so the two need no order, and one waits for its stage and buffer while
+//     the other's MMAs run (one issuing thread left the tensor cores idle for 300 of
+//     800 cycles a block).
+//   * Warps 4-11 are the epilogue: two warps a TMEM lane quarter, each with half of
+//     the columns (64 of gate and the same 64 of up, or 128 of down).  A thread holds
+//     128 sums, so the registers are split unevenly (setmaxnreg).  Sixteen warps of
+//     64 sums were slower (gate/up 217 -> 256 us), and so was waiting in a spin.
 //   * Warp 3 turns scales into factors, row's times tile's, two for each of the 128
 //     rows (gate's and up's, or those of down's two tiles), a block ahead: they lie in
 //     shared memory before a block's products are announced, and cost the epilogue's
@@ -37,6 +40,13 @@
 //     (8192 tokens x 8, 4096 x 1536, 32 experts: 1.5 % faster; 600 rows an expert 14 %
 //     slower, for its larger tiles).
 //   * Every wait is bounded (tc_common.cuh).
+//
+// What bounds it: with few rows an expert the weights' bytes (64 tokens, 65 experts of
+// 7168 x 2048: 432 us for 2.86 GB, 6.6 TB/s); with many the epilogue.  Reading a block's
+// 128 x 256 sums from TMEM takes 160 cycles, adding them 270 (350 without the packed
+// instruction), both together 310 where nothing else runs, and a block's MMAs 512; with
+// barriers, factors and a unit's end (SwiGLU: two special functions a value) a block
+// takes about 950.  Tensor pipe 52 % active in gate/up, 38 % in down (16384 rows).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

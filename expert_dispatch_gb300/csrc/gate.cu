@@ -84,8 +84,9 @@ struct Slot {
   float logit;
 };
 template <typename T>
-__device__ __forceinline__ Slot load_slot(const T* __restrict__ row, const int32_t* __restrict__ ids,
-                                          size_t t, int E, int k, int lane) {
+__device__ __forceinline__ Slot load_slot(const T* __restrict__ row,
+                                          const int32_t* __restrict__ ids, size_t t, int E, int k,
+                                          int lane) {
   Slot s{-1, -INFINITY};
   if (lane < k) {
     const int id = ids[t * k + lane];
@@ -130,8 +131,8 @@ struct Token {
 // single block with a thread for every expert, the results.
 template <int PL, bool SIGMOID, bool NORM, typename T>
 __global__ void __launch_bounds__(32 * warps_of(PL))
-    gate_forward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids, int T_, int E,
-                        int k, float rs, float* __restrict__ w, float* __restrict__ part_p,
+    gate_forward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids, int T_,
+                        int E, int k, float rs, float* __restrict__ w, float* __restrict__ part_p,
                         int32_t* __restrict__ part_c, int32_t* __restrict__ counts,
                         float* __restrict__ prob, float* __restrict__ loss,
                         unsigned* __restrict__ ticket) {
@@ -361,8 +362,8 @@ struct Kernels {
         cudaFuncSetAttribute(gate_forward_kernel<PL, SIGMOID, NORM, T>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return;
-    (void)launch_kernel(gate_forward_kernel<PL, SIGMOID, NORM, T>, blocks, 32 * warps_of(PL), smem, s,
-                        static_cast<const T*>(logits), ids, D.T, D.E, D.k, D.routed_scaling, w,
+    (void)launch_kernel(gate_forward_kernel<PL, SIGMOID, NORM, T>, blocks, 32 * warps_of(PL), smem,
+                        s, static_cast<const T*>(logits), ids, D.T, D.E, D.k, D.routed_scaling, w,
                         part_p, part_c, counts, prob, loss, ticket);
   }
   static void backward(const void* logits, const int32_t* ids, const moe_layer_desc& D,

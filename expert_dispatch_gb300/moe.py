@@ -573,12 +573,12 @@ def moe_quantize_fp8(w, q, scale, stream=None):
     _check(st, "moe_quantize_fp8")
 
 
-def quantize_fp8(w, stream=None) -> Fp8Weight:
-    """w [n, rows, K] (fp32 or bf16) as an Fp8Weight of its own memory."""
+def quantize_fp8(w) -> Fp8Weight:
+    """w [n, rows, K] (fp32 or bf16) as an Fp8Weight of its own memory, on the current stream."""
     n, rows, K = w.shape
     q = torch.empty((n, rows, K), dtype=FP8, device=w.device)
     s = torch.empty((n, _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
-    moe_quantize_fp8(w, q, s, stream)
+    moe_quantize_fp8(w, q, s)
     return Fp8Weight(q, s)
 
 
@@ -891,28 +891,29 @@ def _rows8_p(r, shape, what, device):
     return _p(r.q, FP8, what, device), _p(r.scale, torch.float32, what + "'s scale", device)
 
 
-def pack_rows(x, stream=None) -> Rows8:
-    """x [rows, n] (fp32 or bf16) in 8 bits (moe_pack_rows), in fresh tensors."""
+def pack_rows(x) -> Rows8:
+    """x [rows, n] (fp32 or bf16) in 8 bits (moe_pack_rows), in fresh tensors, on the current
+    stream like all calls that make their results."""
     rows, n, dt = _rows_args(x, "x")
     at = _device(x, "x")
     out = _new_rows8(rows, n, x.device)
     _check(lib().moe_pack_rows(rows, n, dt, _p(x, x.dtype, "x", at), out.q.data_ptr(),
-                               out.scale.data_ptr(), _stream(stream, at)), "moe_pack_rows")
+                               out.scale.data_ptr(), _stream(None, at)), "moe_pack_rows")
     return out
 
 
-def unpack_rows(r: Rows8, dtype=torch.bfloat16, stream=None):
+def unpack_rows(r: Rows8, dtype=torch.bfloat16):
     """The values of 8-bit rows (moe_unpack_rows) in a fresh fp32 or bf16 tensor."""
     at = _device(r.q, "q")
     q, scale = _rows8_p(r, r.q.shape, "q", at)
     out = torch.empty(r.shape, dtype=dtype, device=r.q.device)
     rows, n, dt = _rows_args(out, "out")
-    _check(lib().moe_unpack_rows(rows, n, dt, q, scale, out.data_ptr(), _stream(stream, at)),
+    _check(lib().moe_unpack_rows(rows, n, dt, q, scale, out.data_ptr(), _stream(None, at)),
            "moe_unpack_rows")
     return out
 
 
-def swiglu(gate, up, pack=False, stream=None):
+def swiglu(gate, up, pack=False):
     """silu(gate) * up of rows [rows, n] (moe_swiglu_forward) in a fresh tensor; with pack
     (h, gate, up), the last two as Rows8 for swiglu_backward."""
     rows, n, dt = _rows_args(gate, "gate")
@@ -922,17 +923,17 @@ def swiglu(gate, up, pack=False, stream=None):
     args = [rows, n, dt, _p(gate, gate.dtype, "gate", at), _p(up, gate.dtype, "up", at),
             h.data_ptr()]
     if not pack:
-        _check(lib().moe_swiglu_forward(*args, None, None, None, None, _stream(stream, at)),
+        _check(lib().moe_swiglu_forward(*args, None, None, None, None, _stream(None, at)),
                "moe_swiglu_forward")
         return h
     g8, u8 = _new_rows8(rows, n, gate.device), _new_rows8(rows, n, gate.device)
     _check(lib().moe_swiglu_forward(*args, g8.q.data_ptr(), g8.scale.data_ptr(), u8.q.data_ptr(),
-                                    u8.scale.data_ptr(), _stream(stream, at)),
+                                    u8.scale.data_ptr(), _stream(None, at)),
            "moe_swiglu_forward")
     return h, g8, u8
 
 
-def swiglu_backward(dh, gate, up, want_h=False, stream=None):
+def swiglu_backward(dh, gate, up, want_h=False):
     """(dgate, dup, h) of moe_swiglu_backward in fresh tensors of dh's type; gate and up are
     tensors of that type, or both Rows8.  h is None unless wanted."""
     rows, n, dt = _rows_args(dh, "dh")
@@ -947,7 +948,7 @@ def swiglu_backward(dh, gate, up, want_h=False, stream=None):
     h = torch.empty_like(dh) if want_h else None
     _check(lib().moe_swiglu_backward(rows, n, dt, _p(dh, dh.dtype, "dh", at), *ins,
                                      dgate.data_ptr(), dup.data_ptr(),
-                                     None if h is None else h.data_ptr(), _stream(stream, at)),
+                                     None if h is None else h.data_ptr(), _stream(None, at)),
            "moe_swiglu_backward")
     return dgate, dup, h
 
@@ -987,8 +988,8 @@ def moe_gate_forward(desc, logits, topk_ids, topk_w, counts, prob, loss, ws, str
 
 def moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits, stream=None):
     """dlogits [T, E] from dtopk_w [T, k] and dloss [1], each unless None."""
-    for t, shape, what in ((counts, (desc.E + 1,), "counts"), (dtopk_w, (desc.T, desc.k), "dtopk_w"),
-                           (dloss, (1,), "dloss"), (dlogits, (desc.T, desc.E), "dlogits")):
+    for t, shape, what in ((counts, (desc.E + 1,), "counts"),
+                           (dtopk_w, (desc.T, desc.k), "dtopk_w"), (dloss, (1,), "dloss"), (dlogits, (desc.T, desc.E), "dlogits")):
         if t is not None:
             _need(t, shape, what)
     at, head = _gate_in(desc, logits, topk_ids)
@@ -1005,7 +1006,7 @@ def _gate_workspace(T, E, k):
     return max(moe_gate_workspace_size(make_desc(T, 128, E, k, 128)), 16)
 
 
-def gate(desc, logits, topk_ids, stream=None):
+def gate(desc, logits, topk_ids):
     """(topk_w, counts, prob, loss) of moe_gate_forward in fresh tensors."""
     at, head = _gate_in(desc, logits, topk_ids)
     T, E, k, dev = desc.T, desc.E, desc.k, logits.device
@@ -1017,14 +1018,14 @@ def gate(desc, logits, topk_ids, stream=None):
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     _check(lib().moe_gate_forward(ctypes.byref(desc), *head, w.data_ptr(), counts.data_ptr(),
                                   prob.data_ptr(), loss.data_ptr(), ws.data_ptr(), n,
-                                  _stream(stream, at)), "moe_gate_forward")
+                                  _stream(None, at)), "moe_gate_forward")
     return w, counts, prob, loss
 
 
-def gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, stream=None):
+def gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss):
     """dlogits of moe_gate_backward in a fresh tensor."""
     dlogits = torch.empty_like(logits)
-    moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits, stream)
+    moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits)
     return dlogits
 
 

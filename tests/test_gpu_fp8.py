@@ -81,8 +81,8 @@ def test_pack_and_unpack_rows(rows, n, dtype):
 
 def test_pack_rows_borders():
     """Amounts at 448 times a power of two, zeros, subnormals, the largest, infinities, NaN."""
-    tops = [448.0, math.nextafter(448.0, 500) + 2.0 ** -16, 449.0, 1.75, 1.7500001, 2.0 ** -118 * 448,
-            1e-30, 0.0, 1e-45, 2e-40, 3.4e38, 447.99997, math.inf, NAN, -math.inf, 2.0 ** -126]
+    tops = [448.0, math.nextafter(448.0, 500) + 2.0 ** -16, 449.0, 1.75, 1.7500001,
+            2.0 ** -118 * 448, 1e-30, 0.0, 1e-45, 2e-40, 3.4e38, 447.99997, math.inf, NAN, -math.inf, 2.0 ** -126]
     x = torch.zeros((len(tops), 256), device="cuda")
     x[:, 5] = torch.tensor(tops, device="cuda")
     x[:, 6:100] = x[:, 5:6] * rnd((len(tops), 94), 3).clamp(-1, 1)
@@ -190,7 +190,8 @@ def ffn_reference(x, off, tok, sw, Wg, Wu, Wd):
         m, ex = torch.frexp((h / sc).abs().clamp(min=2.0 ** -6))
         step = pow2(ex - 4) * sc
         tie = (((h / step).abs() % 1) - 0.5).abs() * step <= dh
-        pad = lambda t: torch.nn.functional.pad(t, (0, -I % 128)).view(len(t), -1, 128)  # noqa: E731
+        pad = lambda t: torch.nn.functional.pad(  # noqa: E731
+            t, (0, -I % 128)).view(len(t), -1, 128)
         ph, pd = pad(h).abs(), pad(dh)
         border = scale_of((ph + pd).amax(2)) != scale_of((ph - pd).clamp(min=0).amax(2))
         move = torch.where(tie, step, 0.0) + torch.where(spread(border, I), 2 * step, 0.0)
@@ -198,7 +199,8 @@ def ffn_reference(x, off, tok, sw, Wg, Wu, Wd):
         a = roundings(I) * (H.abs() @ D[e].abs().T) + move @ D[e].abs().T
         w = 1.0 if sw is None else sw[b[e]:b[e + 1], None].double()
         y[b[e]:b[e + 1]] = v * w
-        tol[b[e]:b[e + 1]] = (a + 2.0 ** -8 * (v.abs() + a)) * (w if sw is None else w.abs()) + 1e-30
+        size = 1.0 if sw is None else w.abs()
+        tol[b[e]:b[e + 1]] = (a + 2.0 ** -8 * (v.abs() + a)) * size + 1e-30
     return y, tol
 
 
@@ -292,6 +294,45 @@ def test_ffn_flags_bad_tokens_and_clamps_bad_offsets():
     wrong[2] = 1000
     moe.moe_expert_ffn_fp8(desc, x, wrong, tok, sw, *W, y, ws)
     assert moe.moe_get_device_status(ws, clear=True) == moe.MOE_ERR_DEVICE_INPUT
+
+
+def test_ffn_many_rows_in_two_steps():
+    """Batches large enough that tokens go into 8 bits once and their codes are copied: bad
+    tokens, dropped pairs, a ragged end."""
+    T, d, k = 2100, 2048, 2
+    desc = moe.make_desc(T, d, 5, k, 64)
+    W = weights(5, 64, d, 1), weights(5, 64, d, 2), weights(5, d, 64, 3)
+    x = rnd((T, d), 4).bfloat16()
+    g = torch.Generator().manual_seed(5)
+    ids = torch.rand((T, 5), generator=g).topk(k, 1).indices
+    ids[::50, 0] = 9
+    off, tok = plan_of(ids, 5, 0)
+    n = int(off[-1])
+    assert n < T * k and T * k * d >= 1 << 23
+    tok = torch.cat([tok, torch.full((T * k - len(tok),), -5, dtype=torch.int32, device="cuda")])
+    ws = moe.alloc_workspace(desc)
+    y = torch.full((T * k, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_ffn_fp8(desc, x, off, tok, None, *W, y, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    want, tol = ffn_reference(x, off, tok.clamp(min=0), None, *W)
+    assert bool(((y.double() - want).abs() <= tol)[:n].all()) and bool((y[n:] == 7.0).all())
+    bad = tok.clone()
+    bad[17], bad[n - 1] = -1, T
+    moe.moe_expert_ffn_fp8(desc, x, off, bad, None, *W, y, ws)
+    assert moe.moe_get_device_status(ws, clear=True) == moe.MOE_ERR_DEVICE_INPUT
+    assert not bool(y[[17, n - 1]].any())
+    ok = torch.ones(n, dtype=torch.bool, device="cuda")
+    ok[[17, n - 1]] = False
+    assert bool(((y.double() - want).abs() <= tol)[:n][ok].all())
+
+
+def test_ffn_output_on_any_16_byte_address():
+    desc, x, off, tok, sw, W, ws, y = run_ffn(150, 320, 192, 3, 2, 1)
+    room = torch.zeros(y.numel() + 16, dtype=torch.bfloat16, device="cuda")
+    at = room[8:8 + y.numel()].view(y.shape)
+    assert at.data_ptr() % 32 == 16
+    moe.moe_expert_ffn_fp8(desc, x, off, tok, sw, *W, at, ws)
+    assert torch.equal(at, y) and not bool(room[:8].any()) and not bool(room[-8:].any())
 
 
 def test_ffn_same_bits_every_time_on_any_stream_and_in_a_graph():

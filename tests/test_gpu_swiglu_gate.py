@@ -317,6 +317,29 @@ def test_gate_gradient_against_differences():
             assert abs(float(got[t, j]) - diff) <= e * e / 6 * 8 + 64 * EPS * 8 / e
 
 
+def test_gate_graphs_share_a_workspace():
+    """The ticket that names the last block is set anew by every call."""
+    desc, l, ids = gate_case(700, 130, 3, 1, 1)
+    l2 = (l * 0.5).contiguous()
+    ws = torch.empty(moe.moe_gate_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    ws.fill_(255)
+    want = [moe.gate(desc, t, ids) for t in (l, l2)]
+    outs = [[torch.zeros_like(t) for t in want[0]] for _ in range(2)]
+    graphs = []
+    for t, out in zip((l, l2), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_gate_forward(desc, t, ids, *out, ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        for a, b in zip(out, w):
+            assert torch.equal(a, b)
+
+
 def test_gate_same_bits_in_a_graph_and_on_streams():
     desc, l, ids = gate_case(3000, 256, 8, 0, 0)
     ws = torch.empty(moe.moe_gate_workspace_size(desc), dtype=torch.uint8, device="cuda")
