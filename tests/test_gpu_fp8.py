@@ -82,7 +82,8 @@ def test_pack_and_unpack_rows(rows, n, dtype):
 def test_pack_rows_borders():
     """Amounts at 448 times a power of two, zeros, subnormals, the largest, infinities, NaN."""
     tops = [448.0, math.nextafter(448.0, 500) + 2.0 ** -16, 449.0, 1.75, 1.7500001,
-            2.0 ** -118 * 448, 1e-30, 0.0, 1e-45, 2e-40, 3.4e38, 447.99997, math.inf, NAN, -math.inf, 2.0 ** -126]
+            2.0 ** -118 * 448, 1e-30, 0.0, 1e-45, 2e-40, 3.4e38, 447.99997, math.inf, NAN,
+            -math.inf, 2.0 ** -126]
     x = torch.zeros((len(tops), 256), device="cuda")
     x[:, 5] = torch.tensor(tops, device="cuda")
     x[:, 6:100] = x[:, 5:6] * rnd((len(tops), 94), 3).clamp(-1, 1)
