@@ -42,7 +42,7 @@
 //   * Every wait is bounded (tc_common.cuh).
 //
 // What bounds it: with few rows an expert the weights' bytes (64 tokens, 65 experts of
-// 7168 x 2048: 432 us for 2.86 GB, 6.6 TB/s); with many the epilogue.  Reading a block's
+// 7168 x 2048: 420 us for 2.86 GB, 6.8 TB/s); with many the epilogue.  Reading a block's
 // 128 x 256 sums from TMEM takes 160 cycles, adding them 270 (350 without the packed
 // instruction), both together 310 where nothing else runs, and a block's MMAs 512; with
 // barriers, factors and a unit's end (SwiGLU: two special functions a value) a block
@@ -462,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tq + (it & 1u) * kCols, va);
         float2 f = fac[(it & 1u) * kRows + lrow];
 // 1, 2, 4 blocks a turn: gate/up 686, 672, 638 us (8192 x 8 rows, 4096 x 1536, 32
-// experts), down 454, 429, 432
-#pragma unroll(MODE == MODE_GATEUP ? 4 : 2)
+// experts), down 454, 429, 432; a short call (777 tokens) 70, 70, 75 us: more code to fetch
+#pragma unroll 2
         for (int kb = 0; kb < KB; ++kb) {
           const uint32_t buf = it & 1u, tb = tq + buf * kCols;
           const float f0 = MODE == MODE_GATEUP || half == 0 ? f.x : f.y;
