@@ -70,11 +70,11 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 // 128 x 72 + 256 x 216 = 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsEpi = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsEpi == kThreads * kRegsLaunch, "register split");
-constexpr int kRows = 128;  // token rows of a CTA's unit
+constexpr int kRows = 128;  // token rows of a unit
 constexpr int kCols = 256;  // weight rows of a unit
 constexpr int kBK = 128;    // bytes (= elements) along K of a stage
 
-// Scales of a row lie pitch_of(n) apart, so that four blocks' are one 16-byte load.
+// Scales of a row lie pitch_of(n) apart, so that two blocks' are one 8-byte load.
 __device__ __forceinline__ int pitch_of(int n) { return fp8_scale_pitch(n); }
 
 struct F8Params {
@@ -344,8 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mbar_wait_drain(drain_bar + 8u * buf, 0, p.b.err);
         }
       }
-    }
-    else {
+    } else {
       // ---------------------------------------------------------- factors (warp 3)
       pdl_wait();  // the token rows' scales are the predecessor's
       const int pitch = pitch_of(p.b.K);
