@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads) gather_rows_fp8_kernel(
 }
 
 // The same from token rows that are in 8 bits already: q[r], scale[r] = q1, scale1 of
-// tok[r], 16 bytes at once.  Two rows a thread block.
+// tok[r], 16 bytes at once.  Two rows a thread block.  A token index outside [0, T) takes
+// neither codes nor scales of any token: its row is that of a zero token here too.
 __global__ void __launch_bounds__(kThreads) copy_rows_fp8_kernel(
     const uint4* __restrict__ q1, const float4* __restrict__ scale1,
     const int32_t* __restrict__ tok, const int32_t* __restrict__ total_rows, int P, int T,
@@ -236,8 +237,10 @@ __global__ void __launch_bounds__(kThreads) copy_rows_fp8_kernel(
   uint4* dst = q + (size_t)r * vecs;
 #pragma unroll 4
   for (int i = lane; i < vecs; i += kThreads / 2) dst[i] = good ? src[i] : make_uint4(0, 0, 0, 0);
+  const float zero = fp8::scale_of(0).scale;  // a zero token's
   for (int i = lane; i < scale_vecs; i += kThreads / 2)
-    scale[(size_t)r * scale_vecs + i] = scale1[(size_t)(good ? t : 0) * scale_vecs + i];
+    scale[(size_t)r * scale_vecs + i] = good ? scale1[(size_t)t * scale_vecs + i]
+                                             : make_float4(zero, zero, zero, zero);
 }
 
 unsigned seg_grid(long long segs) {

@@ -327,6 +327,38 @@ def test_ffn_many_rows_in_two_steps():
     assert bool(((y.double() - want).abs() <= tol)[:n][ok].all())
 
 
+def test_ffn_bad_tokens_are_zero_tokens_whatever_token_0_holds():
+    """A row whose token index is out of range is that of a zero token, in batches of either
+    kind (tokens into 8 bits once and copied, or row by row): nothing of token 0's scales, NaN
+    where it holds a NaN or an infinity, gets into it."""
+    for T, d, I in ((2100, 2048, 64), (2100, 2112, 128), (150, 256, 64)):
+        k = 2
+        desc = moe.make_desc(T, d, 5, k, I)
+        W = weights(5, I, d, 1), weights(5, I, d, 2), weights(5, d, I, 3)
+        x = rnd((T, d), 4).bfloat16()
+        x[0, 5], x[0, 200], x[0, d - 1] = NAN, math.inf, -math.inf
+        ids = torch.rand((T, 5), generator=torch.Generator().manual_seed(5)).topk(k, 1).indices
+        off, tok = plan_of(ids, 5, 0)
+        bad = tok.clone()
+        at = [0, 17, 128, T * k - 1]
+        for i, t in zip(at, (-1, T, 1 << 30, -(1 << 31))):
+            bad[i] = t
+        ws = moe.alloc_workspace(desc)
+        y = torch.full((T * k, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        moe.moe_expert_ffn_fp8(desc, x, off, bad, None, *W, y, ws)
+        assert moe.moe_get_device_status(ws) == moe.MOE_ERR_DEVICE_INPUT
+        assert bool((y[at] == 0).all()), (T, d)
+        # the others' rows as ever: token 0's own are NaN
+        clean = x.clone()
+        clean[0] = 0
+        want, tol = ffn_reference(clean, off, tok, None, *W)
+        good = torch.ones(T * k, dtype=torch.bool, device="cuda")
+        good[at] = False
+        assert bool(y[good & (tok == 0)].isnan().all())
+        good &= tok != 0
+        assert bool(((y.double() - want).abs() <= tol)[good].all())
+
+
 def test_ffn_output_on_any_16_byte_address():
     desc, x, off, tok, sw, W, ws, y = run_ffn(150, 320, 192, 3, 2, 1)
     room = torch.zeros(y.numel() + 16, dtype=torch.bfloat16, device="cuda")
