@@ -51,18 +51,31 @@ __device__ __forceinline__ float warp_max(float v) {
 // sigmoid left out there is below 2^-126.
 __device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 
+// s = sigmoid(l) and 1 - s for its slope s (1 - s).  With e = exp(-|l|) they are 1 / (1 + e)
+// and e / (1 + e), whichever is which: neither is a difference, so 1 - s keeps its digits where
+// s is next to 1 (subtracted it was 1 % off at l = 12 and nothing from 17 on).
+struct Sigmoid {
+  float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid_and_rest(float l) {
+  const float e = expf(-fabsf(l));
+  const float large = __fdividef(1.0f, 1.0f + e), small = e * large;
+  return l < 0.f ? Sigmoid{small, large} : Sigmoid{large, small};
+}
+
 // Below this logit a sigmoid is exp(l) to 26 digits; where all logits of a sum
 // lie below it the sum is formed of exp(l - max), which does not underflow.
 constexpr float kSmallLogit = -60.f;
 
 // A token's probabilities: pr[i] of expert lane + 32 i (softmax, or sigmoid over
-// the sum of sigmoids); sg[i] = the sigmoid (SIGMOID only).  l[i] = -inf past E.
+// the sum of sigmoids); rest[i] = 1 - the sigmoid (SIGMOID and REST only).
+// l[i] = -inf past E.
 struct Softmax {
   float max, inv;  // of the softmax: p = exp(l - max) * inv
 };
-template <int PL, bool SIGMOID>
+template <int PL, bool SIGMOID, bool REST>
 __device__ __forceinline__ Softmax probabilities(const float (&l)[PL], float (&pr)[PL],
-                                                 float (&sg)[PL]) {
+                                                 float (&rest)[PL]) {
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
@@ -71,8 +84,14 @@ __device__ __forceinline__ Softmax probabilities(const float (&l)[PL], float (&p
   const bool shift = !SIGMOID || m < kSmallLogit;
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    if (SIGMOID) sg[i] = sigmoid(l[i]);
-    pr[i] = shift ? expf(l[i] - m) : sg[i];
+    float sg = 0.f;
+    if (SIGMOID && REST) {
+      const Sigmoid f = sigmoid_and_rest(l[i]);
+      sg = f.s, rest[i] = f.rest;
+    } else if (SIGMOID) {
+      sg = sigmoid(l[i]);
+    }
+    pr[i] = shift ? expf(l[i] - m) : sg;
     z += pr[i];
   }
   const float inv = 1.0f / warp_sum(z);
@@ -161,8 +180,8 @@ __global__ void __launch_bounds__(32 * warps_of(PL))
     const Slot s = now.s;
     float v = 0.f;
     if (__any_sync(0xffffffffu, s.id >= 0)) {
-      float pr[PL], sg[PL];
-      const Softmax f = probabilities<PL, SIGMOID>(now.l, pr, sg);
+      float pr[PL], rest[PL];
+      const Softmax f = probabilities<PL, SIGMOID, false>(now.l, pr, rest);
 #pragma unroll
       for (int i = 0; i < PL; ++i) sum[i] += pr[i];
       ++tokens;
@@ -303,8 +322,8 @@ __global__ void __launch_bounds__(32 * kBackWarps)
         if (lane + 32 * i < E) out[lane + 32 * i] = (T)0.f;
       continue;
     }
-    float pr[PL], sg[PL];
-    const Softmax f = probabilities<PL, SIGMOID>(now.l, pr, sg);
+    float pr[PL], rest[PL];
+    const Softmax f = probabilities<PL, SIGMOID, true>(now.l, pr, rest);
     float mean = 0.f;  // <c, p>
 #pragma unroll
     for (int i = 0; i < PL; ++i) mean += c[i] * pr[i];
@@ -316,10 +335,10 @@ __global__ void __launch_bounds__(32 * kBackWarps)
         const float q = normalised<SIGMOID>(s);
         const float dot = warp_sum(s.id >= 0 ? g * q : 0.f);
         v = q * (g - dot);
-        if (SIGMOID) v *= 1.0f - sigmoid(s.logit);
+        if (SIGMOID) v *= sigmoid_and_rest(s.logit).rest;
       } else if (SIGMOID) {
-        const float sj = sigmoid(s.logit);
-        v = g * sj * (1.0f - sj);
+        const Sigmoid sj = sigmoid_and_rest(s.logit);
+        v = g * sj.s * sj.rest;
       } else {
         v = g;  // times p_e, known on the expert's lane
         pull = warp_sum(s.id >= 0 ? g * (expf(s.logit - f.max) * f.inv) : 0.f);
@@ -340,7 +359,7 @@ __global__ void __launch_bounds__(32 * kBackWarps)
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       float v = a * pr[i] * (c[i] - mean);
-      if (SIGMOID) v *= 1.0f - sg[i];
+      if (SIGMOID) v *= rest[i];
       if (dw) {
         const float add = add_s[warp][lane + 32 * i];
         v += !NORM && !SIGMOID ? pr[i] * (add - pull) : add;

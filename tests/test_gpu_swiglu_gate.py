@@ -267,6 +267,72 @@ def test_gate_masked_and_far_logits(kind, norm):
         assert torch.equal(x, y)
 
 
+def sigmoid_gradient(l, ids, counts, desc, dw, dl):
+    """dlogits of the sigmoid gate by its formula in 64 bits, 1 - s as sigmoid(-l), and the sum
+    of its terms' sizes: every term has the factor 1 - s."""
+    E, k = desc.E, desc.k
+    there = (ids >= 0) & (ids < E)
+    live = there.any(1)
+    at = torch.where(there, ids, 0).long()
+    l = l.double()
+    p = torch.softmax(torch.nn.functional.logsigmoid(l), 1)
+    rest = torch.sigmoid(-l)
+    c, n = counts[:E].double(), float(counts[E])
+    A = dl * E / (k * n * n)
+    mean = (c * p).sum(1, keepdim=True)
+    out, size = A * p * (c - mean), A * p * (c + mean)
+    g = torch.where(there, 1.5 * dw.double(), 0.0)
+    if desc.norm_topk:
+        own = torch.nn.functional.logsigmoid(l).gather(1, at).masked_fill(~there, -math.inf)
+        q = torch.zeros_like(own)
+        q[live] = torch.softmax(own[live], 1)
+        part = q * (g - (g * q).sum(1, keepdim=True))
+        part_size = q * (g.abs() + (g.abs() * q).sum(1, keepdim=True))
+    else:
+        q = torch.sigmoid(l).gather(1, at)
+        part, part_size = g * q, (g * q).abs()
+    part, part_size = (torch.where(there, t, 0.0) for t in (part, part_size))
+    out = torch.where(live[:, None], out.scatter_add(1, at, part), 0.0) * rest
+    return out, size.scatter_add(1, at, part_size) * rest
+
+
+@pytest.mark.parametrize("norm", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0.0, 10.0, 14.0, 20.0, 30.0, 70.0, -20.0, -58.0, -75.0, -200.0,
+                                   "mixed", "one far"])
+def test_gate_gradient_of_far_logits(shift, dtype, norm):
+    """The sigmoid's slope s (1 - s) keeps its digits where s is next to 1 or 0.
+
+    In units of eps = 2^-24: exp(-|l|) 4 (two steps), s and 1 - s of it another rounding, the
+    fast division's 4 and a product: 12 in all.  p is s over a sum of E, whose additions are
+    5 + E / 32: 2 * 12 + 6 + E / 32 for p; where all logits lie below -60 p is exp(l - max) over
+    a sum of them instead, whose arguments are rounded: another |l - max| + 4.  A term of the
+    result is a product of up to eight such factors and roundings; the mean <c, p> and the slots'
+    sum are as far off as p, relative to the terms' sizes before they cancel."""
+    T, E, k = 40, 60, 4
+    desc, l, ids = gate_case(T, E, k, moe.MOE_GATE_SIGMOID_BIAS, norm, seed=11, pad=0.2,
+                             repeat=True, size=1.0)
+    if shift == "mixed":
+        l = l + torch.tensor([-90.0, -20.0, 0.0, 12.0, 40.0], device="cuda")[
+            torch.arange(E, device="cuda") % 5]
+    elif shift == "one far":
+        l[:, 7] = 25.0
+        ids[::2, 0] = 7
+    else:
+        l = l + shift
+    l = l.to(dtype)
+    dw, dl = rnd((T, k), 5), torch.tensor([0.7], device="cuda")
+    _, counts, _, _ = moe.gate(desc, l, ids)
+    spread_ = float(l.double().amax() - l.double().amin()) if float(l.amax()) < -50 else 0.0
+    p_err = 2 * 12 + 6 + E / 32 + spread_ + 4
+    eps = (2 * p_err + 3 * 12 + 12) * EPS
+    for use_w, use_l in ((1, 1), (1, 0), (0, 1)):
+        got = moe.gate_backward(desc, l, ids, counts if use_l else None, dw if use_w else None,
+                                dl if use_l else None)
+        want, size = sigmoid_gradient(l, ids, counts, desc, use_w * dw, use_l * 0.7)
+        near(got, want, eps * size + HALF[dtype] * (want.abs() + eps * size) + 1e-36)
+
+
 def test_gate_without_any_token():
     desc, l, ids = gate_case(12, 16, 2, 0, 1)
     ids.fill_(-1)
