@@ -183,9 +183,10 @@ class _Swiglu(torch.autograd.Function):
 
 
 def swiglu(gate, up, packed=True):
-    """silu(gate) * up (contiguous, 16-byte aligned, fp32 or bf16).  packed: the backward pass
-    reads gate and up from 8 bits (e4m3, a scale a block of 128 columns: up to 2^-4 off),
-    half of bf16's memory; else from gate and up themselves."""
+    """silu(gate) * up (of one shape, contiguous, 16-byte aligned, fp32 or bf16).  packed: the
+    backward pass reads gate and up from 8 bits (e4m3, a scale a block of 128 columns: up to
+    2^-4 off), half of bf16's memory; else from gate and up themselves."""
+    moe._need(up, gate.shape, "up")  # before the rows are flattened
     return _Swiglu.apply(gate, up, packed)
 
 

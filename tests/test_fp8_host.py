@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from expert_dispatch_gb300 import build as moe_build
-from expert_dispatch_gb300 import moe
+from expert_dispatch_gb300 import moe, training
 from tests.test_training_host import FAKE, ODD, _Elsewhere, _Here
 
 BAD, UNSUP, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_OK
@@ -178,6 +178,16 @@ def test_binding_checks(monkeypatch):
         moe.moe_expert_ffn_fp8(d, _here((4, 64), torch.bfloat16), _here((5,), torch.int32),
                                _here((8,), torch.int32), None, x, x, x,
                                _here((8, 64), torch.bfloat16), None)
+
+
+def test_training_swiglu_compares_shapes_before_it_flattens_rows(monkeypatch):
+    """Tensors of other shapes are refused, also where their rows would fit in flattened order."""
+    monkeypatch.setattr(moe, "swiglu", lambda *a, **kw: pytest.fail("it came to the call"))
+    for a, b in (((2, 3, 8), (3, 2, 8)), ((6, 8), (1, 2, 3, 8)), ((1, 8), (8,)), ((2, 8), (1, 8)),
+                 ((2, 8), (2, 4))):
+        for packed in (True, False):
+            with pytest.raises(ValueError, match="up has shape"), torch.no_grad():
+                training.swiglu(torch.zeros(a), torch.zeros(b), packed)
 
 
 def _here(shape, dtype, cls=_Here):
