@@ -65,14 +65,22 @@ def _grad(g):
     return g if g.data_ptr() % 16 == 0 else g.clone()
 
 
+def _of_rows(f, *t):
+    """f of tensors of one shape as rows [-1, n], in that shape.  The views are made here, under
+    autograd: torch refuses to write in place into one that a function below returns."""
+    shape = t[0].shape
+    if len(shape) == 2:
+        return f(*t)
+    return f(*(x.reshape(-1, shape[-1]) for x in t)).view(shape)
+
+
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, kind, eps):
-        rows = x.reshape(-1, x.shape[-1])
-        y, mean, rstd = moe.norm(rows, gamma, beta, kind=kind, eps=eps, stats=True)
-        ctx.save_for_backward(rows, gamma, mean, rstd)
+        y, mean, rstd = moe.norm(x, gamma, beta, kind=kind, eps=eps, stats=True)
+        ctx.save_for_backward(x, gamma, mean, rstd)
         ctx.kind, ctx.beta_dtype = kind, None if beta is None else beta.dtype
-        return y.view(x.shape)
+        return y
 
     @staticmethod
     @once_differentiable
@@ -87,20 +95,19 @@ class _Norm(torch.autograd.Function):
             ws = torch.empty(moe.moe_norm_workspace_size(desc), dtype=torch.uint8,
                              device=x.device)
         dx = torch.empty_like(x)
-        moe.moe_norm_backward(desc, _grad(dy.reshape(x.shape)), x, gamma, mean, rstd, dx,
-                              dg, db, ws)
-        return (dx.view(dy.shape), dg.to(gamma.dtype) if want_g else None,
+        moe.moe_norm_backward(desc, _grad(dy), x, gamma, mean, rstd, dx, dg, db, ws)
+        return (dx, dg.to(gamma.dtype) if want_g else None,
                 db.to(ctx.beta_dtype) if want_b else None, None, None)
 
 
 def layer_norm(x, gamma=None, beta=None, eps=1e-6):
     """Layer norm over the last dimension of x (contiguous, 16-byte aligned, fp32 or bf16)."""
-    return _Norm.apply(x, gamma, beta, moe.MOE_NORM_LAYER, eps)
+    return _of_rows(lambda r: _Norm.apply(r, gamma, beta, moe.MOE_NORM_LAYER, eps), x)
 
 
 def rms_norm(x, gamma=None, eps=1e-6):
     """RMS norm over the last dimension of x (contiguous, 16-byte aligned, fp32 or bf16)."""
-    return _Norm.apply(x, gamma, None, moe.MOE_NORM_RMS, eps)
+    return _of_rows(lambda r: _Norm.apply(r, gamma, None, moe.MOE_NORM_RMS, eps), x)
 
 
 class _Dispatch(torch.autograd.Function):
@@ -163,23 +170,22 @@ def combine(y_perm, topk_w, plan: Plan, residual=None):
 class _Swiglu(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate, up, packed):
-        rows = (gate.reshape(-1, gate.shape[-1]), up.reshape(-1, up.shape[-1]))
         ctx.packed = packed
         if packed:
-            h, g8, u8 = moe.swiglu(*rows, pack=True)
+            h, g8, u8 = moe.swiglu(gate, up, pack=True)
             ctx.save_for_backward(g8.q, g8.scale, u8.q, u8.scale)
         else:
-            h = moe.swiglu(*rows)
-            ctx.save_for_backward(*rows)
-        return h.view(gate.shape)
+            h = moe.swiglu(gate, up)
+            ctx.save_for_backward(gate, up)
+        return h
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh):
         t = ctx.saved_tensors
         gate, up = (moe.Rows8(*t[:2]), moe.Rows8(*t[2:])) if ctx.packed else t
-        dgate, dup, _ = moe.swiglu_backward(_grad(dh.reshape(-1, dh.shape[-1])), gate, up)
-        return dgate.view(dh.shape), dup.view(dh.shape), None
+        dgate, dup, _ = moe.swiglu_backward(_grad(dh), gate, up)
+        return dgate, dup, None
 
 
 def swiglu(gate, up, packed=True):
@@ -187,7 +193,7 @@ def swiglu(gate, up, packed=True):
     backward pass reads gate and up from 8 bits (e4m3, a scale a block of 128 columns: up to
     2^-4 off), half of bf16's memory; else from gate and up themselves."""
     moe._need(up, gate.shape, "up")  # before the rows are flattened
-    return _Swiglu.apply(gate, up, packed)
+    return _of_rows(lambda g, u: _Swiglu.apply(g, u, packed), gate, up)
 
 
 class _Gate(torch.autograd.Function):
@@ -198,7 +204,7 @@ class _Gate(torch.autograd.Function):
         ctx.save_for_backward(logits, topk_ids, counts)
         ctx.mark_non_differentiable(counts, prob)
         ctx.set_materialize_grads(False)
-        return w, loss.view(()), counts, prob
+        return w, loss, counts, prob
 
     @staticmethod
     @once_differentiable
@@ -208,11 +214,12 @@ class _Gate(torch.autograd.Function):
         logits, topk_ids, counts = ctx.saved_tensors
         return moe.gate_backward(ctx.desc, logits, topk_ids, counts,
                                  None if dw is None else _grad(dw),
-                                 None if dloss is None else _grad(dloss.reshape(1))), None, None
+                                 None if dloss is None else _grad(dloss)), None, None
 
 
 def gate(logits, topk_ids, desc):
     """(topk_w [T, k], balance loss [], counts [E+1] int32, prob [E]) of the slots topk_ids
     [T, k] int32 (an id outside [0, E): a dropped slot, or padding) from router logits [T, E]
     (fp32 or bf16); the first two have gradients, both by one pass over the logits."""
-    return _Gate.apply(logits, topk_ids, desc)
+    w, loss, counts, prob = _Gate.apply(logits, topk_ids, desc)
+    return w, loss.view(()), counts, prob

@@ -118,6 +118,17 @@ def test_gradients_at_any_address():
             assert torch.equal(p, q)
 
 
+def test_norms_may_be_written_in_place():
+    for shape in ((6, 72), (2, 3, 72)):
+        for f in (training.rms_norm, training.layer_norm):
+            a, b = (rnd(shape, 1).requires_grad_() for _ in range(2))
+            y = f(a)
+            y *= 3
+            y.sum().backward()
+            f(b).backward(torch.full(shape, 3.0, device="cuda"))
+            assert torch.equal(a.grad, b.grad)
+
+
 def test_a_plan_written_before_the_backward_pass_is_noticed():
     desc, plan = make()
     x = rnd((desc.T, desc.d), 1).requires_grad_()

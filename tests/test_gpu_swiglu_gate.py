@@ -454,6 +454,28 @@ def test_training_swiglu(packed):
         near(t.view(15, 144), want, tol)
 
 
+def test_training_results_may_be_written_in_place():
+    """They are tensors of their own: torch refuses to write into views made in a function."""
+    for shape in ((6, 72), (2, 3, 72)):
+        for packed in (True, False):
+            a, b = (rnd(shape, i).requires_grad_() for i in (1, 2))
+            h = training.swiglu(a, b, packed)
+            h *= 3
+            h.sum().backward()
+            c, d = (t.detach().clone().requires_grad_() for t in (a, b))
+            training.swiglu(c, d, packed).backward(torch.full(shape, 3.0, device="cuda"))
+            assert torch.equal(a.grad, c.grad) and torch.equal(b.grad, d.grad)
+    desc, l, ids = gate_case(50, 24, 3, 1, 1)
+    x, z = l.clone().requires_grad_(), l.clone().requires_grad_()
+    w, loss, _, _ = training.gate(x, ids, desc)
+    loss *= 0.5
+    w *= 2
+    (loss + w.sum()).backward()
+    w, loss, _, _ = training.gate(z, ids, desc)
+    (0.5 * loss + (2 * w).sum()).backward()
+    assert torch.equal(x.grad, z.grad)
+
+
 def test_training_gate():
     desc, l, ids = gate_case(50, 24, 3, 1, 1)
     for use_w, use_l in ((1, 1), (1, 0), (0, 1)):
