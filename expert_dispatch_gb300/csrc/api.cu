@@ -278,6 +278,39 @@ bool q8_ok(const moe_q8_weight* w) {
   return w && w->q && w->scale && aligned16(w->q) && aligned16(w->scale);
 }
 
+// Bytes from p on; no bytes where p is NULL.
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// Whether an output shares a byte with an input or with another output.  Blocks of
+// values are read and written by different threads in no order, so it must not, not
+// even at the same elements where their sizes differ (codes over values).
+template <size_t O, size_t I>
+bool outputs_overlap(const Span (&out)[O], const Span (&in)[I]) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && (x <= y ? y - x < a.n : x - y < b.n);
+  };
+  for (size_t o = 0; o < O; ++o) {
+    for (size_t i = 0; i < I; ++i)
+      if (meet(out[o], in[i])) return true;
+    for (size_t i = 0; i < o; ++i)
+      if (meet(out[o], out[i])) return true;
+  }
+  return false;
+}
+
+// Rows [rows, n] as values of a dtype, as 8-bit codes, and the codes' scales.
+struct RowBytes {
+  size_t full, codes, scales;
+};
+RowBytes row_bytes(int rows, int n, int dtype) {
+  const size_t e = (size_t)rows * n;
+  return {e * dtype_size(dtype), e, (size_t)rows * (((size_t)n + 127) / 128) * 4};
+}
+
 }  // namespace
 
 RouterPlan router_plan(int dtype, int T, int d, int E) {
@@ -842,6 +875,10 @@ moe_status moe_quantize_fp8(int n_mats, int rows, int K, int src_dtype, const vo
   if (tiles > 0x7fffffffll / n_mats) return MOE_ERR_UNSUPPORTED;
   if (!w || !q || !scale || !aligned16(w) || !aligned16(q) || !aligned16(scale))
     return MOE_ERR_INVALID_ARG;
+  const size_t e = (size_t)n_mats * rows * K;
+  const Span out[] = {{q, e}, {scale, (size_t)tiles * n_mats * 4}};
+  const Span in[] = {{w, e * dtype_size(src_dtype)}};
+  if (outputs_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_quantize_fp8(src_dtype, w, n_mats, rows, K, q, scale,
                                          static_cast<cudaStream_t>(stream)));
 }
@@ -954,8 +991,11 @@ moe_status moe_pack_rows(int rows, int n, int dtype, const void* x, void* q, flo
   const NvtxRange nvtx("moe_pack_rows");
   if (rows < 0 || n <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!x || !q || !scale || x == q || !aligned16(x) || !aligned16(q) || !aligned16(scale))
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale))
     return MOE_ERR_INVALID_ARG;
+  const RowBytes b = row_bytes(rows, n, dtype);
+  const Span out[] = {{q, b.codes}, {scale, b.scales}}, in[] = {{x, b.full}};
+  if (outputs_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       launch_pack_rows(dtype, x, rows, n, q, scale, static_cast<cudaStream_t>(stream)));
 }
@@ -965,8 +1005,11 @@ moe_status moe_unpack_rows(int rows, int n, int dtype, const void* q, const floa
   const NvtxRange nvtx("moe_unpack_rows");
   if (rows < 0 || n <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!x || !q || !scale || x == q || !aligned16(x) || !aligned16(q) || !aligned16(scale))
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale))
     return MOE_ERR_INVALID_ARG;
+  const RowBytes b = row_bytes(rows, n, dtype);
+  const Span out[] = {{x, b.full}}, in[] = {{q, b.codes}, {scale, b.scales}};
+  if (outputs_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       launch_unpack_rows(dtype, q, scale, rows, n, x, static_cast<cudaStream_t>(stream)));
 }
@@ -981,10 +1024,15 @@ moe_status moe_swiglu_forward(int rows, int n, int dtype, const void* gate, cons
       pack != (up_scale != nullptr))
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!gate || !up || !h || h == gate || h == up) return MOE_ERR_INVALID_ARG;
+  if (!gate || !up || !h) return MOE_ERR_INVALID_ARG;
   for (const void* p : {gate, up, (const void*)h, (const void*)gate8, (const void*)gate_scale,
                         (const void*)up8, (const void*)up_scale})
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const RowBytes b = row_bytes(rows, n, dtype);
+  const Span out[] = {{h, b.full}, {gate8, b.codes}, {gate_scale, b.scales}, {up8, b.codes},
+                      {up_scale, b.scales}};
+  const Span in[] = {{gate, b.full}, {up, b.full}};
+  if (outputs_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_swiglu_forward(dtype, gate, up, rows, n, h, gate8, gate_scale, up8,
                                            up_scale, static_cast<cudaStream_t>(stream)));
 }
@@ -999,12 +1047,14 @@ moe_status moe_swiglu_backward(int rows, int n, int dtype, const void* dh, const
   const bool packed = gate8 && gate_scale && up8 && up_scale && !gate && !up;
   const bool plain = gate && up && !gate8 && !gate_scale && !up8 && !up_scale;
   if (!dh || !dgate || !dup || (!packed && !plain)) return MOE_ERR_INVALID_ARG;
-  if (dgate == dup || h == dgate || h == dup) return MOE_ERR_INVALID_ARG;
-  for (const void* in : {dh, gate, up})
-    if (in && (in == dgate || in == dup || in == h)) return MOE_ERR_INVALID_ARG;
   for (const void* p : {dh, gate, up, gate8, (const void*)gate_scale, up8, (const void*)up_scale,
                         (const void*)dgate, (const void*)dup, (const void*)h})
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const RowBytes b = row_bytes(rows, n, dtype);
+  const Span out[] = {{dgate, b.full}, {dup, b.full}, {h, b.full}};
+  const Span in[] = {{dh, b.full}, {gate, b.full}, {up, b.full}, {gate8, b.codes},
+                     {gate_scale, b.scales}, {up8, b.codes}, {up_scale, b.scales}};
+  if (outputs_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_swiglu_backward(dtype, dh, gate, up, gate8, gate_scale, up8, up_scale,
                                             rows, n, dgate, dup, h,
                                             static_cast<cudaStream_t>(stream)));

@@ -297,7 +297,8 @@ typedef struct {
 
 /* moe_quantize_fp8 -- n_mats row-major [rows, K] matrices (fp32 or bf16, src_dtype
    a moe_dtype) in tiles of 128 x 128.  q and scale are device outputs sized as
-   above; any rows, K > 0 (at most 2^31 - 1 tiles, beyond: MOE_ERR_UNSUPPORTED). */
+   above, which overlap neither w nor one another; any rows, K > 0 (at most 2^31 - 1
+   tiles, beyond: MOE_ERR_UNSUPPORTED). */
 moe_status moe_quantize_fp8(int n_mats, int rows, int K, int src_dtype, const void* w, void* q,
                             float* scale, void* stream);
 
@@ -639,7 +640,8 @@ moe_status moe_gate_backward(const moe_layer_desc* desc, int logits_dtype, const
 
 /* Activations kept in 8 bits for the backward pass ("8-bit floating point" above, rows).
    moe_pack_rows: q, scale from x [rows, n] in dtype (a moe_dtype); moe_unpack_rows: the
-   values again, rounded once.  Any n > 0; rows == 0 is a valid no-op. */
+   values again, rounded once.  No output may overlap an input or the other output
+   (MOE_ERR_INVALID_ARG).  Any n > 0; rows == 0 is a valid no-op. */
 moe_status moe_pack_rows(int rows, int n, int dtype, const void* x, void* q, float* scale,
                          void* stream);
 moe_status moe_unpack_rows(int rows, int n, int dtype, const void* q, const float* scale, void* x,
@@ -654,7 +656,8 @@ moe_status moe_unpack_rows(int rows, int n, int dtype, const void* q, const floa
      dgate = dh * up * sigma * (1 + gate * (1 - sigma)),  sigma = sigmoid(gate)
      dup   = dh * silu(gate)
      h     [rows, n] out, or NULL: silu(gate) * up again.
-   No output may be an input.  Any n > 0; rows == 0 is a valid no-op. */
+   No output may overlap an input or another output (MOE_ERR_INVALID_ARG).  Any n > 0;
+   rows == 0 is a valid no-op. */
 moe_status moe_swiglu_forward(int rows, int n, int dtype, const void* gate, const void* up, void* h,
                               void* gate8, float* gate_scale, void* up8, float* up_scale,
                               void* stream);

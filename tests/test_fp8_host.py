@@ -118,6 +118,43 @@ def test_rows_and_swiglu_refuse(L):
     assert fwd(0, 4, 0, *[None] * 7, None) == OK
 
 
+def test_outputs_that_overlap_an_input_or_another_output_are_refused(L):
+    """By their ranges: 40 rows of 100, a buffer's first 16 bytes in the other's last."""
+    def places(*sizes):
+        return [0x1000000 * (i + 1) for i in range(len(sizes))]
+
+    def pairs(call, sizes, outputs):
+        """call with one output moved onto every other buffer: at its start, onto its end."""
+        at = places(*sizes)
+        for o in outputs:
+            for j in range(len(sizes)):
+                if j == o:
+                    continue
+                last = (sizes[j] - 1) // 16 * 16  # the last 16-byte address within it
+                for to in {at[j], at[j] + last, at[j] - (sizes[o] - 1) // 16 * 16}:
+                    args = [ctypes.c_void_p(to if i == o else a) for i, a in enumerate(at)]
+                    assert call(args) == BAD, (o, j, hex(to))
+
+    for es, dt in ((4, moe.MOE_F32), (2, moe.MOE_BF16)):
+        full, codes, scales = 4000 * es, 4000, 40 * 4
+        # x, q, scale
+        pairs(lambda a: L.moe_pack_rows(40, 100, dt, *a, None), [full, codes, scales], (1, 2))
+        # q, scale, x
+        pairs(lambda a: L.moe_unpack_rows(40, 100, dt, *a, None), [codes, scales, full], (2,))
+        # w, q, scale
+        pairs(lambda a: L.moe_quantize_fp8(2, 20, 100, dt, *a, None), [full, codes, 8], (1, 2))
+        # gate, up, h, gate8, gate_scale, up8, up_scale
+        pairs(lambda a: L.moe_swiglu_forward(40, 100, dt, *a, None),
+              [full] * 3 + [codes, scales] * 2, (2, 3, 4, 5, 6))
+        pairs(lambda a: L.moe_swiglu_forward(40, 100, dt, *a, None, None, None, None, None),
+              [full] * 3, (2,))
+        # dh, gate, up, dgate, dup, h and dh, gate8, gate_scale, up8, up_scale, dgate, dup, h
+        pairs(lambda a: L.moe_swiglu_backward(40, 100, dt, *a[:3], *[None] * 4, *a[3:], None),
+              [full] * 6, (3, 4, 5))
+        pairs(lambda a: L.moe_swiglu_backward(40, 100, dt, a[0], None, None, *a[1:], None),
+              [full] + [codes, scales] * 2 + [full] * 3, (5, 6, 7))
+
+
 def test_gate_refuses(L):
     n = ctypes.c_size_t(0)
     d = _layer()
