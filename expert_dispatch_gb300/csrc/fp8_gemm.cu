@@ -39,7 +39,8 @@
 //     built and dropped: the tensor cores wait for the additions, not for operands
 //     (8192 tokens x 8, 4096 x 1536, 32 experts: 1.5 % faster; 600 rows an expert 14 %
 //     slower, for its larger tiles).
-//   * Every wait is bounded (tc_common.cuh).
+//   * Every wait is bounded (tc_common.cuh); that for registers ends because the launcher
+//     has checked that there are enough.
 //
 // What bounds it: with few rows an expert the weights' bytes (64 tokens, 65 experts of
 // 7168 x 2048: 420 us for 2.86 GB, 6.8 TB/s); with many the epilogue.  Reading a block's
@@ -70,6 +71,14 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 // 128 x 72 + 256 x 216 = 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsEpi = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsEpi == kThreads * kRegsLaunch, "register split");
+// Whether a launch with so many registers a thread (given out in steps of 8) covers the split.
+// What the compiler took decides, and a warp that asks for more than the block has left
+// waits without a limit: the launcher asks first.
+constexpr bool covers_split(int regs) {
+  const int given = (regs + 7) / 8 * 8;
+  return given >= kRegsLaunch && given <= kRegsEpi;
+}
+static_assert(covers_split(kRegsLaunch) && !covers_split(kRegsLaunch - 8), "register split");
 constexpr int kRows = 128;  // token rows of a unit
 constexpr int kCols = 256;  // weight rows of a unit
 constexpr int kBK = 128;    // bytes (= elements) along K of a stage
@@ -594,6 +603,9 @@ cudaError_t launch_f8(const CUtensorMap& x, const CUtensorMap& xfull, const CUte
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev]) {
+      cudaFuncAttributes attr;
+      if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
+      if (!covers_split(attr.numRegs)) return cudaErrorInvalidConfiguration;
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
       if (e != cudaSuccess) return e;
       configured[dev] = true;

@@ -1,6 +1,9 @@
 """Argument checks of the 8-bit, SwiGLU and gate calls that need no GPU: every refusal comes
 back before anything is launched."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -116,6 +119,27 @@ def test_rows_and_swiglu_refuse(L):
         assert bwd(4, 4, 0, *args, None) == BAD
     assert bwd(0, 4, 0, *[None] * 10, None) == OK
     assert fwd(0, 4, 0, *[None] * 7, None) == OK
+
+
+def test_products_are_not_launched_on_too_few_registers(tmp_path):
+    """The warps of the products share the registers that the block was launched with, unevenly:
+    72 for each thread of four warps, 216 of eight, of 384 times 168.  A kernel that another
+    compiler gave fewer would wait for the missing ones without a limit, so it is refused
+    before its launch.  The launcher runs on a runtime of its own (fake_launches.cuh)."""
+    lib = str(tmp_path / "fake.so")
+    subprocess.run([moe_build.nvcc(), *moe_build.ARCH, "-std=c++17", "-I", moe_build.INCLUDE, "-I",
+                    moe_build.CSRC, "-Xcompiler", "-fPIC", "-include",
+                    os.path.join(os.path.dirname(__file__), "fake_launches.cuh"), "-shared",
+                    "--cudart", "static", "-o", lib,
+                    os.path.join(moe_build.CSRC, "fp8_gemm.cu")], check=True)
+    n = ctypes.c_int(-1)
+    # registers come in steps of 8: 161 are 168
+    for regs, fine in ((160, False), (128, False), (64, False), (217, False), (161, True),
+                       (168, True)):
+        run = ctypes.CDLL(shutil.copy(lib, str(tmp_path / ("%d.so" % regs)))).fake_products
+        for _ in range(2):  # a refusal is not forgotten
+            status = run(regs, ctypes.byref(n))
+            assert (status, n.value) == ((0, 2) if fine else (9, 0)), regs
 
 
 def test_outputs_that_overlap_an_input_or_another_output_are_refused(L):
