@@ -12,8 +12,8 @@ moe_get_device_status, moe_status_string, moe_launch_count,
 moe_profile_enable, moe_profile_query, moe_profile_list, the Q8_0 and no-alloc variants, the
 slot cache (moe_slot_cache_*), the expert tier (moe_tier_*), the 8-bit floating point layer
 (moe_quantize_fp8, moe_expert_ffn_fp8, moe_layer_forward_fp8*) and the training operators
-(moe_dispatch_rows, moe_norm_*, moe_swiglu_*, moe_gate_*, moe_pack_rows and the gradients
-moe_*_backward).
+(moe_dispatch_rows, moe_norm_*, moe_swiglu_*, moe_gate_*, moe_pack_rows, moe_unpack_rows and the
+gradients moe_*_backward).
 """
 from __future__ import annotations
 
@@ -891,6 +891,71 @@ def _rows8_p(r, shape, what, device):
     return _p(r.q, FP8, what, device), _p(r.scale, torch.float32, what + "'s scale", device)
 
 
+def moe_pack_rows(x, q, scale, stream=None):
+    """Codes q [rows, n] and scales [rows, ceil(n/128)] of x [rows, n] (fp32 or bf16)."""
+    rows, n, dt = _rows_args(x, "x")
+    _need(q, x.shape, "q")
+    _need(scale, (rows, _blocks(n)), "scale")
+    at = _device(x, "x")
+    st = lib().moe_pack_rows(rows, n, dt, _p(x, x.dtype, "x", at), _p(q, FP8, "q", at),
+                             _p(scale, torch.float32, "scale", at), _stream(stream, at))
+    _check(st, "moe_pack_rows")
+
+
+def moe_unpack_rows(q, scale, x, stream=None):
+    """The values of codes q and scales in x [rows, n] (fp32 or bf16)."""
+    rows, n, dt = _rows_args(x, "x")
+    _need(q, x.shape, "q")
+    _need(scale, (rows, _blocks(n)), "scale")
+    at = _device(q, "q")
+    st = lib().moe_unpack_rows(rows, n, dt, _p(q, FP8, "q", at),
+                               _p(scale, torch.float32, "scale", at), _p(x, x.dtype, "x", at),
+                               _stream(stream, at))
+    _check(st, "moe_unpack_rows")
+
+
+def moe_swiglu_forward(gate, up, h, gate8=None, up8=None, stream=None):
+    """h = silu(gate) * up of rows [rows, n]; with gate8 and up8, both Rows8, gate and up in
+    8 bits too."""
+    rows, n, dt = _rows_args(gate, "gate")
+    _need(up, gate.shape, "up")
+    _need(h, gate.shape, "h")
+    if (gate8 is None) != (up8 is None):
+        raise ValueError("gate8 and up8: both or neither")
+    at = _device(gate, "gate")
+    packed = (None,) * 4 if gate8 is None else (*_rows8_p(gate8, gate.shape, "gate8", at),
+                                                *_rows8_p(up8, gate.shape, "up8", at))
+    st = lib().moe_swiglu_forward(rows, n, dt, _p(gate, gate.dtype, "gate", at),
+                                  _p(up, gate.dtype, "up", at), _p(h, gate.dtype, "h", at),
+                                  *packed, _stream(stream, at))
+    _check(st, "moe_swiglu_forward")
+
+
+def _swiglu_in(dh, gate, up, at):
+    """gate, up, gate8, gate_scale, up8, up_scale of moe_swiglu_backward, as pointers."""
+    if isinstance(gate, Rows8):
+        return [None, None, *_rows8_p(gate, dh.shape, "gate", at),
+                *_rows8_p(up, dh.shape, "up", at)]
+    _need(gate, dh.shape, "gate")
+    _need(up, dh.shape, "up")
+    return [_p(gate, dh.dtype, "gate", at), _p(up, dh.dtype, "up", at), None, None, None, None]
+
+
+def moe_swiglu_backward(dh, gate, up, dgate, dup, h=None, stream=None):
+    """dgate, dup and, unless None, h of rows [rows, n] from dh and from gate and up, tensors of
+    dh's type or both Rows8."""
+    rows, n, dt = _rows_args(dh, "dh")
+    for t, what in ((dgate, "dgate"), (dup, "dup"), (h, "h")):
+        if t is not None:
+            _need(t, dh.shape, what)
+    at = _device(dh, "dh")
+    st = lib().moe_swiglu_backward(rows, n, dt, _p(dh, dh.dtype, "dh", at),
+                                   *_swiglu_in(dh, gate, up, at),
+                                   _p(dgate, dh.dtype, "dgate", at), _p(dup, dh.dtype, "dup", at),
+                                   _p(h, dh.dtype, "h", at), _stream(stream, at))
+    _check(st, "moe_swiglu_backward")
+
+
 def pack_rows(x) -> Rows8:
     """x [rows, n] (fp32 or bf16) in 8 bits (moe_pack_rows), in fresh tensors, on the current
     stream like all calls that make their results."""
@@ -938,12 +1003,7 @@ def swiglu_backward(dh, gate, up, want_h=False):
     tensors of that type, or both Rows8.  h is None unless wanted."""
     rows, n, dt = _rows_args(dh, "dh")
     at = _device(dh, "dh")
-    if isinstance(gate, Rows8):
-        ins = [None, None, *_rows8_p(gate, dh.shape, "gate", at), *_rows8_p(up, dh.shape, "up", at)]
-    else:
-        _need(gate, dh.shape, "gate")
-        _need(up, dh.shape, "up")
-        ins = [_p(gate, dh.dtype, "gate", at), _p(up, dh.dtype, "up", at), None, None, None, None]
+    ins = _swiglu_in(dh, gate, up, at)
     dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
     h = torch.empty_like(dh) if want_h else None
     _check(lib().moe_swiglu_backward(rows, n, dt, _p(dh, dh.dtype, "dh", at), *ins,
@@ -989,7 +1049,8 @@ def moe_gate_forward(desc, logits, topk_ids, topk_w, counts, prob, loss, ws, str
 def moe_gate_backward(desc, logits, topk_ids, counts, dtopk_w, dloss, dlogits, stream=None):
     """dlogits [T, E] from dtopk_w [T, k] and dloss [1], each unless None."""
     for t, shape, what in ((counts, (desc.E + 1,), "counts"),
-                           (dtopk_w, (desc.T, desc.k), "dtopk_w"), (dloss, (1,), "dloss"), (dlogits, (desc.T, desc.E), "dlogits")):
+                           (dtopk_w, (desc.T, desc.k), "dtopk_w"), (dloss, (1,), "dloss"),
+                           (dlogits, (desc.T, desc.E), "dlogits")):
         if t is not None:
             _need(t, shape, what)
     at, head = _gate_in(desc, logits, topk_ids)

@@ -251,6 +251,44 @@ def test_training_swiglu_compares_shapes_before_it_flattens_rows(monkeypatch):
                 training.swiglu(torch.zeros(a), torch.zeros(b), packed)
 
 
+def test_calls_with_the_callers_buffers_refuse(L, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    f32, bf16, f8 = torch.float32, torch.bfloat16, moe.FP8
+    x, q, s = ((4, 130), bf16), ((4, 130), f8), ((4, 2), f32)
+    R = moe.Rows8
+    calls = [
+        (moe.moe_pack_rows, (x, q, s)),
+        (moe.moe_unpack_rows, (q, s, x)),
+        (moe.moe_swiglu_forward, (x, x, x)),
+        (lambda g, u, h, a, b, c, d: moe.moe_swiglu_forward(g, u, h, R(a, b), R(c, d)),
+         (x, x, x, q, s, q, s)),
+        (moe.moe_swiglu_backward, (x, x, x, x, x, x)),
+        (lambda dh, a, b, c, d, e, f, h: moe.moe_swiglu_backward(dh, R(a, b), R(c, d), e, f, h),
+         (x, q, s, q, s, x, x, x))]
+    for call, shapes in calls:
+        for i, (shape, dtype) in enumerate(shapes):
+            def args(sh, t, cls=_Here):
+                return [_here(sh, t, cls) if j == i else _here(*a) for j, a in enumerate(shapes)]
+
+            with pytest.raises(ValueError, match="current device is cuda:0"):
+                call(*args(shape, dtype, _Elsewhere))
+            for bad in ((shape[0] + 1, shape[1]), (shape[0], shape[1] - 1), shape[:1]):
+                with pytest.raises(ValueError, match="shape"):
+                    call(*args(bad, dtype))
+            with pytest.raises(TypeError):
+                call(*args(shape, torch.float16))
+            with pytest.raises(ValueError, match="contiguous"):
+                a = args(shape, dtype)
+                a[i] = torch.zeros(shape[::-1], dtype=dtype).t().as_subclass(_Here)
+                call(*a)
+    t, r = _here(*x), R(_here(*q), _here(*s))
+    with pytest.raises(ValueError, match="both or neither"):
+        moe.moe_swiglu_forward(t, t, t, r)
+    for g, u in ((r, t), (t, r)):
+        with pytest.raises(TypeError):
+            moe.moe_swiglu_backward(t, g, u, t, t)
+
+
 def _here(shape, dtype, cls=_Here):
     return torch.zeros(shape, dtype=dtype).as_subclass(cls)
 

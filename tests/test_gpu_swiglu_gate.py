@@ -135,6 +135,69 @@ def test_swiglu_more_than_2_31_elements():
     assert torch.equal(dg[-1:], want[0]) and torch.equal(du[-1:], want[1])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n", [(1, 1), (5, 8), (7, 1111), (33, 2048)])
+def test_calls_with_the_callers_buffers(rows, n, dtype):
+    """The bits of the calls that make their results: in buffers that lie side by side, on another
+    stream, and in a graph that is replayed on new inputs."""
+    gate, up, dh = (rnd((rows, n), i).to(dtype) for i in (1, 2, 3))
+    want = [*moe.swiglu(gate, up, pack=True)]
+    want += [*moe.swiglu_backward(dh, *want[1:], want_h=True)]
+    want += [*moe.swiglu_backward(dh, gate, up)[:2], moe.pack_rows(dh),
+             moe.unpack_rows(moe.pack_rows(dh), dtype)]
+    room = torch.full((1 << 22,), 99, dtype=torch.uint8, device="cuda")
+    ends = []
+
+    def new(shape, t):
+        at = -(-ends[-1] // 16) * 16 if ends else 0  # the next 16-byte address
+        count = math.prod(shape)
+        ends.append(at + count * t.itemsize)
+        return room[at:ends[-1]].view(t).view(shape)
+
+    rows8 = lambda: moe.Rows8(new((rows, n), moe.FP8),  # noqa: E731
+                              new((rows, -(-n // 128)), torch.float32))
+    full = lambda: new((rows, n), dtype)  # noqa: E731
+    out = [full(), rows8(), rows8(), full(), full(), full(), full(), full(), rows8(), full()]
+
+    def run(stream=None):
+        moe.moe_swiglu_forward(gate, up, out[0], out[1], out[2], stream)
+        moe.moe_swiglu_backward(dh, out[1], out[2], out[3], out[4], out[5], stream)
+        moe.moe_swiglu_backward(dh, gate, up, out[6], out[7], stream=stream)
+        moe.moe_pack_rows(dh, out[8].q, out[8].scale, stream)
+        moe.moe_unpack_rows(out[8].q, out[8].scale, out[9], stream)
+
+    def flat(results):
+        return [t for r in results
+                for t in ((r.q.view(torch.uint8), r.scale) if isinstance(r, moe.Rows8) else (r,))]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    run(s)
+    s.synchronize()
+    for a, b in zip(flat(out), flat(want)):
+        assert torch.equal(a, b)
+    gaps = torch.ones_like(room, dtype=torch.bool)  # nothing else is written
+    start = 0
+    for end in ends:
+        gaps[start:end] = False
+        start = -(-end // 16) * 16
+    assert bool((room[gaps] == 99).all())
+    moe.moe_swiglu_forward(gate, up, out[6])  # without the 8-bit rows
+    torch.cuda.synchronize()
+    assert torch.equal(out[6], want[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    old = gate.clone()
+    gate.copy_(up)
+    up.copy_(old)
+    g.replay()
+    torch.cuda.synchronize()
+    again = [*moe.swiglu(gate, up, pack=True)]
+    for a, b in zip(flat(out[:3]), flat(again)):
+        assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- the gate
 def gate_formula(l, ids, desc, rs):
     """(w, counts, prob, loss) in 64 bits; l may require a gradient."""
