@@ -3,8 +3,8 @@
     python examples/train_layer.py [--steps 30] [--dtype bf16|f32]
 
 The layer is residual + combine(experts(dispatch(rms_norm(x)))): the norm, the routing and
-its plan, the gate weights and the balance loss, the row movement, the activation (its
-inputs kept in 8 bits) and all their gradients are the library's; the experts' products,
+its plan, the gate weights and the balance loss, the row movement, the activation (in bf16
+its inputs are kept in 8 bits) and all their gradients are the library's; the experts' products,
 which the library has forward only, are torch's here.  The matrices are updated
 by their averaged gradients made orthogonal (moe.orthogonalize, the Muon optimiser's
 update), the norm's weight by plain descent.  It fits the layer to a fixed random target
@@ -29,7 +29,9 @@ def experts(x_perm, plan, Wg, Wu, Wd):
         out = [rows[lo:hi] @ W[e].T for e, (lo, hi) in enumerate(zip(bounds, bounds[1:]))]
         return torch.cat(out + [rows.new_zeros(len(rows) - bounds[-1], W.shape[1])])
 
-    return each(training.swiglu(each(x_perm, Wg), each(x_perm, Wu)), Wd)
+    # 8-bit gate and up for the backward pass beside bf16 rows; fp32 keeps its precision
+    packed = x_perm.dtype == torch.bfloat16
+    return each(training.swiglu(each(x_perm, Wg), each(x_perm, Wu), packed), Wd)
 
 
 def forward(desc, ws, x, p):

@@ -172,3 +172,33 @@ def test_example_trains(dtype):
     losses = example.train(steps=12, dtype=dtype)
     # the target's mean square is 1, the residual's another 1: descent shows at once
     assert losses[-1] < 0.8 * losses[0] and all(v == v for v in losses)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_example_keeps_8_bit_activations_beside_bf16_only(dtype, monkeypatch):
+    """The example's gradients are those of gate and up in 8 bits in bf16, of themselves in fp32."""
+    spec = importlib.util.spec_from_file_location(
+        "train_layer", os.path.join(ROOT, "examples", "train_layer.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    T, d, E, k, I, S = 64, 128, 4, 2, 128, 1
+    desc = moe.make_desc(T, d, E, k, I, S,
+                         dtype=moe.MOE_BF16 if dtype == torch.bfloat16 else moe.MOE_F32)
+    ws = moe.alloc_workspace(desc)
+    x = rnd((T, d), 1).to(dtype)
+    shapes = {"Wr": (E, d), "Wg": (E + S, I, d), "Wu": (E + S, I, d), "Wd": (E + S, d, I)}
+    swiglu = training.swiglu
+
+    def grads():
+        p = {n: (rnd(s, 2 + i) / s[-1] ** 0.5).to(dtype).requires_grad_()
+             for i, (n, s) in enumerate(shapes.items())}
+        p["gamma"] = torch.ones(d, device="cuda", requires_grad=True)
+        y, balance = example.forward(desc, ws, x, p)
+        (y.square().mean() + balance).backward()
+        return [p[n].grad for n in ("Wr", "Wg", "Wu", "Wd", "gamma")]
+
+    got = grads()
+    for packed in (True, False):
+        monkeypatch.setattr(training, "swiglu", lambda g, u, *_: swiglu(g, u, packed))
+        same = all(torch.equal(a, b) for a, b in zip(got, grads()))
+        assert same == (packed == (dtype == torch.bfloat16))
