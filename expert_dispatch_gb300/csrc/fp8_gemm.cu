@@ -36,18 +36,20 @@
 //     shared memory before a block's products are announced, and cost the epilogue's
 //     warps one load a block (formed there they took a tenth of the time).
 //   * SM pairs (cta_group::2, 256 token rows, half of the weight rows to a CTA) were
-//     built and dropped: the tensor cores wait for the additions, not for operands
+//     built and dropped: the tensor cores do not wait for operands
 //     (8192 tokens x 8, 4096 x 1536, 32 experts: 1.5 % faster; 600 rows an expert 14 %
 //     slower, for its larger tiles).
 //   * Every wait is bounded (tc_common.cuh); that for registers ends because the launcher
 //     has checked that there are enough.
 //
 // What bounds it: with few rows an expert the weights' bytes (64 tokens, 65 experts of
-// 7168 x 2048: 420 us for 2.86 GB, 6.8 TB/s); with many the epilogue.  Reading a block's
-// 128 x 256 sums from TMEM takes 160 cycles, adding them 270 (350 without the packed
-// instruction), both together 310 where nothing else runs, and a block's MMAs 512; with
-// barriers, factors and a unit's end (SwiGLU: two special functions a value) a block
-// takes about 950.  Tensor pipe 52 % active in gate/up, 38 % in down (16384 rows).
+// 7168 x 2048: 420 us for 2.86 GB, 6.8 TB/s; on another GB300 444 us).  With many rows a
+// block takes 910 cycles in gate/up and 1310 in down, units' starts and ends included
+// (tensor pipe 52 and 38 % active, 16384 rows).  Its MMAs take 512; reading its 128 x 256
+// sums from TMEM takes 160 cycles, adding them 270 (350 without the packed instruction),
+// both together 310 where nothing else runs, beside the next block's MMAs.  What fills
+// the rest is not known; barriers, factors and a unit's end (SwiGLU: two special functions
+// a value) are in it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 

@@ -15,9 +15,10 @@
 // One warp a token, expert e on lane e % 32: a token's logits are read once, the
 // next token's while these are worked on, and all sums over experts are warp
 // butterflies.  By its bytes a pass is short (16384 x 256 fp32: 2.5 us forward, 5 us
-// backward at the copy's rate); what is left is latency: the load, three butterflies
-// and the exponentials of a token one after the other, and for the forward pass the
-// joining of the blocks' sums, a launch of its own where there are several blocks.
+// backward at the copy's rate; 11.8 and 12.2 us on the GPU); what is left is latency: the
+// load, three butterflies and the exponentials of a token one after the other, and for
+// the forward pass the joining of the blocks' sums, a launch of its own where there are
+// several blocks.
 #include <cuda_bf16.h>
 
 #include <type_traits>

@@ -120,8 +120,10 @@ __device__ __forceinline__ void store8(T* __restrict__ p, int lane, int n, const
   }
 }
 
-// 1 / (1 + exp(-z)): the fast exponential and division where the result is
-// rounded to bf16 (their relative error of a few 1e-7 is far below 2^-9).
+// 1 / (1 + exp(-z)): the fast exponential and division where the result is rounded
+// to bf16.  Their documented errors, 2 + 1.173 |z| and 2 steps of 2^-23, make at most
+// 107 steps at |z| = 88, 1.3e-5: a three-hundredth of bf16's 2^-8.  Below z = -87.3 the
+// divisor exceeds 2^126 and the result is 0: the sigmoid left out is below 2^-126.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
   return sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
